@@ -401,6 +401,169 @@ int exl3_linear_gemv_noalloc(const uint16_t *x, int k, int n, const uint16_t *tr
  */
 int exl3_noalloc_device_error(exl3_stream_t stream, int *err_out);
 
+/*
+ * Attention between the linears (no counterpart on the source pages, which
+ * leave attention to their hosts; an addition of this library): the head
+ * norms and rotary positions of queries and keys, their append to a paged
+ * cache, and the attention of new tokens over that cache.  Data is fp16 (or
+ * fp32 where stated); integer arrays need only their natural 4-byte
+ * alignment.
+ */
+
+/* Pairing of a head's rotated elements (the first rotary_dim of head_dim). */
+typedef enum {
+  EXL3_ROPE_HALF = 0,   /* element i with element i + rotary_dim / 2 */
+  EXL3_ROPE_PAIRS = 1   /* element 2 i with element 2 i + 1 */
+} exl3_rope_layout;
+
+/* Scalings of the rotary frequencies for contexts longer than trained on. */
+typedef enum {
+  EXL3_ROPE_NONE = 0,
+  EXL3_ROPE_LINEAR = 1,   /* every frequency / factor */
+  EXL3_ROPE_NTK = 2,      /* base * factor^(R / (R - 2)) */
+  EXL3_ROPE_BANDS = 3,    /* by turns within the original context, see below */
+  EXL3_ROPE_YARN = 4      /* by index between two bounds, see below */
+} exl3_rope_scaling;
+
+/*
+ * exl3_rope_frequencies -- the rotary frequencies of a model, computed on the
+ * HOST in double precision and rounded to fp32 (once, at set-up):
+ *   f_i = base^(-2 i / R), i < R / 2, R = rotary_dim (even, >= 2)
+ *   n_i = original_len * f_i / (2 pi), the turns within the trained context
+ *   BANDS  keep_i = clamp((n_i - low) / (high - low), 0, 1)
+ *   YARN   keep_i = 1 - clamp((i - a) / max(b - a, 0.001), 0, 1) with
+ *          p(n) = R ln(original_len / (2 pi n)) / (2 ln base),
+ *          a = max(0, floor(p(high))), b = min(R - 1, ceil(p(low)));
+ *          *magnitude = 0.1 ln(factor) + 1 for factor > 1
+ *          (the published YaRN interpolation; usual bounds low 1, high 32)
+ *   both   f_i = keep_i f_i + (1 - keep_i) f_i / factor
+ *   inv_freq  HOST array of R / 2 floats; magnitude  HOST float (1 unless
+ *   YARN).  original_len, low and high are read by BANDS and YARN only.
+ *   Errors: EXL3_ERR_SHAPE for R odd or < 2 (NTK: < 4); EXL3_ERR_ARG for a
+ *   NULL pointer, an unknown scaling, base <= 1, factor <= 0,
+ *   original_len < 1, or not 0 < low < high.
+ */
+int exl3_rope_frequencies(int rotary_dim, double base, int scaling, double factor, int original_len,
+                          double low, double high, float *inv_freq, float *magnitude);
+
+/* What happens to every query and key head before attention. */
+typedef struct {
+  const uint16_t *q_norm;    /* [head_dim] fp16 weights, or NULL: no query norm */
+  const uint16_t *k_norm;    /* [head_dim] fp16 weights, or NULL: no key norm */
+  float eps;                 /* of both norms, >= 0 */
+  const float *inv_freq;     /* [rotary_dim / 2] fp32 (device), or NULL with rotary_dim 0 */
+  int rotary_dim;            /* even, 0 <= rotary_dim <= head_dim */
+  int layout;                /* exl3_rope_layout */
+  float magnitude;           /* factor on the rotated part (1: a pure rotation) */
+} exl3_head_transform;
+
+/*
+ * exl3_qk_norm_rope -- head norms and rotary positions in one pass:
+ *   n = x * rsqrt(mean(x^2) + eps) * weight       per head, if it has a norm
+ *   (a, b) -> magnitude * (a cos t - b sin t, b cos t + a sin t) per pair,
+ *   t = positions[token] * inv_freq[i]; elements past rotary_dim are kept.
+ *   All arithmetic in fp32, one rounding at the output; the angle is reduced
+ *   to a turn in 64-bit fixed point, so it is exact to 2^-25 turns at every
+ *   int32 position.
+ *   q        [T][heads_q][head_dim], k [T][heads_kv][head_dim], fp16 or fp32
+ *            (in_dtype: EXL3_OUT_F16 / EXL3_OUT_F32); a token's heads are
+ *            dense, tokens are q_stride / k_stride ELEMENTS apart (a multiple
+ *            of 16 bytes).  k may be NULL with heads_kv = 0.
+ *   positions [T] int32 (device); may be NULL if rotary_dim is 0
+ *   q_out, k_out  dense [T][heads][head_dim], fp16 or fp32 (out_dtype).  They
+ *            may be q and k themselves when types and strides agree, and
+ *            must not overlap them otherwise.
+ *   head_dim 64, 128 or 256.  T = 0 enqueues nothing.  No workspace.
+ */
+int exl3_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, int in_dtype, int T,
+                      int heads_q, int heads_kv, int head_dim, const exl3_head_transform *transform,
+                      const int32_t *positions, void *q_out, void *k_out, int out_dtype, exl3_stream_t stream);
+
+/*
+ * A paged cache: element d of key head h of the token at `offset` in `page`
+ * is k[page * stride_page + offset * stride_token + h * stride_head + d],
+ * values likewise in v.  Strides are in elements and multiples of 8, so both
+ * token-major ([pages][page_size][heads][head_dim]) and head-major pages, and
+ * keys and values in one allocation, can be described.
+ */
+typedef struct {
+  uint16_t *k, *v;             /* fp16, 16-byte aligned */
+  int num_pages, page_size;    /* page_size: a multiple of 16 */
+  int heads_kv, head_dim;      /* head_dim 64, 128 or 256 */
+  int64_t stride_page, stride_token, stride_head;
+} exl3_kv_cache;
+
+/*
+ * The sequences of a call (device arrays, read by the kernels only, so one
+ * captured graph serves changing lengths).  Sequence b's new tokens are rows
+ * q_start[b] .. q_start[b + 1] - 1 of the call's T rows (q_start[0] >= 0,
+ * never decreasing); its cache holds kv_len[b] tokens, the new ones last, so
+ * row t has cache index kv_len[b] - (q_start[b + 1] - t).  Rows outside every
+ * sequence are padding.  Entry i of a page table row is the page of cache
+ * indexes i * page_size ..; entries past the sequence's end, and entries
+ * before its attention window, are never read.
+ */
+typedef struct {
+  const int32_t *q_start;      /* [batch + 1] */
+  const int32_t *kv_len;       /* [batch] */
+  const int32_t *page_table;   /* [batch][max_pages] */
+  int batch, max_pages;        /* max_pages * page_size <= 2^30 */
+} exl3_paged_batch;
+
+/*
+ * exl3_qkv_append -- norms and rotary positions as exl3_qk_norm_rope, with
+ * the keys (transformed) and values (as they are) written to the cache in the
+ * same launch and the queries to q_out.
+ *   q [T][heads_q][head_dim], k and v [T][heads_kv][head_dim] of in_dtype,
+ *   strides as above; heads_kv and head_dim are the cache's.
+ *   positions [T] int32, or NULL: a token's position is its cache index.
+ *   q_out    dense [T][heads_q][head_dim] fp16 (may be q itself as above);
+ *            padding rows are set to zero.
+ *   A token whose cache index is negative, past the page table, or whose page
+ *   is outside [0, num_pages) is recorded in the device error word
+ *   (exl3_check_device_error) and not appended (a negative index also zeroes
+ *   its q_out row).  Two tokens must not share a place in the cache.
+ *   workspace of exl3_qkv_append_workspace_size() bytes.
+ */
+size_t exl3_qkv_append_workspace_size(void);
+int exl3_qkv_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                    int64_t v_stride, int in_dtype, int T, int heads_q, const exl3_head_transform *transform,
+                    const int32_t *positions, const exl3_paged_batch *batch, const exl3_kv_cache *cache,
+                    uint16_t *q_out, void *workspace, size_t ws_bytes, exl3_stream_t stream);
+
+/*
+ * exl3_paged_attention -- attention of the new tokens over the paged cache
+ * (which holds their keys and values already):
+ *   s_ij = scale * q_i . k_j     over the cache indexes j that row i sees:
+ *          j <= its own index (causal), j > its own index - window (window >
+ *          0), j < kv_len
+ *   y_i  = sum_j softmax_j(s_ij) v_j,   lse_i = ln sum_j exp(s_ij)
+ *   Query head h reads key head h / (heads_q / heads_kv).  A row that sees
+ *   nothing (padding; an empty cache) has y = 0 and lse = -infinity.
+ *   q        [T][heads_q][head_dim] fp16, tokens q_stride elements apart
+ *   scale    > 0, finite; causal 0 or 1; window 0 (none) or > 0
+ *   y        dense [T][heads_q][head_dim], fp16 or fp32 (out_dtype)
+ *   lse      [T][heads_q] fp32, or NULL
+ *   workspace of exl3_paged_attention_workspace_size(T, heads_q, heads_kv,
+ *   head_dim, batch) bytes; 0 for an unsupported shape.
+ *   Products of fp16 values are accumulated in fp32; the weights exp(s - max)
+ *   are rounded to fp16 before they multiply v.  What lies in the cache
+ *   outside the indexes the call's rows see is ignored, NaN and infinities
+ *   included.  Values v_j seen by some rows of a sequence have to be finite:
+ *   a non-finite one may also reach rows of that sequence that do not see it.
+ *   A page outside [0, num_pages) and lengths that contradict one another
+ *   (kv_len below the number of new tokens or past the page table, q_start
+ *   outside 0 .. T or decreasing) are recorded in the device error word; such
+ *   a page reads as zeros and such lengths are clamped.
+ *   The split of a sequence over the GPU depends on the call's other
+ *   sequences, so bits may differ between batches (exl3_set_row_invariant
+ *   does not apply).  The same call gives the same bits every time.
+ */
+size_t exl3_paged_attention_workspace_size(int T, int heads_q, int heads_kv, int head_dim, int batch);
+int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q, const exl3_paged_batch *batch,
+                         const exl3_kv_cache *cache, float scale, int causal, int window, void *y, int out_dtype,
+                         float *lse, void *workspace, size_t ws_bytes, exl3_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -35,6 +35,14 @@ EXL3_CB_3INST = 3
 EXL3_OUT_F16 = 0
 EXL3_OUT_F32 = 1
 
+EXL3_ROPE_HALF = 0
+EXL3_ROPE_PAIRS = 1
+EXL3_ROPE_NONE = 0
+EXL3_ROPE_LINEAR = 1
+EXL3_ROPE_NTK = 2
+EXL3_ROPE_BANDS = 3
+EXL3_ROPE_YARN = 4
+
 _lock = threading.Lock()
 _lib = None
 
@@ -52,6 +60,26 @@ class ExpertProjMixed(ctypes.Structure):
     _fields_ = [("trellis", ctypes.c_void_p), ("suh", ctypes.c_void_p), ("svh", ctypes.c_void_p),
                 ("K", ctypes.POINTER(ctypes.c_int32)), ("k", ctypes.c_int), ("n", ctypes.c_int),
                 ("codebook", ctypes.c_int), ("nslots", ctypes.c_int)]
+
+
+class HeadTransform(ctypes.Structure):
+    """exl3_head_transform: head norms and rotary positions (device pointers)."""
+    _fields_ = [("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int),
+                ("magnitude", ctypes.c_float)]
+
+
+class KvCache(ctypes.Structure):
+    """exl3_kv_cache: a paged cache of keys and values (device pointers, strides in elements)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("heads_kv", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("stride_page", ctypes.c_int64), ("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
+
+
+class PagedBatch(ctypes.Structure):
+    """exl3_paged_batch: the sequences of a call (device arrays)."""
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("batch", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
 class Exl3Error(RuntimeError):
@@ -106,6 +134,15 @@ def lib():
         L.exl3_set_weight_prefetch.restype = I
         L.exl3_set_row_invariant.argtypes = [I]
         L.exl3_set_row_invariant.restype = I
+        L.exl3_rope_frequencies.argtypes = [I, ctypes.c_double, I, ctypes.c_double, I, ctypes.c_double,
+                                            ctypes.c_double, P, P]
+        L.exl3_qk_norm_rope.argtypes = [P, L64, P, L64, I, I, I, I, I, P, P, P, P, I, P]
+        L.exl3_qkv_append_workspace_size.argtypes = []
+        L.exl3_qkv_append_workspace_size.restype = Z
+        L.exl3_qkv_append.argtypes = [P, L64, P, L64, P, L64, I, I, I, P, P, P, P, P, P, Z, P]
+        L.exl3_paged_attention_workspace_size.argtypes = [I, I, I, I, I]
+        L.exl3_paged_attention_workspace_size.restype = Z
+        L.exl3_paged_attention.argtypes = [P, L64, I, I, P, P, ctypes.c_float, I, I, P, I, P, P, Z, P]
         _lib = L
         return L
 
@@ -445,3 +482,189 @@ def exl3_noalloc_device_error(stream=None) -> int:
     v = ctypes.c_int(0)
     _check(lib().exl3_noalloc_device_error(_stream(stream), ctypes.byref(v)))
     return v.value
+
+
+# ------------------------------------------------------------------ attention
+
+def exl3_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = EXL3_ROPE_NONE, factor: float = 1.0,
+                          original_len: int = 4096, low: float = 1.0, high: float = 32.0):
+    """Rotary frequencies of a model, (inv_freq [rotary_dim / 2] fp32 host tensor, magnitude)."""
+    f = torch.empty(max(rotary_dim // 2, 1), dtype=torch.float32)
+    mag = ctypes.c_float(1.0)
+    _check(lib().exl3_rope_frequencies(rotary_dim, base, scaling, factor, original_len, low, high,
+                                       ctypes.c_void_p(f.data_ptr()), ctypes.byref(mag)))
+    return f, mag.value
+
+
+def head_transform(q_norm=None, k_norm=None, eps: float = 1e-6, inv_freq=None, layout: int = EXL3_ROPE_HALF,
+                   magnitude: float = 1.0) -> HeadTransform:
+    """Descriptor of the head norms (fp16 weights [head_dim] or None) and the rotary
+    positions (inv_freq fp32 [rotary_dim / 2] or None); the tensors are kept alive with it."""
+    if inv_freq is not None and inv_freq.dtype != torch.float32:
+        raise TypeError(f"inv_freq must be torch.float32, got {inv_freq.dtype}")
+    p = lambda t, name, size: None if t is None else _ptr(t, name, size).value
+    d = HeadTransform(p(q_norm, "q_norm", 2), p(k_norm, "k_norm", 2), eps, p(inv_freq, "inv_freq", 4),
+                      0 if inv_freq is None else 2 * inv_freq.numel(), layout, magnitude)
+    d._keep = (q_norm, k_norm, inv_freq)
+    d._norm_sizes = tuple(None if t is None else t.numel() for t in (q_norm, k_norm))
+    return d
+
+
+def kv_cache(k, v) -> KvCache:
+    """Descriptor of a paged cache from keys and values [pages, page_size, heads_kv, head_dim]
+    fp16: any strides with dense head elements, the same for both (head-major pages and one
+    allocation for both are transposed or sliced views); the tensors are kept alive with it."""
+    for t, name in ((k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
+            raise ValueError(f"{name} must be a CUDA tensor [pages, page_size, heads_kv, head_dim]")
+        if t.element_size() != 2:
+            raise TypeError(f"{name} must have 2-byte elements, got {t.dtype}")
+        if t.stride(3) != 1:
+            raise ValueError(f"{name}'s head elements must be dense")
+    if k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError("k and v must have the same shape and strides")
+    pages, page, heads, dim = k.shape
+    # torch gives a dimension of size one any stride: use the dense one
+    stride = [s if n > 1 else heads * dim * page for s, n in zip(k.stride(), k.shape)]
+    d = KvCache(k.data_ptr(), v.data_ptr(), pages, page, heads, dim, stride[0], stride[1], stride[2])
+    d._keep = (k, v)
+    return d
+
+
+def paged_batch(q_start, kv_len, page_table) -> PagedBatch:
+    """Descriptor of a call's sequences: q_start [B + 1], kv_len [B], page_table [B, max_pages],
+    int32 on the device; the tensors are kept alive with it."""
+    for t, name in ((q_start, "q_start"), (kv_len, "kv_len"), (page_table, "page_table")):
+        if isinstance(t, torch.Tensor) and t.dtype != torch.int32:
+            raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    B, max_pages = page_table.shape
+    if q_start.shape != (B + 1,) or kv_len.shape != (B,):
+        raise ValueError(f"q_start must be [{B + 1}] and kv_len [{B}] for a page table of {B} rows")
+    d = PagedBatch(_ptr(q_start, "q_start").value, _ptr(kv_len, "kv_len").value, _ptr(page_table, "page_table").value,
+                   B, max_pages)
+    d._keep = (q_start, kv_len, page_table)
+    return d
+
+
+def _rows(t, name: str, heads: int, dim: int, dtype=None):
+    """Pointer and token stride of [T, heads, dim] rows whose heads are dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [T, {heads}, {dim}], got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    s = t.stride()
+    if (dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim):
+        raise ValueError(f"{name}'s heads must be dense")
+    return ctypes.c_void_p(t.data_ptr()), (s[0] if t.shape[0] > 1 else heads * dim)
+
+
+def _io_dtype(t, name: str) -> int:
+    if t.dtype == torch.float16:
+        return EXL3_OUT_F16
+    if t.dtype == torch.float32:
+        return EXL3_OUT_F32
+    raise TypeError(f"{name} must be torch.float16 or torch.float32, got {t.dtype}")
+
+
+def _out(t, name: str, shape, dtype):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    return _ptr(t, name)
+
+
+def _check_transform(transform: HeadTransform, dim: int):
+    for n in transform._norm_sizes:
+        if n is not None and n != dim:
+            raise ValueError(f"norm weights must have {dim} elements, got {n}")
+
+
+def exl3_qk_norm_rope(q, k, positions, transform: HeadTransform, q_out=None, k_out=None,
+                      out_dtype: int = EXL3_OUT_F16, stream=None):
+    """Head norms and rotary positions of q [T, Hq, D] and k [T, Hkv, D] (or None), fp16 or fp32;
+    positions int32 [T] (None without rotation); returns (q_out, k_out), which may be q and k."""
+    T, Hq, D = q.shape
+    Hkv = 0 if k is None else k.shape[1]
+    in_dtype = _io_dtype(q, "q")
+    odt = torch.float32 if out_dtype == EXL3_OUT_F32 else torch.float16
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=odt, device=q.device)
+    if k_out is None and k is not None:
+        k_out = torch.empty((T, Hkv, D), dtype=odt, device=q.device)
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (T,)):
+        raise ValueError(f"positions must be int32 [{T}]")
+    _check_transform(transform, D)
+    qp, qs = _rows(q, "q", Hq, D)
+    kp, ks, kop = None, 0, None
+    if k is not None:
+        if k.shape[0] != T:
+            raise ValueError(f"k must have {T} rows, got {k.shape[0]}")
+        kp, ks = _rows(k, "k", Hkv, D, q.dtype)
+        kop = _out(k_out, "k_out", (T, Hkv, D), odt)
+    if T == 0:
+        return q_out, k_out
+    _check(lib().exl3_qk_norm_rope(qp, qs, kp, ks, in_dtype, T, Hq, Hkv, D, ctypes.byref(transform),
+                                   _ptr(positions, "positions"), _out(q_out, "q_out", (T, Hq, D), odt), kop,
+                                   out_dtype, _stream(stream)))
+    return q_out, k_out
+
+
+def exl3_qkv_append_workspace_size() -> int:
+    return lib().exl3_qkv_append_workspace_size()
+
+
+def exl3_qkv_append(q, k, v, batch: PagedBatch, cache: KvCache, transform: HeadTransform, positions=None, q_out=None,
+                    workspace_buf=None, stream=None) -> torch.Tensor:
+    """Norm and rotate q [T, Hq, D], k and v [T, Hkv, D] (fp16 or fp32), write k and v to their
+    places in the cache; returns q_out [T, Hq, D] fp16.  positions int32 [T], or None for the
+    tokens' cache indexes."""
+    T, Hq, D = q.shape
+    in_dtype = _io_dtype(q, "q")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=torch.float16, device=q.device)
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (T,)):
+        raise ValueError(f"positions must be int32 [{T}]")
+    if D != cache.head_dim or k.shape[0] != T or v.shape[0] != T:
+        raise ValueError(f"q, k and v must have {T} rows of heads of {cache.head_dim}")
+    _check_transform(transform, D)
+    if T == 0:
+        return q_out
+    ws = workspace_buf if workspace_buf is not None else workspace(exl3_qkv_append_workspace_size(), q.device, stream)
+    qp, qs = _rows(q, "q", Hq, D)
+    kp, ks = _rows(k, "k", cache.heads_kv, D, q.dtype)
+    vp, vs = _rows(v, "v", cache.heads_kv, D, q.dtype)
+    _check(lib().exl3_qkv_append(qp, qs, kp, ks, vp, vs, in_dtype, T, Hq, ctypes.byref(transform),
+                                 _ptr(positions, "positions"), ctypes.byref(batch), ctypes.byref(cache),
+                                 _out(q_out, "q_out", (T, Hq, D), torch.float16), _ptr(ws, "workspace"),
+                                 ws.numel() * ws.element_size(), _stream(stream)))
+    return q_out
+
+
+def exl3_paged_attention_workspace_size(T: int, heads_q: int, heads_kv: int, head_dim: int, batch: int) -> int:
+    return lib().exl3_paged_attention_workspace_size(T, heads_q, heads_kv, head_dim, batch)
+
+
+def exl3_paged_attention(q, batch: PagedBatch, cache: KvCache, scale: float | None = None, causal: bool = True,
+                         window: int = 0, out_dtype: int = EXL3_OUT_F16, y=None, lse=None, workspace_buf=None,
+                         stream=None) -> torch.Tensor:
+    """Attention of the new tokens q [T, Hq, D] fp16 over the paged cache that already holds their
+    keys and values; returns y [T, Hq, D].  scale defaults to D ** -0.5; window > 0 keeps the last
+    `window` tokens; lse, if given, is an fp32 [T, Hq] output (natural logarithm)."""
+    T, Hq, D = q.shape
+    odt = torch.float32 if out_dtype == EXL3_OUT_F32 else torch.float16
+    if y is None:
+        y = torch.empty((T, Hq, D), dtype=odt, device=q.device)
+    if D != cache.head_dim:
+        raise ValueError(f"q has heads of {D}, the cache of {cache.head_dim}")
+    qp, qs = _rows(q, "q", Hq, D, torch.float16)
+    if T == 0:
+        return y
+    need = exl3_paged_attention_workspace_size(T, Hq, cache.heads_kv, D, batch.batch)
+    ws = workspace_buf if workspace_buf is not None else workspace(need, q.device, stream)
+    _check(lib().exl3_paged_attention(qp, qs, T, Hq, ctypes.byref(batch), ctypes.byref(cache),
+                                      D ** -0.5 if scale is None else scale, 1 if causal else 0, window,
+                                      _out(y, "y", (T, Hq, D), odt), out_dtype,
+                                      None if lse is None else _out(lse, "lse", (T, Hq), torch.float32),
+                                      _ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)))
+    return y

@@ -9,6 +9,7 @@
 #include <string>
 #include <vector>
 
+#include "api_util.cuh"
 #include "exl3_common.cuh"
 
 // ---- kernels (other translation units)
@@ -85,6 +86,9 @@ int exl3_launch_moe_fused_down(const uint16_t *hin, int U, int hidden, int inter
 // ---------------------------------------------------------------- errors --
 
 static thread_local std::string g_last_error;
+
+void exl3_clear_error() { g_last_error.clear(); }
+
 static std::atomic<int> g_weight_prefetch{0};
 static std::atomic<int> g_row_invariant{0};
 
@@ -150,36 +154,11 @@ cudaError_t exl3_ensure_smem(const void *kfn, size_t bytes, std::atomic<size_t> 
   return cudaSuccess;
 }
 
-#define EXL3_TRY(expr)            \
-  do {                            \
-    int _rc = (expr);             \
-    if (_rc != EXL3_OK) return _rc; \
-  } while (0)
-
 namespace {
 
-constexpr size_t kAlign = 256;
-constexpr size_t kCtrlBytes = 256;   // device error word and reserved control words
-// Arrival counters live at one fixed place of every workspace, right after
-// the control block, so calls of any shape find them zero (each call resets
-// the counters it used).  Capacity bounds n / 128 of one call.
-constexpr size_t kMaxCounters = 8192;
-constexpr size_t kCounterOff = kCtrlBytes;
-constexpr size_t kDataOff = kCounterOff + kMaxCounters * sizeof(int);
 constexpr int kFusedMaxM = 128;      // 2 <= M <= this: fused decode + tcgen05; above: reconstruct + tcgen05
 constexpr int kRowInvChunk = 32;     // row-invariant mode: MMA width and rows per fused launch
 constexpr int kMaxGemvK = 49152;     // the M = 1 GEMV keeps x' for all of k in shared memory
-
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-
-int check_ptr(const void *p, const char *name, bool required = true) {
-  if (!p) return required ? exl3_fail(EXL3_ERR_ARG, "%s is NULL", name) : EXL3_OK;
-  if (!aligned16(p)) return exl3_fail(EXL3_ERR_ARG, "%s is not 16-byte aligned", name);
-  return EXL3_OK;
-}
 
 int check_bits_codebook(int K, int codebook) {
   if (codebook == EXL3_CB_MCG || codebook == EXL3_CB_3INST)
@@ -443,20 +422,6 @@ bool mixed_gemv_plan(size_t U, int E, int hidden, int inter, const exl3_expert_p
   }
   *partial_floats = pmax;
   return true;
-}
-
-int check_workspace(const void *ws, size_t have, size_t need) {
-  if (need == 0) return EXL3_OK;
-  if (!ws) return exl3_fail(EXL3_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", need);
-  if ((reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0)
-    return exl3_fail(EXL3_ERR_WORKSPACE, "workspace must be %zu-byte aligned", kAlign);
-  if (have < need) return exl3_fail(EXL3_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", have, need);
-  return EXL3_OK;
-}
-
-template <typename T>
-T *at(void *base, size_t off) {
-  return reinterpret_cast<T *>(static_cast<char *>(base) + off);
 }
 
 }  // namespace
