@@ -14,6 +14,11 @@ int exl3_attn_step_keys();
 int exl3_attn_step_grid(int D);
 cudaError_t exl3_launch_attn_step(const CUtensorMap &mk, const CUtensorMap &mv, const exl3::attn::Args &a, int D,
                                   cudaStream_t s);
+int exl3_attn_tc_rows(int D);
+int exl3_attn_tc_keys(int D);
+int exl3_attn_tc_grid();
+cudaError_t exl3_launch_attn_tc(const CUtensorMap &mk, const CUtensorMap &mv, const exl3::attn::Args &a, int D,
+                                cudaStream_t s);
 
 namespace {
 
@@ -117,13 +122,16 @@ int cache_map(CUtensorMap *m, const exl3_kv_cache *c, const void *base, int box,
 // that a CTA shares with its neighbours, two per CTA
 struct AttnWs {
   size_t part_o = 0, part_lse = 0, total = 0;
-  int grid = 0;
 };
 
-AttnWs attn_ws(int D) {
+// Few rows per sequence and key head take the step kernel (16 rows a unit),
+// more the tensor-core kernel (128 rows a tile).
+bool few_rows(int T, int G, int batch) { return (int64_t)T * G <= (int64_t)exl3_attn_step_rows() * batch; }
+
+AttnWs attn_ws(int T, int G, int D, int batch) {
   AttnWs w;
-  w.grid = exl3_attn_step_grid(D);
-  const size_t rows = (size_t)w.grid * 2 * exl3_attn_step_rows();
+  const size_t rows = few_rows(T, G, batch) ? (size_t)exl3_attn_step_grid(D) * 2 * exl3_attn_step_rows()
+                                            : (size_t)exl3_attn_tc_grid() * 2 * exl3_attn_tc_rows(D);
   size_t off = kDataOff;
   w.part_o = off;
   off = align_up(off + sizeof(float) * rows * D);
@@ -273,7 +281,7 @@ int exl3_qkv_append(const void *q, int64_t q_stride, const void *k, int64_t k_st
 
 size_t exl3_paged_attention_workspace_size(int T, int heads_q, int heads_kv, int head_dim, int batch) {
   if (!attn_shape_ok(T, heads_q, heads_kv, head_dim, batch)) return 0;
-  return attn_ws(head_dim).total;
+  return attn_ws(T, heads_q / heads_kv, head_dim, batch).total;
 }
 
 int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q, const exl3_paged_batch *batch,
@@ -292,8 +300,9 @@ int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q
   if (!(scale > 0.0f) || !std::isfinite(scale)) return exl3_fail(EXL3_ERR_ARG, "scale must be > 0 and finite");
   if (causal != 0 && causal != 1) return exl3_fail(EXL3_ERR_ARG, "causal %d invalid", causal);
   if (window < 0) return exl3_fail(EXL3_ERR_ARG, "window = %d < 0", window);
-  const int D = cache->head_dim;
-  const AttnWs L = attn_ws(D);
+  const int D = cache->head_dim, G = heads_q / cache->heads_kv;
+  const bool few = few_rows(T, G, batch->batch);
+  const AttnWs L = attn_ws(T, G, D, batch->batch);
   EXL3_TRY(check_workspace(workspace, ws_bytes, L.total));
   if (T == 0) return EXL3_OK;
   exl3::attn::Args a = {};
@@ -302,7 +311,7 @@ int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q
   a.T = T;
   a.Hq = heads_q;
   a.Hkv = cache->heads_kv;
-  a.G = heads_q / cache->heads_kv;
+  a.G = G;
   a.q_start = batch->q_start;
   a.kv_len = batch->kv_len;
   a.table = batch->page_table;
@@ -310,7 +319,7 @@ int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q
   a.max_pages = batch->max_pages;
   a.page_size = cache->page_size;
   a.num_pages = cache->num_pages;
-  a.box = std::gcd(cache->page_size, exl3_attn_step_keys());
+  a.box = std::gcd(cache->page_size, few ? exl3_attn_step_keys() : exl3_attn_tc_keys(D));
   a.head_first = cache->stride_head < cache->stride_token;
   a.scale_log2 = scale * 1.44269504088896340736f;
   a.causal = causal;
@@ -326,7 +335,8 @@ int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q
   CUtensorMap mk, mv;
   EXL3_TRY(cache_map(&mk, cache, cache->k, a.box, a.head_first));
   EXL3_TRY(cache_map(&mv, cache, cache->v, a.box, a.head_first));
-  return exl3_cuda_check(exl3_launch_attn_step(mk, mv, a, D, stream), "attention launch");
+  return exl3_cuda_check(few ? exl3_launch_attn_step(mk, mv, a, D, stream) : exl3_launch_attn_tc(mk, mv, a, D, stream),
+                         "attention launch");
 }
 
 }  // extern "C"

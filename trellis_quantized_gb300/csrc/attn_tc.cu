@@ -1,0 +1,615 @@
+// attn_tc.cu -- attention of chunks of new tokens over a paged cache on the
+// 5th-generation tensor cores.
+//
+//   S = Q K^T,  P = exp2(S scale_log2 - base),  O += P V,  y = O / sum(P)
+//
+// A unit holds up to 256 rows (D <= 128) or 128 rows (D = 256) of one key
+// head and walks over its keys in blocks of 128: 4 D operations per row and
+// key against 4 D bytes per key, so from about 280 rows per byte-bound key on
+// the tensor cores are the limit.  Both products are tcgen05.mma: Q and K
+// from shared memory into a TMEM slot of 128 x 128 fp32 scores; the softmax
+// warps read the slot (a thread per row), write the fp16 weights over its
+// first half, and the second product takes them from there (A operand in
+// TMEM) with V as it lies in the cache (an MN-major operand: no transposition
+// anywhere) into O, which stays in TMEM for the whole unit.
+//
+// Two slots keep the tensor cores busy while the exponentials run: a unit of
+// more than 128 rows has two row tiles with a slot and a softmax warpgroup
+// each, and the MMAs of one tile run during the softmax of the other; a unit
+// of one tile gives its blocks to the slots in turn, and the scores of the
+// next block are computed during the softmax of this one.
+//
+// The running maximum moves only when it has grown by more than a factor of
+// 2^8 (in the weights; fp16 holds 2^15): then O is read, scaled and written
+// back, which is rare after the first blocks.  Sums, maxima, S and O are
+// fp32; the weights are rounded to fp16 once.
+//
+// Blocks in which some row sees not all keys are masked; their V rows that no
+// row of the unit sees are zeroed in shared memory first, since 0 * NaN would
+// not be 0.
+#include <cudaTypedefs.h>
+
+#include "attn_common.cuh"
+#include "tc_ptx.cuh"
+
+int exl3_attn_tc_grid();
+
+namespace exl3 {
+namespace attn {
+
+constexpr int kTcKeys = 128;
+constexpr float kLazy = 8.0f;      // log2 of the growth that moves the maximum
+
+template <int D>
+struct TcCfg {
+  static constexpr int NQ = D == 256 ? 1 : 2;            // row tiles of a unit
+  static constexpr int ROWS = NQ * 128;
+  static constexpr int OPS = D == 256 ? 2 : 1;           // ring stages of one operand
+  static constexpr int KPARTS_D = D / OPS;               // K part: 128 keys x this many columns
+  static constexpr int VPART_KEYS = kTcKeys / OPS;       // V part: this many keys x D columns
+  static constexpr int STAGE = kTcKeys * D * 2 / OPS;    // 16 KB (D = 64) or 32 KB
+  static constexpr int ST = D == 64 ? 8 : 5;
+  static constexpr int QTILE = 128 * D * 2;
+  static constexpr int QPANEL = 128 * 128;               // 64 columns of 128 rows
+  static constexpr int OFF_RING = NQ * QTILE;
+  static constexpr int SMEM = OFF_RING + ST * STAGE + 1024 /*alignment*/;
+  static constexpr int SM_WARPS = 4 * NQ;                // softmax warps
+  // softmax warpgroups, then one warpgroup with the MMA issuer and the
+  // producer; registers move from the latter to the former (the sum over the
+  // warpgroups is what the launch allots: 3 x 168 or 2 x 248)
+  static constexpr int THREADS = (SM_WARPS + 4) * 32;
+  static constexpr int REGS_SM = NQ == 2 ? 208 : 248, REGS_IO = NQ == 2 ? 88 : 248;
+  static constexpr uint32_t TM_S = 0, TM_O = 256;        // TMEM columns
+  static constexpr uint32_t IDESC_S = tc::idesc_f16(128, kTcKeys);
+  static constexpr uint32_t IDESC_O = tc::idesc_f16(128, D) | (1u << 16);   // B (V) is MN-major
+};
+
+// D[tmem] (+)= A[tmem] * B[smem]: the weights are the A operand.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// MN-major operand, 128-byte swizzle: rows of 64 elements (128 bytes) along
+// N, 8-row atoms of 1024 bytes along K, the next 64 elements `panel` bytes on.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t addr, uint32_t panel) {
+  uint64_t d = 0;
+  d |= (addr >> 4) & 0x3FFFull;
+  d |= (uint64_t)((panel >> 4) & 0x3FFF) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+__device__ __forceinline__ uint64_t sdesc_k_sw128(uint32_t addr) {
+  return ((addr >> 4) & 0x3FFFull) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
+      "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
+      "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap *m, uint64_t *bar, int x, int c1,
+                                               int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(tc::smem_u32(bar)), "r"(x), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void set_registers(bool more) {
+  if (more) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// How often each of the two slots has been given scores.
+struct Uses {
+  int u0 = 0, u1 = 0;
+  __device__ __forceinline__ int get(int s) const { return s ? u1 : u0; }
+  __device__ __forceinline__ void add(int s, int n) {
+    if (s) u1 += n;
+    else u0 += n;
+  }
+};
+
+// One CTA's run of the line: segments of units, the same for every role.
+template <int D>
+struct Run {
+  Walk w;
+  int blk, left, nseg;
+  __device__ __forceinline__ void begin(const Args &a, const Share &sh) {
+    left = 0;
+    const long long start = sh.per * blockIdx.x;
+    if (start >= sh.total || sh.b >= a.B) return;
+    left = (int)min(sh.per, sh.total - start);
+    seek<TcCfg<D>::ROWS, kTcKeys>(a, w, sh.b, sh.off, &blk);
+    nseg = min(w.nblk - blk, left);
+  }
+  __device__ __forceinline__ void advance(const Args &a) {
+    left -= nseg;
+    blk = 0;
+    if (left > 0) {
+      w.next<TcCfg<D>::ROWS, kTcKeys>(a);
+      nseg = min(w.nblk, left);
+    }
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Args a) {
+  using C = TcCfg<D>;
+  constexpr int ST = C::ST, OPS = C::OPS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[ST], empty[ST], s_full[2], p_full[2], pv_done[2], q_full[2];
+  __shared__ Share share;
+  __shared__ long long warp_sums[C::THREADS / 32];
+  __shared__ int last_arrival[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  const uint32_t raw = tc::smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  const uint32_t ring = sbase + C::OFF_RING;
+  volatile int *abort_flag = &abort_word;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < ST; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(&s_full[s], 1);
+      tc::mbar_init(&p_full[s], 4);
+      tc::mbar_init(&pv_done[s], 1);
+      tc::mbar_init(&q_full[s], 4);
+    }
+    abort_word = 0;
+    tc::fence_mbar_init();
+    tc::prefetch_tmap(&tmK);
+    tc::prefetch_tmap(&tmV);
+  }
+  if (warp == C::SM_WARPS) {
+    tc::tmem_alloc(&tmem_slot, 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  pdl_trigger();
+  pdl_wait();
+  make_share<C::ROWS, kTcKeys, C::THREADS>(a, 2, &share, warp_sums);
+  clear_padding<D>(a, C::THREADS);
+
+  // A wait that runs out records the error; every later wait then returns at
+  // once, so that all roles run through their loops and the CTA ends.
+  const auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (*abort_flag) return;
+    if (!tc::mbar_wait(bar, parity)) {
+      set_device_error(a.err, kErrBounds);
+      *abort_flag = 1;
+    }
+  };
+
+  Run<D> run;
+  run.begin(a, share);
+
+  // (every warp of a warpgroup moves its registers, at the head of its role)
+  if (warp == C::SM_WARPS + 1) {
+    // ============================================================ producer
+    if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
+    int it = 0;
+    bool stop = false;
+    for (; run.left > 0 && !stop; run.advance(a)) {
+      const Walk &w = run.w;
+      for (int j = 0; j < run.nseg && !stop; ++j) {
+        const int key0 = (w.lo / kTcKeys + run.blk + j) * kTcKeys;
+#pragma unroll 1
+        for (int part = 0; part < 2 * OPS && !stop; ++part, ++it) {
+          const bool isv = part >= OPS;
+          const int p = isv ? part - OPS : part;
+          // keys of this part, and the boxes of it that some row sees
+          const int nkeys = isv ? C::VPART_KEYS : kTcKeys, npan = isv ? D / 64 : C::KPARTS_D / 64;
+          const int base = key0 + (isv ? p * C::VPART_KEYS : 0);
+          const int k_lo = max(w.lo, base), k_hi = min(w.hi, base + nkeys);
+          const int box0 = k_hi > k_lo ? (k_lo - base) / a.box : 0;
+          const int nbox = k_hi > k_lo ? (k_hi - base + a.box - 1) / a.box - box0 : 0;
+          const bool mine = lane < nbox * npan;
+          const int bx = box0 + lane / npan, panel = lane % npan;
+          int page = 0, off = 0;
+          if (mine) {
+            const int key = base + bx * a.box, pi = key / a.page_size;
+            off = key - pi * a.page_size;
+            page = __ldg(a.table + (int64_t)w.b * a.max_pages + pi);
+            if ((unsigned)page >= (unsigned)a.num_pages) {
+              set_device_error(a.err, kErrBounds);
+              page = a.num_pages;            // past the map's end: reads as zeros
+            }
+          }
+          const int s = it % ST;
+          if (it >= ST) wait(&empty[s], ((it / ST) & 1) ^ 1);
+          __syncwarp();
+          if (__any_sync(0xffffffffu, *abort_flag != 0)) {
+            stop = true;
+            break;
+          }
+          if (lane == 0) {
+            const uint32_t bytes = (uint32_t)(nbox * a.box * 128 * npan);
+            if (bytes) tc::mbar_arrive_expect_tx(&full[s], bytes);
+            else tc::mbar_arrive(&full[s]);
+          }
+          __syncwarp();
+          if (mine) {
+            const uint32_t dst = ring + s * C::STAGE + panel * (nkeys * 128) + bx * a.box * 128;
+            const int x = (isv ? panel : p * (C::KPARTS_D / 64) + panel) * 64;
+            const CUtensorMap *m = isv ? &tmV : &tmK;
+            if (a.head_first) tma_load_4d_at(dst, m, &full[s], x, w.h, off, page);
+            else tma_load_4d_at(dst, m, &full[s], x, off, w.h, page);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (stop)                                // leave no copy in flight behind
+      for (int i = max(0, it - ST); i < it; ++i) tc::mbar_wait(&full[i % ST], (i / ST) & 1);
+  } else if (warp == C::SM_WARPS) {
+    // ========================================================== MMA issuer
+    if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
+    int it = 0;
+    Uses use;
+    const auto issue_s = [&](int t, int slot, int kit) {
+      // the slot's last weights have to be consumed first
+      if (use.get(slot) > 0) wait(&pv_done[slot], (use.get(slot) - 1) & 1);
+      for (int p = 0; p < OPS; ++p) wait(&full[(kit + p) % ST], ((kit + p) / ST) & 1);
+      __syncwarp();
+      tc::tc_fence_after();
+      if (tc::elect_one()) {
+#pragma unroll
+        for (int p = 0; p < OPS; ++p) {
+          const uint32_t ks = ring + ((kit + p) % ST) * C::STAGE;
+          const uint32_t qs = sbase + t * C::QTILE + p * (C::KPARTS_D / 64) * C::QPANEL;
+#pragma unroll
+          for (int kk = 0; kk < C::KPARTS_D / 16; ++kk) {
+            const uint32_t o = (kk / 4) * C::QPANEL + (kk % 4) * 32;
+            tc::mma_f16(tmem + C::TM_S + slot * 128, sdesc_k_sw128(qs + o), sdesc_k_sw128(ks + o), C::IDESC_S,
+                        (p | kk) ? 1u : 0u);
+          }
+        }
+        tc::mma_commit(&s_full[slot]);
+      }
+      __syncwarp();
+      use.add(slot, 1);
+    };
+    const auto issue_pv = [&](int t, int slot, int vit, bool first) {
+      wait(&p_full[slot], (use.get(slot) - 1) & 1);
+      for (int p = 0; p < OPS; ++p) wait(&full[(vit + p) % ST], ((vit + p) / ST) & 1);
+      __syncwarp();
+      tc::tc_fence_after();
+      if (tc::elect_one()) {
+#pragma unroll
+        for (int p = 0; p < OPS; ++p) {
+          const uint32_t vs = ring + ((vit + p) % ST) * C::STAGE;
+#pragma unroll
+          for (int kk = 0; kk < C::VPART_KEYS / 16; ++kk)
+            mma_f16_ts(tmem + C::TM_O + t * D, tmem + C::TM_S + slot * 128 + (p * C::VPART_KEYS / 16 + kk) * 8,
+                       sdesc_mn_sw128(vs + kk * 2048, C::VPART_KEYS * 128), C::IDESC_O,
+                       (!first || p || kk) ? 1u : 0u);
+        }
+        tc::mma_commit(&pv_done[slot]);
+      }
+      __syncwarp();
+    };
+    const auto release = [&](int i0) {       // an operand's stages, once the MMAs issued so far are done
+      if (tc::elect_one())
+        for (int p = 0; p < OPS; ++p) tc::mma_commit(&empty[(i0 + p) % ST]);
+      __syncwarp();
+    };
+    int qphase0 = 0, qphase1 = 0;
+    for (; run.left > 0; run.advance(a)) {
+      const int n = run.nseg;
+      const bool two = C::NQ == 2 && run.w.rows > 128;
+      const auto kit = [&](int j) { return it + 2 * OPS * j; };
+      const auto vit = [&](int j) { return it + 2 * OPS * j + OPS; };
+      wait(&q_full[0], qphase0++ & 1);
+      if (two) {
+        issue_s(0, 0, kit(0));
+        wait(&q_full[1], qphase1++ & 1);
+        issue_s(1, 1, kit(0));
+        release(kit(0));
+        for (int j = 0; j < n; ++j) {
+          issue_pv(0, 0, vit(j), j == 0);
+          if (j + 1 < n) issue_s(0, 0, kit(j + 1));
+          issue_pv(1, 1, vit(j), j == 0);
+          release(vit(j));
+          if (j + 1 < n) {
+            issue_s(1, 1, kit(j + 1));
+            release(kit(j + 1));
+          }
+        }
+      } else {
+        issue_s(0, 0, kit(0));
+        release(kit(0));
+        for (int j = 0; j < n; ++j) {
+          if (j + 1 < n) {
+            issue_s(0, (j + 1) & 1, kit(j + 1));
+            release(kit(j + 1));
+          }
+          issue_pv(0, j & 1, vit(j), j == 0);
+          release(vit(j));
+        }
+      }
+      it += 2 * OPS * n;
+    }
+  } else if (warp < C::SM_WARPS) {
+    // ============================================================= softmax
+    if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_SM>(true);
+    const int t = warp / 4;                  // row tile
+    const int wl = warp & 3;
+    const uint32_t lanes = (uint32_t)(wl * 32) << 16;
+    const int row = wl * 32 + lane;          // within the tile
+    const int ltid = tid - t * 128;
+    int it = 0;
+    Uses use;
+    const long long line_end =
+        share.per * blockIdx.x + min(share.per, share.total - share.per * (long long)blockIdx.x);
+    const auto group_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory"); };
+    for (; run.left > 0; run.advance(a)) {
+      const Walk &w = run.w;
+      const int n = run.nseg;
+      const bool two = C::NQ == 2 && w.rows > 128;
+      if (t == 1 && !two) {
+        // a unit of one tile uses both slots: follow the second one's phases
+        for (int j = 1; j < n; j += 2) wait(&s_full[1], use.u1++ & 1);
+        use.u0 += (n + 1) / 2;
+        it += 2 * OPS * n;
+        continue;
+      }
+      // ---- this tile's rows of q
+      const int t0 = w.r0 + t * 128;
+      const int rows = min(128, w.rows - t * 128);
+      for (int i = ltid; i < 128 * (D / 8); i += 128) {
+        const int r = i / (D / 8), c8 = i % (D / 8);
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (r < rows) {
+          const int tok = (t0 + r) / a.G;
+          u = *reinterpret_cast<const uint4 *>(a.q + (int64_t)(w.s.t0 + tok) * a.q_stride +
+                                               (int64_t)(w.h * a.G + t0 + r - tok * a.G) * D + c8 * 8);
+        }
+        const uint32_t dst = sbase + t * C::QTILE + (c8 >> 3) * C::QPANEL + r * 128 + (((c8 & 7) ^ (r & 7)) << 4);
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w)
+                     : "memory");
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&q_full[t]);
+
+      int lo = 0, hi = 0, all_lo, all_hi, tmp;
+      if (row < rows) row_range(a, w.s, t0 + row, lo, hi);
+      row_range(a, w.s, t0, tmp, all_hi);
+      row_range(a, w.s, t0 + rows - 1, all_lo, tmp);
+
+      float m = neg_inf(), l = 0.0f;         // the exponent's base (in scores) and the sum of weights
+      int last_slot = 0, last_use = 0;
+      for (int j = 0; j < n; ++j) {
+        const int slot = two ? t : (j & 1);
+        const int u = use.get(slot);
+        use.add(slot, 1);
+        const int key0 = (w.lo / kTcKeys + run.blk + j) * kTcKeys;
+        if (key0 < w.lo || key0 + kTcKeys > w.hi) {
+          // V rows that no row of the unit sees: zeros
+          const int vi = it + 2 * OPS * j + OPS + ltid / C::VPART_KEYS;
+          wait(&full[vi % ST], (vi / ST) & 1);
+          const int key = key0 + ltid;
+          if (key < w.lo || key >= w.hi) {
+            const uint32_t dst = ring + (vi % ST) * C::STAGE + (ltid % C::VPART_KEYS) * 128;
+#pragma unroll
+            for (int p = 0; p < D / 64; ++p)
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + p * C::VPART_KEYS * 128 + c * 16),
+                             "r"(0)
+                             : "memory");
+          }
+          fence_async_shared();
+        }
+        wait(&s_full[slot], u & 1);
+        __syncwarp();
+        tc::tc_fence_after();
+        float s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          tc::tmem_ld32(tmem + C::TM_S + slot * 128 + lanes + 32 * c, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[32 * c + i] = v[i];
+        }
+        tc::tmem_ld_wait();
+        if (key0 < all_lo || key0 + kTcKeys > all_hi) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (key0 + i < lo || key0 + i >= hi) s[i] = neg_inf();
+        }
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = s[i];
+#pragma unroll
+        for (int i = 8; i < 128; ++i) x[i & 7] = fmaxf(x[i & 7], s[i]);
+        const float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+        const bool grow = m != neg_inf() && (mx - m) * a.scale_log2 > kLazy;
+        if (__any_sync(0xffffffffu, grow)) {
+          // O so far has to be complete before it is scaled
+          wait(&pv_done[last_slot], last_use & 1);
+          __syncwarp();
+          tc::tc_fence_after();
+          const float f = grow ? exp2_approx((m - mx) * a.scale_log2) : 1.0f;
+          l *= f;
+          if (grow) m = mx;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float v[32];
+            tc::tmem_ld32(tmem + C::TM_O + t * D + lanes + 32 * c, v);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= f;
+            tc::tmem_st32(tmem + C::TM_O + t * D + lanes + 32 * c, v);
+          }
+          tc::tmem_st_wait();
+        }
+        if (m == neg_inf()) m = mx;          // a row's first keys: O and the sum are zero
+        const float base = m == neg_inf() ? 0.0f : m * a.scale_log2;
+        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nb2 = make_float2(-base, -base);
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float2 e = __ffma2_rn(make_float2(s[64 * c + 2 * i], s[64 * c + 2 * i + 1]), sc2, nb2);
+            const float2 p = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+            sum[i & 1] = __fadd2_rn(sum[i & 1], p);
+            const __half2 h = __floats2half2_rn(p.x, p.y);
+            pk[i] = *reinterpret_cast<const uint32_t *>(&h);
+          }
+          tmem_st32u(tmem + C::TM_S + slot * 128 + lanes + 32 * c, pk);
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&p_full[slot]);
+        last_slot = slot;
+        last_use = u;
+      }
+      if (two) use.add(1 - t, n);
+      it += 2 * OPS * n;
+
+      // ---- O complete: y, or this CTA's part of it
+      wait(&pv_done[last_slot], last_use & 1);
+      __syncwarp();
+      tc::tc_fence_after();
+      const bool whole = n == w.nblk;
+      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);      // (NaN stays)
+      const float lse2 = l == 0.0f ? neg_inf() : m * a.scale_log2 + log2f(l);
+      const int slot_out = run.blk == 0 ? 1 : 0;
+      const int tok = (t0 + row) / a.G;
+      const int64_t head = (int64_t)(w.s.t0 + tok) * a.Hq + w.h * a.G + (t0 + row) - tok * a.G;
+      const int64_t pr = ((int64_t)blockIdx.x * 2 + slot_out) * C::ROWS + t * 128 + row;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float v[32];
+        tc::tmem_ld32(tmem + C::TM_O + t * D + lanes + 32 * c, v);
+        tc::tmem_ld_wait();
+        if (row < rows) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 o = make_float4(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv);
+            if (whole) store4(a, head * D + 32 * c + i, o);
+            else *reinterpret_cast<float4 *>(a.part_o + pr * D + 32 * c + i) = o;
+          }
+        }
+      }
+      if (row < rows) {
+        if (!whole) a.part_lse[pr] = lse2;
+        else if (a.lse) a.lse[head] = lse2 * 0.69314718055994530942f;
+      }
+      tc::tc_fence_before();
+      if (!whole) {
+        // ---- the CTA that arrives last adds the parts in line order
+        const long long unit0 = line_end - run.left - run.blk;
+        const int c0 = (int)(unit0 / share.per), c1 = (int)((unit0 + w.nblk - 1) / share.per);
+        __threadfence();
+        group_sync();
+        if (ltid == 0) {
+          const int parts = c1 - c0 + 1, old = atomicAdd(a.counters + c0 * 2 + t, 1);
+          if (old >= parts) set_device_error(a.err, kErrDirtyCounter);
+          last_arrival[t] = old == parts - 1;
+          if (old >= parts - 1) a.counters[c0 * 2 + t] = 0;
+        }
+        group_sync();
+        if (last_arrival[t]) {
+          __threadfence();
+          for (int i = ltid; i < rows * (D / 4); i += 128) {
+            const int r = i / (D / 4), c4 = (i % (D / 4)) * 4;
+            const auto part = [&](int c) { return ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * C::ROWS + t * 128 + r; };
+            float mr = neg_inf();
+            for (int c = c0; c <= c1; ++c) mr = fmaxf(mr, __ldcg(a.part_lse + part(c)));
+            float sum = 0.0f;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) {
+              const float ls = __ldcg(a.part_lse + part(c));
+              const float f = ls == neg_inf() ? 0.0f : exp2_approx(ls - mr);
+              const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + part(c) * D + c4));
+              sum += f;
+              acc.x = fmaf(f, v.x, acc.x);
+              acc.y = fmaf(f, v.y, acc.y);
+              acc.z = fmaf(f, v.z, acc.z);
+              acc.w = fmaf(f, v.w, acc.w);
+            }
+            const float iv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+            const int tk = (t0 + r) / a.G;
+            const int64_t hd = (int64_t)(w.s.t0 + tk) * a.Hq + w.h * a.G + (t0 + r) - tk * a.G;
+            store4(a, hd * D + c4, make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv));
+            if (a.lse && c4 == 0)
+              a.lse[hd] = sum == 0.0f ? neg_inf() : (mr + log2f(sum)) * 0.69314718055994530942f;
+          }
+        }
+        group_sync();
+      }
+    }
+  } else {
+    if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == C::SM_WARPS) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_tc(const CUtensorMap &mk, const CUtensorMap &mv, const Args &a, cudaStream_t s) {
+  static std::atomic<size_t> per_dev[kMaxDevices];
+  cudaError_t e = exl3_ensure_smem(reinterpret_cast<const void *>(attn_tc_kernel<D>), TcCfg<D>::SMEM, per_dev);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_tc_kernel<D>, dim3(exl3_attn_tc_grid()), dim3(TcCfg<D>::THREADS), TcCfg<D>::SMEM, s, mk, mv,
+                    a);
+}
+
+}  // namespace attn
+}  // namespace exl3
+
+int exl3_attn_tc_rows(int D) { return D == 256 ? 128 : 256; }
+// Keys that one tensor copy must not straddle: a block, or a part of its V.
+int exl3_attn_tc_keys(int D) { return D == 256 ? 64 : exl3::attn::kTcKeys; }
+int exl3_attn_tc_grid() { return exl3_sm_count(); }
+
+cudaError_t exl3_launch_attn_tc(const CUtensorMap &mk, const CUtensorMap &mv, const exl3::attn::Args &a, int D,
+                                cudaStream_t s) {
+  using namespace exl3::attn;
+  switch (D) {
+    case 64: return launch_tc<64>(mk, mv, a, s);
+    case 128: return launch_tc<128>(mk, mv, a, s);
+    default: return launch_tc<256>(mk, mv, a, s);
+  }
+}
