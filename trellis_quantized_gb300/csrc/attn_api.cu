@@ -19,6 +19,7 @@ int exl3_attn_tc_keys(int D);
 int exl3_attn_tc_grid();
 cudaError_t exl3_launch_attn_tc(const CUtensorMap &mk, const CUtensorMap &mv, const exl3::attn::Args &a, int D,
                                 cudaStream_t s);
+cudaError_t exl3_launch_attn_join(const exl3::attn::Args &a, int D, int ctas, int tile_rows, cudaStream_t s);
 
 namespace {
 
@@ -118,21 +119,26 @@ int cache_map(CUtensorMap *m, const exl3_kv_cache *c, const void *base, int box,
   return EXL3_OK;
 }
 
-// ---- exl3_paged_attention workspace layout: partial results of the units
-// that a CTA shares with its neighbours, two per CTA
-struct AttnWs {
-  size_t part_o = 0, part_lse = 0, total = 0;
-};
-
 // Few rows per sequence and key head take the step kernel (16 rows a unit),
 // more the tensor-core kernel (128 rows a tile).
 bool few_rows(int T, int G, int batch) { return (int64_t)T * G <= (int64_t)exl3_attn_step_rows() * batch; }
 
+// ---- exl3_paged_attention workspace layout: a record per CTA of the unit
+// that it leaves unfinished, and two partial results per CTA
+struct AttnWs {
+  size_t cuts = 0, part_o = 0, part_lse = 0, total = 0;
+  int grid = 0, rows = 0;
+};
+
 AttnWs attn_ws(int T, int G, int D, int batch) {
   AttnWs w;
-  const size_t rows = few_rows(T, G, batch) ? (size_t)exl3_attn_step_grid(D) * 2 * exl3_attn_step_rows()
-                                            : (size_t)exl3_attn_tc_grid() * 2 * exl3_attn_tc_rows(D);
+  const bool few = few_rows(T, G, batch);
+  w.grid = few ? exl3_attn_step_grid(D) : exl3_attn_tc_grid();
+  w.rows = few ? exl3_attn_step_rows() : exl3_attn_tc_rows(D);
+  const size_t rows = (size_t)w.grid * 2 * w.rows;
   size_t off = kDataOff;
+  w.cuts = off;
+  off = align_up(off + sizeof(exl3::attn::Cut) * w.grid);
   w.part_o = off;
   off = align_up(off + sizeof(float) * rows * D);
   w.part_lse = off;
@@ -330,13 +336,15 @@ int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q
   a.lse = lse;
   a.part_o = at<float>(workspace, L.part_o);
   a.part_lse = at<float>(workspace, L.part_lse);
-  a.counters = at<int>(workspace, kCounterOff);
+  a.cuts = at<exl3::attn::Cut>(workspace, L.cuts);
   a.err = at<int>(workspace, 0);
   CUtensorMap mk, mv;
   EXL3_TRY(cache_map(&mk, cache, cache->k, a.box, a.head_first));
   EXL3_TRY(cache_map(&mv, cache, cache->v, a.box, a.head_first));
-  return exl3_cuda_check(few ? exl3_launch_attn_step(mk, mv, a, D, stream) : exl3_launch_attn_tc(mk, mv, a, D, stream),
-                         "attention launch");
+  EXL3_TRY(exl3_cuda_check(few ? exl3_launch_attn_step(mk, mv, a, D, stream)
+                               : exl3_launch_attn_tc(mk, mv, a, D, stream),
+                           "attention launch"));
+  return exl3_cuda_check(exl3_launch_attn_join(a, D, L.grid, L.rows, stream), "attention join launch");
 }
 
 }  // extern "C"

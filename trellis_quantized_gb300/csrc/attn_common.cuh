@@ -7,10 +7,11 @@
 // keys and values.  A unit's keys are cut into blocks of KB; every unit has
 // at least one block (a unit whose rows see nothing still has its zeros to
 // write).  The blocks of all units, in order of (sequence, tile, key head),
-// form one line that the CTAs share in equal runs: no host knowledge of the
-// lengths, no idle CTA behind a long sequence.  A unit cut by a run's border
-// leaves one partial result per CTA in the workspace and the CTA that
-// arrives last adds them in the order of the line.
+// form one line (with a few places more for each unit's start and end) that
+// the CTAs share in equal runs: no host knowledge of the lengths, no idle CTA
+// behind a long sequence.  A unit cut by a run's border leaves one partial
+// result per CTA in the workspace, which a second kernel joins in the order of
+// the line (attn_join.cu).
 #pragma once
 
 #include "exl3_common.cuh"
@@ -33,8 +34,16 @@ struct Args {
   float *lse;                // [T][Hq] or null
   float *part_o;             // partial results: [grid][2][rows][D] fp32
   float *part_lse;           // [grid][2][rows], log2 of the sum
-  int *counters;             // [grid] arrival counters, zero between calls
+  struct Cut *cuts;          // [grid] the unit that begins in a CTA and ends in a later one
   int *err;
+};
+
+// A unit in parts: its first part is slot 1 of the CTA that the record
+// belongs to, the others slot 0 of the CTAs up to `last`.
+struct Cut {
+  int rows;                  // 0: no such unit
+  int last;
+  int t0, r0, h;             // the sequence's first row of the call, the tile's first row, the key head
 };
 
 // One sequence: first row, new tokens, tokens in the cache.
@@ -82,6 +91,12 @@ __device__ __forceinline__ void store4(const Args &a, int64_t i, const float4 &v
   }
 }
 
+// Output row of a unit's row r: (token, query head).
+__device__ __forceinline__ int64_t out_head(const Args &a, int t0, int h, int r) {
+  const int tok = r / a.G;
+  return (int64_t)(t0 + tok) * a.Hq + h * a.G + r - tok * a.G;
+}
+
 // Rows of the call that belong to no sequence: y = 0, lse = -infinity.
 template <int D>
 __device__ __forceinline__ void clear_padding(const Args &a, int nthreads) {
@@ -110,77 +125,77 @@ __device__ __forceinline__ int range_blocks(int lo, int hi) {
   return lo >= hi ? 1 : (hi + KB - 1) / KB - lo / KB;
 }
 
-// Blocks of one sequence in the line.
-template <int ROWS, int KB>
-__device__ long long seq_blocks(const Args &a, const Seq &s) {
+// The work of one unit on the line: its blocks, and OV more for its start
+// and end (reading q, joining and writing y), during which no block is done.
+template <int ROWS, int KB, int OV>
+__device__ __forceinline__ int tile_cost(const Args &a, const Seq &s, int r0) {
+  int lo, hi;
+  tile_range(a, s, r0, min(ROWS, s.nq * a.G - r0), lo, hi);
+  return range_blocks<KB>(lo, hi) + OV;
+}
+
+// What every CTA works out for itself at its start.
+struct Share {
+  long long total;     // length of the line
+  long long per;       // each CTA's part of it
+  int b, r0;           // tile that holds the CTA's first place (b = B: none)
+  int off;             // that place within the tile's units
+};
+
+// The costs of up to 32 sequences, lane i that of sequence b + i (0 past
+// `end`).  Sequences of many tiles are summed by the whole warp.
+template <int ROWS, int KB, int OV>
+__device__ long long warp_costs(const Args &a, int b, int end, bool report, Seq &s) {
+  const int lane = threadIdx.x & 31;
+  s = Seq{0, 0, 0};
+  if (b + lane < end) s = load_seq(a, b + lane, report);
   const int rows = s.nq * a.G;
+  const bool many = rows > 8 * ROWS;
   long long n = 0;
-  for (int r0 = 0; r0 < rows; r0 += ROWS) {
-    int lo, hi;
-    tile_range(a, s, r0, min(ROWS, rows - r0), lo, hi);
-    n += range_blocks<KB>(lo, hi);
+  if (!many)
+    for (int r0 = 0; r0 < rows; r0 += ROWS) n += tile_cost<ROWS, KB, OV>(a, s, r0);
+  unsigned todo = __ballot_sync(0xffffffffu, many);
+  while (todo) {
+    const int i = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const Seq q = {__shfl_sync(0xffffffffu, s.t0, i), __shfl_sync(0xffffffffu, s.nq, i),
+                   __shfl_sync(0xffffffffu, s.len, i)};
+    long long c = 0;
+    for (int r0 = lane * ROWS; r0 < q.nq * a.G; r0 += 32 * ROWS) c += tile_cost<ROWS, KB, OV>(a, q, r0);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
+    if (lane == i) n = c;
   }
   return n * a.Hkv;
 }
 
-// A place in the line: block `blk` of the unit (b, tile at r0, head h).
-struct Walk {
-  int b, r0, rows, h;
-  int lo, hi;          // keys of the unit
-  int nblk;            // its blocks
-  Seq s;
-
-  template <int ROWS, int KB>
-  __device__ __forceinline__ void set_tile(const Args &a) {
-    rows = min(ROWS, s.nq * a.G - r0);
-    tile_range(a, s, r0, rows, lo, hi);
-    nblk = range_blocks<KB>(lo, hi);
-  }
-
-  // The unit after this one (the caller knows that there is one).
-  template <int ROWS, int KB>
-  __device__ __forceinline__ void next(const Args &a) {
-    if (++h < a.Hkv) return;
-    h = 0;
-    r0 += ROWS;
-    while (r0 >= s.nq * a.G) {
-      r0 = 0;
-      if (++b >= a.B) {
-        rows = 0;
-        return;
-      }
-      s = load_seq(a, b, false);
-    }
-    set_tile<ROWS, KB>(a);
-  }
-};
-
-// What every CTA works out for itself at its start.
-struct Share {
-  long long total;     // blocks in the line
-  long long per;       // blocks per CTA
-  int b;               // sequence that holds the CTA's first block
-  long long off;       // that block's index within the sequence's blocks
-};
-
-// Scan of the sequences' block counts by the whole CTA; `sh` needs
-// NT / 32 + 1 entries and a Share of its own.  CTA 0 also reports lengths
-// that contradict one another.
-template <int ROWS, int KB, int NT>
-__device__ void make_share(const Args &a, int min_per, Share *out, long long *warp_sums) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int NW = NT / 32;
-  const int chunk = (a.B + NT - 1) / NT;
-  const int b0 = min(a.B, tid * chunk), b1 = min(a.B, b0 + chunk);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_blocks<ROWS, KB>(a, load_seq(a, b, blockIdx.x == 0));
-  long long inc = mine;
+__device__ __forceinline__ long long warp_scan(long long v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, inc, d);
-    if (lane >= d) inc += o;
+    const long long o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
   }
-  if (lane == 31) warp_sums[warp] = inc;
+  return v;
+}
+
+// Cuts the line into the CTAs' parts and finds this CTA's first tile: each
+// warp sums a run of sequences, the warp whose run holds the place looks for
+// it.  `warp_sums` has NT / 32 entries.  CTA 0 also reports lengths that
+// contradict one another.
+template <int ROWS, int KB, int OV, int NT>
+__device__ void make_share(const Args &a, int min_per, Share *out, long long *warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int NW = NT / 32;
+  const int chunk = (a.B + NW - 1) / NW;
+  const int b0 = min(a.B, warp * chunk), b1 = min(a.B, b0 + chunk);
+  long long mine = 0;
+  Seq s;
+  for (int b = b0; b < b1; b += 32) mine += warp_costs<ROWS, KB, OV>(a, b, b1, blockIdx.x == 0, s);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+  if (lane == 0) warp_sums[warp] = mine;
+  if (threadIdx.x == 0) out->b = a.B;
   __syncthreads();
   long long before = 0, total = 0;
 #pragma unroll
@@ -191,43 +206,114 @@ __device__ void make_share(const Args &a, int min_per, Share *out, long long *wa
   long long per = (total + gridDim.x - 1) / gridDim.x;
   if (per < min_per) per = min_per;
   const long long start = per * blockIdx.x;
-  long long ex = before + inc - mine;
-  if (tid == 0) {
+  if (threadIdx.x == 0) {
     out->total = total;
     out->per = per;
-    out->b = a.B;
   }
-  __syncthreads();
-  if (start < total && start >= ex && start < ex + mine) {
-    for (int b = b0; b < b1; ++b) {
-      const long long n = seq_blocks<ROWS, KB>(a, load_seq(a, b, false));
-      if (start < ex + n) {
-        out->b = b;
-        out->off = start - ex;
+  if (start >= before && start < before + mine) {
+    long long at = before;
+    for (int b = b0; b < b1; b += 32) {
+      const long long n = warp_costs<ROWS, KB, OV>(a, b, b1, false, s);
+      const long long inc = at + warp_scan(n);
+      const unsigned hit = __ballot_sync(0xffffffffu, start < inc && start >= inc - n);
+      if (hit) {
+        const int i = __ffs(hit) - 1;
+        const Seq q = {__shfl_sync(0xffffffffu, s.t0, i), __shfl_sync(0xffffffffu, s.nq, i),
+                       __shfl_sync(0xffffffffu, s.len, i)};
+        long long tile_at = __shfl_sync(0xffffffffu, inc - n, i);
+        for (int g0 = 0; g0 < q.nq * a.G; g0 += 32 * ROWS) {
+          const int r0 = g0 + lane * ROWS;
+          const long long c = r0 < q.nq * a.G ? (long long)tile_cost<ROWS, KB, OV>(a, q, r0) * a.Hkv : 0;
+          const long long e = tile_at + warp_scan(c);
+          if (start < e && start >= e - c) {
+            out->b = b + i;
+            out->r0 = r0;
+            out->off = (int)(start - (e - c));
+          }
+          tile_at = __shfl_sync(0xffffffffu, e, 31);
+          if (start < tile_at) break;
+        }
         break;
       }
-      ex += n;
+      at = __shfl_sync(0xffffffffu, inc, 31);
     }
   }
   __syncthreads();
 }
 
-// The unit that holds block `off` of sequence w.b; *blk: the block within it.
-template <int ROWS, int KB>
-__device__ void seek(const Args &a, Walk &w, int b, long long off, int *blk) {
-  w.b = b;
-  w.h = 0;
-  w.r0 = 0;
-  w.s = load_seq(a, b, false);
-  w.set_tile<ROWS, KB>(a);
-  while (off >= (long long)w.nblk * a.Hkv && w.r0 + ROWS < w.s.nq * a.G) {
-    off -= (long long)w.nblk * a.Hkv;
-    w.r0 += ROWS;
-    w.set_tile<ROWS, KB>(a);
+// One CTA's part of the line, unit by unit: rows r0 .. of sequence b against
+// key head h, blocks blk .. blk + nseg - 1 of the nblk blocks that hold keys
+// [lo, hi).
+template <int ROWS, int KB, int OV>
+struct Walk {
+  int b, r0, rows, h;
+  int lo, hi, nblk;
+  int blk, nseg;
+  Seq s;
+  long long at;        // place of the unit on the line
+  int x;               // first place within the unit
+  int left;            // places left, this unit's included
+
+  __device__ __forceinline__ void set_tile(const Args &a) {
+    rows = min(ROWS, s.nq * a.G - r0);
+    tile_range(a, s, r0, rows, lo, hi);
+    nblk = range_blocks<KB>(lo, hi);
   }
-  w.h = (int)(off / w.nblk);
-  *blk = (int)(off % w.nblk);
-}
+
+  // The unit's places from OV on are its blocks.
+  __device__ __forceinline__ void set_segment() {
+    const int end = min(nblk + OV, x + left);
+    blk = max(0, x - OV);
+    nseg = max(0, end - OV) - blk;
+    if (nseg <= 0) left = 0;           // (only places without blocks: the next CTA has the unit)
+  }
+
+  __device__ __forceinline__ void begin(const Args &a, const Share &sh) {
+    left = 0;
+    const long long start = sh.per * blockIdx.x;
+    if (start >= sh.total || sh.b >= a.B) return;
+    left = (int)min(sh.per, sh.total - start);
+    b = sh.b;
+    r0 = sh.r0;
+    s = load_seq(a, b, false);
+    set_tile(a);
+    h = sh.off / (nblk + OV);
+    x = sh.off - h * (nblk + OV);
+    at = start - x;
+    set_segment();
+  }
+
+  __device__ __forceinline__ void next(const Args &a) {
+    const int used = min(nblk + OV, x + left) - x;
+    left -= used;
+    if (left <= 0) return;
+    at += nblk + OV;
+    x = 0;
+    if (++h >= a.Hkv) {
+      h = 0;
+      r0 += ROWS;
+      while (r0 >= s.nq * a.G) {
+        r0 = 0;
+        if (++b >= a.B) {
+          left = 0;
+          return;
+        }
+        s = load_seq(a, b, false);
+      }
+      set_tile(a);
+    }
+    set_segment();
+  }
+
+  __device__ __forceinline__ bool whole() const { return nseg == nblk; }
+  // Where a part goes: a unit's first part to slot 1, one that continues a
+  // unit (at most one per CTA, its first) to slot 0.
+  __device__ __forceinline__ int slot() const { return blk == 0 ? 1 : 0; }
+  // The record of the unit that this CTA leaves unfinished.
+  __device__ __forceinline__ Cut cut(const Share &sh) const {
+    return Cut{rows, (int)((at + OV + nblk - 1) / sh.per), s.t0, r0, h};
+  }
+};
 
 }  // namespace attn
 }  // namespace exl3

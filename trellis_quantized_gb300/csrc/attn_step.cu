@@ -27,6 +27,7 @@ namespace exl3 {
 namespace attn {
 
 constexpr int kStepRows = 16, kStepKeys = 64;
+constexpr int kStepCost = 1;            // a unit's start and end, in blocks
 constexpr int kStepThreads = 160;       // four consumer warps and the producer
 
 template <int D>
@@ -91,7 +92,6 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
   __shared__ Share share;
   __shared__ long long warp_sums[kStepThreads / 32];
   __shared__ float sm_m[4][kStepRows], sm_l[4][kStepRows];
-  __shared__ int last_arrival;
   __shared__ int abort_word;
   const uint32_t raw = tc::smem_u32(smem_raw);
   uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -111,21 +111,18 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
   }
   pdl_trigger();
   pdl_wait();
-  make_share<kStepRows, kStepKeys, kStepThreads>(a, 1, &share, warp_sums);   // (its barriers publish the above)
+  make_share<kStepRows, kStepKeys, kStepCost, kStepThreads>(a, 1 + kStepCost, &share, warp_sums);
   clear_padding<D>(a, kStepThreads);
-  const long long start = share.per * blockIdx.x;
-  if (start >= share.total || share.b >= a.B) return;
-  int left = (int)min(share.per, share.total - start);
-  Walk w;
-  int blk;
-  seek<kStepRows, kStepKeys>(a, w, share.b, share.off, &blk);
+  Walk<kStepRows, kStepKeys, kStepCost> w;
+  w.begin(a, share);
+  if (tid == 0) a.cuts[blockIdx.x].rows = 0;           // (the thread that may fill the record in below)
 
   if (warp == 4) {
     // ------------------------------------------------------------ producer
     int it = 0;
     bool stop = false;
-    for (; left > 0 && !stop; ++it, --left) {
-      const int key0 = (w.lo / kStepKeys + blk) * kStepKeys;
+    for (; w.left > 0 && !stop; w.next(a)) for (int i = 0; i < w.nseg; ++i, ++it) {
+      const int key0 = (w.lo / kStepKeys + w.blk + i) * kStepKeys;
       const int k_lo = max(w.lo, key0), k_hi = min(w.hi, key0 + kStepKeys);
       const int box0 = (k_lo - key0) / a.box;
       const int nbox = k_hi > k_lo ? (k_hi - key0 + a.box - 1) / a.box - box0 : 0;
@@ -164,10 +161,6 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
         else tma_load_4d(dst, isv ? &tmV : &tmK, &full[s], panel * 64, off, w.h, page);
       }
       __syncwarp();
-      if (++blk >= w.nblk) {
-        blk = 0;
-        if (left > 1) w.next<kStepRows, kStepKeys>(a);
-      }
     }
     if (stop) {                            // leave no copy in flight behind
       for (int j = max(0, it - ST); j < it; ++j) tc::mbar_wait(&full[j % ST], (j / ST) & 1);
@@ -187,9 +180,8 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
   const uint32_t kbase = kkey * 128, vbase = vkey * 128;
   const uint32_t qbase = sq_addr + (((lane >> 3) & 1) * 8 + (lane & 7)) * C::QPITCH * 2 + ((lane >> 4) & 1) * 16;
   int it = 0;
-  while (left > 0) {
-    const int nseg = min(w.nblk - blk, left);
-    const bool whole = nseg == w.nblk;
+  for (; w.left > 0; w.next(a)) {
+    const bool whole = w.whole();
     // ---- the unit's rows of q (rows past the unit's are zero)
     for (int i = tid; i < kStepRows * (D / 8); i += 128) {
       const int r = i / (D / 8), c8 = i % (D / 8);
@@ -222,14 +214,14 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
 #pragma unroll
     for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
 
-    for (int i = 0; i < nseg; ++i, ++it) {
+    for (int i = 0; i < w.nseg; ++i, ++it) {
       const int s = it % ST;
       if (!*abort_flag && !tc::mbar_wait(&full[s], (it / ST) & 1)) {
         set_device_error(a.err, kErrBounds);
         *abort_flag = 1;
       }
       __syncwarp();
-      const int key0 = (w.lo / kStepKeys + blk + i) * kStepKeys + warp * 16;
+      const int key0 = (w.lo / kStepKeys + w.blk + i) * kStepKeys + warp * 16;
       if (key0 < w.hi && key0 + 16 > w.lo) {         // (else no row sees any of this warp's keys)
         const uint32_t ks = sbase + s * C::STAGE, vs = ks + C::OPERAND;
         // ---- s = q k^T, two tiles of 8 keys
@@ -333,11 +325,6 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
       sm_l[warp][rl + 8] = l1;
     }
     consumer_sync();
-    // the CTAs that hold blocks of this unit: first, last, and this one's place
-    const long long line = start + (share.per < share.total - start ? share.per : share.total - start) - left;
-    const long long unit0 = line - blk;                 // the unit's first block in the line
-    const int c0 = (int)(unit0 / share.per), c1 = (int)((unit0 + w.nblk - 1) / share.per);
-    const int slot = blk == 0 ? 1 : 0;
 #pragma unroll 1
     for (int part = 0; part < (two ? 2 : 1); ++part) {
       const int row = part * 8 + rl;
@@ -375,62 +362,18 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
         const float4 res = make_float4((u.x + v.x) * inv, (u.y + v.y) * inv, (u.z + v.z) * inv, (u.w + v.w) * inv);
         const float lse2 = l == 0.0f ? neg_inf() : mr + log2f(l);
         if (whole) {
-          const int rr = w.r0 + r, tok = rr / a.G;
-          const int64_t head = (int64_t)(w.s.t0 + tok) * a.Hq + w.h * a.G + rr - tok * a.G;
+          const int64_t head = out_head(a, w.s.t0, w.h, w.r0 + r);
           store4(a, head * D + c4, res);
           if (a.lse && c4 == 0) a.lse[head] = lse2 * 0.69314718055994530942f;
         } else {
-          const int64_t pr = ((int64_t)blockIdx.x * 2 + slot) * kStepRows + r;
+          const int64_t pr = ((int64_t)blockIdx.x * 2 + w.slot()) * kStepRows + r;
           *reinterpret_cast<float4 *>(a.part_o + pr * D + c4) = res;
           if (c4 == 0) a.part_lse[pr] = lse2;
         }
       }
       consumer_sync();
     }
-    if (!whole) {
-      // ---- the CTA that arrives last adds the unit's parts in line order
-      __threadfence();
-      consumer_sync();
-      if (tid == 0) {
-        const int n = c1 - c0 + 1, old = atomicAdd(a.counters + c0, 1);
-        if (old >= n) set_device_error(a.err, kErrDirtyCounter);
-        last_arrival = old == n - 1;
-        if (old >= n - 1) a.counters[c0] = 0;
-      }
-      consumer_sync();
-      if (last_arrival) {
-        __threadfence();
-        for (int i = tid; i < w.rows * (D / 4); i += 128) {
-          const int r = i / (D / 4), c4 = (i % (D / 4)) * 4;
-          float mr = neg_inf();
-          for (int c = c0; c <= c1; ++c)
-            mr = fmaxf(mr, __ldcg(a.part_lse + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * kStepRows + r));
-          float l = 0.0f;
-          float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-          for (int c = c0; c <= c1; ++c) {
-            const int64_t pr = ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * kStepRows + r;
-            const float ls = __ldcg(a.part_lse + pr);
-            const float f = ls == neg_inf() ? 0.0f : exp2_approx(ls - mr);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + pr * D + c4));
-            l += f;
-            acc.x = fmaf(f, v.x, acc.x);
-            acc.y = fmaf(f, v.y, acc.y);
-            acc.z = fmaf(f, v.z, acc.z);
-            acc.w = fmaf(f, v.w, acc.w);
-          }
-          const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-          const int rr = w.r0 + r, tok = rr / a.G;
-          const int64_t head = (int64_t)(w.s.t0 + tok) * a.Hq + w.h * a.G + rr - tok * a.G;
-          store4(a, head * D + c4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-          if (a.lse && c4 == 0)
-            a.lse[head] = l == 0.0f ? neg_inf() : (mr + log2f(l)) * 0.69314718055994530942f;
-        }
-      }
-    }
-    left -= nseg;
-    blk = 0;
-    if (left > 0) w.next<kStepRows, kStepKeys>(a);
+    if (tid == 0 && !whole && w.slot() == 1) a.cuts[blockIdx.x] = w.cut(share);
   }
 }
 

@@ -38,6 +38,7 @@ namespace exl3 {
 namespace attn {
 
 constexpr int kTcKeys = 128;
+constexpr int kTcCost = 3;         // a unit's start and end, in blocks
 constexpr float kLazy = 8.0f;      // log2 of the growth that moves the maximum
 
 template <int D>
@@ -129,25 +130,32 @@ struct Uses {
   }
 };
 
-// One CTA's run of the line: segments of units, the same for every role.
+// A row tile's rows of q: 16 bytes per thread and step, row-major.
 template <int D>
-struct Run {
-  Walk w;
-  int blk, left, nseg;
-  __device__ __forceinline__ void begin(const Args &a, const Share &sh) {
-    left = 0;
-    const long long start = sh.per * blockIdx.x;
-    if (start >= sh.total || sh.b >= a.B) return;
-    left = (int)min(sh.per, sh.total - start);
-    seek<TcCfg<D>::ROWS, kTcKeys>(a, w, sh.b, sh.off, &blk);
-    nseg = min(w.nblk - blk, left);
+struct QRows {
+  static constexpr int N = 128 * (D / 8) / 128;        // 16-byte pieces per thread
+  uint4 u[N];
+  __device__ __forceinline__ void load(const Args &a, const Seq &s, int h, int t0, int rows, int tid) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = tid + n * 128, r = i / (D / 8), c8 = i % (D / 8);
+      u[n] = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const int tok = (t0 + r) / a.G;
+        u[n] = *reinterpret_cast<const uint4 *>(a.q + (int64_t)(s.t0 + tok) * a.q_stride +
+                                                (int64_t)(h * a.G + t0 + r - tok * a.G) * D + c8 * 8);
+      }
+    }
   }
-  __device__ __forceinline__ void advance(const Args &a) {
-    left -= nseg;
-    blk = 0;
-    if (left > 0) {
-      w.next<TcCfg<D>::ROWS, kTcKeys>(a);
-      nseg = min(w.nblk, left);
+  // into 64-column panels of 128-byte rows, 128-byte swizzle
+  __device__ __forceinline__ void store(uint32_t dst, int tid) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = tid + n * 128, r = i / (D / 8), c8 = i % (D / 8);
+      const uint32_t p = dst + (c8 >> 3) * (128 * 128) + r * 128 + (((c8 & 7) ^ (r & 7)) << 4);
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(p), "r"(u[n].x), "r"(u[n].y), "r"(u[n].z),
+                   "r"(u[n].w)
+                   : "memory");
     }
   }
 };
@@ -161,7 +169,6 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   __shared__ uint64_t full[ST], empty[ST], s_full[2], p_full[2], pv_done[2], q_full[2];
   __shared__ Share share;
   __shared__ long long warp_sums[C::THREADS / 32];
-  __shared__ int last_arrival[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   const uint32_t raw = tc::smem_u32(smem_raw);
@@ -196,7 +203,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   const uint32_t tmem = tmem_slot;
   pdl_trigger();
   pdl_wait();
-  make_share<C::ROWS, kTcKeys, C::THREADS>(a, 2, &share, warp_sums);
+  make_share<C::ROWS, kTcKeys, kTcCost, C::THREADS>(a, 1 + kTcCost, &share, warp_sums);
   clear_padding<D>(a, C::THREADS);
 
   // A wait that runs out records the error; every later wait then returns at
@@ -209,8 +216,9 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     }
   };
 
-  Run<D> run;
-  run.begin(a, share);
+  Walk<C::ROWS, kTcKeys, kTcCost> w;
+  w.begin(a, share);
+  if (tid == 0) a.cuts[blockIdx.x].rows = 0;           // (the thread that may fill the record in below)
 
   // (every warp of a warpgroup moves its registers, at the head of its role)
   if (warp == C::SM_WARPS + 1) {
@@ -218,10 +226,9 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
     int it = 0;
     bool stop = false;
-    for (; run.left > 0 && !stop; run.advance(a)) {
-      const Walk &w = run.w;
-      for (int j = 0; j < run.nseg && !stop; ++j) {
-        const int key0 = (w.lo / kTcKeys + run.blk + j) * kTcKeys;
+    for (; w.left > 0 && !stop; w.next(a)) {
+      for (int j = 0; j < w.nseg && !stop; ++j) {
+        const int key0 = (w.lo / kTcKeys + w.blk + j) * kTcKeys;
 #pragma unroll 1
         for (int part = 0; part < 2 * OPS && !stop; ++part, ++it) {
           const bool isv = part >= OPS;
@@ -323,9 +330,9 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       __syncwarp();
     };
     int qphase0 = 0, qphase1 = 0;
-    for (; run.left > 0; run.advance(a)) {
-      const int n = run.nseg;
-      const bool two = C::NQ == 2 && run.w.rows > 128;
+    for (; w.left > 0; w.next(a)) {
+      const int n = w.nseg;
+      const bool two = C::NQ == 2 && w.rows > 128;
       const auto kit = [&](int j) { return it + 2 * OPS * j; };
       const auto vit = [&](int j) { return it + 2 * OPS * j + OPS; };
       wait(&q_full[0], qphase0++ & 1);
@@ -368,39 +375,35 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     const int ltid = tid - t * 128;
     int it = 0;
     Uses use;
-    const long long line_end =
-        share.per * blockIdx.x + min(share.per, share.total - share.per * (long long)blockIdx.x);
-    const auto group_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory"); };
-    for (; run.left > 0; run.advance(a)) {
-      const Walk &w = run.w;
-      const int n = run.nseg;
+    // q goes to shared memory a unit ahead, as soon as the scores of the last
+    // block are there, so that the next unit's first scores are computed
+    // while this one's output is written
+    const auto bring_q = [&](const auto &u) {
+      if (u.left <= 0 || u.rows <= t * 128) return;
+      QRows<D> q;
+      q.load(a, u.s, u.h, u.r0 + t * 128, min(128, u.rows - t * 128), ltid);
+      q.store(sbase + t * C::QTILE, ltid);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&q_full[t]);
+    };
+    bring_q(w);
+    while (w.left > 0) {
+      auto ahead = w;
+      ahead.next(a);
+      const int n = w.nseg;
       const bool two = C::NQ == 2 && w.rows > 128;
       if (t == 1 && !two) {
         // a unit of one tile uses both slots: follow the second one's phases
         for (int j = 1; j < n; j += 2) wait(&s_full[1], use.u1++ & 1);
         use.u0 += (n + 1) / 2;
         it += 2 * OPS * n;
+        bring_q(ahead);
+        w = ahead;
         continue;
       }
-      // ---- this tile's rows of q
       const int t0 = w.r0 + t * 128;
       const int rows = min(128, w.rows - t * 128);
-      for (int i = ltid; i < 128 * (D / 8); i += 128) {
-        const int r = i / (D / 8), c8 = i % (D / 8);
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (r < rows) {
-          const int tok = (t0 + r) / a.G;
-          u = *reinterpret_cast<const uint4 *>(a.q + (int64_t)(w.s.t0 + tok) * a.q_stride +
-                                               (int64_t)(w.h * a.G + t0 + r - tok * a.G) * D + c8 * 8);
-        }
-        const uint32_t dst = sbase + t * C::QTILE + (c8 >> 3) * C::QPANEL + r * 128 + (((c8 & 7) ^ (r & 7)) << 4);
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w)
-                     : "memory");
-      }
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&q_full[t]);
-
       int lo = 0, hi = 0, all_lo, all_hi, tmp;
       if (row < rows) row_range(a, w.s, t0 + row, lo, hi);
       row_range(a, w.s, t0, tmp, all_hi);
@@ -412,24 +415,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         const int slot = two ? t : (j & 1);
         const int u = use.get(slot);
         use.add(slot, 1);
-        const int key0 = (w.lo / kTcKeys + run.blk + j) * kTcKeys;
-        if (key0 < w.lo || key0 + kTcKeys > w.hi) {
-          // V rows that no row of the unit sees: zeros
-          const int vi = it + 2 * OPS * j + OPS + ltid / C::VPART_KEYS;
-          wait(&full[vi % ST], (vi / ST) & 1);
-          const int key = key0 + ltid;
-          if (key < w.lo || key >= w.hi) {
-            const uint32_t dst = ring + (vi % ST) * C::STAGE + (ltid % C::VPART_KEYS) * 128;
-#pragma unroll
-            for (int p = 0; p < D / 64; ++p)
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + p * C::VPART_KEYS * 128 + c * 16),
-                             "r"(0)
-                             : "memory");
-          }
-          fence_async_shared();
-        }
+        const int key0 = (w.lo / kTcKeys + w.blk + j) * kTcKeys;
         wait(&s_full[slot], u & 1);
         __syncwarp();
         tc::tc_fence_after();
@@ -490,6 +476,26 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
           }
           tmem_st32u(tmem + C::TM_S + slot * 128 + lanes + 32 * c, pk);
         }
+        if (key0 < w.lo || key0 + kTcKeys > w.hi) {
+          // V rows that no row of the unit sees: zeros.  The last block's
+          // product has to be over before `full` of this block's V is looked
+          // at: until then the ring may be a whole turn behind it.
+          if (j > 0) wait(&pv_done[last_slot], last_use & 1);
+          const int vi = it + 2 * OPS * j + OPS + ltid / C::VPART_KEYS;
+          wait(&full[vi % ST], (vi / ST) & 1);
+          const int key = key0 + ltid;
+          if (key < w.lo || key >= w.hi) {
+            const uint32_t dst = ring + (vi % ST) * C::STAGE + (ltid % C::VPART_KEYS) * 128;
+#pragma unroll
+            for (int p = 0; p < D / 64; ++p)
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + p * C::VPART_KEYS * 128 + c * 16),
+                             "r"(0)
+                             : "memory");
+          }
+          fence_async_shared();
+        }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tc::tmem_st_wait();
         tc::tc_fence_before();
@@ -501,17 +507,16 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       if (two) use.add(1 - t, n);
       it += 2 * OPS * n;
 
+      bring_q(ahead);
       // ---- O complete: y, or this CTA's part of it
       wait(&pv_done[last_slot], last_use & 1);
       __syncwarp();
       tc::tc_fence_after();
-      const bool whole = n == w.nblk;
+      const bool whole = w.whole();
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);      // (NaN stays)
       const float lse2 = l == 0.0f ? neg_inf() : m * a.scale_log2 + log2f(l);
-      const int slot_out = run.blk == 0 ? 1 : 0;
-      const int tok = (t0 + row) / a.G;
-      const int64_t head = (int64_t)(w.s.t0 + tok) * a.Hq + w.h * a.G + (t0 + row) - tok * a.G;
-      const int64_t pr = ((int64_t)blockIdx.x * 2 + slot_out) * C::ROWS + t * 128 + row;
+      const int64_t head = out_head(a, w.s.t0, w.h, t0 + row);
+      const int64_t pr = ((int64_t)blockIdx.x * 2 + w.slot()) * C::ROWS + t * 128 + row;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float v[32];
@@ -519,10 +524,21 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         tc::tmem_ld_wait();
         if (row < rows) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 o = make_float4(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv);
-            if (whole) store4(a, head * D + 32 * c + i, o);
-            else *reinterpret_cast<float4 *>(a.part_o + pr * D + 32 * c + i) = o;
+          for (int i = 0; i < 32; ++i) v[i] *= inv;
+          if (whole && !a.f32out) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              __half2 h[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) h[k] = __floats2half2_rn(v[i + 2 * k], v[i + 2 * k + 1]);
+              *reinterpret_cast<uint4 *>(static_cast<__half *>(a.y) + head * D + 32 * c + i) =
+                  *reinterpret_cast<uint4 *>(h);
+            }
+          } else {
+            float *dst = whole ? static_cast<float *>(a.y) + head * D : a.part_o + pr * D;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4 *>(dst + 32 * c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
         }
       }
@@ -531,49 +547,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         else if (a.lse) a.lse[head] = lse2 * 0.69314718055994530942f;
       }
       tc::tc_fence_before();
-      if (!whole) {
-        // ---- the CTA that arrives last adds the parts in line order
-        const long long unit0 = line_end - run.left - run.blk;
-        const int c0 = (int)(unit0 / share.per), c1 = (int)((unit0 + w.nblk - 1) / share.per);
-        __threadfence();
-        group_sync();
-        if (ltid == 0) {
-          const int parts = c1 - c0 + 1, old = atomicAdd(a.counters + c0 * 2 + t, 1);
-          if (old >= parts) set_device_error(a.err, kErrDirtyCounter);
-          last_arrival[t] = old == parts - 1;
-          if (old >= parts - 1) a.counters[c0 * 2 + t] = 0;
-        }
-        group_sync();
-        if (last_arrival[t]) {
-          __threadfence();
-          for (int i = ltid; i < rows * (D / 4); i += 128) {
-            const int r = i / (D / 4), c4 = (i % (D / 4)) * 4;
-            const auto part = [&](int c) { return ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * C::ROWS + t * 128 + r; };
-            float mr = neg_inf();
-            for (int c = c0; c <= c1; ++c) mr = fmaxf(mr, __ldcg(a.part_lse + part(c)));
-            float sum = 0.0f;
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) {
-              const float ls = __ldcg(a.part_lse + part(c));
-              const float f = ls == neg_inf() ? 0.0f : exp2_approx(ls - mr);
-              const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + part(c) * D + c4));
-              sum += f;
-              acc.x = fmaf(f, v.x, acc.x);
-              acc.y = fmaf(f, v.y, acc.y);
-              acc.z = fmaf(f, v.z, acc.z);
-              acc.w = fmaf(f, v.w, acc.w);
-            }
-            const float iv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-            const int tk = (t0 + r) / a.G;
-            const int64_t hd = (int64_t)(w.s.t0 + tk) * a.Hq + w.h * a.G + (t0 + r) - tk * a.G;
-            store4(a, hd * D + c4, make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv));
-            if (a.lse && c4 == 0)
-              a.lse[hd] = sum == 0.0f ? neg_inf() : (mr + log2f(sum)) * 0.69314718055994530942f;
-          }
-        }
-        group_sync();
-      }
+      if (tid == 0 && !whole && w.slot() == 1) a.cuts[blockIdx.x] = w.cut(share);
+      w = ahead;
     }
   } else {
     if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
