@@ -20,7 +20,7 @@ namespace attn {
 constexpr int kJoinWarps = 8, kJoinMaxCtas = 1024;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const Args a, int ctas, int tile_rows) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 6) attn_join_kernel(const Args a, int ctas, int tile_rows) {
   constexpr int V = D / 32;                  // elements per lane: 2, 4 or 8
   __shared__ int first[kJoinMaxCtas + 1];    // rows before each CTA's record
   __shared__ int sums[kJoinWarps];
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const Args a
         wgt = ls == neg_inf() ? 0.0f : exp2_approx(ls - mx);
       }
       const int n = min(32, parts - p0);
-#pragma unroll 8
+#pragma unroll 4
       for (int k = 0; k < n; ++k) {
         const float f = __shfl_sync(0xffffffffu, wgt, k);
         const float *src = a.part_o + place(p0 + k) * D + lane * V;
@@ -117,7 +117,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const Args a
 cudaError_t exl3_launch_attn_join(const exl3::attn::Args &a, int D, int ctas, int tile_rows, cudaStream_t s) {
   using namespace exl3::attn;
   if (ctas > kJoinMaxCtas) return cudaErrorInvalidConfiguration;
-  const dim3 grid(exl3_sm_count()), block(kJoinWarps * 32);
+  // a warp per row as far as that many can be resident
+  const int most = (ctas * tile_rows + kJoinWarps - 1) / kJoinWarps, resident = 6 * exl3_sm_count();
+  const dim3 grid(most < resident ? most : resident), block(kJoinWarps * 32);
   switch (D) {
     case 64: return exl3::launch_pdl(attn_join_kernel<64>, grid, block, 0, s, a, ctas, tile_rows);
     case 128: return exl3::launch_pdl(attn_join_kernel<128>, grid, block, 0, s, a, ctas, tile_rows);
