@@ -538,8 +538,9 @@ int exl3_qkv_append(const void *q, int64_t q_stride, const void *k, int64_t k_st
  *          j <= its own index (causal), j > its own index - window (window >
  *          0), j < kv_len
  *   y_i  = sum_j softmax_j(s_ij) v_j,   lse_i = ln sum_j exp(s_ij)
- *   Query head h reads key head h / (heads_q / heads_kv).  A row that sees
- *   nothing (padding; an empty cache) has y = 0 and lse = -infinity.
+ *   Query head h reads key head h / (heads_q / heads_kv); heads_q is 1 to 128
+ *   times heads_kv.  A row that sees nothing (padding; an empty cache) has
+ *   y = 0 and lse = -infinity.
  *   q        [T][heads_q][head_dim] fp16, tokens q_stride elements apart
  *   scale    > 0, finite; causal 0 or 1; window 0 (none) or > 0
  *   y        dense [T][heads_q][head_dim], fp16 or fp32 (out_dtype)

@@ -141,7 +141,7 @@ def test_append_refuses(kw, code, text):
 @pytest.mark.parametrize("kw,code,text", [
     (dict(q=FAKE_MIS), tq.EXL3_ERR_ARG, "q is"), (dict(y=None), tq.EXL3_ERR_ARG, "y is NULL"),
     (dict(odt=7), tq.EXL3_ERR_ARG, "out_dtype"), (dict(hq=44), tq.EXL3_ERR_SHAPE, "multiple of heads_kv"),
-    (dict(hq=4), tq.EXL3_ERR_SHAPE, "multiple of heads_kv"), (dict(T=1 << 30), tq.EXL3_ERR_SHAPE, "2^31"),
+    (dict(hq=4), tq.EXL3_ERR_SHAPE, "multiple of heads_kv"), (dict(hq=8 * 129, qs=8 * 129 * 128), tq.EXL3_ERR_SHAPE, "128 times"), (dict(T=1 << 30), tq.EXL3_ERR_SHAPE, "2^31"),
     (dict(scale=0.0), tq.EXL3_ERR_ARG, "scale"), (dict(scale=math.inf), tq.EXL3_ERR_ARG, "scale"),
     (dict(scale=math.nan), tq.EXL3_ERR_ARG, "scale"), (dict(causal=2), tq.EXL3_ERR_ARG, "causal"),
     (dict(window=-1), tq.EXL3_ERR_ARG, "window"), (dict(lse=FAKE_ODD), tq.EXL3_ERR_ARG, "lse"),

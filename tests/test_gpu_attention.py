@@ -70,7 +70,7 @@ def _run(new, old, Hq, Hkv, D, page=16, order="tokens", causal=True, window=0, o
     return y
 
 
-HEADS = [(40, 8, 128), (16, 2, 256), (24, 8, 64), (8, 8, 128), (7, 1, 128), (32, 1, 64)]
+HEADS = [(40, 8, 128), (16, 2, 256), (24, 8, 64), (8, 8, 128), (7, 1, 128), (32, 1, 64), (100, 1, 128)]
 
 
 @pytest.mark.parametrize("Hq,Hkv,D", HEADS)

@@ -17,8 +17,8 @@ cudaError_t exl3_launch_attn_step(const CUtensorMap &mk, const CUtensorMap &mv, 
 int exl3_attn_tc_rows(int D);
 int exl3_attn_tc_keys(int D);
 int exl3_attn_tc_grid();
-cudaError_t exl3_launch_attn_tc(const CUtensorMap &mk, const CUtensorMap &mv, const exl3::attn::Args &a, int D,
-                                cudaStream_t s);
+cudaError_t exl3_launch_attn_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                                const exl3::attn::Args &a, int D, cudaStream_t s);
 cudaError_t exl3_launch_attn_join(const exl3::attn::Args &a, int D, int ctas, int tile_rows, cudaStream_t s);
 
 namespace {
@@ -121,7 +121,25 @@ int cache_map(CUtensorMap *m, const exl3_kv_cache *c, const void *base, int box,
 
 // Few rows per sequence and key head take the step kernel (16 rows a unit),
 // more the tensor-core kernel (128 rows a tile).
-bool few_rows(int T, int G, int batch) { return (int64_t)T * G <= (int64_t)exl3_attn_step_rows() * batch; }
+bool few_rows(int T, int G, int batch) {
+  return G <= exl3_attn_step_rows() && (int64_t)T * G <= (int64_t)exl3_attn_step_rows() * batch;
+}
+
+// Tensor map of the queries: G heads of `tokens` tokens, 64 columns, 128-byte
+// swizzle.
+int query_map(CUtensorMap *m, const void *q, int64_t stride, int T, int heads, int D, int G, int tokens) {
+  auto fn = exl3_tmap_encode_fn();
+  if (!fn) return exl3_fail(EXL3_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return exl3_fail(EXL3_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return EXL3_OK;
+}
 
 // ---- exl3_paged_attention workspace layout: a record per CTA of the unit
 // that it leaves unfinished, and two partial results per CTA
@@ -149,7 +167,7 @@ AttnWs attn_ws(int T, int G, int D, int batch) {
 
 bool attn_shape_ok(int T, int heads_q, int heads_kv, int D, int batch) {
   return (D == 64 || D == 128 || D == 256) && T >= 0 && heads_kv >= 1 && heads_q >= heads_kv && heads_q <= 65536 &&
-         heads_q % heads_kv == 0 && batch >= 1 && batch <= (1 << 20) && (int64_t)T * heads_q <= INT32_MAX;
+         heads_q % heads_kv == 0 && heads_q / heads_kv <= 128 && batch >= 1 && batch <= (1 << 20) && (int64_t)T * heads_q <= INT32_MAX;
 }
 
 }  // namespace
@@ -298,7 +316,8 @@ int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q
   EXL3_TRY(check_batch(batch, cache));
   EXL3_TRY(check_heads(T, heads_q, cache->heads_kv, cache->head_dim));
   if (!attn_shape_ok(T, heads_q, cache->heads_kv, cache->head_dim, batch->batch))
-    return exl3_fail(EXL3_ERR_SHAPE, "heads_q = %d must be a multiple of heads_kv = %d, and T * heads_q below 2^31",
+    return exl3_fail(EXL3_ERR_SHAPE,
+                     "heads_q = %d must be a multiple of heads_kv = %d, at most 128 times it, and T * heads_q below 2^31",
                      heads_q, cache->heads_kv);
   EXL3_TRY(check_rows(q, "q", q_stride, heads_q, cache->head_dim, EXL3_OUT_F16));
   EXL3_TRY(check_ptr(y, "y"));
@@ -318,6 +337,9 @@ int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q
   a.Hq = heads_q;
   a.Hkv = cache->heads_kv;
   a.G = G;
+  a.g_inv = G > 1 ? (unsigned)((((uint64_t)1 << 32) + G - 1) / G) : 0u;
+  a.tile_tok = (few ? exl3_attn_step_rows() : 128) / G;
+  a.unit_tok = few ? a.tile_tok : a.tile_tok * (exl3_attn_tc_rows(D) / 128);
   a.q_start = batch->q_start;
   a.kv_len = batch->kv_len;
   a.table = batch->page_table;
@@ -341,9 +363,13 @@ int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q
   CUtensorMap mk, mv;
   EXL3_TRY(cache_map(&mk, cache, cache->k, a.box, a.head_first));
   EXL3_TRY(cache_map(&mv, cache, cache->v, a.box, a.head_first));
-  EXL3_TRY(exl3_cuda_check(few ? exl3_launch_attn_step(mk, mv, a, D, stream)
-                               : exl3_launch_attn_tc(mk, mv, a, D, stream),
-                           "attention launch"));
+  if (few) {
+    EXL3_TRY(exl3_cuda_check(exl3_launch_attn_step(mk, mv, a, D, stream), "attention launch"));
+  } else {
+    CUtensorMap mq;
+    EXL3_TRY(query_map(&mq, q, q_stride, T, heads_q, D, G, a.tile_tok));
+    EXL3_TRY(exl3_cuda_check(exl3_launch_attn_tc(mq, mk, mv, a, D, stream), "attention launch"));
+  }
   return exl3_cuda_check(exl3_launch_attn_join(a, D, L.grid, L.rows, stream), "attention join launch");
 }
 

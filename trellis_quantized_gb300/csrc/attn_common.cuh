@@ -1,10 +1,10 @@
 // attn_common.cuh -- arguments and work division shared by the attention
 // kernels (attn_step.cu, attn_tc.cu).
 //
-// A unit of work is (sequence, row tile, key head): the rows of a tile are
-// the sequence's new tokens times the G query heads of one key head, row r
-// being token r / G and head r % G, so that all rows of a unit read the same
-// keys and values.  A unit's keys are cut into blocks of KB; every unit has
+// A unit of work is (sequence, tile of new tokens, key head): its rows are
+// those tokens times the G query heads of the key head, row r being token
+// r / G and head r % G, so that all rows of a unit read the same keys and
+// values.  A unit's keys are cut into blocks of KB; every unit has
 // at least one block (a unit whose rows see nothing still has its zeros to
 // write).  The blocks of all units, in order of (sequence, tile, key head),
 // form one line (with a few places more for each unit's start and end) that
@@ -23,6 +23,9 @@ struct Args {
   const __half *q;
   int64_t q_stride;          // elements between tokens
   int T, Hq, Hkv, G;
+  unsigned g_inv;            // ceil(2^32 / G), G > 1: r / G for a unit's rows
+  int unit_tok;              // tokens of a unit
+  int tile_tok;              // tokens of one of its row tiles (attn_tc)
   const int *q_start, *kv_len, *table;
   int B, max_pages, page_size, num_pages;
   int box;                   // rows of one TMA copy: gcd(page_size, KB)
@@ -43,7 +46,7 @@ struct Args {
 struct Cut {
   int rows;                  // 0: no such unit
   int last;
-  int t0, r0, h;             // the sequence's first row of the call, the tile's first row, the key head
+  int t, h;                  // first token (row of the call) and key head
 };
 
 // One sequence: first row, new tokens, tokens in the cache.
@@ -63,10 +66,15 @@ __device__ __forceinline__ Seq load_seq(const Args &a, int b, bool report) {
   return s;
 }
 
-// Keys [lo, hi) that rows r0 .. r0 + rows - 1 of a sequence see between them.
-__device__ __forceinline__ void tile_range(const Args &a, const Seq &s, int r0, int rows, int &lo, int &hi) {
-  const int base = s.len - s.nq;                       // cache index of the sequence's first new token
-  const int p0 = base + r0 / a.G, p1 = base + (r0 + rows - 1) / a.G;
+// r / G for a row of a unit (r < 2^16).
+__device__ __forceinline__ int row_token(const Args &a, int r) {
+  return a.G == 1 ? r : (int)__umulhi((unsigned)r, a.g_inv);
+}
+
+// Keys [lo, hi) that the tokens i0 .. i0 + n - 1 of a sequence see between
+// them.
+__device__ __forceinline__ void token_range(const Args &a, const Seq &s, int i0, int n, int &lo, int &hi) {
+  const int p0 = s.len - s.nq + i0, p1 = p0 + n - 1;   // cache indexes
   hi = a.causal ? min(max(p1 + 1, 0), s.len) : s.len;
   lo = a.window ? max(0, max(p0, 0) - a.window + 1) : 0;
   if (lo > hi) lo = hi;
@@ -91,10 +99,11 @@ __device__ __forceinline__ void store4(const Args &a, int64_t i, const float4 &v
   }
 }
 
-// Output row of a unit's row r: (token, query head).
-__device__ __forceinline__ int64_t out_head(const Args &a, int t0, int h, int r) {
-  const int tok = r / a.G;
-  return (int64_t)(t0 + tok) * a.Hq + h * a.G + r - tok * a.G;
+// Output row (token, query head) of row r of a unit whose first token is row
+// t of the call.
+__device__ __forceinline__ int64_t out_head(const Args &a, int t, int h, int r) {
+  const int tok = row_token(a, r);
+  return (int64_t)(t + tok) * a.Hq + h * a.G + r - tok * a.G;
 }
 
 // Rows of the call that belong to no sequence: y = 0, lse = -infinity.
@@ -112,14 +121,6 @@ __device__ __forceinline__ void clear_padding(const Args &a, int nthreads) {
   }
 }
 
-// Keys [lo, hi) that row r sees.
-__device__ __forceinline__ void row_range(const Args &a, const Seq &s, int r, int &lo, int &hi) {
-  const int p = s.len - s.nq + r / a.G;
-  hi = a.causal ? min(max(p + 1, 0), s.len) : s.len;
-  lo = a.window ? max(0, max(p, 0) - a.window + 1) : 0;
-  if (lo > hi) lo = hi;
-}
-
 template <int KB>
 __device__ __forceinline__ int range_blocks(int lo, int hi) {
   return lo >= hi ? 1 : (hi + KB - 1) / KB - lo / KB;
@@ -127,10 +128,10 @@ __device__ __forceinline__ int range_blocks(int lo, int hi) {
 
 // The work of one unit on the line: its blocks, and OV more for its start
 // and end (reading q, joining and writing y), during which no block is done.
-template <int ROWS, int KB, int OV>
-__device__ __forceinline__ int tile_cost(const Args &a, const Seq &s, int r0) {
+template <int KB, int OV>
+__device__ __forceinline__ int tile_cost(const Args &a, const Seq &s, int i0) {
   int lo, hi;
-  tile_range(a, s, r0, min(ROWS, s.nq * a.G - r0), lo, hi);
+  token_range(a, s, i0, min(a.unit_tok, s.nq - i0), lo, hi);
   return range_blocks<KB>(lo, hi) + OV;
 }
 
@@ -138,22 +139,21 @@ __device__ __forceinline__ int tile_cost(const Args &a, const Seq &s, int r0) {
 struct Share {
   long long total;     // length of the line
   long long per;       // each CTA's part of it
-  int b, r0;           // tile that holds the CTA's first place (b = B: none)
+  int b, i0;           // tile that holds the CTA's first place (b = B: none)
   int off;             // that place within the tile's units
 };
 
 // The costs of up to 32 sequences, lane i that of sequence b + i (0 past
 // `end`).  Sequences of many tiles are summed by the whole warp.
-template <int ROWS, int KB, int OV>
+template <int KB, int OV>
 __device__ long long warp_costs(const Args &a, int b, int end, bool report, Seq &s) {
   const int lane = threadIdx.x & 31;
   s = Seq{0, 0, 0};
   if (b + lane < end) s = load_seq(a, b + lane, report);
-  const int rows = s.nq * a.G;
-  const bool many = rows > 8 * ROWS;
+  const bool many = s.nq > 4 * a.unit_tok;
   long long n = 0;
   if (!many)
-    for (int r0 = 0; r0 < rows; r0 += ROWS) n += tile_cost<ROWS, KB, OV>(a, s, r0);
+    for (int i0 = 0; i0 < s.nq; i0 += a.unit_tok) n += tile_cost<KB, OV>(a, s, i0);
   unsigned todo = __ballot_sync(0xffffffffu, many);
   while (todo) {
     const int i = __ffs(todo) - 1;
@@ -161,7 +161,7 @@ __device__ long long warp_costs(const Args &a, int b, int end, bool report, Seq 
     const Seq q = {__shfl_sync(0xffffffffu, s.t0, i), __shfl_sync(0xffffffffu, s.nq, i),
                    __shfl_sync(0xffffffffu, s.len, i)};
     long long c = 0;
-    for (int r0 = lane * ROWS; r0 < q.nq * a.G; r0 += 32 * ROWS) c += tile_cost<ROWS, KB, OV>(a, q, r0);
+    for (int i0 = lane * a.unit_tok; i0 < q.nq; i0 += 32 * a.unit_tok) c += tile_cost<KB, OV>(a, q, i0);
 #pragma unroll
     for (int d = 16; d; d >>= 1) c += __shfl_xor_sync(0xffffffffu, c, d);
     if (lane == i) n = c;
@@ -183,7 +183,7 @@ __device__ __forceinline__ long long warp_scan(long long v) {
 // warp sums a run of sequences, the warp whose run holds the place looks for
 // it.  `warp_sums` has NT / 32 entries.  CTA 0 also reports lengths that
 // contradict one another.
-template <int ROWS, int KB, int OV, int NT>
+template <int KB, int OV, int NT>
 __device__ void make_share(const Args &a, int min_per, Share *out, long long *warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int NW = NT / 32;
@@ -191,7 +191,7 @@ __device__ void make_share(const Args &a, int min_per, Share *out, long long *wa
   const int b0 = min(a.B, warp * chunk), b1 = min(a.B, b0 + chunk);
   long long mine = 0;
   Seq s;
-  for (int b = b0; b < b1; b += 32) mine += warp_costs<ROWS, KB, OV>(a, b, b1, blockIdx.x == 0, s);
+  for (int b = b0; b < b1; b += 32) mine += warp_costs<KB, OV>(a, b, b1, blockIdx.x == 0, s);
 #pragma unroll
   for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
   if (lane == 0) warp_sums[warp] = mine;
@@ -213,7 +213,7 @@ __device__ void make_share(const Args &a, int min_per, Share *out, long long *wa
   if (start >= before && start < before + mine) {
     long long at = before;
     for (int b = b0; b < b1; b += 32) {
-      const long long n = warp_costs<ROWS, KB, OV>(a, b, b1, false, s);
+      const long long n = warp_costs<KB, OV>(a, b, b1, false, s);
       const long long inc = at + warp_scan(n);
       const unsigned hit = __ballot_sync(0xffffffffu, start < inc && start >= inc - n);
       if (hit) {
@@ -221,13 +221,13 @@ __device__ void make_share(const Args &a, int min_per, Share *out, long long *wa
         const Seq q = {__shfl_sync(0xffffffffu, s.t0, i), __shfl_sync(0xffffffffu, s.nq, i),
                        __shfl_sync(0xffffffffu, s.len, i)};
         long long tile_at = __shfl_sync(0xffffffffu, inc - n, i);
-        for (int g0 = 0; g0 < q.nq * a.G; g0 += 32 * ROWS) {
-          const int r0 = g0 + lane * ROWS;
-          const long long c = r0 < q.nq * a.G ? (long long)tile_cost<ROWS, KB, OV>(a, q, r0) * a.Hkv : 0;
+        for (int g0 = 0; g0 < q.nq; g0 += 32 * a.unit_tok) {
+          const int i0 = g0 + lane * a.unit_tok;
+          const long long c = i0 < q.nq ? (long long)tile_cost<KB, OV>(a, q, i0) * a.Hkv : 0;
           const long long e = tile_at + warp_scan(c);
           if (start < e && start >= e - c) {
             out->b = b + i;
-            out->r0 = r0;
+            out->i0 = i0;
             out->off = (int)(start - (e - c));
           }
           tile_at = __shfl_sync(0xffffffffu, e, 31);
@@ -241,12 +241,12 @@ __device__ void make_share(const Args &a, int min_per, Share *out, long long *wa
   __syncthreads();
 }
 
-// One CTA's part of the line, unit by unit: rows r0 .. of sequence b against
-// key head h, blocks blk .. blk + nseg - 1 of the nblk blocks that hold keys
-// [lo, hi).
-template <int ROWS, int KB, int OV>
+// One CTA's part of the line, unit by unit: tokens i0 .. i0 + ntok - 1 of
+// sequence b (`rows` rows) against key head h, blocks blk .. blk + nseg - 1 of
+// the nblk blocks that hold keys [lo, hi).
+template <int KB, int OV>
 struct Walk {
-  int b, r0, rows, h;
+  int b, i0, ntok, rows, h;
   int lo, hi, nblk;
   int blk, nseg;
   Seq s;
@@ -255,8 +255,9 @@ struct Walk {
   int left;            // places left, this unit's included
 
   __device__ __forceinline__ void set_tile(const Args &a) {
-    rows = min(ROWS, s.nq * a.G - r0);
-    tile_range(a, s, r0, rows, lo, hi);
+    ntok = min(a.unit_tok, s.nq - i0);
+    rows = ntok * a.G;
+    token_range(a, s, i0, ntok, lo, hi);
     nblk = range_blocks<KB>(lo, hi);
   }
 
@@ -274,7 +275,7 @@ struct Walk {
     if (start >= sh.total || sh.b >= a.B) return;
     left = (int)min(sh.per, sh.total - start);
     b = sh.b;
-    r0 = sh.r0;
+    i0 = sh.i0;
     s = load_seq(a, b, false);
     set_tile(a);
     h = sh.off / (nblk + OV);
@@ -291,9 +292,9 @@ struct Walk {
     x = 0;
     if (++h >= a.Hkv) {
       h = 0;
-      r0 += ROWS;
-      while (r0 >= s.nq * a.G) {
-        r0 = 0;
+      i0 += a.unit_tok;
+      while (i0 >= s.nq) {
+        i0 = 0;
         if (++b >= a.B) {
           left = 0;
           return;
@@ -311,7 +312,7 @@ struct Walk {
   __device__ __forceinline__ int slot() const { return blk == 0 ? 1 : 0; }
   // The record of the unit that this CTA leaves unfinished.
   __device__ __forceinline__ Cut cut(const Share &sh) const {
-    return Cut{rows, (int)((at + OV + nblk - 1) / sh.per), s.t0, r0, h};
+    return Cut{rows, (int)((at + OV + nblk - 1) / sh.per), s.t0 + i0, h};
   }
 };
 

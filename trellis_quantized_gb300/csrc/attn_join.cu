@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 6) attn_join_kernel(const Arg
       }
     }
     const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);    // (NaN stays)
-    const int64_t head = out_head(a, cut.t0, cut.h, cut.r0 + r);
+    const int64_t head = out_head(a, cut.t, cut.h, r);
     if constexpr (V == 2) {
       const float2 o = make_float2(acc[0] * inv, acc[1] * inv);
       if (a.f32out) *reinterpret_cast<float2 *>(static_cast<float *>(a.y) + head * D + lane * V) = o;

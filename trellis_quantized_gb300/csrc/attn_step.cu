@@ -111,17 +111,34 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
   }
   pdl_trigger();
   pdl_wait();
-  make_share<kStepRows, kStepKeys, kStepCost, kStepThreads>(a, 1 + kStepCost, &share, warp_sums);
+  make_share<kStepKeys, kStepCost, kStepThreads>(a, 1 + kStepCost, &share, warp_sums);
   clear_padding<D>(a, kStepThreads);
-  Walk<kStepRows, kStepKeys, kStepCost> w;
+  Walk<kStepKeys, kStepCost> w;
   w.begin(a, share);
   if (tid == 0) a.cuts[blockIdx.x].rows = 0;           // (the thread that may fill the record in below)
 
   if (warp == 4) {
     // ------------------------------------------------------------ producer
+    // the pages of a block's boxes, lane i box i (at most 4), looked up while
+    // the block before is under way
+    const auto look = [&](const auto &u, int blk, int &page, int &off) {
+      const int key = (u.lo / kStepKeys + blk) * kStepKeys + lane * a.box;
+      page = -1;
+      off = 0;
+      if (u.left > 0 && lane < kStepKeys / a.box && key + a.box > u.lo && key < u.hi) {
+        const int pi = key / a.page_size;
+        off = key - pi * a.page_size;
+        page = __ldg(a.table + (int64_t)u.b * a.max_pages + pi);
+      }
+    };
     int it = 0;
     bool stop = false;
-    for (; w.left > 0 && !stop; w.next(a)) for (int i = 0; i < w.nseg; ++i, ++it) {
+    int page, off;
+    look(w, w.blk, page, off);
+    while (w.left > 0 && !stop) {
+      auto ahead = w;
+      ahead.next(a);
+      for (int i = 0; i < w.nseg; ++i, ++it) {
       const int key0 = (w.lo / kStepKeys + w.blk + i) * kStepKeys;
       const int k_lo = max(w.lo, key0), k_hi = min(w.hi, key0 + kStepKeys);
       const int box0 = (k_lo - key0) / a.box;
@@ -129,16 +146,14 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
       // one copy per lane: (box, panel, K or V); at most 4 boxes x 4 panels x 2
       const bool mine = lane < nbox * NP * 2;
       const int bx = box0 + lane / (NP * 2), panel = (lane >> 1) % NP, isv = lane & 1;
-      int page = 0, off = 0;
-      if (mine) {
-        const int key = key0 + bx * a.box, pi = key / a.page_size;
-        off = key - pi * a.page_size;
-        page = __ldg(a.table + (int64_t)w.b * a.max_pages + pi);
-        if ((unsigned)page >= (unsigned)a.num_pages) {
-          set_device_error(a.err, kErrBounds);
-          page = a.num_pages;              // past the map's end: reads as zeros
-        }
+      int my_page = __shfl_sync(0xffffffffu, page, bx & 31);
+      const int my_off = __shfl_sync(0xffffffffu, off, bx & 31);
+      if (mine && (unsigned)my_page >= (unsigned)a.num_pages) {
+        set_device_error(a.err, kErrBounds);
+        my_page = a.num_pages;             // past the map's end: reads as zeros
       }
+      if (i + 1 < w.nseg) look(w, w.blk + i + 1, page, off);
+      else look(ahead, ahead.blk, page, off);
       const int s = it % ST;
       if (it >= ST) {
         const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty[s], ((it / ST) & 1) ^ 1));
@@ -157,10 +172,12 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
       __syncwarp();
       if (mine) {
         const uint32_t dst = sbase + s * C::STAGE + isv * C::OPERAND + panel * C::PANEL + bx * a.box * 128;
-        if (a.head_first) tma_load_4d(dst, isv ? &tmV : &tmK, &full[s], panel * 64, w.h, off, page);
-        else tma_load_4d(dst, isv ? &tmV : &tmK, &full[s], panel * 64, off, w.h, page);
+        if (a.head_first) tma_load_4d(dst, isv ? &tmV : &tmK, &full[s], panel * 64, w.h, my_off, my_page);
+        else tma_load_4d(dst, isv ? &tmV : &tmK, &full[s], panel * 64, my_off, w.h, my_page);
       }
       __syncwarp();
+      }
+      w = ahead;
     }
     if (stop) {                            // leave no copy in flight behind
       for (int j = max(0, it - ST); j < it; ++j) tc::mbar_wait(&full[j % ST], (j / ST) & 1);
@@ -187,9 +204,9 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
       const int r = i / (D / 8), c8 = i % (D / 8);
       uint4 u = make_uint4(0, 0, 0, 0);
       if (r < w.rows) {
-        const int rr = w.r0 + r, tok = rr / a.G;
-        u = *reinterpret_cast<const uint4 *>(a.q + (int64_t)(w.s.t0 + tok) * a.q_stride +
-                                             (int64_t)(w.h * a.G + rr - tok * a.G) * D + c8 * 8);
+        const int tok = row_token(a, r);
+        u = *reinterpret_cast<const uint4 *>(a.q + (int64_t)(w.s.t0 + w.i0 + tok) * a.q_stride +
+                                             (int64_t)(w.h * a.G + r - tok * a.G) * D + c8 * 8);
       }
       *reinterpret_cast<uint4 *>(sq + r * C::QPITCH + c8 * 8) = u;
     }
@@ -202,12 +219,12 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
     }
     const bool two = w.rows > 8;
     int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0;
-    if (rl < w.rows) row_range(a, w.s, w.r0 + rl, lo0, hi0);
-    if (rl + 8 < w.rows) row_range(a, w.s, w.r0 + rl + 8, lo1, hi1);
+    if (rl < w.rows) token_range(a, w.s, w.i0 + row_token(a, rl), 1, lo0, hi0);
+    if (rl + 8 < w.rows) token_range(a, w.s, w.i0 + row_token(a, rl + 8), 1, lo1, hi1);
     // keys that every row sees need no mask
     int all_lo, all_hi, tmp;
-    row_range(a, w.s, w.r0, tmp, all_hi);
-    row_range(a, w.s, w.r0 + w.rows - 1, all_lo, tmp);
+    token_range(a, w.s, w.i0, 1, tmp, all_hi);
+    token_range(a, w.s, w.i0 + w.ntok - 1, 1, all_lo, tmp);
 
     float m0 = neg_inf(), m1 = neg_inf(), l0 = 0.0f, l1 = 0.0f;
     float o[D / 8][4];
@@ -362,7 +379,7 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
         const float4 res = make_float4((u.x + v.x) * inv, (u.y + v.y) * inv, (u.z + v.z) * inv, (u.w + v.w) * inv);
         const float lse2 = l == 0.0f ? neg_inf() : mr + log2f(l);
         if (whole) {
-          const int64_t head = out_head(a, w.s.t0, w.h, w.r0 + r);
+          const int64_t head = out_head(a, w.s.t0 + w.i0, w.h, r);
           store4(a, head * D + c4, res);
           if (a.lse && c4 == 0) a.lse[head] = lse2 * 0.69314718055994530942f;
         } else {

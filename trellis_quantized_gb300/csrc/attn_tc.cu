@@ -41,15 +41,20 @@ constexpr int kTcKeys = 128;
 constexpr int kTcCost = 3;         // a unit's start and end, in blocks
 constexpr float kLazy = 8.0f;      // log2 of the growth that moves the maximum
 
+#ifndef OPS_OF
+#define OPS_OF(D) ((D) == 256 ? 2 : 1)
+#endif
 template <int D>
 struct TcCfg {
   static constexpr int NQ = D == 256 ? 1 : 2;            // row tiles of a unit
   static constexpr int ROWS = NQ * 128;
-  static constexpr int OPS = D == 256 ? 2 : 1;           // ring stages of one operand
-  static constexpr int KPARTS_D = D / OPS;               // K part: 128 keys x this many columns
-  static constexpr int VPART_KEYS = kTcKeys / OPS;       // V part: this many keys x D columns
-  static constexpr int STAGE = kTcKeys * D * 2 / OPS;    // 16 KB (D = 64) or 32 KB
-  static constexpr int ST = D == 64 ? 8 : 5;
+  // The ring's stages are parts of an operand, so that a part's place is free
+  // again as soon as its MMAs are done.
+  static constexpr int OPS = OPS_OF(D);                  // parts of one operand
+  static constexpr int KPANELS = D / 64 / OPS;           // K part: 128 keys x this many 64-column panels
+  static constexpr int VPART_KEYS = kTcKeys / OPS;       // V part: these keys x D columns
+  static constexpr int STAGE = kTcKeys * D * 2 / OPS;
+  static constexpr int ST = 163840 / STAGE;              // 160 KB
   static constexpr int QTILE = 128 * D * 2;
   static constexpr int QPANEL = 128 * 128;               // 64 columns of 128 rows
   static constexpr int OFF_RING = NQ * QTILE;
@@ -112,6 +117,15 @@ __device__ __forceinline__ void tma_load_4d_at(uint32_t dst, const CUtensorMap *
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d_at(uint32_t dst, const CUtensorMap *m, uint64_t *bar, int x, int c1,
+                                               int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(tc::smem_u32(bar)), "r"(x), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 template <int N>
@@ -130,43 +144,30 @@ struct Uses {
   }
 };
 
-// A row tile's rows of q: 16 bytes per thread and step, row-major.
-template <int D>
-struct QRows {
-  static constexpr int N = 128 * (D / 8) / 128;        // 16-byte pieces per thread
-  uint4 u[N];
-  __device__ __forceinline__ void load(const Args &a, const Seq &s, int h, int t0, int rows, int tid) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int i = tid + n * 128, r = i / (D / 8), c8 = i % (D / 8);
-      u[n] = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
-        const int tok = (t0 + r) / a.G;
-        u[n] = *reinterpret_cast<const uint4 *>(a.q + (int64_t)(s.t0 + tok) * a.q_stride +
-                                                (int64_t)(h * a.G + t0 + r - tok * a.G) * D + c8 * 8);
-      }
-    }
+// Order of a unit's operands in the ring, that of their use: with two row
+// tiles K0 V0 K1 V1 ..., with one (whose next scores come before this block's
+// weights) K0 K1 V0 K2 V1 ... V(n-1).  The o-th operand's block:
+__device__ __forceinline__ int operand(bool two, int n, int o, bool &isv) {
+  if (two) {
+    isv = o & 1;
+    return o >> 1;
   }
-  // into 64-column panels of 128-byte rows, 128-byte swizzle
-  __device__ __forceinline__ void store(uint32_t dst, int tid) const {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int i = tid + n * 128, r = i / (D / 8), c8 = i % (D / 8);
-      const uint32_t p = dst + (c8 >> 3) * (128 * 128) + r * 128 + (((c8 & 7) ^ (r & 7)) << 4);
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(p), "r"(u[n].x), "r"(u[n].y), "r"(u[n].z),
-                   "r"(u[n].w)
-                   : "memory");
-    }
-  }
-};
+  isv = o > 0 && (o % 2 == 0 || o == 2 * n - 1);
+  return o == 2 * n - 1 ? n - 1 : isv ? o / 2 - 1 : (o + 1) / 2;
+}
+
+// ... and the place of block j's K or V among them.
+__device__ __forceinline__ int k_place(bool two, int j) { return two ? 2 * j : max(0, 2 * j - 1); }
+__device__ __forceinline__ int v_place(bool two, int n, int j) { return two || j == n - 1 ? 2 * j + 1 : 2 * j + 2; }
 
 template <int D>
 __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
-    attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Args a) {
+    attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const Args a) {
   using C = TcCfg<D>;
   constexpr int ST = C::ST, OPS = C::OPS;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[ST], empty[ST], s_full[2], p_full[2], pv_done[2], q_full[2];
+  __shared__ uint64_t full[ST], empty[ST], s_full[2], p_full[2], pv_done[2], q_full[2], q_empty[2];
   __shared__ Share share;
   __shared__ long long warp_sums[C::THREADS / 32];
   __shared__ uint32_t tmem_slot;
@@ -186,10 +187,12 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       tc::mbar_init(&s_full[s], 1);
       tc::mbar_init(&p_full[s], 4);
       tc::mbar_init(&pv_done[s], 1);
-      tc::mbar_init(&q_full[s], 4);
+      tc::mbar_init(&q_full[s], 1);
+      tc::mbar_init(&q_empty[s], 1);
     }
     abort_word = 0;
     tc::fence_mbar_init();
+    tc::prefetch_tmap(&tmQ);
     tc::prefetch_tmap(&tmK);
     tc::prefetch_tmap(&tmV);
   }
@@ -203,7 +206,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   const uint32_t tmem = tmem_slot;
   pdl_trigger();
   pdl_wait();
-  make_share<C::ROWS, kTcKeys, kTcCost, C::THREADS>(a, 1 + kTcCost, &share, warp_sums);
+  make_share<kTcKeys, kTcCost, C::THREADS>(a, 1 + kTcCost, &share, warp_sums);
   clear_padding<D>(a, C::THREADS);
 
   // A wait that runs out records the error; every later wait then returns at
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     }
   };
 
-  Walk<C::ROWS, kTcKeys, kTcCost> w;
+  Walk<kTcKeys, kTcCost> w;
   w.begin(a, share);
   if (tid == 0) a.cuts[blockIdx.x].rows = 0;           // (the thread that may fill the record in below)
 
@@ -224,32 +227,60 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   if (warp == C::SM_WARPS + 1) {
     // ============================================================ producer
     if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
-    int it = 0;
+    // the pages of a block's boxes, lane i box i (at most 8), looked up while
+    // the block before is under way
+    const auto look = [&](const auto &u, int blk, int &page, int &off) {
+      const int key = (u.lo / kTcKeys + blk) * kTcKeys + lane * a.box;
+      page = -1;
+      off = 0;
+      if (u.left > 0 && lane < kTcKeys / a.box && key + a.box > u.lo && key < u.hi) {
+        const int pi = key / a.page_size;
+        off = key - pi * a.page_size;
+        page = __ldg(a.table + (int64_t)u.b * a.max_pages + pi);
+      }
+    };
+    int it = 0, qn0 = 0, qn1 = 0;
     bool stop = false;
-    for (; w.left > 0 && !stop; w.next(a)) {
-      for (int j = 0; j < w.nseg && !stop; ++j) {
+    // K and V of a unit are asked for in the order of their use, which may
+    // have block j + 1's K before block j's V: pages of two blocks are held
+    int page[2], off[2], next_page, next_off;
+    look(w, w.blk, next_page, next_off);
+    while (w.left > 0 && !stop) {
+      auto ahead = w;
+      ahead.next(a);
+      const int n = w.nseg;
+      const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
+      for (int o = 0; o < 2 * n && !stop; ++o) {
+        bool isv;
+        const int j = operand(two, n, o, isv);
+        if (!isv) {
+          page[1] = page[0];
+          off[1] = off[0];
+          page[0] = next_page;
+          off[0] = next_off;
+          if (j + 1 < n) look(w, w.blk + j + 1, next_page, next_off);
+          else look(ahead, ahead.blk, next_page, next_off);
+        }
+        // block j is the newest whose K was asked for, or the one before it
+        const int newest = two ? j : min(n - 1, o == 0 ? 0 : (o + 1) / 2);
+        const int old = isv && j < newest;
         const int key0 = (w.lo / kTcKeys + w.blk + j) * kTcKeys;
 #pragma unroll 1
-        for (int part = 0; part < 2 * OPS && !stop; ++part, ++it) {
-          const bool isv = part >= OPS;
-          const int p = isv ? part - OPS : part;
-          // keys of this part, and the boxes of it that some row sees
-          const int nkeys = isv ? C::VPART_KEYS : kTcKeys, npan = isv ? D / 64 : C::KPARTS_D / 64;
+        for (int p = 0; p < OPS && !stop; ++p, ++it) {
+          // the boxes of this part that some row sees
+          const int nkeys = isv ? C::VPART_KEYS : kTcKeys, npan = isv ? D / 64 : C::KPANELS;
           const int base = key0 + (isv ? p * C::VPART_KEYS : 0);
           const int k_lo = max(w.lo, base), k_hi = min(w.hi, base + nkeys);
           const int box0 = k_hi > k_lo ? (k_lo - base) / a.box : 0;
           const int nbox = k_hi > k_lo ? (k_hi - base + a.box - 1) / a.box - box0 : 0;
           const bool mine = lane < nbox * npan;
           const int bx = box0 + lane / npan, panel = lane % npan;
-          int page = 0, off = 0;
-          if (mine) {
-            const int key = base + bx * a.box, pi = key / a.page_size;
-            off = key - pi * a.page_size;
-            page = __ldg(a.table + (int64_t)w.b * a.max_pages + pi);
-            if ((unsigned)page >= (unsigned)a.num_pages) {
-              set_device_error(a.err, kErrBounds);
-              page = a.num_pages;            // past the map's end: reads as zeros
-            }
+          const int src = ((isv ? p * C::VPART_KEYS / a.box : 0) + bx) & 31;
+          int my_page = __shfl_sync(0xffffffffu, old ? page[1] : page[0], src);
+          const int my_off = __shfl_sync(0xffffffffu, old ? off[1] : off[0], src);
+          if (mine && (unsigned)my_page >= (unsigned)a.num_pages) {
+            set_device_error(a.err, kErrBounds);
+            my_page = a.num_pages;           // past the map's end: reads as zeros
           }
           const int s = it % ST;
           if (it >= ST) wait(&empty[s], ((it / ST) & 1) ^ 1);
@@ -266,101 +297,113 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
           __syncwarp();
           if (mine) {
             const uint32_t dst = ring + s * C::STAGE + panel * (nkeys * 128) + bx * a.box * 128;
-            const int x = (isv ? panel : p * (C::KPARTS_D / 64) + panel) * 64;
+            const int x = (isv ? panel : p * C::KPANELS + panel) * 64;
             const CUtensorMap *m = isv ? &tmV : &tmK;
-            if (a.head_first) tma_load_4d_at(dst, m, &full[s], x, w.h, off, page);
-            else tma_load_4d_at(dst, m, &full[s], x, off, w.h, page);
+            if (a.head_first) tma_load_4d_at(dst, m, &full[s], x, w.h, my_off, my_page);
+            else tma_load_4d_at(dst, m, &full[s], x, my_off, w.h, my_page);
           }
           __syncwarp();
         }
+        if (o == 0 && !stop) {
+          // the unit's q, as soon as the last unit's scores are done with its
+          // place: G heads of tile_tok tokens are the tile's rows in order
+          // (tokens past the unit's are rows that nobody writes)
+#pragma unroll 1
+          for (int t = 0; t < (two ? 2 : 1); ++t) {
+            const int u = t ? qn1++ : qn0++;
+            if (u > 0) wait(&q_empty[t], (u - 1) & 1);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_expect_tx(&q_full[t], (uint32_t)(a.tile_tok * a.G * D * 2));
+            __syncwarp();
+            if (lane < D / 64)
+              tma_load_3d_at(sbase + t * C::QTILE + lane * C::QPANEL, &tmQ, &q_full[t], lane * 64, w.h * a.G,
+                             w.s.t0 + w.i0 + t * a.tile_tok);
+            __syncwarp();
+          }
+        }
       }
+      w = ahead;
     }
-    if (stop)                                // leave no copy in flight behind
+    if (stop) {                              // leave no copy in flight behind
       for (int i = max(0, it - ST); i < it; ++i) tc::mbar_wait(&full[i % ST], (i / ST) & 1);
+      if (qn0 > 0) tc::mbar_wait(&q_full[0], (qn0 - 1) & 1);
+      if (qn1 > 0) tc::mbar_wait(&q_full[1], (qn1 - 1) & 1);
+    }
   } else if (warp == C::SM_WARPS) {
     // ========================================================== MMA issuer
     if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
     int it = 0;
     Uses use;
-    const auto issue_s = [&](int t, int slot, int kit) {
+    // Scores of a block into a slot; `free_k`: nobody reads these K parts
+    // after, `free_q`: nor this tile's q.
+    const auto issue_s = [&](int t, int slot, int kit, bool free_k, bool free_q) {
       // the slot's last weights have to be consumed first
       if (use.get(slot) > 0) wait(&pv_done[slot], (use.get(slot) - 1) & 1);
-      for (int p = 0; p < OPS; ++p) wait(&full[(kit + p) % ST], ((kit + p) / ST) & 1);
-      __syncwarp();
-      tc::tc_fence_after();
-      if (tc::elect_one()) {
 #pragma unroll
-        for (int p = 0; p < OPS; ++p) {
-          const uint32_t ks = ring + ((kit + p) % ST) * C::STAGE;
-          const uint32_t qs = sbase + t * C::QTILE + p * (C::KPARTS_D / 64) * C::QPANEL;
+      for (int p = 0; p < OPS; ++p) {
+        const int st = (kit + p) % ST;
+        wait(&full[st], ((kit + p) / ST) & 1);
+        __syncwarp();
+        tc::tc_fence_after();
+        if (tc::elect_one()) {
+          const uint64_t ad = sdesc_k_sw128(sbase + t * C::QTILE + p * C::KPANELS * C::QPANEL);
+          const uint64_t bd = sdesc_k_sw128(ring + st * C::STAGE);
 #pragma unroll
-          for (int kk = 0; kk < C::KPARTS_D / 16; ++kk) {
-            const uint32_t o = (kk / 4) * C::QPANEL + (kk % 4) * 32;
-            tc::mma_f16(tmem + C::TM_S + slot * 128, sdesc_k_sw128(qs + o), sdesc_k_sw128(ks + o), C::IDESC_S,
-                        (p | kk) ? 1u : 0u);
+          for (int kk = 0; kk < C::KPANELS * 4; ++kk) {
+            const int o = (kk / 4) * (C::QPANEL >> 4) + (kk % 4) * 2;
+            tc::mma_f16(tmem + C::TM_S + slot * 128, ad + o, bd + o, C::IDESC_S, (p | kk) ? 1u : 0u);
           }
+          if (p == OPS - 1) tc::mma_commit(&s_full[slot]);
+          if (free_k) tc::mma_commit(&empty[st]);
+          if (p == OPS - 1 && free_q) tc::mma_commit(&q_empty[t]);
         }
-        tc::mma_commit(&s_full[slot]);
+        __syncwarp();
       }
-      __syncwarp();
       use.add(slot, 1);
     };
-    const auto issue_pv = [&](int t, int slot, int vit, bool first) {
+    // O += weights of a slot times a block's V.
+    const auto issue_pv = [&](int t, int slot, int vit, bool first, bool free_v) {
       wait(&p_full[slot], (use.get(slot) - 1) & 1);
-      for (int p = 0; p < OPS; ++p) wait(&full[(vit + p) % ST], ((vit + p) / ST) & 1);
-      __syncwarp();
-      tc::tc_fence_after();
-      if (tc::elect_one()) {
 #pragma unroll
-        for (int p = 0; p < OPS; ++p) {
-          const uint32_t vs = ring + ((vit + p) % ST) * C::STAGE;
+      for (int p = 0; p < OPS; ++p) {
+        const int st = (vit + p) % ST;
+        wait(&full[st], ((vit + p) / ST) & 1);
+        __syncwarp();
+        tc::tc_fence_after();
+        if (tc::elect_one()) {
+          const uint64_t bd = sdesc_mn_sw128(ring + st * C::STAGE, C::VPART_KEYS * 128);
 #pragma unroll
           for (int kk = 0; kk < C::VPART_KEYS / 16; ++kk)
             mma_f16_ts(tmem + C::TM_O + t * D, tmem + C::TM_S + slot * 128 + (p * C::VPART_KEYS / 16 + kk) * 8,
-                       sdesc_mn_sw128(vs + kk * 2048, C::VPART_KEYS * 128), C::IDESC_O,
-                       (!first || p || kk) ? 1u : 0u);
+                       bd + kk * (2048 >> 4), C::IDESC_O, (!first || p || kk) ? 1u : 0u);
+          if (p == OPS - 1) tc::mma_commit(&pv_done[slot]);
+          if (free_v) tc::mma_commit(&empty[st]);
         }
-        tc::mma_commit(&pv_done[slot]);
+        __syncwarp();
       }
-      __syncwarp();
-    };
-    const auto release = [&](int i0) {       // an operand's stages, once the MMAs issued so far are done
-      if (tc::elect_one())
-        for (int p = 0; p < OPS; ++p) tc::mma_commit(&empty[(i0 + p) % ST]);
-      __syncwarp();
     };
     int qphase0 = 0, qphase1 = 0;
     for (; w.left > 0; w.next(a)) {
       const int n = w.nseg;
-      const bool two = C::NQ == 2 && w.rows > 128;
-      const auto kit = [&](int j) { return it + 2 * OPS * j; };
-      const auto vit = [&](int j) { return it + 2 * OPS * j + OPS; };
+      const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
+      const auto kit = [&](int j) { return it + OPS * k_place(two, j); };
+      const auto vit = [&](int j) { return it + OPS * v_place(two, n, j); };
       wait(&q_full[0], qphase0++ & 1);
       if (two) {
-        issue_s(0, 0, kit(0));
+        issue_s(0, 0, kit(0), false, n == 1);
         wait(&q_full[1], qphase1++ & 1);
-        issue_s(1, 1, kit(0));
-        release(kit(0));
+        issue_s(1, 1, kit(0), true, n == 1);
         for (int j = 0; j < n; ++j) {
-          issue_pv(0, 0, vit(j), j == 0);
-          if (j + 1 < n) issue_s(0, 0, kit(j + 1));
-          issue_pv(1, 1, vit(j), j == 0);
-          release(vit(j));
-          if (j + 1 < n) {
-            issue_s(1, 1, kit(j + 1));
-            release(kit(j + 1));
-          }
+          issue_pv(0, 0, vit(j), j == 0, false);
+          if (j + 1 < n) issue_s(0, 0, kit(j + 1), false, j + 2 == n);
+          issue_pv(1, 1, vit(j), j == 0, true);
+          if (j + 1 < n) issue_s(1, 1, kit(j + 1), true, j + 2 == n);
         }
       } else {
-        issue_s(0, 0, kit(0));
-        release(kit(0));
+        issue_s(0, 0, kit(0), true, n == 1);
         for (int j = 0; j < n; ++j) {
-          if (j + 1 < n) {
-            issue_s(0, (j + 1) & 1, kit(j + 1));
-            release(kit(j + 1));
-          }
-          issue_pv(0, j & 1, vit(j), j == 0);
-          release(vit(j));
+          if (j + 1 < n) issue_s(0, (j + 1) & 1, kit(j + 1), true, j + 2 == n);
+          issue_pv(0, j & 1, vit(j), j == 0, true);
         }
       }
       it += 2 * OPS * n;
@@ -375,39 +418,23 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     const int ltid = tid - t * 128;
     int it = 0;
     Uses use;
-    // q goes to shared memory a unit ahead, as soon as the scores of the last
-    // block are there, so that the next unit's first scores are computed
-    // while this one's output is written
-    const auto bring_q = [&](const auto &u) {
-      if (u.left <= 0 || u.rows <= t * 128) return;
-      QRows<D> q;
-      q.load(a, u.s, u.h, u.r0 + t * 128, min(128, u.rows - t * 128), ltid);
-      q.store(sbase + t * C::QTILE, ltid);
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&q_full[t]);
-    };
-    bring_q(w);
-    while (w.left > 0) {
-      auto ahead = w;
-      ahead.next(a);
+    for (; w.left > 0; w.next(a)) {
       const int n = w.nseg;
-      const bool two = C::NQ == 2 && w.rows > 128;
+      const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
       if (t == 1 && !two) {
         // a unit of one tile uses both slots: follow the second one's phases
         for (int j = 1; j < n; j += 2) wait(&s_full[1], use.u1++ & 1);
         use.u0 += (n + 1) / 2;
         it += 2 * OPS * n;
-        bring_q(ahead);
-        w = ahead;
         continue;
       }
-      const int t0 = w.r0 + t * 128;
-      const int rows = min(128, w.rows - t * 128);
+      // this tile's tokens and rows, and the keys that this thread's row sees
+      const int i0 = w.i0 + t * a.tile_tok, ntok = min(a.tile_tok, w.ntok - t * a.tile_tok);
+      const int rows = ntok * a.G;
       int lo = 0, hi = 0, all_lo, all_hi, tmp;
-      if (row < rows) row_range(a, w.s, t0 + row, lo, hi);
-      row_range(a, w.s, t0, tmp, all_hi);
-      row_range(a, w.s, t0 + rows - 1, all_lo, tmp);
+      if (row < rows) token_range(a, w.s, i0 + row_token(a, row), 1, lo, hi);
+      token_range(a, w.s, i0, 1, tmp, all_hi);
+      token_range(a, w.s, i0 + ntok - 1, 1, all_lo, tmp);
 
       float m = neg_inf(), l = 0.0f;         // the exponent's base (in scores) and the sum of weights
       int last_slot = 0, last_use = 0;
@@ -481,7 +508,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
           // product has to be over before `full` of this block's V is looked
           // at: until then the ring may be a whole turn behind it.
           if (j > 0) wait(&pv_done[last_slot], last_use & 1);
-          const int vi = it + 2 * OPS * j + OPS + ltid / C::VPART_KEYS;
+          const int vi = it + OPS * v_place(two, n, j) + ltid / C::VPART_KEYS;
           wait(&full[vi % ST], (vi / ST) & 1);
           const int key = key0 + ltid;
           if (key < w.lo || key >= w.hi) {
@@ -507,7 +534,6 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       if (two) use.add(1 - t, n);
       it += 2 * OPS * n;
 
-      bring_q(ahead);
       // ---- O complete: y, or this CTA's part of it
       wait(&pv_done[last_slot], last_use & 1);
       __syncwarp();
@@ -515,8 +541,9 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       const bool whole = w.whole();
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);      // (NaN stays)
       const float lse2 = l == 0.0f ? neg_inf() : m * a.scale_log2 + log2f(l);
-      const int64_t head = out_head(a, w.s.t0, w.h, t0 + row);
-      const int64_t pr = ((int64_t)blockIdx.x * 2 + w.slot()) * C::ROWS + t * 128 + row;
+      // (parts of a cut unit: the rows of its tiles one after the other)
+      const int64_t head = out_head(a, w.s.t0 + i0, w.h, row);
+      const int64_t pr = ((int64_t)blockIdx.x * 2 + w.slot()) * C::ROWS + t * a.tile_tok * a.G + row;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float v[32];
@@ -548,7 +575,6 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       }
       tc::tc_fence_before();
       if (tid == 0 && !whole && w.slot() == 1) a.cuts[blockIdx.x] = w.cut(share);
-      w = ahead;
     }
   } else {
     if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
@@ -563,12 +589,12 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
 }
 
 template <int D>
-cudaError_t launch_tc(const CUtensorMap &mk, const CUtensorMap &mv, const Args &a, cudaStream_t s) {
+cudaError_t launch_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const Args &a, cudaStream_t s) {
   static std::atomic<size_t> per_dev[kMaxDevices];
   cudaError_t e = exl3_ensure_smem(reinterpret_cast<const void *>(attn_tc_kernel<D>), TcCfg<D>::SMEM, per_dev);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_tc_kernel<D>, dim3(exl3_attn_tc_grid()), dim3(TcCfg<D>::THREADS), TcCfg<D>::SMEM, s, mk, mv,
-                    a);
+  return launch_pdl(attn_tc_kernel<D>, dim3(exl3_attn_tc_grid()), dim3(TcCfg<D>::THREADS), TcCfg<D>::SMEM, s, mq, mk,
+                    mv, a);
 }
 
 }  // namespace attn
@@ -576,15 +602,15 @@ cudaError_t launch_tc(const CUtensorMap &mk, const CUtensorMap &mv, const Args &
 
 int exl3_attn_tc_rows(int D) { return D == 256 ? 128 : 256; }
 // Keys that one tensor copy must not straddle: a block, or a part of its V.
-int exl3_attn_tc_keys(int D) { return D == 256 ? 64 : exl3::attn::kTcKeys; }
+int exl3_attn_tc_keys(int D) { return exl3::attn::kTcKeys / OPS_OF(D); }
 int exl3_attn_tc_grid() { return exl3_sm_count(); }
 
-cudaError_t exl3_launch_attn_tc(const CUtensorMap &mk, const CUtensorMap &mv, const exl3::attn::Args &a, int D,
-                                cudaStream_t s) {
+cudaError_t exl3_launch_attn_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                                const exl3::attn::Args &a, int D, cudaStream_t s) {
   using namespace exl3::attn;
   switch (D) {
-    case 64: return launch_tc<64>(mk, mv, a, s);
-    case 128: return launch_tc<128>(mk, mv, a, s);
-    default: return launch_tc<256>(mk, mv, a, s);
+    case 64: return launch_tc<64>(mq, mk, mv, a, s);
+    case 128: return launch_tc<128>(mq, mk, mv, a, s);
+    default: return launch_tc<256>(mq, mk, mv, a, s);
   }
 }
