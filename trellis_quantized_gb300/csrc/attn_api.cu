@@ -347,7 +347,8 @@ int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q
   a.max_pages = batch->max_pages;
   a.page_size = cache->page_size;
   a.num_pages = cache->num_pages;
-  a.box = std::gcd(cache->page_size, few ? exl3_attn_step_keys() : exl3_attn_tc_keys(D));
+  const int box = std::gcd(cache->page_size, few ? exl3_attn_step_keys() : exl3_attn_tc_keys(D));
+  while ((1 << a.box_log2) < box) ++a.box_log2;        // (a power of two: a block is)
   a.head_first = cache->stride_head < cache->stride_token;
   a.scale_log2 = scale * 1.44269504088896340736f;
   a.causal = causal;
@@ -361,8 +362,8 @@ int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q
   a.cuts = at<exl3::attn::Cut>(workspace, L.cuts);
   a.err = at<int>(workspace, 0);
   CUtensorMap mk, mv;
-  EXL3_TRY(cache_map(&mk, cache, cache->k, a.box, a.head_first));
-  EXL3_TRY(cache_map(&mv, cache, cache->v, a.box, a.head_first));
+  EXL3_TRY(cache_map(&mk, cache, cache->k, box, a.head_first));
+  EXL3_TRY(cache_map(&mv, cache, cache->v, box, a.head_first));
   if (few) {
     EXL3_TRY(exl3_cuda_check(exl3_launch_attn_step(mk, mv, a, D, stream), "attention launch"));
   } else {

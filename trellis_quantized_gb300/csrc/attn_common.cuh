@@ -28,7 +28,7 @@ struct Args {
   int tile_tok;              // tokens of one of its row tiles (attn_tc)
   const int *q_start, *kv_len, *table;
   int B, max_pages, page_size, num_pages;
-  int box;                   // rows of one TMA copy: gcd(page_size, KB)
+  int box_log2;              // tokens of one TMA copy: the largest power of two in page_size, at most a block's
   int head_first;            // tensor map order: (d, head, token, page), else (d, token, head, page)
   float scale_log2;          // scale * log2(e)
   int causal, window;        // window 0: none
@@ -313,6 +313,38 @@ struct Walk {
   // The record of the unit that this CTA leaves unfinished.
   __device__ __forceinline__ Cut cut(const Share &sh) const {
     return Cut{rows, (int)((at + OV + nblk - 1) / sh.per), s.t0 + i0, h};
+  }
+};
+
+// The pages of a unit's blocks, followed block by block by a warp whose lane i
+// looks up box i of the block (the division is left to the start of a unit).
+template <int KB>
+struct PageWalk {
+  int64_t row;       // the sequence's first entry in the page table
+  int lo, hi;        // keys that are looked at
+  int key, index, off;
+
+  template <class W>
+  __device__ __forceinline__ void begin(const Args &a, const W &w) {
+    row = (int64_t)w.b * a.max_pages;
+    lo = w.lo;
+    hi = w.hi;
+    key = (w.lo / KB + w.blk) * KB + ((int)(threadIdx.x & 31) << a.box_log2);
+    index = key / a.page_size;
+    off = key - index * a.page_size;
+  }
+  // This block's page (-1: not needed) and the offset in it; on to the next.
+  __device__ __forceinline__ void next(const Args &a, int &page, int &offset) {
+    page = -1;
+    offset = off;
+    const int lane = threadIdx.x & 31;
+    if (lane < (KB >> a.box_log2) && key + (1 << a.box_log2) > lo && key < hi) page = __ldg(a.table + row + index);
+    key += KB;
+    off += KB;
+    while (off >= a.page_size) {
+      off -= a.page_size;
+      ++index;
+    }
   }
 };
 

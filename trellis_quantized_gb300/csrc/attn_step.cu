@@ -121,28 +121,22 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
     // ------------------------------------------------------------ producer
     // the pages of a block's boxes, lane i box i (at most 4), looked up while
     // the block before is under way
-    const auto look = [&](const auto &u, int blk, int &page, int &off) {
-      const int key = (u.lo / kStepKeys + blk) * kStepKeys + lane * a.box;
-      page = -1;
-      off = 0;
-      if (u.left > 0 && lane < kStepKeys / a.box && key + a.box > u.lo && key < u.hi) {
-        const int pi = key / a.page_size;
-        off = key - pi * a.page_size;
-        page = __ldg(a.table + (int64_t)u.b * a.max_pages + pi);
-      }
-    };
     int it = 0;
     bool stop = false;
-    int page, off;
-    look(w, w.blk, page, off);
+    int page = -1, off = 0;
+    PageWalk<kStepKeys> pages;
+    if (w.left > 0) {
+      pages.begin(a, w);
+      pages.next(a, page, off);
+    }
     while (w.left > 0 && !stop) {
       auto ahead = w;
       ahead.next(a);
       for (int i = 0; i < w.nseg; ++i, ++it) {
       const int key0 = (w.lo / kStepKeys + w.blk + i) * kStepKeys;
-      const int k_lo = max(w.lo, key0), k_hi = min(w.hi, key0 + kStepKeys);
-      const int box0 = (k_lo - key0) / a.box;
-      const int nbox = k_hi > k_lo ? (k_hi - key0 + a.box - 1) / a.box - box0 : 0;
+      const int k_lo = max(w.lo, key0), k_hi = min(w.hi, key0 + kStepKeys), box = 1 << a.box_log2;
+      const int box0 = (k_lo - key0) >> a.box_log2;
+      const int nbox = k_hi > k_lo ? ((k_hi - key0 + box - 1) >> a.box_log2) - box0 : 0;
       // one copy per lane: (box, panel, K or V); at most 4 boxes x 4 panels x 2
       const bool mine = lane < nbox * NP * 2;
       const int bx = box0 + lane / (NP * 2), panel = (lane >> 1) % NP, isv = lane & 1;
@@ -152,8 +146,12 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
         set_device_error(a.err, kErrBounds);
         my_page = a.num_pages;             // past the map's end: reads as zeros
       }
-      if (i + 1 < w.nseg) look(w, w.blk + i + 1, page, off);
-      else look(ahead, ahead.blk, page, off);
+      if (i + 1 < w.nseg) {
+        pages.next(a, page, off);
+      } else if (ahead.left > 0) {
+        pages.begin(a, ahead);
+        pages.next(a, page, off);
+      }
       const int s = it % ST;
       if (it >= ST) {
         const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty[s], ((it / ST) & 1) ^ 1));
@@ -165,13 +163,13 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
         }
       }
       if (lane == 0) {
-        const uint32_t bytes = (uint32_t)(nbox * a.box * 128 * NP * 2);
+        const uint32_t bytes = (uint32_t)((nbox << a.box_log2) * 128 * NP * 2);
         if (bytes) tc::mbar_arrive_expect_tx(&full[s], bytes);
         else tc::mbar_arrive(&full[s]);
       }
       __syncwarp();
       if (mine) {
-        const uint32_t dst = sbase + s * C::STAGE + isv * C::OPERAND + panel * C::PANEL + bx * a.box * 128;
+        const uint32_t dst = sbase + s * C::STAGE + isv * C::OPERAND + panel * C::PANEL + (bx << a.box_log2) * 128;
         if (a.head_first) tma_load_4d(dst, isv ? &tmV : &tmK, &full[s], panel * 64, w.h, my_off, my_page);
         else tma_load_4d(dst, isv ? &tmV : &tmK, &full[s], panel * 64, my_off, w.h, my_page);
       }

@@ -211,12 +211,17 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
 
   // A wait that runs out records the error; every later wait then returns at
   // once, so that all roles run through their loops and the CTA ends.
-  const auto wait = [&](uint64_t *bar, uint32_t parity) {
-    if (*abort_flag) return;
-    if (!tc::mbar_wait(bar, parity)) {
-      set_device_error(a.err, kErrBounds);
-      *abort_flag = 1;
+  const auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!*abort_flag) {
+      if (tc::mbar_try_wait(bar, parity)) return true;
+      if (clock64() - t0 > tc::kWaitLimit) {
+        set_device_error(a.err, kErrBounds);
+        *abort_flag = 1;
+      }
     }
+    return false;
   };
 
   Walk<kTcKeys, kTcCost> w;
@@ -227,24 +232,18 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   if (warp == C::SM_WARPS + 1) {
     // ============================================================ producer
     if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
-    // the pages of a block's boxes, lane i box i (at most 8), looked up while
-    // the block before is under way
-    const auto look = [&](const auto &u, int blk, int &page, int &off) {
-      const int key = (u.lo / kTcKeys + blk) * kTcKeys + lane * a.box;
-      page = -1;
-      off = 0;
-      if (u.left > 0 && lane < kTcKeys / a.box && key + a.box > u.lo && key < u.hi) {
-        const int pi = key / a.page_size;
-        off = key - pi * a.page_size;
-        page = __ldg(a.table + (int64_t)u.b * a.max_pages + pi);
-      }
-    };
     int it = 0, qn0 = 0, qn1 = 0;
     bool stop = false;
-    // K and V of a unit are asked for in the order of their use, which may
-    // have block j + 1's K before block j's V: pages of two blocks are held
-    int page[2], off[2], next_page, next_off;
-    look(w, w.blk, next_page, next_off);
+    // the pages of a block's boxes, lane i box i (at most 8), looked up while
+    // the block before is under way; K and V of a unit are asked for in the
+    // order of their use, which may have block j + 1's K before block j's V,
+    // so the pages of two blocks are held
+    int page[2], off[2], next_page = -1, next_off = 0;
+    PageWalk<kTcKeys> pages;
+    if (w.left > 0) {
+      pages.begin(a, w);
+      pages.next(a, next_page, next_off);
+    }
     while (w.left > 0 && !stop) {
       auto ahead = w;
       ahead.next(a);
@@ -258,8 +257,12 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
           off[1] = off[0];
           page[0] = next_page;
           off[0] = next_off;
-          if (j + 1 < n) look(w, w.blk + j + 1, next_page, next_off);
-          else look(ahead, ahead.blk, next_page, next_off);
+          if (j + 1 < n) {
+            pages.next(a, next_page, next_off);
+          } else if (ahead.left > 0) {
+            pages.begin(a, ahead);
+            pages.next(a, next_page, next_off);
+          }
         }
         // block j is the newest whose K was asked for, or the one before it
         const int newest = two ? j : min(n - 1, o == 0 ? 0 : (o + 1) / 2);
@@ -271,38 +274,43 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
           const int nkeys = isv ? C::VPART_KEYS : kTcKeys, npan = isv ? D / 64 : C::KPANELS;
           const int base = key0 + (isv ? p * C::VPART_KEYS : 0);
           const int k_lo = max(w.lo, base), k_hi = min(w.hi, base + nkeys);
-          const int box0 = k_hi > k_lo ? (k_lo - base) / a.box : 0;
-          const int nbox = k_hi > k_lo ? (k_hi - base + a.box - 1) / a.box - box0 : 0;
-          const bool mine = lane < nbox * npan;
-          const int bx = box0 + lane / npan, panel = lane % npan;
-          const int src = ((isv ? p * C::VPART_KEYS / a.box : 0) + bx) & 31;
-          int my_page = __shfl_sync(0xffffffffu, old ? page[1] : page[0], src);
-          const int my_off = __shfl_sync(0xffffffffu, old ? off[1] : off[0], src);
-          if (mine && (unsigned)my_page >= (unsigned)a.num_pages) {
-            set_device_error(a.err, kErrBounds);
-            my_page = a.num_pages;           // past the map's end: reads as zeros
-          }
+          const int box = 1 << a.box_log2;
+          const int box0 = k_hi > k_lo ? (k_lo - base) >> a.box_log2 : 0;
+          const int nbox = k_hi > k_lo ? ((k_hi - base + box - 1) >> a.box_log2) - box0 : 0;
+          const int first = (isv ? (p * C::VPART_KEYS) >> a.box_log2 : 0) + box0;   // of the block's boxes
           const int s = it % ST;
-          if (it >= ST) wait(&empty[s], ((it / ST) & 1) ^ 1);
-          __syncwarp();
-          if (__any_sync(0xffffffffu, *abort_flag != 0)) {
-            stop = true;
-            break;
-          }
+          if (it >= ST) stop = !__all_sync(0xffffffffu, wait(&empty[s], ((it / ST) & 1) ^ 1));
+          if (stop) break;
+          const uint32_t bytes = (uint32_t)((nbox << a.box_log2) * 128 * npan);
           if (lane == 0) {
-            const uint32_t bytes = (uint32_t)(nbox * a.box * 128 * npan);
             if (bytes) tc::mbar_arrive_expect_tx(&full[s], bytes);
             else tc::mbar_arrive(&full[s]);
           }
           __syncwarp();
-          if (mine) {
-            const uint32_t dst = ring + s * C::STAGE + panel * (nkeys * 128) + bx * a.box * 128;
-            const int x = (isv ? panel : p * C::KPANELS + panel) * 64;
-            const CUtensorMap *m = isv ? &tmV : &tmK;
-            if (a.head_first) tma_load_4d_at(dst, m, &full[s], x, w.h, my_off, my_page);
-            else tma_load_4d_at(dst, m, &full[s], x, my_off, w.h, my_page);
+          // one lane asks for the boxes: everything here is uniform, and
+          // copies asked for by several lanes would be issued one by one too
+          for (int bx = 0; bx < nbox; ++bx) {
+            int my_page = __shfl_sync(0xffffffffu, old ? page[1] : page[0], first + bx);
+            const int my_off = __shfl_sync(0xffffffffu, old ? off[1] : off[0], first + bx);
+            if ((unsigned)my_page >= (unsigned)a.num_pages) {
+              if (lane == 0) set_device_error(a.err, kErrBounds);
+              my_page = a.num_pages;         // past the map's end: reads as zeros
+            }
+            const uint32_t dst = ring + s * C::STAGE + ((box0 + bx) << a.box_log2) * 128;
+            const int c1 = a.head_first ? w.h : my_off, c2 = a.head_first ? my_off : w.h;
+            if (tc::elect_one()) {
+              if (isv) {
+#pragma unroll
+                for (int q = 0; q < D / 64; ++q)
+                  tma_load_4d_at(dst + q * (C::VPART_KEYS * 128), &tmV, &full[s], q * 64, c1, c2, my_page);
+              } else {
+#pragma unroll
+                for (int q = 0; q < C::KPANELS; ++q)
+                  tma_load_4d_at(dst + q * (kTcKeys * 128), &tmK, &full[s], (p * C::KPANELS + q) * 64, c1, c2, my_page);
+              }
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
         if (o == 0 && !stop) {
           // the unit's q, as soon as the last unit's scores are done with its
@@ -311,13 +319,16 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
 #pragma unroll 1
           for (int t = 0; t < (two ? 2 : 1); ++t) {
             const int u = t ? qn1++ : qn0++;
-            if (u > 0) wait(&q_empty[t], (u - 1) & 1);
-            __syncwarp();
+            if (u > 0) stop = !__all_sync(0xffffffffu, wait(&q_empty[t], (u - 1) & 1));
+            if (stop) break;
             if (lane == 0) tc::mbar_arrive_expect_tx(&q_full[t], (uint32_t)(a.tile_tok * a.G * D * 2));
             __syncwarp();
-            if (lane < D / 64)
-              tma_load_3d_at(sbase + t * C::QTILE + lane * C::QPANEL, &tmQ, &q_full[t], lane * 64, w.h * a.G,
-                             w.s.t0 + w.i0 + t * a.tile_tok);
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int q = 0; q < D / 64; ++q)
+                tma_load_3d_at(sbase + t * C::QTILE + q * C::QPANEL, &tmQ, &q_full[t], q * 64, w.h * a.G,
+                               w.s.t0 + w.i0 + t * a.tile_tok);
+            }
             __syncwarp();
           }
         }
@@ -326,6 +337,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     }
     if (stop) {                              // leave no copy in flight behind
       for (int i = max(0, it - ST); i < it; ++i) tc::mbar_wait(&full[i % ST], (i / ST) & 1);
+      // (a phase that q was not asked for in has no copy either)
       if (qn0 > 0) tc::mbar_wait(&q_full[0], (qn0 - 1) & 1);
       if (qn1 > 0) tc::mbar_wait(&q_full[1], (qn1 - 1) & 1);
     }
