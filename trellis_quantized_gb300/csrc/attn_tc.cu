@@ -4,20 +4,22 @@
 //   S = Q K^T,  P = exp2(S scale_log2 - base),  O += P V,  y = O / sum(P)
 //
 // A unit holds up to 256 rows (D <= 128) or 128 rows (D = 256) of one key
-// head and walks over its keys in blocks of 128: 4 D operations per row and
-// key against 4 D bytes per key, so from about 280 rows per byte-bound key on
-// the tensor cores are the limit.  Both products are tcgen05.mma: Q and K
-// from shared memory into a TMEM slot of 128 x 128 fp32 scores; the softmax
+// head and walks over its keys in blocks of 64: 4 D operations per row and
+// key against 4 D bytes per key, so from about 280 rows per key read from
+// memory the tensor cores are the limit.  Both products are tcgen05.mma: Q and
+// K from shared memory into a TMEM slot of 128 x 64 fp32 scores; the softmax
 // warps read the slot (a thread per row), write the fp16 weights over its
 // first half, and the second product takes them from there (A operand in
 // TMEM) with V as it lies in the cache (an MN-major operand: no transposition
 // anywhere) into O, which stays in TMEM for the whole unit.
 //
-// Two slots keep the tensor cores busy while the exponentials run: a unit of
-// more than 128 rows has two row tiles with a slot and a softmax warpgroup
-// each, and the MMAs of one tile run during the softmax of the other; a unit
-// of one tile gives its blocks to the slots in turn, and the scores of the
-// next block are computed during the softmax of this one.
+// Every row tile of 128 has two slots that its blocks take in turn and a
+// softmax warpgroup: the scores of block j + 1 are computed while the weights
+// of block j are, and only the softmax of a tile is a chain.  (Blocks of 128
+// keys leave room for one slot per tile; then the scores of the next block
+// wait for the product that reads the weights, and the chain of softmax, both
+// products and four barriers takes 3160 cycles per 128 keys at D = 128 where
+// the tensor cores need 2048.)
 //
 // The running maximum moves only when it has grown by more than a factor of
 // 2^8 (in the weights; fp16 holds 2^15): then O is read, scaled and written
@@ -37,35 +39,49 @@ int exl3_attn_tc_grid();
 namespace exl3 {
 namespace attn {
 
-constexpr int kTcKeys = 128;
-constexpr int kTcCost = 3;         // a unit's start and end, in blocks
+constexpr int kTcKeys = 64;
+#ifndef TCCOST
+#define TCCOST 6
+#endif
+constexpr int kTcCost = TCCOST;        // a unit's start and end, in blocks
 constexpr float kLazy = 8.0f;      // log2 of the growth that moves the maximum
 
-#ifndef OPS_OF
-#define OPS_OF(D) ((D) == 256 ? 2 : 1)
+#ifndef KOPS_OF
+#define KOPS_OF(D) 1
+#endif
+#ifndef VOPS_OF
+#define VOPS_OF(D) 1
+#endif
+#ifndef KST_OF
+#define KST_OF(D) ((D) == 64 ? 8 : (D) == 128 ? 5 : 3)
+#endif
+#ifndef VST_OF
+#define VST_OF(D) ((D) == 64 ? 8 : (D) == 128 ? 5 : 2)
 #endif
 template <int D>
 struct TcCfg {
   static constexpr int NQ = D == 256 ? 1 : 2;            // row tiles of a unit
   static constexpr int ROWS = NQ * 128;
-  // The ring's stages are parts of an operand, so that a part's place is free
-  // again as soon as its MMAs are done.
-  static constexpr int OPS = OPS_OF(D);                  // parts of one operand
-  static constexpr int KPANELS = D / 64 / OPS;           // K part: 128 keys x this many 64-column panels
-  static constexpr int VPART_KEYS = kTcKeys / OPS;       // V part: these keys x D columns
-  static constexpr int STAGE = kTcKeys * D * 2 / OPS;
-  static constexpr int ST = 163840 / STAGE;              // 160 KB
+  // K and V have a ring each, written by one warp and read by one.  A ring's
+  // stages are parts of an operand, so that a part's place is free again as
+  // soon as its MMAs are done; 160 KB in all.
+  static constexpr int KOPS = KOPS_OF(D), VOPS = VOPS_OF(D);   // parts of a block's K and V
+  static constexpr int KPANELS = D / 64 / KOPS;          // K part: a block's keys x this many 64-column panels
+  static constexpr int KPANEL = kTcKeys * 128;           // bytes
+  static constexpr int VPART_KEYS = kTcKeys / VOPS;      // V part: these keys x D columns
+  static constexpr int KSTAGE = kTcKeys * D * 2 / KOPS, VSTAGE = kTcKeys * D * 2 / VOPS;
+  static constexpr int KST = KST_OF(D), VST = VST_OF(D);
   static constexpr int QTILE = 128 * D * 2;
   static constexpr int QPANEL = 128 * 128;               // 64 columns of 128 rows
-  static constexpr int OFF_RING = NQ * QTILE;
-  static constexpr int SMEM = OFF_RING + ST * STAGE + 1024 /*alignment*/;
+  static constexpr int OFF_K = NQ * QTILE, OFF_V = OFF_K + KST * KSTAGE;
+  static constexpr int SMEM = OFF_V + VST * VSTAGE + 1024 /*alignment*/;
   static constexpr int SM_WARPS = 4 * NQ;                // softmax warps
-  // softmax warpgroups, then one warpgroup with the MMA issuer and the
-  // producer; registers move from the latter to the former (the sum over the
-  // warpgroups is what the launch allots: 3 x 168 or 2 x 248)
+  // softmax warpgroups, then one warpgroup with the MMA issuers and the
+  // producers; registers move from the latter to the former (the sum over the
+  // warpgroups is what the launch allots: 3 x 168, or 2 x 248)
   static constexpr int THREADS = (SM_WARPS + 4) * 32;
-  static constexpr int REGS_SM = NQ == 2 ? 208 : 248, REGS_IO = NQ == 2 ? 88 : 248;
-  static constexpr uint32_t TM_S = 0, TM_O = 256;        // TMEM columns
+  static constexpr int REGS_SM = NQ == 2 ? 200 : 248, REGS_IO = NQ == 2 ? 104 : 248;
+  static constexpr uint32_t TM_S = 0, TM_O = 256;        // TMEM columns: slots of 64, two per tile; O
   static constexpr uint32_t IDESC_S = tc::idesc_f16(128, kTcKeys);
   static constexpr uint32_t IDESC_O = tc::idesc_f16(128, D) | (1u << 16);   // B (V) is MN-major
 };
@@ -134,59 +150,143 @@ __device__ __forceinline__ void set_registers(bool more) {
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// How often each of the two slots has been given scores.
-struct Uses {
-  int u0 = 0, u1 = 0;
-  __device__ __forceinline__ int get(int s) const { return s ? u1 : u0; }
-  __device__ __forceinline__ void add(int s, int n) {
-    if (s) u1 += n;
-    else u0 += n;
+// A producer warp: brings the K (or V) parts of every block to their ring.  K
+// and V have a warp each: the arithmetic, barriers and issue of one part take
+// a warp about as long as a part's MMAs take the tensor cores.
+template <int D, bool V, class Wait>
+__device__ __forceinline__ void produce(const Args &a, Walk<kTcKeys, kTcCost> w, const CUtensorMap *tmQ,
+                                        const CUtensorMap *tm, uint32_t sbase, uint64_t *full, uint64_t *empty,
+                                        uint64_t *q_full, uint64_t *q_empty, const Wait &wait) {
+  using C = TcCfg<D>;
+  constexpr int OPS = V ? C::VOPS : C::KOPS, ST = V ? C::VST : C::KST, STAGE = V ? C::VSTAGE : C::KSTAGE;
+  constexpr int NKEYS = V ? C::VPART_KEYS : kTcKeys, NPAN = V ? D / 64 : C::KPANELS;
+  const int lane = threadIdx.x & 31, box = 1 << a.box_log2;
+  int it = 0, qn0 = 0, qn1 = 0;
+  bool stop = false;
+  // the pages of a block's boxes, lane i box i (at most 4), looked up while
+  // the block before is under way
+  int page = -1, off = 0;
+  PageWalk<kTcKeys> pages;
+  if (w.left > 0) {
+    pages.begin(a, w);
+    pages.next(a, page, off);
   }
-};
-
-// Order of a unit's operands in the ring, that of their use: with two row
-// tiles K0 V0 K1 V1 ..., with one (whose next scores come before this block's
-// weights) K0 K1 V0 K2 V1 ... V(n-1).  The o-th operand's block:
-__device__ __forceinline__ int operand(bool two, int n, int o, bool &isv) {
-  if (two) {
-    isv = o & 1;
-    return o >> 1;
+  while (w.left > 0 && !stop) {
+    auto ahead = w;
+    ahead.next(a);
+    const int n = w.nseg;
+    const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
+    for (int j = 0; j < n && !stop; ++j) {
+      const int key0 = (w.lo / kTcKeys + w.blk + j) * kTcKeys;
+      int my_page = page;
+      const int my_off = off;
+      if (j + 1 < n) {
+        pages.next(a, page, off);
+      } else if (ahead.left > 0) {
+        pages.begin(a, ahead);
+        pages.next(a, page, off);
+      }
+      const int lo = max(w.lo - key0, 0), hi = min(w.hi - key0, kTcKeys);     // keys of the block that some row sees
+      if (lane >= (lo >> a.box_log2) && lane << a.box_log2 < hi && (unsigned)my_page >= (unsigned)a.num_pages) {
+        set_device_error(a.err, kErrBounds);
+        my_page = a.num_pages;                 // past the map's end: reads as zeros
+      }
+      // every lane holds the boxes' pages before the wait, so that after it one
+      // lane has nothing to do but ask
+      int pg[4], c1[4], c2[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        pg[b] = __shfl_sync(0xffffffffu, my_page, b);
+        const int po = __shfl_sync(0xffffffffu, my_off, b);
+        c1[b] = a.head_first ? w.h : po;
+        c2[b] = a.head_first ? po : w.h;
+      }
+#pragma unroll
+      for (int p = 0; p < OPS; ++p) {
+        const int item = it + OPS * j + p, s = item % ST;
+        // the boxes of this part that some row sees
+        const int base = V ? p * NKEYS : 0;
+        const int b0 = max(lo, base) >> a.box_log2, b1 = (min(hi, base + NKEYS) + box - 1) >> a.box_log2;
+        const uint32_t dst = sbase + (V ? C::OFF_V : C::OFF_K) + s * STAGE;
+        if (item >= ST) stop = !__all_sync(0xffffffffu, wait(&empty[s], ((item / ST) & 1) ^ 1));
+        if (stop) break;
+        if (tc::elect_one()) {
+          if (b1 > b0) tc::mbar_arrive_expect_tx(&full[s], (uint32_t)(((b1 - b0) << a.box_log2) * 128 * NPAN));
+          else tc::mbar_arrive(&full[s]);
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (b >= b0 && b < b1) {
+#pragma unroll
+              for (int q = 0; q < NPAN; ++q)
+                tma_load_4d_at(dst + ((b << a.box_log2) - base) * 128 + q * (NKEYS * 128), tm, &full[s],
+                               (V ? q : p * NPAN + q) * 64, c1[b], c2[b], pg[b]);
+            }
+        }
+        __syncwarp();
+      }
+      if (!V && j == 0 && !stop) {
+        // the unit's q, as soon as the last unit's scores are done with its
+        // place: G heads of tile_tok tokens are the tile's rows in order
+        // (tokens past the unit's are rows that nobody writes)
+#pragma unroll 1
+        for (int t = 0; t < (two ? 2 : 1); ++t) {
+          const int u = t ? qn1 : qn0;
+          if (u > 0) stop = !__all_sync(0xffffffffu, wait(&q_empty[t], (u - 1) & 1));
+          if (stop) break;
+          if (t) ++qn1;
+          else ++qn0;
+          if (tc::elect_one()) {
+            tc::mbar_arrive_expect_tx(&q_full[t], (uint32_t)(a.tile_tok * a.G * D * 2));
+#pragma unroll
+            for (int q = 0; q < D / 64; ++q)
+              tma_load_3d_at(sbase + t * C::QTILE + q * C::QPANEL, tmQ, &q_full[t], q * 64, w.h * a.G,
+                             w.s.t0 + w.i0 + t * a.tile_tok);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    it += OPS * n;
+    w = ahead;
   }
-  isv = o > 0 && (o % 2 == 0 || o == 2 * n - 1);
-  return o == 2 * n - 1 ? n - 1 : isv ? o / 2 - 1 : (o + 1) / 2;
+  // After a wait that ran out nobody consumes any more: give the copies in
+  // flight their time before the CTA's memory goes to another.
+  if (stop) __nanosleep(1000000);
 }
-
-// ... and the place of block j's K or V among them.
-__device__ __forceinline__ int k_place(bool two, int j) { return two ? 2 * j : max(0, 2 * j - 1); }
-__device__ __forceinline__ int v_place(bool two, int n, int j) { return two || j == n - 1 ? 2 * j + 1 : 2 * j + 2; }
 
 template <int D>
 __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const Args a) {
   using C = TcCfg<D>;
-  constexpr int ST = C::ST, OPS = C::OPS;
+  constexpr int KST = C::KST, VST = C::VST, KOPS = C::KOPS, VOPS = C::VOPS;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[ST], empty[ST], s_full[2], p_full[2], pv_done[2], q_full[2], q_empty[2];
+  __shared__ uint64_t k_full[KST], k_empty[KST], v_full[VST], v_empty[VST], s_full[4], p_full[4], pv_done[4], q_full[2],
+      q_empty[2];
   __shared__ Share share;
   __shared__ long long warp_sums[C::THREADS / 32];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   const uint32_t raw = tc::smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
-  const uint32_t ring = sbase + C::OFF_RING;
   volatile int *abort_flag = &abort_word;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int s = 0; s < ST; ++s) {
-      tc::mbar_init(&full[s], 1);
-      tc::mbar_init(&empty[s], 1);
+    for (int s = 0; s < KST; ++s) {
+      tc::mbar_init(&k_full[s], 1);
+      tc::mbar_init(&k_empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < VST; ++s) {
+      tc::mbar_init(&v_full[s], 1);
+      tc::mbar_init(&v_empty[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) {
       tc::mbar_init(&s_full[s], 1);
       tc::mbar_init(&p_full[s], 4);
       tc::mbar_init(&pv_done[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&q_full[s], 1);
       tc::mbar_init(&q_empty[s], 1);
     }
@@ -229,196 +329,88 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   if (tid == 0) a.cuts[blockIdx.x].rows = 0;           // (the thread that may fill the record in below)
 
   // (every warp of a warpgroup moves its registers, at the head of its role)
-  if (warp == C::SM_WARPS + 1) {
-    // ============================================================ producer
+  if (warp == C::SM_WARPS + 2) {
+    // =========================================================== producers
     if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
-    int it = 0, qn0 = 0, qn1 = 0;
-    bool stop = false;
-    // the pages of a block's boxes, lane i box i (at most 8), looked up while
-    // the block before is under way; K and V of a unit are asked for in the
-    // order of their use, which may have block j + 1's K before block j's V,
-    // so the pages of two blocks are held
-    int page[2], off[2], next_page = -1, next_off = 0;
-    PageWalk<kTcKeys> pages;
-    if (w.left > 0) {
-      pages.begin(a, w);
-      pages.next(a, next_page, next_off);
-    }
-    while (w.left > 0 && !stop) {
-      auto ahead = w;
-      ahead.next(a);
-      const int n = w.nseg;
-      const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
-      for (int o = 0; o < 2 * n && !stop; ++o) {
-        bool isv;
-        const int j = operand(two, n, o, isv);
-        if (!isv) {
-          page[1] = page[0];
-          off[1] = off[0];
-          page[0] = next_page;
-          off[0] = next_off;
-          if (j + 1 < n) {
-            pages.next(a, next_page, next_off);
-          } else if (ahead.left > 0) {
-            pages.begin(a, ahead);
-            pages.next(a, next_page, next_off);
-          }
-        }
-        // block j is the newest whose K was asked for, or the one before it
-        const int newest = two ? j : min(n - 1, o == 0 ? 0 : (o + 1) / 2);
-        const int old = isv && j < newest;
-        const int key0 = (w.lo / kTcKeys + w.blk + j) * kTcKeys;
-#pragma unroll 1
-        for (int p = 0; p < OPS && !stop; ++p, ++it) {
-          // the boxes of this part that some row sees
-          const int nkeys = isv ? C::VPART_KEYS : kTcKeys, npan = isv ? D / 64 : C::KPANELS;
-          const int base = key0 + (isv ? p * C::VPART_KEYS : 0);
-          const int k_lo = max(w.lo, base), k_hi = min(w.hi, base + nkeys);
-          const int box = 1 << a.box_log2;
-          const int box0 = k_hi > k_lo ? (k_lo - base) >> a.box_log2 : 0;
-          const int nbox = k_hi > k_lo ? ((k_hi - base + box - 1) >> a.box_log2) - box0 : 0;
-          const int first = (isv ? (p * C::VPART_KEYS) >> a.box_log2 : 0) + box0;   // of the block's boxes
-          const int s = it % ST;
-          if (it >= ST) stop = !__all_sync(0xffffffffu, wait(&empty[s], ((it / ST) & 1) ^ 1));
-          if (stop) break;
-          const uint32_t bytes = (uint32_t)((nbox << a.box_log2) * 128 * npan);
-          if (lane == 0) {
-            if (bytes) tc::mbar_arrive_expect_tx(&full[s], bytes);
-            else tc::mbar_arrive(&full[s]);
-          }
-          __syncwarp();
-          // one lane asks for the boxes: everything here is uniform, and
-          // copies asked for by several lanes would be issued one by one too
-          for (int bx = 0; bx < nbox; ++bx) {
-            int my_page = __shfl_sync(0xffffffffu, old ? page[1] : page[0], first + bx);
-            const int my_off = __shfl_sync(0xffffffffu, old ? off[1] : off[0], first + bx);
-            if ((unsigned)my_page >= (unsigned)a.num_pages) {
-              if (lane == 0) set_device_error(a.err, kErrBounds);
-              my_page = a.num_pages;         // past the map's end: reads as zeros
-            }
-            const uint32_t dst = ring + s * C::STAGE + ((box0 + bx) << a.box_log2) * 128;
-            const int c1 = a.head_first ? w.h : my_off, c2 = a.head_first ? my_off : w.h;
-            if (tc::elect_one()) {
-              if (isv) {
-#pragma unroll
-                for (int q = 0; q < D / 64; ++q)
-                  tma_load_4d_at(dst + q * (C::VPART_KEYS * 128), &tmV, &full[s], q * 64, c1, c2, my_page);
-              } else {
-#pragma unroll
-                for (int q = 0; q < C::KPANELS; ++q)
-                  tma_load_4d_at(dst + q * (kTcKeys * 128), &tmK, &full[s], (p * C::KPANELS + q) * 64, c1, c2, my_page);
-              }
-            }
-            __syncwarp();
-          }
-        }
-        if (o == 0 && !stop) {
-          // the unit's q, as soon as the last unit's scores are done with its
-          // place: G heads of tile_tok tokens are the tile's rows in order
-          // (tokens past the unit's are rows that nobody writes)
-#pragma unroll 1
-          for (int t = 0; t < (two ? 2 : 1); ++t) {
-            const int u = t ? qn1++ : qn0++;
-            if (u > 0) stop = !__all_sync(0xffffffffu, wait(&q_empty[t], (u - 1) & 1));
-            if (stop) break;
-            if (lane == 0) tc::mbar_arrive_expect_tx(&q_full[t], (uint32_t)(a.tile_tok * a.G * D * 2));
-            __syncwarp();
-            if (tc::elect_one()) {
-#pragma unroll
-              for (int q = 0; q < D / 64; ++q)
-                tma_load_3d_at(sbase + t * C::QTILE + q * C::QPANEL, &tmQ, &q_full[t], q * 64, w.h * a.G,
-                               w.s.t0 + w.i0 + t * a.tile_tok);
-            }
-            __syncwarp();
-          }
-        }
-      }
-      w = ahead;
-    }
-    if (stop) {                              // leave no copy in flight behind
-      for (int i = max(0, it - ST); i < it; ++i) tc::mbar_wait(&full[i % ST], (i / ST) & 1);
-      // (a phase that q was not asked for in has no copy either)
-      if (qn0 > 0) tc::mbar_wait(&q_full[0], (qn0 - 1) & 1);
-      if (qn1 > 0) tc::mbar_wait(&q_full[1], (qn1 - 1) & 1);
-    }
+    produce<D, false>(a, w, &tmQ, &tmK, sbase, k_full, k_empty, q_full, q_empty, wait);
+  } else if (warp == C::SM_WARPS + 3) {
+    if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
+    produce<D, true>(a, w, &tmQ, &tmV, sbase, v_full, v_empty, q_full, q_empty, wait);
   } else if (warp == C::SM_WARPS) {
-    // ========================================================== MMA issuer
+    // ======================================================== MMAs: scores
+    // A tile's blocks are counted through all its units: block c takes slot
+    // c % 2 of the tile, and is the slot's use c / 2.
     if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
-    int it = 0;
-    Uses use;
-    // Scores of a block into a slot; `free_k`: nobody reads these K parts
-    // after, `free_q`: nor this tile's q.
-    const auto issue_s = [&](int t, int slot, int kit, bool free_k, bool free_q) {
-      // the slot's last weights have to be consumed first
-      if (use.get(slot) > 0) wait(&pv_done[slot], (use.get(slot) - 1) & 1);
-#pragma unroll
-      for (int p = 0; p < OPS; ++p) {
-        const int st = (kit + p) % ST;
-        wait(&full[st], ((kit + p) / ST) & 1);
-        __syncwarp();
-        tc::tc_fence_after();
-        if (tc::elect_one()) {
-          const uint64_t ad = sdesc_k_sw128(sbase + t * C::QTILE + p * C::KPANELS * C::QPANEL);
-          const uint64_t bd = sdesc_k_sw128(ring + st * C::STAGE);
-#pragma unroll
-          for (int kk = 0; kk < C::KPANELS * 4; ++kk) {
-            const int o = (kk / 4) * (C::QPANEL >> 4) + (kk % 4) * 2;
-            tc::mma_f16(tmem + C::TM_S + slot * 128, ad + o, bd + o, C::IDESC_S, (p | kk) ? 1u : 0u);
-          }
-          if (p == OPS - 1) tc::mma_commit(&s_full[slot]);
-          if (free_k) tc::mma_commit(&empty[st]);
-          if (p == OPS - 1 && free_q) tc::mma_commit(&q_empty[t]);
-        }
-        __syncwarp();
-      }
-      use.add(slot, 1);
-    };
-    // O += weights of a slot times a block's V.
-    const auto issue_pv = [&](int t, int slot, int vit, bool first, bool free_v) {
-      wait(&p_full[slot], (use.get(slot) - 1) & 1);
-#pragma unroll
-      for (int p = 0; p < OPS; ++p) {
-        const int st = (vit + p) % ST;
-        wait(&full[st], ((vit + p) / ST) & 1);
-        __syncwarp();
-        tc::tc_fence_after();
-        if (tc::elect_one()) {
-          const uint64_t bd = sdesc_mn_sw128(ring + st * C::STAGE, C::VPART_KEYS * 128);
-#pragma unroll
-          for (int kk = 0; kk < C::VPART_KEYS / 16; ++kk)
-            mma_f16_ts(tmem + C::TM_O + t * D, tmem + C::TM_S + slot * 128 + (p * C::VPART_KEYS / 16 + kk) * 8,
-                       bd + kk * (2048 >> 4), C::IDESC_O, (!first || p || kk) ? 1u : 0u);
-          if (p == OPS - 1) tc::mma_commit(&pv_done[slot]);
-          if (free_v) tc::mma_commit(&empty[st]);
-        }
-        __syncwarp();
-      }
-    };
-    int qphase0 = 0, qphase1 = 0;
+    int it = 0, units0 = 0, units1 = 0, c0 = 0, c1 = 0;
     for (; w.left > 0; w.next(a)) {
       const int n = w.nseg;
       const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
-      const auto kit = [&](int j) { return it + OPS * k_place(two, j); };
-      const auto vit = [&](int j) { return it + OPS * v_place(two, n, j); };
-      wait(&q_full[0], qphase0++ & 1);
-      if (two) {
-        issue_s(0, 0, kit(0), false, n == 1);
-        wait(&q_full[1], qphase1++ & 1);
-        issue_s(1, 1, kit(0), true, n == 1);
-        for (int j = 0; j < n; ++j) {
-          issue_pv(0, 0, vit(j), j == 0, false);
-          if (j + 1 < n) issue_s(0, 0, kit(j + 1), false, j + 2 == n);
-          issue_pv(1, 1, vit(j), j == 0, true);
-          if (j + 1 < n) issue_s(1, 1, kit(j + 1), true, j + 2 == n);
-        }
-      } else {
-        issue_s(0, 0, kit(0), true, n == 1);
-        for (int j = 0; j < n; ++j) {
-          if (j + 1 < n) issue_s(0, (j + 1) & 1, kit(j + 1), true, j + 2 == n);
-          issue_pv(0, j & 1, vit(j), j == 0, true);
+      for (int j = 0; j < n; ++j) {
+        const int k0 = it + KOPS * j;
+        for (int t = 0; t < (two ? 2 : 1); ++t) {
+          const int c = (t ? c1 : c0) + j, slot = 2 * t + (c & 1);
+          if (j == 0) wait(&q_full[t], (t ? units1++ : units0++) & 1);
+          // the slot's last weights have to be consumed first
+          if (c >= 2) wait(&pv_done[slot], ((c >> 1) - 1) & 1);
+#pragma unroll
+          for (int p = 0; p < KOPS; ++p) {
+            const int st = (k0 + p) % KST;
+            wait(&k_full[st], ((k0 + p) / KST) & 1);
+            __syncwarp();
+            tc::tc_fence_after();
+            if (tc::elect_one()) {
+              const uint64_t ad = sdesc_k_sw128(sbase + t * C::QTILE + p * C::KPANELS * C::QPANEL);
+              const uint64_t bd = sdesc_k_sw128(sbase + C::OFF_K + st * C::KSTAGE);
+#pragma unroll
+              for (int kk = 0; kk < C::KPANELS * 4; ++kk)
+                tc::mma_f16(tmem + C::TM_S + slot * 64, ad + (kk / 4) * (C::QPANEL >> 4) + (kk % 4) * 2,
+                            bd + (kk / 4) * (C::KPANEL >> 4) + (kk % 4) * 2, C::IDESC_S, (p | kk) ? 1u : 0u);
+              if (p == KOPS - 1) tc::mma_commit(&s_full[slot]);
+              if (!two || t == 1) tc::mma_commit(&k_empty[st]);              // nobody reads this K part after
+              if (p == KOPS - 1 && j == n - 1) tc::mma_commit(&q_empty[t]);   // nor this q
+            }
+            __syncwarp();
+          }
         }
       }
-      it += 2 * OPS * n;
+      it += KOPS * n;
+      c0 += n;
+      c1 += two ? n : 0;
+    }
+  } else if (warp == C::SM_WARPS + 1) {
+    // ================================================ MMAs: weighted values
+    if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
+    int it = 0, c0 = 0, c1 = 0;
+    for (; w.left > 0; w.next(a)) {
+      const int n = w.nseg;
+      const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
+      for (int j = 0; j < n; ++j) {
+        const int v0 = it + VOPS * j;
+        for (int t = 0; t < (two ? 2 : 1); ++t) {
+          const int c = (t ? c1 : c0) + j, slot = 2 * t + (c & 1);
+          wait(&p_full[slot], (c >> 1) & 1);
+#pragma unroll
+          for (int p = 0; p < VOPS; ++p) {
+            const int st = (v0 + p) % VST;
+            wait(&v_full[st], ((v0 + p) / VST) & 1);
+            __syncwarp();
+            tc::tc_fence_after();
+            if (tc::elect_one()) {
+              const uint64_t bd = sdesc_mn_sw128(sbase + C::OFF_V + st * C::VSTAGE, C::VPART_KEYS * 128);
+#pragma unroll
+              for (int kk = 0; kk < C::VPART_KEYS / 16; ++kk)
+                mma_f16_ts(tmem + C::TM_O + t * D, tmem + C::TM_S + slot * 64 + (p * C::VPART_KEYS / 16 + kk) * 8,
+                           bd + kk * (2048 >> 4), C::IDESC_O, (j || p || kk) ? 1u : 0u);
+              if (p == VOPS - 1) tc::mma_commit(&pv_done[slot]);
+              if (!two || t == 1) tc::mma_commit(&v_empty[st]);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      it += VOPS * n;
+      c0 += n;
+      c1 += two ? n : 0;
     }
   } else if (warp < C::SM_WARPS) {
     // ============================================================= softmax
@@ -428,16 +420,12 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     const uint32_t lanes = (uint32_t)(wl * 32) << 16;
     const int row = wl * 32 + lane;          // within the tile
     const int ltid = tid - t * 128;
-    int it = 0;
-    Uses use;
+    int it = 0, c = 0;                       // ring parts before the unit; blocks of this tile before
     for (; w.left > 0; w.next(a)) {
       const int n = w.nseg;
       const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
       if (t == 1 && !two) {
-        // a unit of one tile uses both slots: follow the second one's phases
-        for (int j = 1; j < n; j += 2) wait(&s_full[1], use.u1++ & 1);
-        use.u0 += (n + 1) / 2;
-        it += 2 * OPS * n;
+        it += VOPS * n;
         continue;
       }
       // this tile's tokens and rows, and the keys that this thread's row sees
@@ -449,52 +437,50 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       token_range(a, w.s, i0 + ntok - 1, 1, all_lo, tmp);
 
       float m = neg_inf(), l = 0.0f;         // the exponent's base (in scores) and the sum of weights
-      int last_slot = 0, last_use = 0;
-      for (int j = 0; j < n; ++j) {
-        const int slot = two ? t : (j & 1);
-        const int u = use.get(slot);
-        use.add(slot, 1);
+      for (int j = 0; j < n; ++j, ++c) {
+        const int slot = 2 * t + (c & 1);
+        const uint32_t tm_s = tmem + C::TM_S + slot * 64 + lanes;
         const int key0 = (w.lo / kTcKeys + w.blk + j) * kTcKeys;
-        wait(&s_full[slot], u & 1);
+        wait(&s_full[slot], (c >> 1) & 1);
         __syncwarp();
         tc::tc_fence_after();
-        float s[128];
+        float s[64];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int q = 0; q < 2; ++q) {
           float v[32];
-          tc::tmem_ld32(tmem + C::TM_S + slot * 128 + lanes + 32 * c, v);
+          tc::tmem_ld32(tm_s + 32 * q, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s[32 * c + i] = v[i];
+          for (int i = 0; i < 32; ++i) s[32 * q + i] = v[i];
         }
         tc::tmem_ld_wait();
         if (key0 < all_lo || key0 + kTcKeys > all_hi) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
+          for (int i = 0; i < 64; ++i)
             if (key0 + i < lo || key0 + i >= hi) s[i] = neg_inf();
         }
-        float x[8];
+        float x[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = s[i];
+        for (int i = 0; i < 4; ++i) x[i] = s[i];
 #pragma unroll
-        for (int i = 8; i < 128; ++i) x[i & 7] = fmaxf(x[i & 7], s[i]);
-        const float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+        for (int i = 4; i < 64; ++i) x[i & 3] = fmaxf(x[i & 3], s[i]);
+        const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         const bool grow = m != neg_inf() && (mx - m) * a.scale_log2 > kLazy;
         if (__any_sync(0xffffffffu, grow)) {
           // O so far has to be complete before it is scaled
-          wait(&pv_done[last_slot], last_use & 1);
+          wait(&pv_done[slot ^ 1], ((c - 1) >> 1) & 1);
           __syncwarp();
           tc::tc_fence_after();
           const float f = grow ? exp2_approx((m - mx) * a.scale_log2) : 1.0f;
           l *= f;
           if (grow) m = mx;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int q = 0; q < D / 32; ++q) {
             float v[32];
-            tc::tmem_ld32(tmem + C::TM_O + t * D + lanes + 32 * c, v);
+            tc::tmem_ld32(tmem + C::TM_O + t * D + lanes + 32 * q, v);
             tc::tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] *= f;
-            tc::tmem_st32(tmem + C::TM_O + t * D + lanes + 32 * c, v);
+            tc::tmem_st32(tmem + C::TM_O + t * D + lanes + 32 * q, v);
           }
           tc::tmem_st_wait();
         }
@@ -502,36 +488,34 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         const float base = m == neg_inf() ? 0.0f : m * a.scale_log2;
         const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nb2 = make_float2(-base, -base);
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        uint32_t pk[32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float2 e = __ffma2_rn(make_float2(s[64 * c + 2 * i], s[64 * c + 2 * i + 1]), sc2, nb2);
-            const float2 p = make_float2(exp2_approx(e.x), exp2_approx(e.y));
-            sum[i & 1] = __fadd2_rn(sum[i & 1], p);
-            const __half2 h = __floats2half2_rn(p.x, p.y);
-            pk[i] = *reinterpret_cast<const uint32_t *>(&h);
-          }
-          tmem_st32u(tmem + C::TM_S + slot * 128 + lanes + 32 * c, pk);
+        for (int i = 0; i < 32; ++i) {
+          const float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), sc2, nb2);
+          const float2 p = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+          sum[i & 1] = __fadd2_rn(sum[i & 1], p);
+          const __half2 h = __floats2half2_rn(p.x, p.y);
+          pk[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
+        tmem_st32u(tm_s, pk);
         if (key0 < w.lo || key0 + kTcKeys > w.hi) {
-          // V rows that no row of the unit sees: zeros.  The last block's
-          // product has to be over before `full` of this block's V is looked
-          // at: until then the ring may be a whole turn behind it.
-          if (j > 0) wait(&pv_done[last_slot], last_use & 1);
-          const int vi = it + OPS * v_place(two, n, j) + ltid / C::VPART_KEYS;
-          wait(&full[vi % ST], (vi / ST) & 1);
-          const int key = key0 + ltid;
-          if (key < w.lo || key >= w.hi) {
-            const uint32_t dst = ring + (vi % ST) * C::STAGE + (ltid % C::VPART_KEYS) * 128;
+          // V rows that no row of the unit sees: zeros.  (The part's barrier
+          // is at most one turn behind: the scores of this block were only
+          // computed after the product of the block before the last.)
+          if (ltid < kTcKeys) {
+            const int vi = it + VOPS * j + ltid / C::VPART_KEYS;
+            wait(&v_full[vi % VST], (vi / VST) & 1);
+            const int key = key0 + ltid;
+            if (key < w.lo || key >= w.hi) {
+              const uint32_t dst = sbase + C::OFF_V + (vi % VST) * C::VSTAGE + (ltid % C::VPART_KEYS) * 128;
 #pragma unroll
-            for (int p = 0; p < D / 64; ++p)
+              for (int p = 0; p < D / 64; ++p)
 #pragma unroll
-              for (int c = 0; c < 8; ++c)
-                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + p * C::VPART_KEYS * 128 + c * 16),
-                             "r"(0)
-                             : "memory");
+                for (int q = 0; q < 8; ++q)
+                  asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + p * C::VPART_KEYS * 128 + q * 16),
+                               "r"(0)
+                               : "memory");
+            }
           }
           fence_async_shared();
         }
@@ -540,14 +524,11 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&p_full[slot]);
-        last_slot = slot;
-        last_use = u;
       }
-      if (two) use.add(1 - t, n);
-      it += 2 * OPS * n;
+      it += VOPS * n;
 
       // ---- O complete: y, or this CTA's part of it
-      wait(&pv_done[last_slot], last_use & 1);
+      wait(&pv_done[2 * t + ((c - 1) & 1)], ((c - 1) >> 1) & 1);
       __syncwarp();
       tc::tc_fence_after();
       const bool whole = w.whole();
@@ -614,7 +595,7 @@ cudaError_t launch_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtens
 
 int exl3_attn_tc_rows(int D) { return D == 256 ? 128 : 256; }
 // Keys that one tensor copy must not straddle: a block, or a part of its V.
-int exl3_attn_tc_keys(int D) { return exl3::attn::kTcKeys / OPS_OF(D); }
+int exl3_attn_tc_keys(int D) { return exl3::attn::kTcKeys / VOPS_OF(D); }
 int exl3_attn_tc_grid() { return exl3_sm_count(); }
 
 cudaError_t exl3_launch_attn_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
