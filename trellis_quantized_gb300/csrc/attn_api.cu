@@ -15,7 +15,7 @@ int exl3_attn_step_grid(int D);
 cudaError_t exl3_launch_attn_step(const CUtensorMap &mk, const CUtensorMap &mv, const exl3::attn::Args &a, int D,
                                   cudaStream_t s);
 int exl3_attn_tc_rows(int D);
-int exl3_attn_tc_keys(int D);
+int exl3_attn_tc_keys();
 int exl3_attn_tc_grid();
 cudaError_t exl3_launch_attn_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                                 const exl3::attn::Args &a, int D, cudaStream_t s);
@@ -347,7 +347,7 @@ int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q
   a.max_pages = batch->max_pages;
   a.page_size = cache->page_size;
   a.num_pages = cache->num_pages;
-  const int box = std::gcd(cache->page_size, few ? exl3_attn_step_keys() : exl3_attn_tc_keys(D));
+  const int box = std::gcd(cache->page_size, few ? exl3_attn_step_keys() : exl3_attn_tc_keys());
   while ((1 << a.box_log2) < box) ++a.box_log2;        // (a power of two: a block is)
   a.head_first = cache->stride_head < cache->stride_token;
   a.scale_log2 = scale * 1.44269504088896340736f;

@@ -40,41 +40,22 @@ namespace exl3 {
 namespace attn {
 
 constexpr int kTcKeys = 64;
-#ifndef TCCOST
-#define TCCOST 6
-#endif
-constexpr int kTcCost = TCCOST;        // a unit's start and end, in blocks
+constexpr int kTcCost = 6;         // a unit's start and end, in blocks
 constexpr float kLazy = 8.0f;      // log2 of the growth that moves the maximum
 
-#ifndef KOPS_OF
-#define KOPS_OF(D) 1
-#endif
-#ifndef VOPS_OF
-#define VOPS_OF(D) 1
-#endif
-#ifndef KST_OF
-#define KST_OF(D) ((D) == 64 ? 8 : (D) == 128 ? 5 : 3)
-#endif
-#ifndef VST_OF
-#define VST_OF(D) ((D) == 64 ? 8 : (D) == 128 ? 5 : 2)
-#endif
 template <int D>
 struct TcCfg {
   static constexpr int NQ = D == 256 ? 1 : 2;            // row tiles of a unit
   static constexpr int ROWS = NQ * 128;
-  // K and V have a ring each, written by one warp and read by one.  A ring's
-  // stages are parts of an operand, so that a part's place is free again as
-  // soon as its MMAs are done; 160 KB in all.
-  static constexpr int KOPS = KOPS_OF(D), VOPS = VOPS_OF(D);   // parts of a block's K and V
-  static constexpr int KPANELS = D / 64 / KOPS;          // K part: a block's keys x this many 64-column panels
-  static constexpr int KPANEL = kTcKeys * 128;           // bytes
-  static constexpr int VPART_KEYS = kTcKeys / VOPS;      // V part: these keys x D columns
-  static constexpr int KSTAGE = kTcKeys * D * 2 / KOPS, VSTAGE = kTcKeys * D * 2 / VOPS;
-  static constexpr int KST = KST_OF(D), VST = VST_OF(D);
+  // K and V have a ring each, written by one warp and read by one: a stage is
+  // a block's K (64-column panels of 64 keys) or V; up to 160 KB in all.
+  static constexpr int PANEL = kTcKeys * 128;            // bytes
+  static constexpr int STAGE = kTcKeys * D * 2;
+  static constexpr int KST = D == 64 ? 8 : D == 128 ? 5 : 3, VST = D == 64 ? 8 : D == 128 ? 5 : 2;
   static constexpr int QTILE = 128 * D * 2;
   static constexpr int QPANEL = 128 * 128;               // 64 columns of 128 rows
-  static constexpr int OFF_K = NQ * QTILE, OFF_V = OFF_K + KST * KSTAGE;
-  static constexpr int SMEM = OFF_V + VST * VSTAGE + 1024 /*alignment*/;
+  static constexpr int OFF_K = NQ * QTILE, OFF_V = OFF_K + KST * STAGE;
+  static constexpr int SMEM = OFF_V + VST * STAGE + 1024 /*alignment*/;
   static constexpr int SM_WARPS = 4 * NQ;                // softmax warps
   // softmax warpgroups, then one warpgroup with the MMA issuers and the
   // producers; registers move from the latter to the former (the sum over the
@@ -144,22 +125,32 @@ __device__ __forceinline__ void tma_load_3d_at(uint32_t dst, const CUtensorMap *
 
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+__device__ __forceinline__ bool try_wait_plain(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 template <int N>
 __device__ __forceinline__ void set_registers(bool more) {
   if (more) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// A producer warp: brings the K (or V) parts of every block to their ring.  K
-// and V have a warp each: the arithmetic, barriers and issue of one part take
-// a warp about as long as a part's MMAs take the tensor cores.
+// A producer warp: brings every block's K (or V) to its ring.  K and V have a
+// warp each: the arithmetic, barriers and issue of one operand take a warp
+// about half as long as its MMAs take the tensor cores, and a chain of both
+// in one warp held the rest up.
 template <int D, bool V, class Wait>
 __device__ __forceinline__ void produce(const Args &a, Walk<kTcKeys, kTcCost> w, const CUtensorMap *tmQ,
                                         const CUtensorMap *tm, uint32_t sbase, uint64_t *full, uint64_t *empty,
                                         uint64_t *q_full, uint64_t *q_empty, const Wait &wait) {
   using C = TcCfg<D>;
-  constexpr int OPS = V ? C::VOPS : C::KOPS, ST = V ? C::VST : C::KST, STAGE = V ? C::VSTAGE : C::KSTAGE;
-  constexpr int NKEYS = V ? C::VPART_KEYS : kTcKeys, NPAN = V ? D / 64 : C::KPANELS;
+  constexpr int ST = V ? C::VST : C::KST;
   const int lane = threadIdx.x & 31, box = 1 << a.box_log2;
   int it = 0, qn0 = 0, qn1 = 0;
   bool stop = false;
@@ -201,29 +192,23 @@ __device__ __forceinline__ void produce(const Args &a, Walk<kTcKeys, kTcCost> w,
         c1[b] = a.head_first ? w.h : po;
         c2[b] = a.head_first ? po : w.h;
       }
+      const int item = it + j, st = item % ST;
+      const int b0 = lo >> a.box_log2, b1 = (hi + box - 1) >> a.box_log2;      // the boxes that some row sees
+      const uint32_t dst = sbase + (V ? C::OFF_V : C::OFF_K) + st * C::STAGE;
+      if (item >= ST) stop = !__all_sync(0xffffffffu, wait(&empty[st], ((item / ST) & 1) ^ 1));
+      if (stop) break;
+      if (tc::elect_one()) {
+        if (b1 > b0) tc::mbar_arrive_expect_tx(&full[st], (uint32_t)(((b1 - b0) << a.box_log2) * D * 2));
+        else tc::mbar_arrive(&full[st]);
 #pragma unroll
-      for (int p = 0; p < OPS; ++p) {
-        const int item = it + OPS * j + p, s = item % ST;
-        // the boxes of this part that some row sees
-        const int base = V ? p * NKEYS : 0;
-        const int b0 = max(lo, base) >> a.box_log2, b1 = (min(hi, base + NKEYS) + box - 1) >> a.box_log2;
-        const uint32_t dst = sbase + (V ? C::OFF_V : C::OFF_K) + s * STAGE;
-        if (item >= ST) stop = !__all_sync(0xffffffffu, wait(&empty[s], ((item / ST) & 1) ^ 1));
-        if (stop) break;
-        if (tc::elect_one()) {
-          if (b1 > b0) tc::mbar_arrive_expect_tx(&full[s], (uint32_t)(((b1 - b0) << a.box_log2) * 128 * NPAN));
-          else tc::mbar_arrive(&full[s]);
+        for (int b = 0; b < 4; ++b)
+          if (b >= b0 && b < b1) {
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
-            if (b >= b0 && b < b1) {
-#pragma unroll
-              for (int q = 0; q < NPAN; ++q)
-                tma_load_4d_at(dst + ((b << a.box_log2) - base) * 128 + q * (NKEYS * 128), tm, &full[s],
-                               (V ? q : p * NPAN + q) * 64, c1[b], c2[b], pg[b]);
-            }
-        }
-        __syncwarp();
+            for (int q = 0; q < D / 64; ++q)
+              tma_load_4d_at(dst + (b << a.box_log2) * 128 + q * C::PANEL, tm, &full[st], q * 64, c1[b], c2[b], pg[b]);
+          }
       }
+      __syncwarp();
       if (!V && j == 0 && !stop) {
         // the unit's q, as soon as the last unit's scores are done with its
         // place: G heads of tile_tok tokens are the tile's rows in order
@@ -246,7 +231,7 @@ __device__ __forceinline__ void produce(const Args &a, Walk<kTcKeys, kTcCost> w,
         }
       }
     }
-    it += OPS * n;
+    it += n;
     w = ahead;
   }
   // After a wait that ran out nobody consumes any more: give the copies in
@@ -259,7 +244,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const Args a) {
   using C = TcCfg<D>;
-  constexpr int KST = C::KST, VST = C::VST, KOPS = C::KOPS, VOPS = C::VOPS;
+  constexpr int KST = C::KST, VST = C::VST;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t k_full[KST], k_empty[KST], v_full[VST], v_empty[VST], s_full[4], p_full[4], pv_done[4], q_full[2],
       q_empty[2];
@@ -311,11 +296,13 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
 
   // A wait that runs out records the error; every later wait then returns at
   // once, so that all roles run through their loops and the CTA ends.
+  // (Waits without a suspend-time hint: with one, waking up costs 4 % of a
+  // long chunk; spinning on test_wait costs as much in issue slots.)
   const auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-    if (tc::mbar_try_wait(bar, parity)) return true;
+    if (try_wait_plain(bar, parity)) return true;
     const long long t0 = clock64();
     while (!*abort_flag) {
-      if (tc::mbar_try_wait(bar, parity)) return true;
+      if (try_wait_plain(bar, parity)) return true;
       if (clock64() - t0 > tc::kWaitLimit) {
         set_device_error(a.err, kErrBounds);
         *abort_flag = 1;
@@ -346,34 +333,30 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       const int n = w.nseg;
       const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
       for (int j = 0; j < n; ++j) {
-        const int k0 = it + KOPS * j;
+        const int st = (it + j) % KST;
         for (int t = 0; t < (two ? 2 : 1); ++t) {
           const int c = (t ? c1 : c0) + j, slot = 2 * t + (c & 1);
           if (j == 0) wait(&q_full[t], (t ? units1++ : units0++) & 1);
           // the slot's last weights have to be consumed first
           if (c >= 2) wait(&pv_done[slot], ((c >> 1) - 1) & 1);
+          if (t == 0) wait(&k_full[st], ((it + j) / KST) & 1);
+          __syncwarp();
+          tc::tc_fence_after();
+          if (tc::elect_one()) {
+            const uint64_t ad = sdesc_k_sw128(sbase + t * C::QTILE);
+            const uint64_t bd = sdesc_k_sw128(sbase + C::OFF_K + st * C::STAGE);
 #pragma unroll
-          for (int p = 0; p < KOPS; ++p) {
-            const int st = (k0 + p) % KST;
-            wait(&k_full[st], ((k0 + p) / KST) & 1);
-            __syncwarp();
-            tc::tc_fence_after();
-            if (tc::elect_one()) {
-              const uint64_t ad = sdesc_k_sw128(sbase + t * C::QTILE + p * C::KPANELS * C::QPANEL);
-              const uint64_t bd = sdesc_k_sw128(sbase + C::OFF_K + st * C::KSTAGE);
-#pragma unroll
-              for (int kk = 0; kk < C::KPANELS * 4; ++kk)
-                tc::mma_f16(tmem + C::TM_S + slot * 64, ad + (kk / 4) * (C::QPANEL >> 4) + (kk % 4) * 2,
-                            bd + (kk / 4) * (C::KPANEL >> 4) + (kk % 4) * 2, C::IDESC_S, (p | kk) ? 1u : 0u);
-              if (p == KOPS - 1) tc::mma_commit(&s_full[slot]);
-              if (!two || t == 1) tc::mma_commit(&k_empty[st]);              // nobody reads this K part after
-              if (p == KOPS - 1 && j == n - 1) tc::mma_commit(&q_empty[t]);   // nor this q
-            }
-            __syncwarp();
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma_f16(tmem + C::TM_S + slot * 64, ad + (kk / 4) * (C::QPANEL >> 4) + (kk % 4) * 2,
+                          bd + (kk / 4) * (C::PANEL >> 4) + (kk % 4) * 2, C::IDESC_S, kk ? 1u : 0u);
+            tc::mma_commit(&s_full[slot]);
+            if (!two || t == 1) tc::mma_commit(&k_empty[st]);   // nobody reads this K after
+            if (j == n - 1) tc::mma_commit(&q_empty[t]);        // nor this q
           }
+          __syncwarp();
         }
       }
-      it += KOPS * n;
+      it += n;
       c0 += n;
       c1 += two ? n : 0;
     }
@@ -385,30 +368,26 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       const int n = w.nseg;
       const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
       for (int j = 0; j < n; ++j) {
-        const int v0 = it + VOPS * j;
+        const int st = (it + j) % VST;
         for (int t = 0; t < (two ? 2 : 1); ++t) {
           const int c = (t ? c1 : c0) + j, slot = 2 * t + (c & 1);
           wait(&p_full[slot], (c >> 1) & 1);
+          if (t == 0) wait(&v_full[st], ((it + j) / VST) & 1);
+          __syncwarp();
+          tc::tc_fence_after();
+          if (tc::elect_one()) {
+            const uint64_t bd = sdesc_mn_sw128(sbase + C::OFF_V + st * C::STAGE, C::PANEL);
 #pragma unroll
-          for (int p = 0; p < VOPS; ++p) {
-            const int st = (v0 + p) % VST;
-            wait(&v_full[st], ((v0 + p) / VST) & 1);
-            __syncwarp();
-            tc::tc_fence_after();
-            if (tc::elect_one()) {
-              const uint64_t bd = sdesc_mn_sw128(sbase + C::OFF_V + st * C::VSTAGE, C::VPART_KEYS * 128);
-#pragma unroll
-              for (int kk = 0; kk < C::VPART_KEYS / 16; ++kk)
-                mma_f16_ts(tmem + C::TM_O + t * D, tmem + C::TM_S + slot * 64 + (p * C::VPART_KEYS / 16 + kk) * 8,
-                           bd + kk * (2048 >> 4), C::IDESC_O, (j || p || kk) ? 1u : 0u);
-              if (p == VOPS - 1) tc::mma_commit(&pv_done[slot]);
-              if (!two || t == 1) tc::mma_commit(&v_empty[st]);
-            }
-            __syncwarp();
+            for (int kk = 0; kk < kTcKeys / 16; ++kk)
+              mma_f16_ts(tmem + C::TM_O + t * D, tmem + C::TM_S + slot * 64 + kk * 8, bd + kk * (2048 >> 4), C::IDESC_O,
+                         (j | kk) ? 1u : 0u);
+            tc::mma_commit(&pv_done[slot]);
+            if (!two || t == 1) tc::mma_commit(&v_empty[st]);
           }
+          __syncwarp();
         }
       }
-      it += VOPS * n;
+      it += n;
       c0 += n;
       c1 += two ? n : 0;
     }
@@ -425,7 +404,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       const int n = w.nseg;
       const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
       if (t == 1 && !two) {
-        it += VOPS * n;
+        it += n;
         continue;
       }
       // this tile's tokens and rows, and the keys that this thread's row sees
@@ -499,20 +478,20 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         }
         tmem_st32u(tm_s, pk);
         if (key0 < w.lo || key0 + kTcKeys > w.hi) {
-          // V rows that no row of the unit sees: zeros.  (The part's barrier
+          // V rows that no row of the unit sees: zeros.  (The stage's barrier
           // is at most one turn behind: the scores of this block were only
           // computed after the product of the block before the last.)
           if (ltid < kTcKeys) {
-            const int vi = it + VOPS * j + ltid / C::VPART_KEYS;
+            const int vi = it + j;
             wait(&v_full[vi % VST], (vi / VST) & 1);
             const int key = key0 + ltid;
             if (key < w.lo || key >= w.hi) {
-              const uint32_t dst = sbase + C::OFF_V + (vi % VST) * C::VSTAGE + (ltid % C::VPART_KEYS) * 128;
+              const uint32_t dst = sbase + C::OFF_V + (vi % VST) * C::STAGE + ltid * 128;
 #pragma unroll
               for (int p = 0; p < D / 64; ++p)
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
-                  asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + p * C::VPART_KEYS * 128 + q * 16),
+                  asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + p * C::PANEL + q * 16),
                                "r"(0)
                                : "memory");
             }
@@ -525,7 +504,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&p_full[slot]);
       }
-      it += VOPS * n;
+      it += n;
 
       // ---- O complete: y, or this CTA's part of it
       wait(&pv_done[2 * t + ((c - 1) & 1)], ((c - 1) >> 1) & 1);
@@ -594,8 +573,8 @@ cudaError_t launch_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtens
 }  // namespace exl3
 
 int exl3_attn_tc_rows(int D) { return D == 256 ? 128 : 256; }
-// Keys that one tensor copy must not straddle: a block, or a part of its V.
-int exl3_attn_tc_keys(int D) { return exl3::attn::kTcKeys / VOPS_OF(D); }
+// Keys that one tensor copy must not straddle.
+int exl3_attn_tc_keys() { return exl3::attn::kTcKeys; }
 int exl3_attn_tc_grid() { return exl3_sm_count(); }
 
 cudaError_t exl3_launch_attn_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
