@@ -6,52 +6,78 @@
 //
 // Both calls are bound by memory: each input is read once and each output
 // written once, 2 to 4 bytes either way against about seven operations an
-// element.  A CTA takes one token; a thread holds eight neighbouring elements
-// (16 bytes of fp16) of a head, so D / 8 lanes hold a head, the mean is a few
-// shuffles, and the thread keeps its place in the head while the CTA walks
-// over the token's heads: the norm weights and the eight cosines and sines of
-// its elements stay in registers.  They come from a table that the CTA fills
-// once per token.
+// element.  A warp takes a token, or some of its heads where there are few
+// tokens, and nothing is shared between warps: no block-wide barrier, and 24
+// warps per SM with two loads in flight each cover the memory's latency.  A
+// lane holds eight neighbouring elements (16 bytes of fp16) of a head, so D / 8
+// lanes hold a head, the mean is a few shuffles, and the lane keeps its place
+// in the head while the warp walks over the token's heads: the norm weights
+// and the cosines and sines of its elements stay in registers.  The warp works
+// out the token's R / 2 angles once, 32 at a time.
 //
 // Angles.  A position times a frequency has to be known to a fraction of a
-// turn however far the position is.  The frequency in turns (f / 2 pi, one
-// double-precision product) is held as a 64-bit fixed-point fraction; its
-// product with the int32 position, modulo 2^64, is the angle modulo a turn
-// with an error below |position| * 2^-55 turns, and its upper 32 bits go to
-// sincospif.  No reduction of a large argument is left to do.
+// turn however far the position is.  The frequency in turns (f / 2 pi) is held
+// as a 64-bit fixed-point fraction, from f's 24-bit significand times 2^64 / 2
+// pi in integers (an FP64 product would be exact enough too, but GB300 has few
+// FP64 units); its product with the int32 position, modulo 2^64, is the angle
+// modulo a turn with an error below |position| * 2^-62 turns for f <= 1, and
+// its upper 32 bits go to sincospif.  No large argument is left to reduce.
 #include "exl3_common.cuh"
 #include "head_transform.cuh"
 
 namespace exl3 {
 namespace ht {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kCtas = 6;   // per CTA, per SM
 
-// The upper 32 bits of position * f as a fraction of a turn, in half turns.
-__device__ __forceinline__ float half_turns(int pos, float freq) {
-  constexpr double kInv2Pi = 0.15915494309189533577;
-  double t = (double)freq * kInv2Pi;
-  t -= floor(t);
-  const unsigned long long step = (unsigned long long)(t * 18446744073709551616.0);   // * 2^64, t < 1
+// The frequency in turns, modulo one, times 2^64: |f| = m 2^-s.
+__device__ __forceinline__ unsigned long long turn_step(float freq) {
+  constexpr unsigned long long kInv2Pi = 0x28be60db9391054aull;   // floor(2^64 / 2 pi)
+  const unsigned bits = __float_as_uint(freq), ex = (bits >> 23) & 255;
+  const unsigned long long m = ex ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
+  const int s = 150 - (ex ? (int)ex : 1);
+  const unsigned long long lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+  unsigned long long r;
+  if (s <= 0) r = -s < 64 ? lo << -s : 0;
+  else if (s < 64) r = (lo >> s) | (hi << (64 - s));
+  else r = s < 128 ? hi >> (s - 64) : 0;
+  return bits >> 31 ? 0 - r : r;
+}
+
+// An angle in half turns, within [-1, 1].
+__device__ __forceinline__ float half_turns(int pos, unsigned long long step) {
   const unsigned long long ang = step * (unsigned long long)(long long)pos;
-  return (float)(int)(unsigned)(ang >> 32) * 4.656612873077393e-10f;                  // * 2^-31: [-1, 1]
+  return (float)(int)(unsigned)(ang >> 32) * 4.656612873077393e-10f;   // * 2^-31
 }
 
 struct Row8 {
   float v[8];
 };
 
+// Eight elements as they lie in memory.
 template <bool F32>
-__device__ __forceinline__ Row8 load8(const void *base, int64_t i) {
+struct Raw8 {
+  uint4 u[F32 ? 2 : 1];
+};
+
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load_raw(const void *base, int64_t i) {
+  Raw8<F32> r;
+  const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(base) + i * (F32 ? 4 : 2));
+  r.u[0] = p[0];
+  if constexpr (F32) r.u[1] = p[1];
+  return r;
+}
+
+template <bool F32>
+__device__ __forceinline__ Row8 unpack(const Raw8<F32> &w) {
   Row8 r;
-  if (F32) {
-    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + i);
-    const float4 x = p[0], y = p[1];
+  if constexpr (F32) {
+    const float4 x = *reinterpret_cast<const float4 *>(&w.u[0]), y = *reinterpret_cast<const float4 *>(&w.u[1]);
     r.v[0] = x.x; r.v[1] = x.y; r.v[2] = x.z; r.v[3] = x.w;
     r.v[4] = y.x; r.v[5] = y.y; r.v[6] = y.z; r.v[7] = y.w;
   } else {
-    const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(base) + i);
-    const __half2 *h = reinterpret_cast<const __half2 *>(&u);
+    const __half2 *h = reinterpret_cast<const __half2 *>(&w.u[0]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 f = __half22float2(h[j]);
@@ -91,135 +117,160 @@ __device__ __forceinline__ int find_seq(const int *q_start, int B, int t, int la
   return lo;
 }
 
+// `chunk`: passes over the heads (32 / LPH heads each) that a warp makes for a
+// token; `chunks` of them make up the token.
 template <int D, bool F32IN, bool APPEND>
-__global__ void __launch_bounds__(kThreads) head_transform_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const Args a, int chunk, int chunks) {
   constexpr int LPH = D / 8;               // lanes per head
-  constexpr int HPP = kThreads / LPH;      // heads per pass of the CTA
-  __shared__ float2 cs[D / 2];
-  __shared__ float stage[kThreads][9];     // half layout with an odd number of eights: partners through here
-  __shared__ int place[3];                 // position, page (-1: not appended), offset in the page
+  constexpr int HPP = 32 / LPH;            // heads per pass
+  __shared__ __align__(16) float2 table[kWarps][D / 2];
+  __shared__ float stage_mem[kWarps][32][9];   // half layout with an odd number of eights: partners through here
 
-  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-  const int c = tid % LPH, e0 = 8 * c;     // this thread's eight elements of its heads
-  const int h0 = blockIdx.y * HPP + tid / LPH, hstep = gridDim.y * HPP;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = lane % LPH, e0 = 8 * c;    // this lane's eight elements of its heads
   const int nheads = a.Hq + a.Hkv + (APPEND ? a.Hkv : 0);
+  const int passes = (nheads + HPP - 1) / HPP;
   const int R = a.rotary_dim, half = R / 2;
+  float2 *cs = table[warp];
+  float(*stage)[9] = stage_mem[warp];
   pdl_trigger();
   pdl_wait();
 
-  const auto load_head = [&](int h) -> Row8 {
-    if (h < a.Hq) return load8<F32IN>(a.q, (int64_t)t * a.q_stride + (int64_t)h * D + e0);
-    if (h < a.Hq + a.Hkv) return load8<F32IN>(a.k, (int64_t)t * a.k_stride + (int64_t)(h - a.Hq) * D + e0);
-    return load8<F32IN>(a.v, (int64_t)t * a.v_stride + (int64_t)(h - a.Hq - a.Hkv) * D + e0);
-  };
-  // the first head's data is under way while the angles are worked out
-  Row8 x;
-  if (h0 < nheads) x = load_head(h0);
-
-  if (APPEND && tid < 32) {
-    const int b = find_seq(a.q_start, a.B, t, lane);
-    if (lane == 0) {
-      int pos = -1, page = -1, off = 0;
-      if (b < a.B) {
-        pos = a.kv_len[b] - (a.q_start[b + 1] - t);
-        const int i = pos < 0 ? a.max_pages : pos / a.page_size;
-        if (i < a.max_pages) {
-          page = a.table[(int64_t)b * a.max_pages + i];
-          off = pos - i * a.page_size;
-        }
-        if ((unsigned)page >= (unsigned)a.num_pages) {
-          set_device_error(a.err, kErrBounds);
-          page = -1;
-        }
-      }
-      place[0] = pos;
-      place[1] = page;
-      place[2] = off;
-    }
-  }
-  if (APPEND) __syncthreads();
-  const int index = APPEND ? place[0] : 0;           // cache index; negative: padding
-  if (tid < half) {
-    const int pos = a.positions ? a.positions[t] : index;
-    float s, co;
-    sincospif(half_turns(pos, a.inv_freq[tid]), &s, &co);
-    cs[tid] = make_float2(co * a.magnitude, s * a.magnitude);
-  }
-  __syncthreads();
-
-  // where this thread's elements stand in the rotation
+  // where this lane's elements stand in the rotation
   const bool pairs = a.layout == EXL3_ROPE_PAIRS;
   const bool by_lane = !pairs && half % 8 == 0;      // half layout, partners eight by eight
   const bool by_smem = !pairs && R > 0 && half % 8 != 0;
-  const bool second = e0 >= half;                    // (by_lane) upper element of its pairs
   const bool rotated = e0 < R;
-  const int partner = (lane - c % 32) + (c + (second ? -half : half) / 8) % 32;   // (by_lane) lane of the other eight
-  float co[8], si[8];
+  const int partner = rotated ? lane + (e0 >= half ? -half : half) / 8 : lane;   // (by_lane) lane of the other eight
+  unsigned long long step[D / 64];                   // of frequencies lane, lane + 32, ...
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    int i;
-    if (pairs) i = (e0 + j) / 2;
-    else i = (e0 + j) % (half > 0 ? half : 1);
-    const bool in = e0 + j < R;
-    const float2 w = in ? cs[i] : make_float2(1.0f, 0.0f);
-    co[j] = w.x;
-    // out = own * co + partner * si
-    const bool upper = pairs ? (j & 1) : (e0 + j >= half);
-    si[j] = upper ? w.y : -w.y;
-  }
-  Row8 wq, wk;
-  if (a.q_norm) wq = load8<false>(a.q_norm, e0);
-  if (a.k_norm) wk = load8<false>(a.k_norm, e0);
+  for (int k = 0; k < D / 64; ++k) step[k] = lane + 32 * k < half ? turn_step(a.inv_freq[lane + 32 * k]) : 0;
+  Raw8<false> wq = {}, wk = {};
+  if (a.q_norm) wq = load_raw<false>(a.q_norm, e0);
+  if (a.k_norm) wk = load_raw<false>(a.k_norm, e0);
 
-  for (int hb = blockIdx.y * HPP; hb < nheads; hb += hstep) {
-    const int h = hb + tid / LPH;
-    const bool live = h < nheads;
-    const bool isq = h < a.Hq, isk = !isq && h < a.Hq + a.Hkv;
-    Row8 nx;
-    if (h + hstep < nheads) nx = load_head(h + hstep);
-    if (!live) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x.v[j] = 0.0f;
+  for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < (int64_t)a.T * chunks;
+       item += (int64_t)gridDim.x * kWarps) {
+    const int t = (int)(item / chunks), p0 = (int)(item - (int64_t)t * chunks) * chunk;
+    const int p1 = min(passes, p0 + chunk);
+    const auto load_pass = [&](int p) -> Raw8<F32IN> {
+      const int h = p * HPP + lane / LPH;
+      if (h < a.Hq) return load_raw<F32IN>(a.q, (int64_t)t * a.q_stride + (int64_t)h * D + e0);
+      if (h < a.Hq + a.Hkv) return load_raw<F32IN>(a.k, (int64_t)t * a.k_stride + (int64_t)(h - a.Hq) * D + e0);
+      if (APPEND && h < nheads)
+        return load_raw<F32IN>(a.v, (int64_t)t * a.v_stride + (int64_t)(h - a.Hq - a.Hkv) * D + e0);
+      return Raw8<F32IN>{};
+    };
+    // the first heads' data is under way while the angles are worked out
+    Raw8<F32IN> next = load_pass(p0), next2 = p0 + 1 < p1 ? load_pass(p0 + 1) : Raw8<F32IN>{};
+
+    int index = 0, page = -1, off = 0;               // cache index (negative: padding) and place
+    if (APPEND) {
+      const int b = find_seq(a.q_start, a.B, t, lane);
+      index = -1;
+      if (b < a.B) {
+        index = a.kv_len[b] - (a.q_start[b + 1] - t);
+        const int i = index < 0 ? a.max_pages : index / a.page_size;
+        if (i < a.max_pages) {
+          page = a.table[(int64_t)b * a.max_pages + i];
+          off = index - i * a.page_size;
+        }
+        if ((unsigned)page >= (unsigned)a.num_pages) {
+          if (lane == 0) set_device_error(a.err, kErrBounds);
+          page = -1;
+        }
+      }
     }
-    const bool norm = isq ? a.q_norm != nullptr : (isk && a.k_norm != nullptr);
-    float ss = 0.0f;
+    const int pos = a.positions ? a.positions[t] : index;
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(x.v[j], x.v[j], ss);
-#pragma unroll
-    for (int m = 1; m < LPH; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-    Row8 o = x;
-    if (norm) {
-      const float r = rsqrtf(ss * (1.0f / D) + a.eps);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o.v[j] = x.v[j] * r * (isq ? wq.v[j] : wk.v[j]);
+    for (int k = 0; k < D / 64; ++k) {
+      const int f = lane + 32 * k;
+      if (f < half) {
+        float si, co;
+        sincospif(half_turns(pos, step[k]), &si, &co);
+        cs[f] = make_float2(co * a.magnitude, si * a.magnitude);
+      }
     }
-    Row8 p;                                          // the partner of each element
+    __syncwarp();
+    // out = own * co + partner * si
+    float co[8], si[8];
     if (pairs) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) p.v[j] = o.v[j ^ 1];
+      for (int j = 0; j < 4; ++j) {
+        const float2 w = e0 + 2 * j < R ? cs[e0 / 2 + j] : make_float2(1.0f, 0.0f);
+        co[2 * j] = co[2 * j + 1] = w.x;
+        si[2 * j] = -w.y;
+        si[2 * j + 1] = w.y;
+      }
     } else if (by_lane) {
+      const float4 *p = reinterpret_cast<const float4 *>(cs + (rotated ? (e0 >= half ? e0 - half : e0) : 0));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) p.v[j] = __shfl_sync(0xffffffffu, o.v[j], rotated ? partner : lane);
-    } else if (by_smem) {
-      __syncwarp();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) stage[tid][j] = o.v[j];
-      __syncwarp();
+      for (int j = 0; j < 4; ++j) {
+        const float4 w = rotated ? p[j] : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+        const float sg = e0 >= half ? 1.0f : -1.0f;
+        co[2 * j] = w.x;
+        co[2 * j + 1] = w.z;
+        si[2 * j] = sg * w.y;
+        si[2 * j + 1] = sg * w.w;
+      }
+    } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int e = e0 + j;
-        const int q = e < half ? e + half : (e < R ? e - half : e);
-        p.v[j] = stage[tid - c + q / 8][q % 8];
+        const float2 w = e < R ? cs[e >= half ? e - half : e] : make_float2(1.0f, 0.0f);
+        co[j] = w.x;
+        si[j] = e >= half ? w.y : -w.y;
       }
-    } else {
-      p = o;
     }
-    if (isq || isk) {
+
+    for (int p = p0; p < p1; ++p) {
+      const int h = p * HPP + lane / LPH;
+      const bool live = h < nheads, isq = h < a.Hq, isk = !isq && h < a.Hq + a.Hkv;
+      Row8 o = unpack<F32IN>(next);
+      next = next2;
+      if (p + 2 < p1) next2 = load_pass(p + 2);
+      float ss = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (e0 + j < R) o.v[j] = fmaf(o.v[j], co[j], p.v[j] * si[j]);
-    }
-    if (live) {
+      for (int j = 0; j < 8; ++j) ss = fmaf(o.v[j], o.v[j], ss);
+#pragma unroll
+      for (int m = 1; m < LPH; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+      if (isq ? a.q_norm != nullptr : (isk && a.k_norm != nullptr)) {
+        const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+        Raw8<false> ws;
+        ws.u[0] = make_uint4(isq ? wq.u[0].x : wk.u[0].x, isq ? wq.u[0].y : wk.u[0].y, isq ? wq.u[0].z : wk.u[0].z,
+                             isq ? wq.u[0].w : wk.u[0].w);
+        const Row8 w = unpack<false>(ws);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.v[j] = o.v[j] * r * w.v[j];
+      }
+      Row8 q;                                          // the partner of each element
+      if (pairs) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q.v[j] = o.v[j ^ 1];
+      } else if (by_lane) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q.v[j] = __shfl_sync(0xffffffffu, o.v[j], partner);
+      } else if (by_smem) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) stage[lane][j] = o.v[j];
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int e = e0 + j;
+          const int m = e < half ? e + half : (e < R ? e - half : e);
+          q.v[j] = stage[lane - c + m / 8][m % 8];
+        }
+      } else {
+        q = o;
+      }
+      if (isq || isk) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (e0 + j < R) o.v[j] = fmaf(o.v[j], co[j], q.v[j] * si[j]);
+      }
+      if (!live) continue;
       if (isq) {
         if (APPEND && index < 0) {
 #pragma unroll
@@ -228,25 +279,30 @@ __global__ void __launch_bounds__(kThreads) head_transform_kernel(const Args a) 
         store8(a.q_out, ((int64_t)t * a.Hq + h) * D + e0, o, !APPEND && a.f32out);
       } else if (!APPEND) {
         store8(a.k_out, ((int64_t)t * a.Hkv + (h - a.Hq)) * D + e0, o, a.f32out);
-      } else if (place[1] >= 0) {
+      } else if (page >= 0) {
         const int hk = isk ? h - a.Hq : h - a.Hq - a.Hkv;
-        const int64_t at = (int64_t)place[1] * a.stride_page + (int64_t)place[2] * a.stride_token +
+        const int64_t at = (int64_t)page * a.stride_page + (int64_t)off * a.stride_token +
                            (int64_t)hk * a.stride_head + e0;
         store8(isk ? a.k_cache : a.v_cache, at, o, false);
       }
     }
-    x = nx;
   }
 }
 
 template <int D, bool F32IN, bool APPEND>
 cudaError_t launch(const Args &a, cudaStream_t s) {
-  constexpr int HPP = kThreads / (D / 8);
+  constexpr int HPP = 32 / (D / 8);
   const int heads = a.Hq + a.Hkv + (APPEND ? a.Hkv : 0);
   const int passes = ceil_div(heads, HPP);
-  // few tokens: a CTA for every pass over the heads
-  const int gy = a.T >= 4 * exl3_sm_count() ? 1 : passes;
-  return launch_pdl(head_transform_kernel<D, F32IN, APPEND>, dim3(a.T, gy), dim3(kThreads), 0, s, a);
+  // as many passes per warp as leave every warp that fits on the GPU some
+  const int64_t warps = (int64_t)exl3_sm_count() * kCtas * kWarps;
+  int64_t chunk = ((int64_t)a.T * passes + warps - 1) / warps;
+  if (chunk > passes) chunk = passes;
+  const int chunks = ceil_div(passes, (int)chunk);
+  int64_t grid = ((int64_t)a.T * chunks + kWarps - 1) / kWarps;
+  if (grid > (int64_t)exl3_sm_count() * kCtas) grid = (int64_t)exl3_sm_count() * kCtas;
+  return launch_pdl(head_transform_kernel<D, F32IN, APPEND>, dim3((unsigned)grid), dim3(kThreads), 0, s, a, (int)chunk,
+                    chunks);
 }
 
 template <bool F32IN, bool APPEND>
