@@ -95,6 +95,8 @@ def lib_path() -> str:
 def lib():
     """Load libexl3.so (building it first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -179,9 +181,15 @@ def _ptr_pinned(t, name: str):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _raw_stream(stream=None) -> int:
+    """The stream's handle: the given one, or the current device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return ctypes.c_void_p(_raw_stream(stream))
 
 
 _ws_cache: dict = {}
@@ -192,13 +200,18 @@ def workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
 
     Every libexl3 call leaves its counters at zero again, so one cleared
     workspace serves any number of calls made in stream order."""
-    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    key = (dev.index, s.cuda_stream)
+    if device is None:
+        index = torch.cuda.current_device()
+    else:
+        device = torch.device(device)
+        index = torch.cuda.current_device() if device.index is None else device.index
+    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+    key = (index, raw)
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
+        dev = torch.device("cuda", index)
         buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        exl3_workspace_clear(buf, stream=s)
+        exl3_workspace_clear(buf, stream=stream if stream is not None else torch.cuda.current_stream(dev))
         _ws_cache[key] = buf
     return buf
 
@@ -546,32 +559,46 @@ def paged_batch(q_start, kv_len, page_table) -> PagedBatch:
     return d
 
 
-def _rows(t, name: str, heads: int, dim: int, dtype=None):
-    """Pointer and token stride of [T, heads, dim] rows whose heads are dense."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+# (These run at every decode step: pointers as plain integers, each tensor
+# property asked for once.)
+
+def _rows(t, name: str, heads: int, dim: int, dtype):
+    """Address and token stride of [T, heads, dim] CUDA rows whose heads are dense."""
+    shape, s = t.shape, t.stride()
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [T, {heads}, {dim}], got {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    s = t.stride()
-    if (dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim):
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [T, {heads}, {dim}], got {tuple(shape)}")
+    if s[2] != 1 or (s[1] != dim and heads > 1):
         raise ValueError(f"{name}'s heads must be dense")
-    return ctypes.c_void_p(t.data_ptr()), (s[0] if t.shape[0] > 1 else heads * dim)
+    return t.data_ptr(), (s[0] if shape[0] > 1 else heads * dim)
+
+
+_IO_DTYPES = {torch.float16: EXL3_OUT_F16, torch.float32: EXL3_OUT_F32}
+_OUT_DTYPES = {EXL3_OUT_F16: torch.float16, EXL3_OUT_F32: torch.float32}
 
 
 def _io_dtype(t, name: str) -> int:
-    if t.dtype == torch.float16:
-        return EXL3_OUT_F16
-    if t.dtype == torch.float32:
-        return EXL3_OUT_F32
-    raise TypeError(f"{name} must be torch.float16 or torch.float32, got {t.dtype}")
+    if not isinstance(t, torch.Tensor) or t.dtype not in _IO_DTYPES:
+        raise TypeError(f"{name} must be a torch.float16 or torch.float32 tensor")
+    return _IO_DTYPES[t.dtype]
 
 
-def _out(t, name: str, shape, dtype):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{name} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
-    return _ptr(t, name)
+def _out(t, name: str, shape, dtype) -> int:
+    """Address of a dense CUDA output of the given shape and type."""
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor {shape} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    return t.data_ptr()
+
+
+def _positions(t, T: int):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.shape != (T,) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"positions must be a contiguous CUDA int32 tensor of {T}")
+    return t.data_ptr()
 
 
 def _check_transform(transform: HeadTransform, dim: int):
@@ -584,29 +611,25 @@ def exl3_qk_norm_rope(q, k, positions, transform: HeadTransform, q_out=None, k_o
                       out_dtype: int = EXL3_OUT_F16, stream=None):
     """Head norms and rotary positions of q [T, Hq, D] and k [T, Hkv, D] (or None), fp16 or fp32;
     positions int32 [T] (None without rotation); returns (q_out, k_out), which may be q and k."""
+    in_dtype, odt = _io_dtype(q, "q"), _OUT_DTYPES.get(out_dtype, torch.float16)
     T, Hq, D = q.shape
     Hkv = 0 if k is None else k.shape[1]
-    in_dtype = _io_dtype(q, "q")
-    odt = torch.float32 if out_dtype == EXL3_OUT_F32 else torch.float16
     if q_out is None:
         q_out = torch.empty((T, Hq, D), dtype=odt, device=q.device)
     if k_out is None and k is not None:
         k_out = torch.empty((T, Hkv, D), dtype=odt, device=q.device)
-    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (T,)):
-        raise ValueError(f"positions must be int32 [{T}]")
     _check_transform(transform, D)
-    qp, qs = _rows(q, "q", Hq, D)
+    qp, qs = _rows(q, "q", Hq, D, q.dtype)
     kp, ks, kop = None, 0, None
     if k is not None:
         if k.shape[0] != T:
             raise ValueError(f"k must have {T} rows, got {k.shape[0]}")
         kp, ks = _rows(k, "k", Hkv, D, q.dtype)
         kop = _out(k_out, "k_out", (T, Hkv, D), odt)
-    if T == 0:
-        return q_out, k_out
-    _check(lib().exl3_qk_norm_rope(qp, qs, kp, ks, in_dtype, T, Hq, Hkv, D, ctypes.byref(transform),
-                                   _ptr(positions, "positions"), _out(q_out, "q_out", (T, Hq, D), odt), kop,
-                                   out_dtype, _stream(stream)))
+    qop, pp = _out(q_out, "q_out", (T, Hq, D), odt), _positions(positions, T)
+    if T:
+        _check(lib().exl3_qk_norm_rope(qp, qs, kp, ks, in_dtype, T, Hq, Hkv, D, ctypes.byref(transform), pp, qop, kop,
+                                       out_dtype, _raw_stream(stream)))
     return q_out, k_out
 
 
@@ -619,25 +642,24 @@ def exl3_qkv_append(q, k, v, batch: PagedBatch, cache: KvCache, transform: HeadT
     """Norm and rotate q [T, Hq, D], k and v [T, Hkv, D] (fp16 or fp32), write k and v to their
     places in the cache; returns q_out [T, Hq, D] fp16.  positions int32 [T], or None for the
     tokens' cache indexes."""
-    T, Hq, D = q.shape
     in_dtype = _io_dtype(q, "q")
+    T, Hq, D = q.shape
     if q_out is None:
         q_out = torch.empty((T, Hq, D), dtype=torch.float16, device=q.device)
-    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (T,)):
-        raise ValueError(f"positions must be int32 [{T}]")
     if D != cache.head_dim or k.shape[0] != T or v.shape[0] != T:
         raise ValueError(f"q, k and v must have {T} rows of heads of {cache.head_dim}")
     _check_transform(transform, D)
-    if T == 0:
-        return q_out
-    ws = workspace_buf if workspace_buf is not None else workspace(exl3_qkv_append_workspace_size(), q.device, stream)
-    qp, qs = _rows(q, "q", Hq, D)
+    qp, qs = _rows(q, "q", Hq, D, q.dtype)
     kp, ks = _rows(k, "k", cache.heads_kv, D, q.dtype)
     vp, vs = _rows(v, "v", cache.heads_kv, D, q.dtype)
-    _check(lib().exl3_qkv_append(qp, qs, kp, ks, vp, vs, in_dtype, T, Hq, ctypes.byref(transform),
-                                 _ptr(positions, "positions"), ctypes.byref(batch), ctypes.byref(cache),
-                                 _out(q_out, "q_out", (T, Hq, D), torch.float16), _ptr(ws, "workspace"),
-                                 ws.numel() * ws.element_size(), _stream(stream)))
+    qop, pp = _out(q_out, "q_out", (T, Hq, D), torch.float16), _positions(positions, T)
+    if T:
+        L = lib()
+        ws = workspace_buf if workspace_buf is not None else workspace(L.exl3_qkv_append_workspace_size(), q.device,
+                                                                       stream)
+        _check(L.exl3_qkv_append(qp, qs, kp, ks, vp, vs, in_dtype, T, Hq, ctypes.byref(transform), pp,
+                                 ctypes.byref(batch), ctypes.byref(cache), qop, _ptr(ws, "workspace"),
+                                 ws.numel() * ws.element_size(), _raw_stream(stream)))
     return q_out
 
 
@@ -652,19 +674,22 @@ def exl3_paged_attention(q, batch: PagedBatch, cache: KvCache, scale: float | No
     keys and values; returns y [T, Hq, D].  scale defaults to D ** -0.5; window > 0 keeps the last
     `window` tokens; lse, if given, is an fp32 [T, Hq] output (natural logarithm)."""
     T, Hq, D = q.shape
-    odt = torch.float32 if out_dtype == EXL3_OUT_F32 else torch.float16
+    odt = _OUT_DTYPES.get(out_dtype, torch.float16)
     if y is None:
         y = torch.empty((T, Hq, D), dtype=odt, device=q.device)
     if D != cache.head_dim:
         raise ValueError(f"q has heads of {D}, the cache of {cache.head_dim}")
     qp, qs = _rows(q, "q", Hq, D, torch.float16)
-    if T == 0:
-        return y
-    need = exl3_paged_attention_workspace_size(T, Hq, cache.heads_kv, D, batch.batch)
-    ws = workspace_buf if workspace_buf is not None else workspace(need, q.device, stream)
-    _check(lib().exl3_paged_attention(qp, qs, T, Hq, ctypes.byref(batch), ctypes.byref(cache),
-                                      D ** -0.5 if scale is None else scale, 1 if causal else 0, window,
-                                      _out(y, "y", (T, Hq, D), odt), out_dtype,
-                                      None if lse is None else _out(lse, "lse", (T, Hq), torch.float32),
-                                      _ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)))
+    yp = _out(y, "y", (T, Hq, D), odt)
+    lp = None if lse is None else _out(lse, "lse", (T, Hq), torch.float32)
+    if T:
+        L = lib()
+        ws = workspace_buf
+        if ws is None:
+            ws = workspace(L.exl3_paged_attention_workspace_size(T, Hq, cache.heads_kv, D, batch.batch), q.device,
+                           stream)
+        _check(L.exl3_paged_attention(qp, qs, T, Hq, ctypes.byref(batch), ctypes.byref(cache),
+                                      D ** -0.5 if scale is None else scale, 1 if causal else 0, window, yp, out_dtype,
+                                      lp, _ptr(ws, "workspace"), ws.numel() * ws.element_size(),
+                                      _raw_stream(stream)))
     return y

@@ -43,7 +43,7 @@ struct Args {
 
 // A unit in parts: its first part is slot 1 of the CTA that the record
 // belongs to, the others slot 0 of the CTAs up to `last`.
-struct Cut {
+struct __align__(16) Cut {
   int rows;                  // 0: no such unit
   int last;
   int t, h;                  // first token (row of the call) and key head

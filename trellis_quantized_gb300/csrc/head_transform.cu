@@ -117,8 +117,22 @@ __device__ __forceinline__ int find_seq(const int *q_start, int B, int t, int la
   return lo;
 }
 
-// `chunk`: passes over the heads (32 / LPH heads each) that a warp makes for a
-// token; `chunks` of them make up the token.
+// The passes over a token's heads, 32 / LPH heads each: queries, keys, values.
+struct Passes {
+  int q, k, all;
+};
+
+__host__ __device__ inline Passes count_passes(int Hq, int Hkv, int per_pass, bool append) {
+  Passes p;
+  p.q = (Hq + per_pass - 1) / per_pass;
+  const int kv = (Hkv + per_pass - 1) / per_pass;
+  p.k = p.q + kv;
+  p.all = p.k + (append ? kv : 0);
+  return p;
+}
+
+// `chunk`: passes that a warp makes for a token; `chunks` of them make up the
+// token.
 template <int D, bool F32IN, bool APPEND>
 __global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const Args a, int chunk, int chunks) {
   constexpr int LPH = D / 8;               // lanes per head
@@ -128,8 +142,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const A
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = lane % LPH, e0 = 8 * c;    // this lane's eight elements of its heads
-  const int nheads = a.Hq + a.Hkv + (APPEND ? a.Hkv : 0);
-  const int passes = (nheads + HPP - 1) / HPP;
+  const Passes ps = count_passes(a.Hq, a.Hkv, HPP, APPEND);
   const int R = a.rotary_dim, half = R / 2;
   float2 *cs = table[warp];
   float(*stage)[9] = stage_mem[warp];
@@ -152,13 +165,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const A
   for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < (int64_t)a.T * chunks;
        item += (int64_t)gridDim.x * kWarps) {
     const int t = (int)(item / chunks), p0 = (int)(item - (int64_t)t * chunks) * chunk;
-    const int p1 = min(passes, p0 + chunk);
+    const int p1 = min(ps.all, p0 + chunk);
+    // lane's offset in the pass's heads; a pass holds heads of one kind only
+    const int lane_el = lane * 8;
     const auto load_pass = [&](int p) -> Raw8<F32IN> {
-      const int h = p * HPP + lane / LPH;
-      if (h < a.Hq) return load_raw<F32IN>(a.q, (int64_t)t * a.q_stride + (int64_t)h * D + e0);
-      if (h < a.Hq + a.Hkv) return load_raw<F32IN>(a.k, (int64_t)t * a.k_stride + (int64_t)(h - a.Hq) * D + e0);
-      if (APPEND && h < nheads)
-        return load_raw<F32IN>(a.v, (int64_t)t * a.v_stride + (int64_t)(h - a.Hq - a.Hkv) * D + e0);
+      const void *src = p < ps.q ? a.q : p < ps.k ? a.k : a.v;
+      const int64_t stride = p < ps.q ? a.q_stride : p < ps.k ? a.k_stride : a.v_stride;
+      const int el = (p < ps.q ? p : p < ps.k ? p - ps.q : p - ps.k) * (HPP * D) + lane_el;
+      if (el < (p < ps.q ? a.Hq : a.Hkv) * D) return load_raw<F32IN>(src, t * stride + el);
       return Raw8<F32IN>{};
     };
     // the first heads' data is under way while the angles are worked out
@@ -224,18 +238,29 @@ __global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const A
       }
     }
 
+    const int64_t cache_at = APPEND ? (int64_t)page * a.stride_page + (int64_t)off * a.stride_token : 0;
     for (int p = p0; p < p1; ++p) {
-      const int h = p * HPP + lane / LPH;
-      const bool live = h < nheads, isq = h < a.Hq, isk = !isq && h < a.Hq + a.Hkv;
-      Row8 o = unpack<F32IN>(next);
+      const bool isq = p < ps.q, isv = APPEND && p >= ps.k;
+      const int el = (isq ? p : isv ? p - ps.k : p - ps.q) * (HPP * D) + lane_el;    // within the token's heads of a kind
+      const bool live = el < (isq ? a.Hq : a.Hkv) * D;
+      const Raw8<F32IN> raw = next;
       next = next2;
       if (p + 2 < p1) next2 = load_pass(p + 2);
-      float ss = 0.0f;
+      const int64_t place = APPEND ? cache_at + (int64_t)(el / D) * a.stride_head + e0 : 0;
+      if (isv) {                                       // values go as they are
+        if (live && page >= 0) {
+          if constexpr (F32IN) store8(a.v_cache, place, unpack<F32IN>(raw), false);
+          else *reinterpret_cast<uint4 *>(static_cast<__half *>(a.v_cache) + place) = raw.u[0];
+        }
+        continue;
+      }
+      Row8 o = unpack<F32IN>(raw);
+      if (isq ? a.q_norm != nullptr : a.k_norm != nullptr) {
+        float ss = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(o.v[j], o.v[j], ss);
+        for (int j = 0; j < 8; ++j) ss = fmaf(o.v[j], o.v[j], ss);
 #pragma unroll
-      for (int m = 1; m < LPH; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-      if (isq ? a.q_norm != nullptr : (isk && a.k_norm != nullptr)) {
+        for (int m = 1; m < LPH; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
         const float r = rsqrtf(ss * (1.0f / D) + a.eps);
         Raw8<false> ws;
         ws.u[0] = make_uint4(isq ? wq.u[0].x : wk.u[0].x, isq ? wq.u[0].y : wk.u[0].y, isq ? wq.u[0].z : wk.u[0].z,
@@ -244,13 +269,21 @@ __global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const A
 #pragma unroll
         for (int j = 0; j < 8; ++j) o.v[j] = o.v[j] * r * w.v[j];
       }
-      Row8 q;                                          // the partner of each element
       if (pairs) {
+        float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q.v[j] = o.v[j ^ 1];
+        for (int j = 0; j < 8; ++j) x[j] = o.v[j ^ 1];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (e0 + j < R) o.v[j] = fmaf(o.v[j], co[j], x[j] * si[j]);
       } else if (by_lane) {
+        float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q.v[j] = __shfl_sync(0xffffffffu, o.v[j], partner);
+        for (int j = 0; j < 8; ++j) x[j] = __shfl_sync(0xffffffffu, o.v[j], partner);
+        if (rotated) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o.v[j] = fmaf(o.v[j], co[j], x[j] * si[j]);
+        }
       } else if (by_smem) {
         __syncwarp();
 #pragma unroll
@@ -260,15 +293,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const A
         for (int j = 0; j < 8; ++j) {
           const int e = e0 + j;
           const int m = e < half ? e + half : (e < R ? e - half : e);
-          q.v[j] = stage[lane - c + m / 8][m % 8];
+          if (e < R) o.v[j] = fmaf(o.v[j], co[j], stage[lane - c + m / 8][m % 8] * si[j]);
         }
-      } else {
-        q = o;
-      }
-      if (isq || isk) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (e0 + j < R) o.v[j] = fmaf(o.v[j], co[j], q.v[j] * si[j]);
       }
       if (!live) continue;
       if (isq) {
@@ -276,14 +302,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const A
 #pragma unroll
           for (int j = 0; j < 8; ++j) o.v[j] = 0.0f;
         }
-        store8(a.q_out, ((int64_t)t * a.Hq + h) * D + e0, o, !APPEND && a.f32out);
+        store8(a.q_out, (int64_t)t * a.Hq * D + el, o, !APPEND && a.f32out);
       } else if (!APPEND) {
-        store8(a.k_out, ((int64_t)t * a.Hkv + (h - a.Hq)) * D + e0, o, a.f32out);
+        store8(a.k_out, (int64_t)t * a.Hkv * D + el, o, a.f32out);
       } else if (page >= 0) {
-        const int hk = isk ? h - a.Hq : h - a.Hq - a.Hkv;
-        const int64_t at = (int64_t)page * a.stride_page + (int64_t)off * a.stride_token +
-                           (int64_t)hk * a.stride_head + e0;
-        store8(isk ? a.k_cache : a.v_cache, at, o, false);
+        store8(a.k_cache, place, o, false);
       }
     }
   }
@@ -291,9 +314,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const A
 
 template <int D, bool F32IN, bool APPEND>
 cudaError_t launch(const Args &a, cudaStream_t s) {
-  constexpr int HPP = 32 / (D / 8);
-  const int heads = a.Hq + a.Hkv + (APPEND ? a.Hkv : 0);
-  const int passes = ceil_div(heads, HPP);
+  const int passes = count_passes(a.Hq, a.Hkv, 32 / (D / 8), APPEND).all;
   // as many passes per warp as leave every warp that fits on the GPU some
   const int64_t warps = (int64_t)exl3_sm_count() * kCtas * kWarps;
   int64_t chunk = ((int64_t)a.T * passes + warps - 1) / warps;
