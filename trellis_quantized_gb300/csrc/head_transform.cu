@@ -131,14 +131,19 @@ __host__ __device__ inline Passes count_passes(int Hq, int Hkv, int per_pass, bo
   return p;
 }
 
+// How a lane's eight elements meet their partners: all eight in another lane
+// (half layout, R / 2 a multiple of 8, or no rotation), in the same lane
+// (pairs, R a multiple of 8), or one by one.
+enum { kByLane, kInLane, kAny };
+
 // `chunk`: passes that a warp makes for a token; `chunks` of them make up the
 // token.
-template <int D, bool F32IN, bool APPEND>
-__global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const Args a, int chunk, int chunks) {
+template <int D, bool F32IN, bool APPEND, int MODE>
+__global__ void __launch_bounds__(kThreads, F32IN ? kCtas - 1 : kCtas) head_transform_kernel(const Args a, int chunk, int chunks) {
   constexpr int LPH = D / 8;               // lanes per head
   constexpr int HPP = 32 / LPH;            // heads per pass
   __shared__ __align__(16) float2 table[kWarps][D / 2];
-  __shared__ float stage_mem[kWarps][32][9];   // half layout with an odd number of eights: partners through here
+  __shared__ float stage_mem[kWarps][MODE == kAny ? 32 : 1][9];   // partners that are looked up one by one
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = lane % LPH, e0 = 8 * c;    // this lane's eight elements of its heads
@@ -149,34 +154,46 @@ __global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const A
   pdl_trigger();
   pdl_wait();
 
-  // where this lane's elements stand in the rotation
-  const bool pairs = a.layout == EXL3_ROPE_PAIRS;
-  const bool by_lane = !pairs && half % 8 == 0;      // half layout, partners eight by eight
-  const bool by_smem = !pairs && R > 0 && half % 8 != 0;
-  const bool rotated = e0 < R;
-  const int partner = rotated ? lane + (e0 >= half ? -half : half) / 8 : lane;   // (by_lane) lane of the other eight
+  const bool pairs = MODE == kInLane || (MODE == kAny && a.layout == EXL3_ROPE_PAIRS);
+  const bool rotated = e0 < R, second = e0 >= half;
+  const int away = second ? -half : half;            // (by lane) the partner elements
+  const int partner = rotated ? lane + away / 8 : lane;
   unsigned long long step[D / 64];                   // of frequencies lane, lane + 32, ...
 #pragma unroll
   for (int k = 0; k < D / 64; ++k) step[k] = lane + 32 * k < half ? turn_step(a.inv_freq[lane + 32 * k]) : 0;
-  Raw8<false> wq = {}, wk = {};
-  if (a.q_norm) wq = load_raw<false>(a.q_norm, e0);
-  if (a.k_norm) wk = load_raw<false>(a.k_norm, e0);
+  // this lane's place in a token's rows, in bytes
+  constexpr int kIn = HPP * D * (F32IN ? 4 : 2);     // a pass
+  const char *q_in = static_cast<const char *>(a.q) + lane * 8 * (F32IN ? 4 : 2);
+  const char *k_in = static_cast<const char *>(a.k) + lane * 8 * (F32IN ? 4 : 2);
+  const char *v_in = static_cast<const char *>(a.v) + lane * 8 * (F32IN ? 4 : 2);
+  const int64_t q_row = a.q_stride * (F32IN ? 4 : 2), k_row = a.k_stride * (F32IN ? 4 : 2),
+                v_row = a.v_stride * (F32IN ? 4 : 2);
+  const bool last_q = (ps.q - 1) * HPP + lane / LPH < a.Hq;
+  const bool last_kv = (ps.k - ps.q - 1) * HPP + lane / LPH < a.Hkv;
 
   for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < (int64_t)a.T * chunks;
        item += (int64_t)gridDim.x * kWarps) {
     const int t = (int)(item / chunks), p0 = (int)(item - (int64_t)t * chunks) * chunk;
     const int p1 = min(ps.all, p0 + chunk);
-    // lane's offset in the pass's heads; a pass holds heads of one kind only
-    const int lane_el = lane * 8;
-    const auto load_pass = [&](int p) -> Raw8<F32IN> {
-      const void *src = p < ps.q ? a.q : p < ps.k ? a.k : a.v;
-      const int64_t stride = p < ps.q ? a.q_stride : p < ps.k ? a.k_stride : a.v_stride;
-      const int el = (p < ps.q ? p : p < ps.k ? p - ps.q : p - ps.k) * (HPP * D) + lane_el;
-      if (el < (p < ps.q ? a.Hq : a.Hkv) * D) return load_raw<F32IN>(src, t * stride + el);
-      return Raw8<F32IN>{};
+    // one pass after the other is fetched: queries, keys, values (a pass holds
+    // heads of one kind only; the last of a kind may leave lanes without one)
+    int fp = p0;
+    const char *src = p0 < ps.q   ? q_in + t * q_row + (int64_t)p0 * kIn
+                      : p0 < ps.k ? k_in + t * k_row + (int64_t)(p0 - ps.q) * kIn
+                                  : v_in + t * v_row + (int64_t)(p0 - ps.k) * kIn;
+    const auto fetch = [&]() -> Raw8<F32IN> {
+      Raw8<F32IN> r = {};
+      if (fp < p1) {
+        if (fp + 1 == ps.q ? last_q : (fp + 1 == ps.k || fp + 1 == ps.all) ? last_kv : true)
+          r = load_raw<F32IN>(src, 0);
+        src += kIn;
+        if (++fp == ps.q) src = k_in + t * k_row;
+        else if (fp == ps.k) src = v_in + t * v_row;
+      }
+      return r;
     };
     // the first heads' data is under way while the angles are worked out
-    Raw8<F32IN> next = load_pass(p0), next2 = p0 + 1 < p1 ? load_pass(p0 + 1) : Raw8<F32IN>{};
+    Raw8<F32IN> next = fetch(), next2 = fetch();
 
     int index = 0, page = -1, off = 0;               // cache index (negative: padding) and place
     if (APPEND) {
@@ -207,94 +224,114 @@ __global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const A
       }
     }
     __syncwarp();
-    // out = own * co + partner * si
-    float co[8], si[8];
-    if (pairs) {
+    // out = r (own * own_w + partner * partner_w): the norm weight of each
+    // element times its cosine or sine, for one kind of head at a time
+    float own_w[8], partner_w[8];
+    const auto set_weights = [&](const void *norm) {
+      Row8 w, wp;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 w = e0 + 2 * j < R ? cs[e0 / 2 + j] : make_float2(1.0f, 0.0f);
-        co[2 * j] = co[2 * j + 1] = w.x;
-        si[2 * j] = -w.y;
-        si[2 * j + 1] = w.y;
-      }
-    } else if (by_lane) {
-      const float4 *p = reinterpret_cast<const float4 *>(cs + (rotated ? (e0 >= half ? e0 - half : e0) : 0));
+      for (int j = 0; j < 8; ++j) w.v[j] = wp.v[j] = 1.0f;
+      if (norm) w = unpack<false>(load_raw<false>(norm, e0));
+      if constexpr (MODE != kAny) {
+        if (rotated) {
+          if (MODE == kByLane && norm) wp = unpack<false>(load_raw<false>(norm, e0 + away));
+          const float4 *tab = reinterpret_cast<const float4 *>(cs + (MODE == kInLane ? e0 / 2 : second ? e0 - half : e0));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 w = rotated ? p[j] : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-        const float sg = e0 >= half ? 1.0f : -1.0f;
-        co[2 * j] = w.x;
-        co[2 * j + 1] = w.z;
-        si[2 * j] = sg * w.y;
-        si[2 * j + 1] = sg * w.w;
-      }
-    } else {
+          for (int j = 0; j < 8; j += 2) {
+            if (MODE == kInLane && (j & 3)) continue;
+            const float4 t = tab[MODE == kInLane ? j / 4 : j / 2];
+            if constexpr (MODE == kByLane) {
+              const float sg = second ? 1.0f : -1.0f;
+              own_w[j] = w.v[j] * t.x;
+              own_w[j + 1] = w.v[j + 1] * t.z;
+              partner_w[j] = sg * t.y * wp.v[j];
+              partner_w[j + 1] = sg * t.w * wp.v[j + 1];
+            } else {
+              own_w[j] = w.v[j] * t.x;
+              own_w[j + 1] = w.v[j + 1] * t.x;
+              own_w[j + 2] = w.v[j + 2] * t.z;
+              own_w[j + 3] = w.v[j + 3] * t.z;
+              partner_w[j] = -t.y * w.v[j + 1];
+              partner_w[j + 1] = t.y * w.v[j];
+              partner_w[j + 2] = -t.w * w.v[j + 3];
+              partner_w[j + 3] = t.w * w.v[j + 2];
+            }
+          }
+        } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int e = e0 + j;
-        const float2 w = e < R ? cs[e >= half ? e - half : e] : make_float2(1.0f, 0.0f);
-        co[j] = w.x;
-        si[j] = e >= half ? w.y : -w.y;
+          for (int j = 0; j < 8; ++j) own_w[j] = w.v[j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int e = e0 + j, m = pairs ? e ^ 1 : e >= half ? e - half : e + half;
+          const float2 t = e < R ? cs[pairs ? e / 2 : e >= half ? e - half : e] : make_float2(1.0f, 0.0f);
+          const float v = norm && e < R ? __half2float(static_cast<const __half *>(norm)[m]) : 1.0f;
+          own_w[j] = w.v[j] * t.x;
+          partner_w[j] = ((pairs ? j & 1 : e >= half) ? t.y : -t.y) * v;
+        }
       }
-    }
+    };
+    set_weights(p0 < ps.q ? a.q_norm : a.k_norm);
 
-    const int64_t cache_at = APPEND ? (int64_t)page * a.stride_page + (int64_t)off * a.stride_token : 0;
+    const int64_t cache_at = APPEND ? (int64_t)page * a.stride_page + (int64_t)off * a.stride_token + e0 : 0;
     for (int p = p0; p < p1; ++p) {
       const bool isq = p < ps.q, isv = APPEND && p >= ps.k;
-      const int el = (isq ? p : isv ? p - ps.k : p - ps.q) * (HPP * D) + lane_el;    // within the token's heads of a kind
-      const bool live = el < (isq ? a.Hq : a.Hkv) * D;
       const Raw8<F32IN> raw = next;
       next = next2;
-      if (p + 2 < p1) next2 = load_pass(p + 2);
-      const int64_t place = APPEND ? cache_at + (int64_t)(el / D) * a.stride_head + e0 : 0;
+      next2 = fetch();
+      const int head = (isq ? p : isv ? p - ps.k : p - ps.q) * HPP + lane / LPH;
+      const bool live = head < (isq ? a.Hq : a.Hkv);
       if (isv) {                                       // values go as they are
         if (live && page >= 0) {
+          const int64_t place = cache_at + head * a.stride_head;
           if constexpr (F32IN) store8(a.v_cache, place, unpack<F32IN>(raw), false);
           else *reinterpret_cast<uint4 *>(static_cast<__half *>(a.v_cache) + place) = raw.u[0];
         }
         continue;
       }
+      if (p == ps.q && p > p0) set_weights(a.k_norm);
       Row8 o = unpack<F32IN>(raw);
+      float r = 1.0f;
       if (isq ? a.q_norm != nullptr : a.k_norm != nullptr) {
         float ss = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = fmaf(o.v[j], o.v[j], ss);
 #pragma unroll
         for (int m = 1; m < LPH; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-        const float r = rsqrtf(ss * (1.0f / D) + a.eps);
-        Raw8<false> ws;
-        ws.u[0] = make_uint4(isq ? wq.u[0].x : wk.u[0].x, isq ? wq.u[0].y : wk.u[0].y, isq ? wq.u[0].z : wk.u[0].z,
-                             isq ? wq.u[0].w : wk.u[0].w);
-        const Row8 w = unpack<false>(ws);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o.v[j] = o.v[j] * r * w.v[j];
+        r = rsqrtf(ss * (1.0f / D) + a.eps);
       }
-      if (pairs) {
-        float x[8];
+      if constexpr (MODE == kInLane) {
+        if (rotated) {
+          float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = o.v[j ^ 1];
+          for (int j = 0; j < 8; ++j) x[j] = o.v[j ^ 1];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (e0 + j < R) o.v[j] = fmaf(o.v[j], co[j], x[j] * si[j]);
-      } else if (by_lane) {
+          for (int j = 0; j < 8; ++j) o.v[j] = fmaf(x[j], partner_w[j], o.v[j] * own_w[j]) * r;
+        }
+      } else if constexpr (MODE == kByLane) {
         float x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = __shfl_sync(0xffffffffu, o.v[j], partner);
         if (rotated) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o.v[j] = fmaf(o.v[j], co[j], x[j] * si[j]);
+          for (int j = 0; j < 8; ++j) o.v[j] = fmaf(x[j], partner_w[j], o.v[j] * own_w[j]) * r;
         }
-      } else if (by_smem) {
+      } else {
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 8; ++j) stage[lane][j] = o.v[j];
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int e = e0 + j;
-          const int m = e < half ? e + half : (e < R ? e - half : e);
-          if (e < R) o.v[j] = fmaf(o.v[j], co[j], stage[lane - c + m / 8][m % 8] * si[j]);
+          const int e = e0 + j, m = e >= R ? e : pairs ? e ^ 1 : e < half ? e + half : e - half;
+          const float y = o.v[j] * own_w[j], x = stage[lane - c + m / 8][m % 8];
+          o.v[j] = (e < R ? fmaf(x, partner_w[j], y) : y) * r;
         }
+      }
+      if (MODE != kAny && !rotated) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.v[j] *= own_w[j] * r;
       }
       if (!live) continue;
       if (isq) {
@@ -302,11 +339,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const A
 #pragma unroll
           for (int j = 0; j < 8; ++j) o.v[j] = 0.0f;
         }
-        store8(a.q_out, (int64_t)t * a.Hq * D + el, o, !APPEND && a.f32out);
+        store8(a.q_out, ((int64_t)t * a.Hq + head) * D + e0, o, !APPEND && a.f32out);
       } else if (!APPEND) {
-        store8(a.k_out, (int64_t)t * a.Hkv * D + el, o, a.f32out);
+        store8(a.k_out, ((int64_t)t * a.Hkv + head) * D + e0, o, a.f32out);
       } else if (page >= 0) {
-        store8(a.k_cache, place, o, false);
+        store8(a.k_cache, cache_at + head * a.stride_head, o, false);
       }
     }
   }
@@ -322,8 +359,13 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
   const int chunks = ceil_div(passes, (int)chunk);
   int64_t grid = ((int64_t)a.T * chunks + kWarps - 1) / kWarps;
   if (grid > (int64_t)exl3_sm_count() * kCtas) grid = (int64_t)exl3_sm_count() * kCtas;
-  return launch_pdl(head_transform_kernel<D, F32IN, APPEND>, dim3((unsigned)grid), dim3(kThreads), 0, s, a, (int)chunk,
-                    chunks);
+  const dim3 g((unsigned)grid), b(kThreads);
+  const bool pairs = a.layout == EXL3_ROPE_PAIRS;
+  if (pairs ? a.rotary_dim == 0 : a.rotary_dim % 16 == 0)
+    return launch_pdl(head_transform_kernel<D, F32IN, APPEND, kByLane>, g, b, 0, s, a, (int)chunk, chunks);
+  if (pairs && a.rotary_dim % 8 == 0)
+    return launch_pdl(head_transform_kernel<D, F32IN, APPEND, kInLane>, g, b, 0, s, a, (int)chunk, chunks);
+  return launch_pdl(head_transform_kernel<D, F32IN, APPEND, kAny>, g, b, 0, s, a, (int)chunk, chunks);
 }
 
 template <bool F32IN, bool APPEND>
