@@ -168,32 +168,25 @@ __global__ void __launch_bounds__(kThreads, F32IN ? kCtas - 1 : kCtas) head_tran
   const char *v_in = static_cast<const char *>(a.v) + lane * 8 * (F32IN ? 4 : 2);
   const int64_t q_row = a.q_stride * (F32IN ? 4 : 2), k_row = a.k_stride * (F32IN ? 4 : 2),
                 v_row = a.v_stride * (F32IN ? 4 : 2);
-  const bool last_q = (ps.q - 1) * HPP + lane / LPH < a.Hq;
-  const bool last_kv = (ps.k - ps.q - 1) * HPP + lane / LPH < a.Hkv;
+  // passes of a kind that have a head for this lane: all, or all but the last
+  const int live_q = ps.q - ((ps.q - 1) * HPP + lane / LPH < a.Hq ? 0 : 1);
+  const int live_kv = ps.k - ps.q - ((ps.k - ps.q - 1) * HPP + lane / LPH < a.Hkv ? 0 : 1);
 
   for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < (int64_t)a.T * chunks;
        item += (int64_t)gridDim.x * kWarps) {
     const int t = (int)(item / chunks), p0 = (int)(item - (int64_t)t * chunks) * chunk;
     const int p1 = min(ps.all, p0 + chunk);
-    // one pass after the other is fetched: queries, keys, values (a pass holds
-    // heads of one kind only; the last of a kind may leave lanes without one)
-    int fp = p0;
-    const char *src = p0 < ps.q   ? q_in + t * q_row + (int64_t)p0 * kIn
-                      : p0 < ps.k ? k_in + t * k_row + (int64_t)(p0 - ps.q) * kIn
-                                  : v_in + t * v_row + (int64_t)(p0 - ps.k) * kIn;
-    const auto fetch = [&]() -> Raw8<F32IN> {
-      Raw8<F32IN> r = {};
-      if (fp < p1) {
-        if (fp + 1 == ps.q ? last_q : (fp + 1 == ps.k || fp + 1 == ps.all) ? last_kv : true)
-          r = load_raw<F32IN>(src, 0);
-        src += kIn;
-        if (++fp == ps.q) src = k_in + t * k_row;
-        else if (fp == ps.k) src = v_in + t * v_row;
-      }
-      return r;
+    // the first heads of every kind are under way while the angles are worked out
+    const int qa = p0, qb = min(p1, ps.q), ka = max(p0 - ps.q, 0), kb = min(p1, ps.k) - ps.q;
+    const int va = max(p0 - ps.k, 0), vb = p1 - ps.k;
+    const char *q_src = q_in + t * q_row + (int64_t)qa * kIn, *k_src = k_in + t * k_row + (int64_t)ka * kIn,
+               *v_src = v_in + t * v_row + (int64_t)va * kIn;
+    const auto load_if = [&](bool ok, const char *p) -> Raw8<F32IN> {
+      if (ok) return load_raw<F32IN>(p, 0);
+      return Raw8<F32IN>{};
     };
-    // the first heads' data is under way while the angles are worked out
-    Raw8<F32IN> next = fetch(), next2 = fetch();
+    const Raw8<F32IN> q0 = load_if(qa < min(qb, live_q), q_src), k0 = load_if(ka < min(kb, live_kv), k_src),
+                      v0 = load_if(APPEND && va < min(vb, live_kv), v_src);
 
     int index = 0, page = -1, off = 0;               // cache index (negative: padding) and place
     if (APPEND) {
@@ -272,78 +265,91 @@ __global__ void __launch_bounds__(kThreads, F32IN ? kCtas - 1 : kCtas) head_tran
         }
       }
     };
-    set_weights(p0 < ps.q ? a.q_norm : a.k_norm);
-
-    const int64_t cache_at = APPEND ? (int64_t)page * a.stride_page + (int64_t)off * a.stride_token + e0 : 0;
-    for (int p = p0; p < p1; ++p) {
-      const bool isq = p < ps.q, isv = APPEND && p >= ps.k;
-      const Raw8<F32IN> raw = next;
-      next = next2;
-      next2 = fetch();
-      const int head = (isq ? p : isv ? p - ps.k : p - ps.q) * HPP + lane / LPH;
-      const bool live = head < (isq ? a.Hq : a.Hkv);
-      if (isv) {                                       // values go as they are
-        if (live && page >= 0) {
-          const int64_t place = cache_at + head * a.stride_head;
-          if constexpr (F32IN) store8(a.v_cache, place, unpack<F32IN>(raw), false);
-          else *reinterpret_cast<uint4 *>(static_cast<__half *>(a.v_cache) + place) = raw.u[0];
+    // Passes pa .. pb - 1 of one kind, two loads ahead of the arithmetic.
+    const auto walk = [&](int pa, int pb, int live, const char *src, Raw8<F32IN> raw, char *dst, int64_t step,
+                          bool f32out, bool norm, bool zero, bool write) {
+      Raw8<F32IN> next = load_if(pa + 1 < min(pb, live), src + kIn);
+      src += 2 * kIn;
+#pragma unroll 1
+      for (int p = pa; p < pb; ++p, src += kIn, dst += step) {
+        Row8 o = unpack<F32IN>(raw);
+        raw = next;
+        next = load_if(p + 2 < min(pb, live), src);
+        float r = 1.0f;
+        if (norm) {
+          float ss = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ss = fmaf(o.v[j], o.v[j], ss);
+#pragma unroll
+          for (int m = 1; m < LPH; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+          r = rsqrtf(ss * (1.0f / D) + a.eps);
         }
-        continue;
-      }
-      if (p == ps.q && p > p0) set_weights(a.k_norm);
-      Row8 o = unpack<F32IN>(raw);
-      float r = 1.0f;
-      if (isq ? a.q_norm != nullptr : a.k_norm != nullptr) {
-        float ss = 0.0f;
+        if constexpr (MODE == kInLane) {
+          if (rotated) {
+            float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(o.v[j], o.v[j], ss);
+            for (int j = 0; j < 8; ++j) x[j] = o.v[j ^ 1];
 #pragma unroll
-        for (int m = 1; m < LPH; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-        r = rsqrtf(ss * (1.0f / D) + a.eps);
-      }
-      if constexpr (MODE == kInLane) {
-        if (rotated) {
+            for (int j = 0; j < 8; ++j) o.v[j] = fmaf(x[j], partner_w[j], o.v[j] * own_w[j]) * r;
+          }
+        } else if constexpr (MODE == kByLane) {
           float x[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = o.v[j ^ 1];
+          for (int j = 0; j < 8; ++j) x[j] = __shfl_sync(0xffffffffu, o.v[j], partner);
+          if (rotated) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o.v[j] = fmaf(x[j], partner_w[j], o.v[j] * own_w[j]) * r;
+            for (int j = 0; j < 8; ++j) o.v[j] = fmaf(x[j], partner_w[j], o.v[j] * own_w[j]) * r;
+          }
+        } else {
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) stage[lane][j] = o.v[j];
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int e = e0 + j, m = e >= R ? e : pairs ? e ^ 1 : e < half ? e + half : e - half;
+            const float y = o.v[j] * own_w[j], x = stage[lane - c + m / 8][m % 8];
+            o.v[j] = (e < R ? fmaf(x, partner_w[j], y) : y) * r;
+          }
         }
-      } else if constexpr (MODE == kByLane) {
-        float x[8];
+        if (MODE != kAny && !rotated) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __shfl_sync(0xffffffffu, o.v[j], partner);
-        if (rotated) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o.v[j] = fmaf(x[j], partner_w[j], o.v[j] * own_w[j]) * r;
+          for (int j = 0; j < 8; ++j) o.v[j] *= own_w[j] * r;
         }
-      } else {
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) stage[lane][j] = o.v[j];
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int e = e0 + j, m = e >= R ? e : pairs ? e ^ 1 : e < half ? e + half : e - half;
-          const float y = o.v[j] * own_w[j], x = stage[lane - c + m / 8][m % 8];
-          o.v[j] = (e < R ? fmaf(x, partner_w[j], y) : y) * r;
-        }
+        if (APPEND && zero) o = Row8{};
+        if (p < live && write) store8(dst, 0, o, f32out);
       }
-      if (MODE != kAny && !rotated) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o.v[j] *= own_w[j] * r;
-      }
-      if (!live) continue;
-      if (isq) {
-        if (APPEND && index < 0) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o.v[j] = 0.0f;
+    };
+    const bool f32out = !APPEND && a.f32out;
+    const int osz = f32out ? 4 : 2;
+    const bool place = !APPEND || page >= 0;
+    const int64_t cache_at = APPEND ? (int64_t)page * a.stride_page + (int64_t)off * a.stride_token + e0 : 0;
+    const int64_t cache_step = HPP * a.stride_head * 2;
+    if (qa < qb) {
+      set_weights(a.q_norm);
+      walk(qa, qb, live_q, q_src, q0,
+           static_cast<char *>(a.q_out) + ((int64_t)t * a.Hq * D + (int64_t)qa * (HPP * D) + lane * 8) * osz,
+           HPP * D * osz, f32out, a.q_norm != nullptr, index < 0, true);
+    }
+    if (ka < kb) {
+      set_weights(a.k_norm);
+      char *dst = APPEND ? static_cast<char *>(a.k_cache) + (cache_at + (ka * HPP + lane / LPH) * a.stride_head) * 2
+                         : static_cast<char *>(a.k_out) +
+                               ((int64_t)t * a.Hkv * D + (int64_t)ka * (HPP * D) + lane * 8) * osz;
+      walk(ka, kb, live_kv, k_src, k0, dst, APPEND ? cache_step : HPP * D * osz, f32out, a.k_norm != nullptr, false,
+           place);
+    }
+    if (APPEND && va < vb) {                           // values go as they are
+      char *dst = static_cast<char *>(a.v_cache) + (cache_at + (va * HPP + lane / LPH) * a.stride_head) * 2;
+      Raw8<F32IN> raw = v0;
+      for (int p = va; p < vb; ++p, dst += cache_step) {
+        v_src += kIn;
+        const Raw8<F32IN> next = load_if(p + 1 < min(vb, live_kv), v_src);
+        if (p < live_kv && place) {
+          if constexpr (F32IN) store8(dst, 0, unpack<F32IN>(raw), false);
+          else *reinterpret_cast<uint4 *>(dst) = raw.u[0];
         }
-        store8(a.q_out, ((int64_t)t * a.Hq + head) * D + e0, o, !APPEND && a.f32out);
-      } else if (!APPEND) {
-        store8(a.k_out, ((int64_t)t * a.Hkv + head) * D + e0, o, a.f32out);
-      } else if (page >= 0) {
-        store8(a.k_cache, cache_at + head * a.stride_head, o, false);
+        raw = next;
       }
     }
   }
