@@ -7,8 +7,8 @@
 // Both calls are bound by memory: each input is read once and each output
 // written once, 2 to 4 bytes either way against about seven operations an
 // element.  A warp takes a token, or some of its heads where there are few
-// tokens, and nothing is shared between warps: no block-wide barrier, and 24
-// warps per SM with two loads in flight each cover the memory's latency.  A
+// tokens, and nothing is shared between warps: no block-wide barrier, and 20
+// warps per SM with up to four loads in flight each cover the memory's latency.  A
 // lane holds eight neighbouring elements (16 bytes of fp16) of a head, so D / 8
 // lanes hold a head, the mean is a few shuffles, and the lane keeps its place
 // in the head while the warp walks over the token's heads: the norm weights
@@ -28,7 +28,15 @@
 namespace exl3 {
 namespace ht {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kCtas = 6;   // per CTA, per SM
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kCtas = 5;   // per CTA, per SM
+// Passes whose data is under way beside the one at hand, and passes per turn
+// of the loop: fp32 rows are twice as long and need no more than one (at T =
+// 1777, 64-wide heads: 5.2 us; three ahead 5.6 us), fp16 rows gain from three
+// (append of 9310 tokens at 40/8 heads of 128: 59 us; one ahead 65 us).
+template <bool F32>
+constexpr int kAhead = F32 ? 1 : 3;
+template <bool F32>
+constexpr int kUnroll = F32 ? 1 : 4;
 
 // The frequency in turns, modulo one, times 2^64: |f| = m 2^-s.
 __device__ __forceinline__ unsigned long long turn_step(float freq) {
@@ -139,7 +147,7 @@ enum { kByLane, kInLane, kAny };
 // `chunk`: passes that a warp makes for a token; `chunks` of them make up the
 // token.
 template <int D, bool F32IN, bool APPEND, int MODE>
-__global__ void __launch_bounds__(kThreads, F32IN ? kCtas - 1 : kCtas) head_transform_kernel(const Args a, int chunk, int chunks) {
+__global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const Args a, int chunk, int chunks) {
   constexpr int LPH = D / 8;               // lanes per head
   constexpr int HPP = 32 / LPH;            // heads per pass
   __shared__ __align__(16) float2 table[kWarps][D / 2];
@@ -268,13 +276,19 @@ __global__ void __launch_bounds__(kThreads, F32IN ? kCtas - 1 : kCtas) head_tran
     // Passes pa .. pb - 1 of one kind, two loads ahead of the arithmetic.
     const auto walk = [&](int pa, int pb, int live, const char *src, Raw8<F32IN> raw, char *dst, int64_t step,
                           bool f32out, bool norm, bool zero, bool write) {
-      Raw8<F32IN> next = load_if(pa + 1 < min(pb, live), src + kIn);
-      src += 2 * kIn;
-#pragma unroll 1
+      const int end = min(pb, live);
+      constexpr int AHEAD = kAhead<F32IN>, UNROLL = kUnroll<F32IN>;
+      Raw8<F32IN> ahead[AHEAD];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) ahead[k] = load_if(pa + 1 + k < end, src + (k + 1) * kIn);
+      src += (AHEAD + 1) * kIn;
+#pragma unroll UNROLL
       for (int p = pa; p < pb; ++p, src += kIn, dst += step) {
         Row8 o = unpack<F32IN>(raw);
-        raw = next;
-        next = load_if(p + 2 < min(pb, live), src);
+        raw = ahead[0];
+#pragma unroll
+        for (int k = 0; k + 1 < AHEAD; ++k) ahead[k] = ahead[k + 1];
+        ahead[AHEAD - 1] = load_if(p + 1 + AHEAD < end, src);
         float r = 1.0f;
         if (norm) {
           float ss = 0.0f;
