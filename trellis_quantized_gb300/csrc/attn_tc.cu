@@ -57,11 +57,11 @@ struct TcCfg {
   static constexpr int OFF_K = NQ * QTILE, OFF_V = OFF_K + KST * STAGE;
   static constexpr int SMEM = OFF_V + VST * STAGE + 1024 /*alignment*/;
   static constexpr int SM_WARPS = 4 * NQ;                // softmax warps
-  // softmax warpgroups, then one warpgroup with the MMA issuers and the
+  // softmax warpgroups, then two warpgroups with the MMA issuers and the
   // producers; registers move from the latter to the former (the sum over the
-  // warpgroups is what the launch allots: 3 x 168, or 2 x 248)
-  static constexpr int THREADS = (SM_WARPS + 4) * 32;
-  static constexpr int REGS_SM = NQ == 2 ? 200 : 248, REGS_IO = NQ == 2 ? 104 : 248;
+  // warpgroups is what the launch allots: 4 x 128, or 3 x 168)
+  static constexpr int THREADS = (SM_WARPS + 8) * 32;
+  static constexpr int REGS_SM = NQ == 2 ? 176 : 216, REGS_IO = NQ == 2 ? 80 : 144;
   static constexpr uint32_t TM_S = 0, TM_O = 256;        // TMEM columns: slots of 64, two per tile; O
   static constexpr uint32_t IDESC_S = tc::idesc_f16(128, kTcKeys);
   static constexpr uint32_t IDESC_O = tc::idesc_f16(128, D) | (1u << 16);   // B (V) is MN-major
@@ -260,11 +260,11 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   if (tid == 0) {
     for (int s = 0; s < KST; ++s) {
       tc::mbar_init(&k_full[s], 1);
-      tc::mbar_init(&k_empty[s], 1);
+      tc::mbar_init(&k_empty[s], 2);
     }
     for (int s = 0; s < VST; ++s) {
       tc::mbar_init(&v_full[s], 1);
-      tc::mbar_init(&v_empty[s], 1);
+      tc::mbar_init(&v_empty[s], C::NQ);
     }
     for (int s = 0; s < 4; ++s) {
       tc::mbar_init(&s_full[s], 1);
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     }
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&q_full[s], 1);
-      tc::mbar_init(&q_empty[s], 1);
+      tc::mbar_init(&q_empty[s], 3 - C::NQ);
     }
     abort_word = 0;
     tc::fence_mbar_init();
@@ -316,33 +316,36 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   if (tid == 0) a.cuts[blockIdx.x].rows = 0;           // (the thread that may fill the record in below)
 
   // (every warp of a warpgroup moves its registers, at the head of its role)
-  if (warp == C::SM_WARPS + 2) {
+  if (warp == C::SM_WARPS + 4) {
     // =========================================================== producers
-    if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
+    set_registers<C::REGS_IO>(false);
     produce<D, false>(a, w, &tmQ, &tmK, sbase, k_full, k_empty, q_full, q_empty, wait);
-  } else if (warp == C::SM_WARPS + 3) {
-    if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
+  } else if (warp == C::SM_WARPS + 5) {
+    set_registers<C::REGS_IO>(false);
     produce<D, true>(a, w, &tmQ, &tmV, sbase, v_full, v_empty, q_full, q_empty, wait);
-  } else if (warp == C::SM_WARPS) {
+  } else if (warp == C::SM_WARPS || warp == C::SM_WARPS + 1) {
     // ======================================================== MMAs: scores
-    // A tile's blocks are counted through all its units: block c takes slot
+    // Two warps: one per tile, or (one tile) one per slot, so that the waits,
+    // commits and descriptors of one are covered by the MMAs of the other.  A
+    // tile's blocks are counted through all its units: block c takes slot
     // c % 2 of the tile, and is the slot's use c / 2.
-    if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
-    int it = 0, units0 = 0, units1 = 0, c0 = 0, c1 = 0;
+    set_registers<C::REGS_IO>(false);
+    const int me = warp - C::SM_WARPS, t = C::NQ == 2 ? me : 0;
+    int it = 0, units = 0, c0 = 0;
     for (; w.left > 0; w.next(a)) {
       const int n = w.nseg;
-      const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
+      const bool live = t == 0 || w.ntok > a.tile_tok;          // this unit has the tile
+      if (live) wait(&q_full[t], units++ & 1);
       for (int j = 0; j < n; ++j) {
-        const int st = (it + j) % KST;
-        for (int t = 0; t < (two ? 2 : 1); ++t) {
-          const int c = (t ? c1 : c0) + j, slot = 2 * t + (c & 1);
-          if (j == 0) wait(&q_full[t], (t ? units1++ : units0++) & 1);
-          // the slot's last weights have to be consumed first
-          if (c >= 2) wait(&pv_done[slot], ((c >> 1) - 1) & 1);
-          if (t == 0) wait(&k_full[st], ((it + j) / KST) & 1);
-          __syncwarp();
-          tc::tc_fence_after();
-          if (tc::elect_one()) {
+        const int st = (it + j) % KST, c = c0 + j, slot = 2 * t + (c & 1);
+        const bool mine = C::NQ == 2 ? live : (c & 1) == me;
+        // the slot's last weights have to be consumed first
+        if (mine && c >= 2) wait(&pv_done[slot], ((c >> 1) - 1) & 1);
+        wait(&k_full[st], ((it + j) / KST) & 1);
+        __syncwarp();
+        tc::tc_fence_after();
+        if (tc::elect_one()) {
+          if (mine) {
             const uint64_t ad = sdesc_k_sw128(sbase + t * C::QTILE);
             const uint64_t bd = sdesc_k_sw128(sbase + C::OFF_K + st * C::STAGE);
 #pragma unroll
@@ -350,63 +353,76 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
               tc::mma_f16(tmem + C::TM_S + slot * 64, ad + (kk / 4) * (C::QPANEL >> 4) + (kk % 4) * 2,
                           bd + (kk / 4) * (C::PANEL >> 4) + (kk % 4) * 2, C::IDESC_S, kk ? 1u : 0u);
             tc::mma_commit(&s_full[slot]);
-            if (!two || t == 1) tc::mma_commit(&k_empty[st]);   // nobody reads this K after
-            if (j == n - 1) tc::mma_commit(&q_empty[t]);        // nor this q
+            tc::mma_commit(&k_empty[st]);
+          } else {
+            tc::mbar_arrive(&k_empty[st]);
           }
-          __syncwarp();
+          // this warp's last scores of the unit: q is free when they are done
+          if (live && j == n - 1) tc::mma_commit(&q_empty[t]);
         }
+        __syncwarp();
       }
       it += n;
-      c0 += n;
-      c1 += two ? n : 0;
+      if (live) c0 += n;
     }
-  } else if (warp == C::SM_WARPS + 1) {
+  } else if (warp == C::SM_WARPS + 2 || (C::NQ == 2 && warp == C::SM_WARPS + 3)) {
     // ================================================ MMAs: weighted values
-    if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
-    int it = 0, c0 = 0, c1 = 0;
+    set_registers<C::REGS_IO>(false);
+    const int t = warp - C::SM_WARPS - 2;
+    int it = 0, c0 = 0;
     for (; w.left > 0; w.next(a)) {
       const int n = w.nseg;
-      const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
+      const bool live = t == 0 || w.ntok > a.tile_tok;
       for (int j = 0; j < n; ++j) {
-        const int st = (it + j) % VST;
-        for (int t = 0; t < (two ? 2 : 1); ++t) {
-          const int c = (t ? c1 : c0) + j, slot = 2 * t + (c & 1);
-          wait(&p_full[slot], (c >> 1) & 1);
-          if (t == 0) wait(&v_full[st], ((it + j) / VST) & 1);
-          __syncwarp();
-          tc::tc_fence_after();
-          if (tc::elect_one()) {
+        const int st = (it + j) % VST, c = c0 + j, slot = 2 * t + (c & 1);
+        if (live) wait(&p_full[slot], (c >> 1) & 1);
+        wait(&v_full[st], ((it + j) / VST) & 1);
+        const int key0 = (w.lo / kTcKeys + w.blk + j) * kTcKeys;
+        if (live && (key0 < w.lo || key0 + kTcKeys > w.hi)) {
+          // V rows that no row of the unit sees may hold anything: zeros (the
+          // other tile's warp may be writing the same)
+          for (int i = lane; i < kTcKeys * (D / 8); i += 32) {
+            const int r = i & (kTcKeys - 1), q = i / kTcKeys;      // row, 16-byte column
+            if (key0 + r < w.lo || key0 + r >= w.hi)
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                               sbase + C::OFF_V + st * C::STAGE + (q >> 3) * C::PANEL + r * 128 + (q & 7) * 16),
+                           "r"(0)
+                           : "memory");
+          }
+          fence_async_shared();
+        }
+        __syncwarp();
+        tc::tc_fence_after();
+        if (tc::elect_one()) {
+          if (live) {
             const uint64_t bd = sdesc_mn_sw128(sbase + C::OFF_V + st * C::STAGE, C::PANEL);
 #pragma unroll
             for (int kk = 0; kk < kTcKeys / 16; ++kk)
               mma_f16_ts(tmem + C::TM_O + t * D, tmem + C::TM_S + slot * 64 + kk * 8, bd + kk * (2048 >> 4), C::IDESC_O,
                          (j | kk) ? 1u : 0u);
             tc::mma_commit(&pv_done[slot]);
-            if (!two || t == 1) tc::mma_commit(&v_empty[st]);
+            tc::mma_commit(&v_empty[st]);
+          } else {
+            tc::mbar_arrive(&v_empty[st]);
           }
-          __syncwarp();
         }
+        __syncwarp();
       }
       it += n;
-      c0 += n;
-      c1 += two ? n : 0;
+      if (live) c0 += n;
     }
   } else if (warp < C::SM_WARPS) {
     // ============================================================= softmax
-    if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_SM>(true);
+    set_registers<C::REGS_SM>(true);
     const int t = warp / 4;                  // row tile
     const int wl = warp & 3;
     const uint32_t lanes = (uint32_t)(wl * 32) << 16;
     const int row = wl * 32 + lane;          // within the tile
-    const int ltid = tid - t * 128;
-    int it = 0, c = 0;                       // ring parts before the unit; blocks of this tile before
+    int c = 0;                               // blocks of this tile so far
     for (; w.left > 0; w.next(a)) {
       const int n = w.nseg;
       const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
-      if (t == 1 && !two) {
-        it += n;
-        continue;
-      }
+      if (t == 1 && !two) continue;
       // this tile's tokens and rows, and the keys that this thread's row sees
       const int i0 = w.i0 + t * a.tile_tok, ntok = min(a.tile_tok, w.ntok - t * a.tile_tok);
       const int rows = ntok * a.G;
@@ -477,34 +493,12 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
           pk[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
         tmem_st32u(tm_s, pk);
-        if (key0 < w.lo || key0 + kTcKeys > w.hi) {
-          // V rows that no row of the unit sees: zeros.  (The stage's barrier
-          // is at most one turn behind: the scores of this block were only
-          // computed after the product of the block before the last.)
-          if (ltid < kTcKeys) {
-            const int vi = it + j;
-            wait(&v_full[vi % VST], (vi / VST) & 1);
-            const int key = key0 + ltid;
-            if (key < w.lo || key >= w.hi) {
-              const uint32_t dst = sbase + C::OFF_V + (vi % VST) * C::STAGE + ltid * 128;
-#pragma unroll
-              for (int p = 0; p < D / 64; ++p)
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + p * C::PANEL + q * 16),
-                               "r"(0)
-                               : "memory");
-            }
-          }
-          fence_async_shared();
-        }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tc::tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&p_full[slot]);
       }
-      it += n;
 
       // ---- O complete: y, or this CTA's part of it
       wait(&pv_done[2 * t + ((c - 1) & 1)], ((c - 1) >> 1) & 1);
@@ -549,7 +543,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       if (tid == 0 && !whole && w.slot() == 1) a.cuts[blockIdx.x] = w.cut(share);
     }
   } else {
-    if constexpr (C::REGS_IO < C::REGS_SM) set_registers<C::REGS_IO>(false);
+    set_registers<C::REGS_IO>(false);
   }
 
   tc::tc_fence_before();
