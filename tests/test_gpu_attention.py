@@ -174,6 +174,26 @@ def test_strided_queries_other_stream_and_repeat(new, old):
     _compare(y0, None, q, dense, new, old, True, 0, 128 ** -0.5)
 
 
+@pytest.mark.parametrize("out", [tq.EXL3_OUT_F16, tq.EXL3_OUT_F32])
+@pytest.mark.parametrize("new,old", [([1, 2], [300, 20]), ([90, 300], [33, 0])])
+def test_buffers_on_16_byte_boundaries(new, old, out):
+    """q, y and the cache start 16 bytes past a 32-byte boundary."""
+    q, k, v, table, dense, q_start, kv_len = _setup(new, old, 16, 2, 128, 16, "tokens")
+    dt = torch.float32 if out == tq.EXL3_OUT_F32 else torch.float16
+
+    def shifted(t, dtype):
+        per16 = 16 // torch.empty(0, dtype=dtype).element_size()
+        buf = torch.zeros(t.numel() + 2 * per16, dtype=dtype, device="cuda")
+        off = per16 if buf.data_ptr() % 32 == 0 else 2 * per16
+        return buf[off:off + t.numel()].view(t.shape)
+
+    qs, ks, vs, ys = shifted(q, torch.float16), shifted(k, torch.float16), shifted(v, torch.float16), shifted(q, dt)
+    qs.copy_(q), ks.copy_(k), vs.copy_(v)
+    assert all(t.data_ptr() % 32 == 16 for t in (qs, ks, vs, ys))
+    tq.exl3_paged_attention(qs, tq.paged_batch(q_start, kv_len, table), tq.kv_cache(ks, vs), out_dtype=out, y=ys)
+    _compare(ys, None, q, dense, new, old, True, 0, 128 ** -0.5)
+
+
 @pytest.mark.parametrize("n", [1, 40])
 def test_graph_with_growing_lengths(n):
     """One captured call serves lengths that change between replays."""

@@ -356,6 +356,7 @@ int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q
   a.window = window > batch->max_pages * cache->page_size ? 0 : window;
   a.y = y;
   a.f32out = out_dtype == EXL3_OUT_F32;
+  a.y_aligned32 = (reinterpret_cast<uintptr_t>(y) & 31u) == 0;
   a.lse = lse;
   a.part_o = at<float>(workspace, L.part_o);
   a.part_lse = at<float>(workspace, L.part_lse);

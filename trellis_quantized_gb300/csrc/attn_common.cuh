@@ -33,7 +33,7 @@ struct Args {
   float scale_log2;          // scale * log2(e)
   int causal, window;        // window 0: none
   void *y;                   // [T][Hq][D]
-  int f32out;
+  int f32out, y_aligned32;
   float *lse;                // [T][Hq] or null
   float *part_o;             // partial results: [grid][2][rows][D] fp32
   float *part_lse;           // [grid][2][rows], log2 of the sum
@@ -189,9 +189,12 @@ __device__ void make_share(const Args &a, int min_per, Share *out, long long *wa
   constexpr int NW = NT / 32;
   const int chunk = (a.B + NW - 1) / NW;
   const int b0 = min(a.B, warp * chunk), b1 = min(a.B, b0 + chunk);
-  long long mine = 0;
+  long long mine = 0, n = 0;
   Seq s;
-  for (int b = b0; b < b1; b += 32) mine += warp_costs<KB, OV>(a, b, b1, blockIdx.x == 0, s);
+  for (int b = b0; b < b1; b += 32) {
+    n = warp_costs<KB, OV>(a, b, b1, blockIdx.x == 0, s);
+    mine += n;
+  }
 #pragma unroll
   for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
   if (lane == 0) warp_sums[warp] = mine;
@@ -213,7 +216,7 @@ __device__ void make_share(const Args &a, int min_per, Share *out, long long *wa
   if (start >= before && start < before + mine) {
     long long at = before;
     for (int b = b0; b < b1; b += 32) {
-      const long long n = warp_costs<KB, OV>(a, b, b1, false, s);
+      if (chunk > 32) n = warp_costs<KB, OV>(a, b, b1, false, s);      // (else as above)
       const long long inc = at + warp_scan(n);
       const unsigned hit = __ballot_sync(0xffffffffu, start < inc && start >= inc - n);
       if (hit) {

@@ -4,7 +4,8 @@
 //   y = sum_c 2^(lse_c - max) y_c / sum_c 2^(lse_c - max)
 //
 // A CTA leaves at most one unit unfinished for its successors: block (c, i)
-// takes rows 8 i .. 8 i + 7 of the one that CTA c left, if there is one.  A
+// takes some rows (2 after the step kernel, 8 after the tensor-core kernel) of
+// the one that CTA c left, if there is one.  A
 // warp per row turns the parts' lse into weights, then the block adds: a
 // thread holds four neighbouring elements of a row, and where the rows do not
 // fill the block several groups of threads share the parts (a single user's
@@ -23,33 +24,43 @@ namespace attn {
 constexpr int kJoinThreads = 256, kJoinRows = 8, kJoinMaxCtas = 512;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const Args a, int ctas, int tile_rows) {
+__global__ void __launch_bounds__(kJoinThreads)
+    attn_join_kernel(const Args a, int ctas, int tile_rows, int block_rows) {
   constexpr int C4 = D / 4;                  // threads per row
   __shared__ float weight[kJoinRows][kJoinMaxCtas];
   __shared__ float row_lse[kJoinRows];
   __shared__ float4 red[kJoinThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int first = blockIdx.x, r0 = blockIdx.y * kJoinRows;
+  const int first = blockIdx.x, r0 = blockIdx.y * block_rows;
   pdl_trigger();
   pdl_wait();
   const int4 cut = __ldcg(reinterpret_cast<const int4 *>(a.cuts + first));   // rows, last, t, h
-  const int rows = min(cut.x - r0, kJoinRows);
+  const int rows = min(cut.x - r0, block_rows);
   if (rows <= 0) return;
   const int parts = min(min(cut.y, ctas - 1) - first + 1, kJoinMaxCtas);
   // row r of part p: slot 1 of the first CTA, slot 0 of the others
   const auto place = [&](int p, int r) { return ((int64_t)(first + p) * 2 + (p == 0 ? 1 : 0)) * tile_rows + r0 + r; };
   for (int r = warp; r < rows; r += kJoinThreads / 32) {
-    float mx = neg_inf();
-    for (int p = lane; p < parts; p += 32) mx = fmaxf(mx, __ldcg(a.part_lse + place(p, r)));
+    // (the first 128 parts' lse stay in registers between the two passes)
+    float ls[4], mx = neg_inf();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      ls[k] = lane + 32 * k < parts ? __ldcg(a.part_lse + place(lane + 32 * k, r)) : neg_inf();
+      mx = fmaxf(mx, ls[k]);
+    }
+    for (int p = lane + 128; p < parts; p += 32) mx = fmaxf(mx, __ldcg(a.part_lse + place(p, r)));
 #pragma unroll
     for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
     float sum = 0.0f;
-    for (int p = lane; p < parts; p += 32) {
-      const float ls = __ldcg(a.part_lse + place(p, r));
-      const float f = ls == neg_inf() ? 0.0f : exp2_approx(ls - mx);
+    const auto weigh = [&](int p, float l) {
+      const float f = l == neg_inf() ? 0.0f : exp2_approx(l - mx);
       weight[r][p] = f;
       sum += f;
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (lane + 32 * k < parts) weigh(lane + 32 * k, ls[k]);
+    for (int p = lane + 128; p < parts; p += 32) weigh(p, __ldcg(a.part_lse + place(p, r)));
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);  // (NaN stays)
@@ -104,10 +115,11 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const Args a, i
 cudaError_t exl3_launch_attn_join(const exl3::attn::Args &a, int D, int ctas, int tile_rows, cudaStream_t s) {
   using namespace exl3::attn;
   if (ctas > kJoinMaxCtas) return cudaErrorInvalidConfiguration;
-  const dim3 grid(ctas, exl3::ceil_div(tile_rows, kJoinRows)), block(kJoinThreads);
+  const int rows = tile_rows > 16 ? kJoinRows : 2;
+  const dim3 grid(ctas, exl3::ceil_div(tile_rows, rows)), block(kJoinThreads);
   switch (D) {
-    case 64: return exl3::launch_pdl(attn_join_kernel<64>, grid, block, 0, s, a, ctas, tile_rows);
-    case 128: return exl3::launch_pdl(attn_join_kernel<128>, grid, block, 0, s, a, ctas, tile_rows);
-    default: return exl3::launch_pdl(attn_join_kernel<256>, grid, block, 0, s, a, ctas, tile_rows);
+    case 64: return exl3::launch_pdl(attn_join_kernel<64>, grid, block, 0, s, a, ctas, tile_rows, rows);
+    case 128: return exl3::launch_pdl(attn_join_kernel<128>, grid, block, 0, s, a, ctas, tile_rows, rows);
+    default: return exl3::launch_pdl(attn_join_kernel<256>, grid, block, 0, s, a, ctas, tile_rows, rows);
   }
 }

@@ -40,7 +40,7 @@ namespace exl3 {
 namespace attn {
 
 constexpr int kTcKeys = 64;
-constexpr int kTcCost = 6;         // a unit's start and end, in blocks
+constexpr int kTcCost = 7;         // a unit's start and end, in blocks
 constexpr float kLazy = 8.0f;      // log2 of the growth that moves the maximum
 
 template <int D>
@@ -133,6 +133,18 @@ __device__ __forceinline__ bool try_wait_plain(uint64_t *bar, uint32_t parity) {
       : "r"(tc::smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
+}
+
+// 32 bytes in one store, or in two where only 16-byte alignment is known.
+__device__ __forceinline__ void store32(void *dst, const uint32_t (&v)[8], bool aligned) {
+  if (!aligned) {
+    reinterpret_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    return;
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 template <int N>
@@ -505,33 +517,42 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       __syncwarp();
       tc::tc_fence_after();
       const bool whole = w.whole();
+      const bool aligned = !whole || a.y_aligned32;
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);      // (NaN stays)
       const float lse2 = l == 0.0f ? neg_inf() : m * a.scale_log2 + log2f(l);
       // (parts of a cut unit: the rows of its tiles one after the other)
       const int64_t head = out_head(a, w.s.t0 + i0, w.h, row);
       const int64_t pr = ((int64_t)blockIdx.x * 2 + w.slot()) * C::ROWS + t * a.tile_tok * a.G + row;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int q = 0; q < D / 32; ++q) {
         float v[32];
-        tc::tmem_ld32(tmem + C::TM_O + t * D + lanes + 32 * c, v);
+        tc::tmem_ld32(tmem + C::TM_O + t * D + lanes + 32 * q, v);
         tc::tmem_ld_wait();
         if (row < rows) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] *= inv;
+          // (32-byte stores: a row's sectors are written whole)
           if (whole && !a.f32out) {
+            __half *dst = static_cast<__half *>(a.y) + head * D + 32 * q;
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              __half2 h[4];
+            for (int i = 0; i < 32; i += 16) {
+              uint32_t h[8];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) h[k] = __floats2half2_rn(v[i + 2 * k], v[i + 2 * k + 1]);
-              *reinterpret_cast<uint4 *>(static_cast<__half *>(a.y) + head * D + 32 * c + i) =
-                  *reinterpret_cast<uint4 *>(h);
+              for (int k = 0; k < 8; ++k) {
+                const __half2 x = __floats2half2_rn(v[i + 2 * k], v[i + 2 * k + 1]);
+                h[k] = *reinterpret_cast<const uint32_t *>(&x);
+              }
+              store32(dst + i, h, aligned);
             }
           } else {
-            float *dst = whole ? static_cast<float *>(a.y) + head * D : a.part_o + pr * D;
+            float *dst = (whole ? static_cast<float *>(a.y) + head * D : a.part_o + pr * D) + 32 * q;
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4 *>(dst + 32 * c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t h[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) h[k] = __float_as_uint(v[i + k]);
+              store32(dst + i, h, aligned);
+            }
           }
         }
       }
