@@ -57,10 +57,12 @@ struct TcCfg {
   // a block's K (64-column panels of 64 keys) or V; up to 160 KB in all.
   static constexpr int PANEL = kTcKeys * 128;            // bytes
   static constexpr int STAGE = kTcKeys * D * 2;
-  static constexpr int KST = D == 64 ? 8 : D == 128 ? 5 : 3, VST = D == 64 ? 8 : D == 128 ? 5 : 2;
+  static constexpr int KST = D == 64 ? 8 : D == 128 ? 5 : 4, VST = D == 64 ? 8 : D == 128 ? 5 : 3;
+  // With one tile of 256-wide heads there is room for q in TMEM.
+  static constexpr bool QTM = D == 256;
   static constexpr int QTILE = 128 * D * 2;
   static constexpr int QPANEL = 128 * 128;               // 64 columns of 128 rows
-  static constexpr int OFF_K = NQ * QTILE, OFF_V = OFF_K + KST * STAGE;
+  static constexpr int OFF_K = QTM ? 0 : NQ * QTILE, OFF_V = OFF_K + KST * STAGE;
   static constexpr int SMEM = OFF_V + VST * STAGE + 1024 /*alignment*/;
   static constexpr int SM_WARPS = 4 * NQ;                // softmax warps
   // softmax warpgroups, then two warpgroups with the MMA issuers and the
@@ -68,7 +70,7 @@ struct TcCfg {
   // warpgroups is what the launch allots: 4 x 128, or 3 x 168)
   static constexpr int THREADS = (SM_WARPS + 8) * 32;
   static constexpr int REGS_SM = NQ == 2 ? 176 : 216, REGS_IO = NQ == 2 ? 80 : 144;
-  static constexpr uint32_t TM_S = 0, TM_O = 256;        // TMEM columns: slots of 64, two per tile; O
+  static constexpr uint32_t TM_S = 0, TM_Q = 128, TM_O = 256;   // TMEM columns: slots of 64, two per tile; q; O
   static constexpr uint32_t IDESC_S = tc::idesc_f16(128, kTcKeys);
   static constexpr uint32_t IDESC_O = tc::idesc_f16(128, D) | (1u << 16);   // B (V) is MN-major
 };
@@ -227,7 +229,7 @@ __device__ __forceinline__ void produce(const Args &a, Walk<kTcKeys, kTcCost> w,
           }
       }
       __syncwarp();
-      if (!V && j == 0 && !stop) {
+      if (!V && !C::QTM && j == 0 && !stop) {
         // the unit's q, as soon as the last unit's scores are done with its
         // place: G heads of tile_tok tokens are the tile's rows in order
         // (tokens past the unit's are rows that nobody writes)
@@ -290,8 +292,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       tc::mbar_init(&pv_done[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      tc::mbar_init(&q_full[s], 1);
-      tc::mbar_init(&q_empty[s], 3 - C::NQ);
+      tc::mbar_init(&q_full[s], C::QTM ? 4 : 1);
+      tc::mbar_init(&q_empty[s], 1);
     }
     abort_word = 0;
     tc::fence_mbar_init();
@@ -367,16 +369,21 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
             const uint64_t ad = sdesc_k_sw128(sbase + t * C::QTILE);
             const uint64_t bd = sdesc_k_sw128(sbase + C::OFF_K + st * C::STAGE);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc::mma_f16(tmem + C::TM_S + slot * 64, ad + (kk / 4) * (C::QPANEL >> 4) + (kk % 4) * 2,
-                          bd + (kk / 4) * (C::PANEL >> 4) + (kk % 4) * 2, C::IDESC_S, kk ? 1u : 0u);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t bk = bd + (kk / 4) * (C::PANEL >> 4) + (kk % 4) * 2;
+              if constexpr (C::QTM)
+                mma_f16_ts(tmem + C::TM_S + slot * 64, tmem + C::TM_Q + kk * 8, bk, C::IDESC_S, kk ? 1u : 0u);
+              else
+                tc::mma_f16(tmem + C::TM_S + slot * 64, ad + (kk / 4) * (C::QPANEL >> 4) + (kk % 4) * 2, bk, C::IDESC_S,
+                            kk ? 1u : 0u);
+            }
             tc::mma_commit(&s_full[slot]);
             tc::mma_commit(&k_empty[st]);
           } else {
             tc::mbar_arrive(&k_empty[st]);
           }
           // this warp's last scores of the unit: q is free when they are done
-          if (live && j == n - 1) tc::mma_commit(&q_empty[t]);
+          if (!C::QTM && live && j == n - 1) tc::mma_commit(&q_empty[t]);
         }
         __syncwarp();
       }
@@ -437,6 +444,32 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     const uint32_t lanes = (uint32_t)(wl * 32) << 16;
     const int row = wl * 32 + lane;          // within the tile
     int c = 0;                               // blocks of this tile so far
+    // q of a unit to TMEM (256-wide heads): a thread brings its row, as the
+    // fp16 pairs that an A operand's columns hold
+    const auto bring_q = [&](const auto &u) {
+      if (u.left <= 0) return;
+      const int tok = row_token(a, row);
+      const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (int64_t)(u.s.t0 + u.i0 + tok) * a.q_stride +
+                                                         (int64_t)(u.h * a.G + row - tok * a.G) * D);
+#pragma unroll
+      for (int q = 0; q < D / 64; ++q) {
+        uint32_t v[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 x = row < u.rows ? src[8 * q + i] : make_uint4(0, 0, 0, 0);
+          v[4 * i] = x.x;
+          v[4 * i + 1] = x.y;
+          v[4 * i + 2] = x.z;
+          v[4 * i + 3] = x.w;
+        }
+        tmem_st32u(tmem + C::TM_Q + lanes + 32 * q, v);
+      }
+      tc::tmem_st_wait();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&q_full[0]);
+    };
+    if constexpr (C::QTM) bring_q(w);
     for (; w.left > 0; w.next(a)) {
       const int n = w.nseg;
       const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
@@ -518,6 +551,12 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         if (lane == 0) tc::mbar_arrive(&p_full[slot]);
       }
 
+      if constexpr (C::QTM) {
+        // (this unit's scores are all there, so its q is no longer read)
+        auto ahead = w;
+        ahead.next(a);
+        bring_q(ahead);
+      }
       // ---- O complete: y, or this CTA's part of it
       wait(&pv_done[2 * t + ((c - 1) & 1)], ((c - 1) >> 1) & 1);
       __syncwarp();
