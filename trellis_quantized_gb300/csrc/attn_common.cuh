@@ -48,6 +48,7 @@ struct __align__(16) Cut {
   int last;
   int t, h;                  // first token (row of the call) and key head
 };
+static_assert(sizeof(Cut) == 16, "read as one int4");
 
 // One sequence: first row, new tokens, tokens in the cache.
 struct Seq {
@@ -179,69 +180,95 @@ __device__ __forceinline__ long long warp_scan(long long v) {
   return v;
 }
 
-// Cuts the line into the CTAs' parts and finds this CTA's first tile: each
-// warp sums a run of sequences, the warp whose run holds the place looks for
-// it.  `warp_sums` has NT / 32 entries.  CTA 0 also reports lengths that
+// The tile that holds place `start`, searched by a whole warp from sequence b
+// on (whose units begin at place `at`); false if it is not below `end`.  `n`
+// and `s`: the costs and sequences b .. b + 31, if the caller has them.
+template <int KB, int OV>
+__device__ __forceinline__ bool find_tile(const Args &a, int b, int end, long long at, long long start, long long n,
+                                          Seq s, bool known, Share &out) {
+  const int lane = threadIdx.x & 31;
+  for (; b < end; b += 32) {
+    if (!known) n = warp_costs<KB, OV>(a, b, end, false, s);
+    known = false;
+    const long long inc = at + warp_scan(n);
+    const unsigned hit = __ballot_sync(0xffffffffu, start < inc && start >= inc - n);
+    at = __shfl_sync(0xffffffffu, inc, 31);
+    if (!hit) continue;
+    const int i = __ffs(hit) - 1;
+    const Seq q = {0, __shfl_sync(0xffffffffu, s.nq, i), __shfl_sync(0xffffffffu, s.len, i)};
+    long long tile_at = __shfl_sync(0xffffffffu, inc - n, i);
+    for (int g0 = 0; g0 < q.nq; g0 += 32 * a.unit_tok) {
+      const int i0 = g0 + lane * a.unit_tok;
+      const long long c = i0 < q.nq ? (long long)tile_cost<KB, OV>(a, q, i0) * a.Hkv : 0;
+      const long long e = tile_at + warp_scan(c);
+      const unsigned tile = __ballot_sync(0xffffffffu, start < e && start >= e - c);
+      if (tile) {
+        const int k = __ffs(tile) - 1;
+        out.b = b + i;
+        out.i0 = g0 + k * a.unit_tok;
+        out.off = __shfl_sync(0xffffffffu, (int)(start - (e - c)), k);
+        return true;
+      }
+      tile_at = __shfl_sync(0xffffffffu, e, 31);
+    }
+    return false;
+  }
+  return false;
+}
+
+// Cuts the line into the CTAs' parts and finds this CTA's first tile.  Up to
+// 32 sequences: every warp works it out for itself, without a barrier (code
+// that all warps share; the start of a launch waits for its instructions).
+// More: each warp sums a run of sequences, the warp whose run holds the place
+// looks for it.  `sums` has NT / 32 entries.  CTA 0 also reports lengths that
 // contradict one another.
 template <int KB, int OV, int NT>
-__device__ void make_share(const Args &a, int min_per, Share *out, long long *warp_sums) {
+__device__ __forceinline__ Share make_share(const Args &a, int min_per, Share *shared, long long *sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int NW = NT / 32;
-  const int chunk = (a.B + NW - 1) / NW;
-  const int b0 = min(a.B, warp * chunk), b1 = min(a.B, b0 + chunk);
-  long long mine = 0, n = 0;
-  Seq s;
+  const bool few = a.B <= 32;
+  const int chunk = few ? 32 : (a.B + NW - 1) / NW;
+  const int b0 = few ? 0 : min(a.B, warp * chunk), b1 = min(a.B, b0 + chunk);
+  long long n = 0, mine = 0;
+  Seq s = {0, 0, 0};
   for (int b = b0; b < b1; b += 32) {
-    n = warp_costs<KB, OV>(a, b, b1, blockIdx.x == 0, s);
+    n = warp_costs<KB, OV>(a, b, b1, blockIdx.x == 0 && (!few || warp == 0), s);
     mine += n;
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-  if (lane == 0) warp_sums[warp] = mine;
-  if (threadIdx.x == 0) out->b = a.B;
-  __syncthreads();
-  long long before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    if (w < warp) before += warp_sums[w];
-    total += warp_sums[w];
-  }
-  long long per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < min_per) per = min_per;
-  const long long start = per * blockIdx.x;
-  if (threadIdx.x == 0) {
-    out->total = total;
-    out->per = per;
-  }
-  if (start >= before && start < before + mine) {
-    long long at = before;
-    for (int b = b0; b < b1; b += 32) {
-      if (chunk > 32) n = warp_costs<KB, OV>(a, b, b1, false, s);      // (else as above)
-      const long long inc = at + warp_scan(n);
-      const unsigned hit = __ballot_sync(0xffffffffu, start < inc && start >= inc - n);
-      if (hit) {
-        const int i = __ffs(hit) - 1;
-        const Seq q = {__shfl_sync(0xffffffffu, s.t0, i), __shfl_sync(0xffffffffu, s.nq, i),
-                       __shfl_sync(0xffffffffu, s.len, i)};
-        long long tile_at = __shfl_sync(0xffffffffu, inc - n, i);
-        for (int g0 = 0; g0 < q.nq; g0 += 32 * a.unit_tok) {
-          const int i0 = g0 + lane * a.unit_tok;
-          const long long c = i0 < q.nq ? (long long)tile_cost<KB, OV>(a, q, i0) * a.Hkv : 0;
-          const long long e = tile_at + warp_scan(c);
-          if (start < e && start >= e - c) {
-            out->b = b + i;
-            out->i0 = i0;
-            out->off = (int)(start - (e - c));
-          }
-          tile_at = __shfl_sync(0xffffffffu, e, 31);
-          if (start < tile_at) break;
-        }
-        break;
-      }
-      at = __shfl_sync(0xffffffffu, inc, 31);
+  long long before = 0;
+  Share out;
+  out.total = mine;
+  if (!few) {
+    if (lane == 0) sums[warp] = mine;
+    if (threadIdx.x == 0) shared->b = a.B;
+    __syncthreads();
+    out.total = 0;
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) before += sums[w];
+      out.total += sums[w];
     }
   }
-  __syncthreads();
+  const long long up = out.total + gridDim.x - 1;
+  out.per = up >> 31 ? up / gridDim.x : (long long)((unsigned)up / gridDim.x);
+  if (out.per < min_per) out.per = min_per;
+  const long long start = out.per * blockIdx.x;
+  out.b = a.B;
+  out.i0 = out.off = 0;
+  bool found = false;
+  if (start >= before && start < before + mine) found = find_tile<KB, OV>(a, b0, b1, before, start, n, s, chunk <= 32, out);
+  if (!few) {
+    if (found && lane == 0) *shared = out;
+    __syncthreads();
+    const int b = shared->b;
+    if (b < a.B) {
+      out.b = b;
+      out.i0 = shared->i0;
+      out.off = shared->off;
+    }
+  }
+  return out;
 }
 
 // One CTA's part of the line, unit by unit: tokens i0 .. i0 + ntok - 1 of

@@ -11,7 +11,10 @@
 // warps read the slot (a thread per row), write the fp16 weights over its
 // first half, and the second product takes them from there (A operand in
 // TMEM) with V as it lies in the cache (an MN-major operand: no transposition
-// anywhere) into O, which stays in TMEM for the whole unit.
+// anywhere) into O, which stays in TMEM for the whole unit.  With 256-wide
+// heads q is an A operand in TMEM too: its 64 KB of shared memory go to the
+// rings and a score product reads K alone (16 on 2 heads, 2,047 tokens behind
+// 63,000: 1.66 to 1.76 ms with q in shared memory, 1.55 to 1.65 so).
 //
 // Every row tile of 128 has two slots that its blocks take in turn and a
 // softmax warpgroup: the scores of block j + 1 are computed while the weights
@@ -21,7 +24,8 @@
 // follow one another: 1.34 PFLOP/s on 4096 tokens behind 64,000 at D = 128,
 // against 1.46.)  64-wide score products read 6 KB of shared memory each, 48
 // cycles where the arithmetic takes 32, which caps the pair of products at 80 %
-// of the tensor cores' rate.
+// of the tensor cores' rate.  At that rate the chip is also held by its power
+// limit: the same launch varies by 4 % between boards.
 //
 // Each MMA warp spends about as long on barriers, descriptors and commits as
 // its products take, so score products have two warps (a tile or a slot each)
@@ -69,7 +73,7 @@ struct TcCfg {
   // producers; registers move from the latter to the former (the sum over the
   // warpgroups is what the launch allots: 4 x 128, or 3 x 168)
   static constexpr int THREADS = (SM_WARPS + 8) * 32;
-  static constexpr int REGS_SM = NQ == 2 ? 176 : 216, REGS_IO = NQ == 2 ? 80 : 144;
+  static constexpr int REGS_SM = NQ == 2 ? 168 : 216, REGS_IO = NQ == 2 ? 88 : 144;
   static constexpr uint32_t TM_S = 0, TM_Q = 128, TM_O = 256;   // TMEM columns: slots of 64, two per tile; q; O
   static constexpr uint32_t IDESC_S = tc::idesc_f16(128, kTcKeys);
   static constexpr uint32_t IDESC_O = tc::idesc_f16(128, D) | (1u << 16);   // B (V) is MN-major
@@ -175,28 +179,20 @@ __device__ __forceinline__ void produce(const Args &a, Walk<kTcKeys, kTcCost> w,
   int it = 0, qn0 = 0, qn1 = 0;
   bool stop = false;
   // the pages of a block's boxes, lane i box i (at most 4), looked up while
-  // the block before is under way
+  // the block before is under way (a unit's first block waits for its look-up:
+  // the ring is blocks ahead of the MMAs, registers are short)
   int page = -1, off = 0;
   PageWalk<kTcKeys> pages;
-  if (w.left > 0) {
+  for (; w.left > 0 && !stop; w.next(a)) {
     pages.begin(a, w);
     pages.next(a, page, off);
-  }
-  while (w.left > 0 && !stop) {
-    auto ahead = w;
-    ahead.next(a);
     const int n = w.nseg;
     const bool two = C::NQ == 2 && w.ntok > a.tile_tok;
     for (int j = 0; j < n && !stop; ++j) {
       const int key0 = (w.lo / kTcKeys + w.blk + j) * kTcKeys;
       int my_page = page;
       const int my_off = off;
-      if (j + 1 < n) {
-        pages.next(a, page, off);
-      } else if (ahead.left > 0) {
-        pages.begin(a, ahead);
-        pages.next(a, page, off);
-      }
+      if (j + 1 < n) pages.next(a, page, off);
       const int lo = max(w.lo - key0, 0), hi = min(w.hi - key0, kTcKeys);     // keys of the block that some row sees
       if (lane >= (lo >> a.box_log2) && lane << a.box_log2 < hi && (unsigned)my_page >= (unsigned)a.num_pages) {
         set_device_error(a.err, kErrBounds);
@@ -252,7 +248,6 @@ __device__ __forceinline__ void produce(const Args &a, Walk<kTcKeys, kTcCost> w,
       }
     }
     it += n;
-    w = ahead;
   }
   // After a wait that ran out nobody consumes any more: give the copies in
   // flight their time before the CTA's memory goes to another.
@@ -268,7 +263,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t k_full[KST], k_empty[KST], v_full[VST], v_empty[VST], s_full[4], p_full[4], pv_done[4], q_full[2],
       q_empty[2];
-  __shared__ Share share;
+  __shared__ Share share_mem;
   __shared__ long long warp_sums[C::THREADS / 32];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
@@ -311,7 +306,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   const uint32_t tmem = tmem_slot;
   pdl_trigger();
   pdl_wait();
-  make_share<kTcKeys, kTcCost, C::THREADS>(a, 1 + kTcCost, &share, warp_sums);
+  const Share share = make_share<kTcKeys, kTcCost, C::THREADS>(a, 1 + kTcCost, &share_mem, warp_sums);
   clear_padding<D>(a, C::THREADS);
 
   // A wait that runs out records the error; every later wait then returns at
@@ -333,110 +328,113 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
 
   Walk<kTcKeys, kTcCost> w;
   w.begin(a, share);
-  if (tid == 0) a.cuts[blockIdx.x].rows = 0;           // (the thread that may fill the record in below)
+  if (tid == 0) {
+    a.cuts[blockIdx.x].rows = 0;           // (the thread that may fill the record in below)
+    share_mem = share;                     // (out of the registers; who still reads it, reads the same)
+  }
 
-  // (every warp of a warpgroup moves its registers, at the head of its role)
-  if (warp == C::SM_WARPS + 4) {
-    // =========================================================== producers
+  // (This branch first: with the softmax ahead of it in the code, the prompt of
+  // 8,192 tokens takes 596 us instead of 522.)
+  if (warp >= C::SM_WARPS) {
     set_registers<C::REGS_IO>(false);
-    produce<D, false>(a, w, &tmQ, &tmK, sbase, k_full, k_empty, q_full, q_empty, wait);
-  } else if (warp == C::SM_WARPS + 5) {
-    set_registers<C::REGS_IO>(false);
-    produce<D, true>(a, w, &tmQ, &tmV, sbase, v_full, v_empty, q_full, q_empty, wait);
-  } else if (warp == C::SM_WARPS || warp == C::SM_WARPS + 1) {
-    // ======================================================== MMAs: scores
-    // Two warps: one per tile, or (one tile) one per slot, so that the waits,
-    // commits and descriptors of one are covered by the MMAs of the other.  A
-    // tile's blocks are counted through all its units: block c takes slot
-    // c % 2 of the tile, and is the slot's use c / 2.
-    set_registers<C::REGS_IO>(false);
-    const int me = warp - C::SM_WARPS, t = C::NQ == 2 ? me : 0;
-    int it = 0, units = 0, c0 = 0;
-    for (; w.left > 0; w.next(a)) {
-      const int n = w.nseg;
-      const bool live = t == 0 || w.ntok > a.tile_tok;          // this unit has the tile
-      if (live) wait(&q_full[t], units++ & 1);
-      for (int j = 0; j < n; ++j) {
-        const int st = (it + j) % KST, c = c0 + j, slot = 2 * t + (c & 1);
-        const bool mine = C::NQ == 2 ? live : (c & 1) == me;
-        // the slot's last weights have to be consumed first
-        if (mine && c >= 2) wait(&pv_done[slot], ((c >> 1) - 1) & 1);
-        wait(&k_full[st], ((it + j) / KST) & 1);
-        __syncwarp();
-        tc::tc_fence_after();
-        if (tc::elect_one()) {
-          if (mine) {
-            const uint64_t ad = sdesc_k_sw128(sbase + t * C::QTILE);
-            const uint64_t bd = sdesc_k_sw128(sbase + C::OFF_K + st * C::STAGE);
+    if (warp == C::SM_WARPS || warp == C::SM_WARPS + 1) {
+      // ======================================================== MMAs: scores
+      // Two warps: one per tile, or (one tile) one per slot, so that the waits,
+      // commits and descriptors of one are covered by the MMAs of the other.  A
+      // tile's blocks are counted through all its units: block c takes slot
+      // c % 2 of the tile, and is the slot's use c / 2.
+      const int me = warp - C::SM_WARPS, t = C::NQ == 2 ? me : 0;
+      int it = 0, units = 0, c0 = 0;
+      for (; w.left > 0; w.next(a)) {
+        const int n = w.nseg;
+        const bool live = t == 0 || w.ntok > a.tile_tok;          // this unit has the tile
+        if (live) wait(&q_full[t], units++ & 1);
+        for (int j = 0; j < n; ++j) {
+          const int st = (it + j) % KST, c = c0 + j, slot = 2 * t + (c & 1);
+          const bool mine = C::NQ == 2 ? live : (c & 1) == me;
+          // the slot's last weights have to be consumed first
+          if (mine && c >= 2) wait(&pv_done[slot], ((c >> 1) - 1) & 1);
+          wait(&k_full[st], ((it + j) / KST) & 1);
+          __syncwarp();
+          tc::tc_fence_after();
+          if (tc::elect_one()) {
+            if (mine) {
+              const uint64_t ad = sdesc_k_sw128(sbase + t * C::QTILE);
+              const uint64_t bd = sdesc_k_sw128(sbase + C::OFF_K + st * C::STAGE);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t bk = bd + (kk / 4) * (C::PANEL >> 4) + (kk % 4) * 2;
-              if constexpr (C::QTM)
-                mma_f16_ts(tmem + C::TM_S + slot * 64, tmem + C::TM_Q + kk * 8, bk, C::IDESC_S, kk ? 1u : 0u);
-              else
-                tc::mma_f16(tmem + C::TM_S + slot * 64, ad + (kk / 4) * (C::QPANEL >> 4) + (kk % 4) * 2, bk, C::IDESC_S,
-                            kk ? 1u : 0u);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t bk = bd + (kk / 4) * (C::PANEL >> 4) + (kk % 4) * 2;
+                if constexpr (C::QTM)
+                  mma_f16_ts(tmem + C::TM_S + slot * 64, tmem + C::TM_Q + kk * 8, bk, C::IDESC_S, kk ? 1u : 0u);
+                else
+                  tc::mma_f16(tmem + C::TM_S + slot * 64, ad + (kk / 4) * (C::QPANEL >> 4) + (kk % 4) * 2, bk, C::IDESC_S,
+                              kk ? 1u : 0u);
+              }
+              tc::mma_commit(&s_full[slot]);
+              tc::mma_commit(&k_empty[st]);
+            } else {
+              tc::mbar_arrive(&k_empty[st]);
             }
-            tc::mma_commit(&s_full[slot]);
-            tc::mma_commit(&k_empty[st]);
-          } else {
-            tc::mbar_arrive(&k_empty[st]);
+            // this warp's last scores of the unit: q is free when they are done
+            if (!C::QTM && live && j == n - 1) tc::mma_commit(&q_empty[t]);
           }
-          // this warp's last scores of the unit: q is free when they are done
-          if (!C::QTM && live && j == n - 1) tc::mma_commit(&q_empty[t]);
+          __syncwarp();
         }
-        __syncwarp();
+        it += n;
+        if (live) c0 += n;
       }
-      it += n;
-      if (live) c0 += n;
-    }
-  } else if (warp == C::SM_WARPS + 2 || (C::NQ == 2 && warp == C::SM_WARPS + 3)) {
-    // ================================================ MMAs: weighted values
-    set_registers<C::REGS_IO>(false);
-    const int t = warp - C::SM_WARPS - 2;
-    int it = 0, c0 = 0;
-    for (; w.left > 0; w.next(a)) {
-      const int n = w.nseg;
-      const bool live = t == 0 || w.ntok > a.tile_tok;
-      for (int j = 0; j < n; ++j) {
-        const int st = (it + j) % VST, c = c0 + j, slot = 2 * t + (c & 1);
-        if (live) wait(&p_full[slot], (c >> 1) & 1);
-        wait(&v_full[st], ((it + j) / VST) & 1);
-        const int key0 = (w.lo / kTcKeys + w.blk + j) * kTcKeys;
-        if (live && (key0 < w.lo || key0 + kTcKeys > w.hi)) {
-          // V rows that no row of the unit sees may hold anything: zeros (the
-          // other tile's warp may be writing the same)
-          for (int i = lane; i < kTcKeys * (D / 8); i += 32) {
-            const int r = i & (kTcKeys - 1), q = i / kTcKeys;      // row, 16-byte column
-            if (key0 + r < w.lo || key0 + r >= w.hi)
-              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
-                               sbase + C::OFF_V + st * C::STAGE + (q >> 3) * C::PANEL + r * 128 + (q & 7) * 16),
-                           "r"(0)
-                           : "memory");
+    } else if (warp == C::SM_WARPS + 2 || (C::NQ == 2 && warp == C::SM_WARPS + 3)) {
+      // ================================================ MMAs: weighted values
+      const int t = warp - C::SM_WARPS - 2;
+      int it = 0, c0 = 0;
+      for (; w.left > 0; w.next(a)) {
+        const int n = w.nseg;
+        const bool live = t == 0 || w.ntok > a.tile_tok;
+        for (int j = 0; j < n; ++j) {
+          const int st = (it + j) % VST, c = c0 + j, slot = 2 * t + (c & 1);
+          if (live) wait(&p_full[slot], (c >> 1) & 1);
+          wait(&v_full[st], ((it + j) / VST) & 1);
+          const int key0 = (w.lo / kTcKeys + w.blk + j) * kTcKeys;
+          if (live && (key0 < w.lo || key0 + kTcKeys > w.hi)) {
+            // V rows that no row of the unit sees may hold anything: zeros (the
+            // other tile's warp may be writing the same)
+            for (int i = lane; i < kTcKeys * (D / 8); i += 32) {
+              const int r = i & (kTcKeys - 1), q = i / kTcKeys;      // row, 16-byte column
+              if (key0 + r < w.lo || key0 + r >= w.hi)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                 sbase + C::OFF_V + st * C::STAGE + (q >> 3) * C::PANEL + r * 128 + (q & 7) * 16),
+                             "r"(0)
+                             : "memory");
+            }
+            fence_async_shared();
           }
-          fence_async_shared();
-        }
-        __syncwarp();
-        tc::tc_fence_after();
-        if (tc::elect_one()) {
-          if (live) {
-            const uint64_t bd = sdesc_mn_sw128(sbase + C::OFF_V + st * C::STAGE, C::PANEL);
+          __syncwarp();
+          tc::tc_fence_after();
+          if (tc::elect_one()) {
+            if (live) {
+              const uint64_t bd = sdesc_mn_sw128(sbase + C::OFF_V + st * C::STAGE, C::PANEL);
 #pragma unroll
-            for (int kk = 0; kk < kTcKeys / 16; ++kk)
-              mma_f16_ts(tmem + C::TM_O + t * D, tmem + C::TM_S + slot * 64 + kk * 8, bd + kk * (2048 >> 4), C::IDESC_O,
-                         (j | kk) ? 1u : 0u);
-            tc::mma_commit(&pv_done[slot]);
-            tc::mma_commit(&v_empty[st]);
-          } else {
-            tc::mbar_arrive(&v_empty[st]);
+              for (int kk = 0; kk < kTcKeys / 16; ++kk)
+                mma_f16_ts(tmem + C::TM_O + t * D, tmem + C::TM_S + slot * 64 + kk * 8, bd + kk * (2048 >> 4), C::IDESC_O,
+                           (j | kk) ? 1u : 0u);
+              tc::mma_commit(&pv_done[slot]);
+              tc::mma_commit(&v_empty[st]);
+            } else {
+              tc::mbar_arrive(&v_empty[st]);
+            }
           }
+          __syncwarp();
         }
-        __syncwarp();
+        it += n;
+        if (live) c0 += n;
       }
-      it += n;
-      if (live) c0 += n;
+    } else if (warp == C::SM_WARPS + 4) {
+      // =========================================================== producers
+      produce<D, false>(a, w, &tmQ, &tmK, sbase, k_full, k_empty, q_full, q_empty, wait);
+    } else if (warp == C::SM_WARPS + 5) {
+      produce<D, true>(a, w, &tmQ, &tmV, sbase, v_full, v_empty, q_full, q_empty, wait);
     }
-  } else if (warp < C::SM_WARPS) {
+  } else {
     // ============================================================= softmax
     set_registers<C::REGS_SM>(true);
     const int t = warp / 4;                  // row tile
@@ -606,15 +604,14 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         else if (a.lse) a.lse[head] = lse2 * 0.69314718055994530942f;
       }
       tc::tc_fence_before();
-      if (tid == 0 && !whole && w.slot() == 1) a.cuts[blockIdx.x] = w.cut(share);
+      if (tid == 0 && !whole && w.slot() == 1) a.cuts[blockIdx.x] = w.cut(share_mem);
     }
-  } else {
-    set_registers<C::REGS_IO>(false);
   }
 
   tc::tc_fence_before();
   __syncthreads();
   if (warp == C::SM_WARPS) {
+    if (*abort_flag) __nanosleep(1000000);   // (MMAs that nobody waited for)
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }
