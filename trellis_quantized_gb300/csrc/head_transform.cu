@@ -144,10 +144,10 @@ __host__ __device__ inline Passes count_passes(int Hq, int Hkv, int per_pass, bo
 // (pairs, R a multiple of 8), or one by one.
 enum { kByLane, kInLane, kAny };
 
-// `chunk`: passes that a warp makes for a token; `chunks` of them make up the
-// token.
+// The passes of all tokens are a line of which every warp takes `run`: whole
+// tokens, but for its first and last one.
 template <int D, bool F32IN, bool APPEND, int MODE>
-__global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const Args a, int chunk, int chunks) {
+__global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const Args a, int run) {
   constexpr int LPH = D / 8;               // lanes per head
   constexpr int HPP = 32 / LPH;            // heads per pass
   __shared__ __align__(16) float2 table[kWarps][D / 2];
@@ -180,10 +180,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const A
   const int live_q = ps.q - ((ps.q - 1) * HPP + lane / LPH < a.Hq ? 0 : 1);
   const int live_kv = ps.k - ps.q - ((ps.k - ps.q - 1) * HPP + lane / LPH < a.Hkv ? 0 : 1);
 
-  for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < (int64_t)a.T * chunks;
-       item += (int64_t)gridDim.x * kWarps) {
-    const int t = (int)(item / chunks), p0 = (int)(item - (int64_t)t * chunks) * chunk;
-    const int p1 = min(ps.all, p0 + chunk);
+  const auto look_up = [&](int b, int index) -> int {          // -1: no such page
+    const int i = index / a.page_size;
+    return index >= 0 && i < a.max_pages ? a.table[(int64_t)b * a.max_pages + i] : -1;
+  };
+  const int64_t first = ((int64_t)blockIdx.x * kWarps + warp) * run;
+  int left = (int)max(min((int64_t)run, (int64_t)a.T * ps.all - first), (int64_t)0);   // passes still to do
+  int t = (int)(first / ps.all), p0 = (int)(first - (int64_t)t * ps.all);
+  // the sequence of the token before, its end, what makes rows cache indexes,
+  // and the next token's page, looked up during the passes of the one before
+  int b = a.B, seq_end = 0, shift = 0, next_page = -1;
+  for (; left > 0; ++t, p0 = 0) {
+    const int p1 = min(ps.all, p0 + left);
+    left -= p1 - p0;
     // the first heads of every kind are under way while the angles are worked out
     const int qa = p0, qb = min(p1, ps.q), ka = max(p0 - ps.q, 0), kb = min(p1, ps.k) - ps.q;
     const int va = max(p0 - ps.k, 0), vb = p1 - ps.k;
@@ -198,19 +207,25 @@ __global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const A
 
     int index = 0, page = -1, off = 0;               // cache index (negative: padding) and place
     if (APPEND) {
-      const int b = find_seq(a.q_start, a.B, t, lane);
+      if (t >= seq_end) {
+        b = find_seq(a.q_start, a.B, t, lane);
+        seq_end = t;                                 // (of no sequence: look again for the next token)
+        if (b < a.B) {
+          seq_end = a.q_start[b + 1];
+          shift = a.kv_len[b] - seq_end;
+          next_page = look_up(b, t + shift);
+        }
+      }
       index = -1;
       if (b < a.B) {
-        index = a.kv_len[b] - (a.q_start[b + 1] - t);
-        const int i = index < 0 ? a.max_pages : index / a.page_size;
-        if (i < a.max_pages) {
-          page = a.table[(int64_t)b * a.max_pages + i];
-          off = index - i * a.page_size;
-        }
+        index = t + shift;
+        page = next_page;
+        off = index % a.page_size;
         if ((unsigned)page >= (unsigned)a.num_pages) {
           if (lane == 0) set_device_error(a.err, kErrBounds);
           page = -1;
         }
+        if (left > 0 && t + 1 < seq_end) next_page = look_up(b, index + 1);
       }
     }
     const int pos = a.positions ? a.positions[t] : index;
@@ -372,20 +387,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const A
 template <int D, bool F32IN, bool APPEND>
 cudaError_t launch(const Args &a, cudaStream_t s) {
   const int passes = count_passes(a.Hq, a.Hkv, 32 / (D / 8), APPEND).all;
-  // as many passes per warp as leave every warp that fits on the GPU some
-  const int64_t warps = (int64_t)exl3_sm_count() * kCtas * kWarps;
-  int64_t chunk = ((int64_t)a.T * passes + warps - 1) / warps;
-  if (chunk > passes) chunk = passes;
-  const int chunks = ceil_div(passes, (int)chunk);
-  int64_t grid = ((int64_t)a.T * chunks + kWarps - 1) / kWarps;
-  if (grid > (int64_t)exl3_sm_count() * kCtas) grid = (int64_t)exl3_sm_count() * kCtas;
+  const int64_t total = (int64_t)a.T * passes, warps = (int64_t)exl3_sm_count() * kCtas * kWarps;
+  const int run = (int)((total + warps - 1) / warps);
+  const int64_t grid = (total + (int64_t)run * kWarps - 1) / ((int64_t)run * kWarps);
   const dim3 g((unsigned)grid), b(kThreads);
   const bool pairs = a.layout == EXL3_ROPE_PAIRS;
   if (pairs ? a.rotary_dim == 0 : a.rotary_dim % 16 == 0)
-    return launch_pdl(head_transform_kernel<D, F32IN, APPEND, kByLane>, g, b, 0, s, a, (int)chunk, chunks);
+    return launch_pdl(head_transform_kernel<D, F32IN, APPEND, kByLane>, g, b, 0, s, a, run);
   if (pairs && a.rotary_dim % 8 == 0)
-    return launch_pdl(head_transform_kernel<D, F32IN, APPEND, kInLane>, g, b, 0, s, a, (int)chunk, chunks);
-  return launch_pdl(head_transform_kernel<D, F32IN, APPEND, kAny>, g, b, 0, s, a, (int)chunk, chunks);
+    return launch_pdl(head_transform_kernel<D, F32IN, APPEND, kInLane>, g, b, 0, s, a, run);
+  return launch_pdl(head_transform_kernel<D, F32IN, APPEND, kAny>, g, b, 0, s, a, run);
 }
 
 template <bool F32IN, bool APPEND>
