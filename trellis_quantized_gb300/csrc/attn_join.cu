@@ -3,15 +3,17 @@
 //
 //   y = sum_c 2^(lse_c - max) y_c / sum_c 2^(lse_c - max)
 //
-// A CTA leaves at most one unit unfinished for its successors: block (c, i)
-// takes some rows (2 after the step kernel, 8 after the tensor-core kernel) of
-// the one that CTA c left, if there is one.  A
-// warp per row turns the parts' lse into weights, then the block adds: a
-// thread holds four neighbouring elements of a row, and where the rows do not
-// fill the block several groups of threads share the parts (a single user's
-// long sequence is cut into up to 76 parts per key head) and are added at the
-// end in their order.  Bound by the latency of three dependent reads of L2,
-// where the parts were just written; eight reads per thread are in flight.
+// A CTA leaves at most one unit unfinished for its successors: the blocks
+// (c, .) share the rows of the one that CTA c left, if there is one, up to 8
+// each after the tensor-core kernel and 2 after the step kernel.  A warp per
+// row turns the parts' lse into weights, then the block adds: a thread holds
+// four neighbouring elements of a row, and where the rows do not fill the
+// block several groups of threads share the parts (a single user's long
+// sequence is cut into up to 76 parts per key head) and are added at the end
+// in their order.  Bound by the latency of dependent reads of L2, where the
+// parts were just written: the record, then the lse together with the first
+// eight parts of every thread (8 users x 5 tokens at 256-wide heads: the call
+// takes 37.4 us; 39.9 with 8 rows to a block and the parts read after the lse).
 //
 // Joining inside the attention kernel, by the CTA that arrived last, cost 115
 // us for eight sequences of up to 20,000 tokens at 256-wide heads against 66
@@ -22,24 +24,40 @@ namespace exl3 {
 namespace attn {
 
 constexpr int kJoinThreads = 256, kJoinRows = 8, kJoinMaxCtas = 512;
+constexpr int kRead = 8;                     // parts that a thread reads at once
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads)
-    attn_join_kernel(const Args a, int ctas, int tile_rows, int block_rows) {
+__global__ void __launch_bounds__(kJoinThreads, 4)
+    attn_join_kernel(const Args a, int ctas, int tile_rows) {
   constexpr int C4 = D / 4;                  // threads per row
   __shared__ float weight[kJoinRows][kJoinMaxCtas];
   __shared__ float row_lse[kJoinRows];
   __shared__ float4 red[kJoinThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int first = blockIdx.x, r0 = blockIdx.y * block_rows;
+  const int first = blockIdx.x;
   pdl_trigger();
   pdl_wait();
   const int4 cut = __ldcg(reinterpret_cast<const int4 *>(a.cuts + first));   // rows, last, t, h
-  const int rows = min(cut.x - r0, block_rows);
+  const int block_rows = max(2, (cut.x + (int)gridDim.y - 1) / (int)gridDim.y);    // at most kJoinRows
+  const int r0 = blockIdx.y * block_rows, rows = min(cut.x - r0, block_rows);
   if (rows <= 0) return;
   const int parts = min(min(cut.y, ctas - 1) - first + 1, kJoinMaxCtas);
   // row r of part p: slot 1 of the first CTA, slot 0 of the others
   const auto place = [&](int p, int r) { return ((int64_t)(first + p) * 2 + (p == 0 ? 1 : 0)) * tile_rows + r0 + r; };
+  const int items = rows * C4;
+  const int groups = items < kJoinThreads ? kJoinThreads / items : 1;
+  const int g = items < kJoinThreads ? tid / items : 0;
+  int i = items < kJoinThreads ? tid - g * items : tid;
+  // a thread's values of kRead parts from part p on
+  const auto read = [&](int p, float4(&v)[kRead]) {
+#pragma unroll
+    for (int k = 0; k < kRead; ++k, p += groups)
+      v[k] = g < groups && i < items && p < parts
+                 ? __ldcg(reinterpret_cast<const float4 *>(a.part_o + place(p, i / C4) * D + (i % C4) * 4))
+                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  };
+  float4 v[kRead];
+  read(g, v);                                  // under way while the weights are worked out
   for (int r = warp; r < rows; r += kJoinThreads / 32) {
     // (the first 128 parts' lse stay in registers between the two passes)
     float ls[4], mx = neg_inf();
@@ -69,23 +87,21 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (lane == 0) row_lse[r] = sum == 0.0f ? neg_inf() : (mx + log2f(sum)) * 0.69314718055994530942f;
   }
   __syncthreads();
-  const int items = rows * C4;
-  const int groups = items < kJoinThreads ? kJoinThreads / items : 1;
   for (int i0 = 0; i0 < items; i0 += kJoinThreads) {
-    const int g = items < kJoinThreads ? tid / items : 0;
-    const int i = items < kJoinThreads ? tid - g * items : i0 + tid;
+    if (i0) i += kJoinThreads;
     const bool mine = g < groups && i < items;
     const int r = mine ? i / C4 : 0, c4 = (i % C4) * 4;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (mine) {
-#pragma unroll 8
-      for (int p = g; p < parts; p += groups) {
-        const float f = weight[r][p];
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + place(p, r) * D + c4));
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
+    for (int p0 = g; p0 < parts; p0 += kRead * groups) {
+      if (i0 || p0 != g) read(p0, v);
+#pragma unroll
+      for (int k = 0; k < kRead; ++k) {
+        const int p = p0 + k * groups;
+        const float f = p < parts ? weight[r][p] : 0.0f;
+        acc.x = fmaf(f, v[k].x, acc.x);
+        acc.y = fmaf(f, v[k].y, acc.y);
+        acc.z = fmaf(f, v[k].z, acc.z);
+        acc.w = fmaf(f, v[k].w, acc.w);
       }
     }
     if (groups > 1) {
@@ -115,11 +131,10 @@ __global__ void __launch_bounds__(kJoinThreads)
 cudaError_t exl3_launch_attn_join(const exl3::attn::Args &a, int D, int ctas, int tile_rows, cudaStream_t s) {
   using namespace exl3::attn;
   if (ctas > kJoinMaxCtas) return cudaErrorInvalidConfiguration;
-  const int rows = tile_rows > 16 ? kJoinRows : 2;
-  const dim3 grid(ctas, exl3::ceil_div(tile_rows, rows)), block(kJoinThreads);
+  const dim3 grid(ctas, tile_rows > 16 ? tile_rows / kJoinRows : tile_rows / 2), block(kJoinThreads);
   switch (D) {
-    case 64: return exl3::launch_pdl(attn_join_kernel<64>, grid, block, 0, s, a, ctas, tile_rows, rows);
-    case 128: return exl3::launch_pdl(attn_join_kernel<128>, grid, block, 0, s, a, ctas, tile_rows, rows);
-    default: return exl3::launch_pdl(attn_join_kernel<256>, grid, block, 0, s, a, ctas, tile_rows, rows);
+    case 64: return exl3::launch_pdl(attn_join_kernel<64>, grid, block, 0, s, a, ctas, tile_rows);
+    case 128: return exl3::launch_pdl(attn_join_kernel<128>, grid, block, 0, s, a, ctas, tile_rows);
+    default: return exl3::launch_pdl(attn_join_kernel<256>, grid, block, 0, s, a, ctas, tile_rows);
   }
 }
