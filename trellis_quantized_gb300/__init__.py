@@ -14,6 +14,7 @@ device.
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 
 import torch
@@ -192,7 +193,7 @@ def _stream(stream=None):
     return ctypes.c_void_p(_raw_stream(stream))
 
 
-_ws_cache: dict = {}
+_ws_cache: dict = {}                      # (device, stream): (buffer, address, bytes)
 
 
 def workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
@@ -207,12 +208,12 @@ def workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
         index = torch.cuda.current_device() if device.index is None else device.index
     raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
     key = (index, raw)
-    buf = _ws_cache.get(key)
-    if buf is None or buf.numel() < nbytes:
+    buf, _, size = _ws_cache.get(key, (None, 0, -1))
+    if size < nbytes:
         dev = torch.device("cuda", index)
         buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
         exl3_workspace_clear(buf, stream=stream if stream is not None else torch.cuda.current_stream(dev))
-        _ws_cache[key] = buf
+        _ws_cache[key] = (buf, buf.data_ptr(), buf.numel())
     return buf
 
 
@@ -593,6 +594,17 @@ def _out(t, name: str, shape, dtype) -> int:
     return t.data_ptr()
 
 
+def _workspace_arg(buf, nbytes: int, device, stream, raw: int):
+    """Address and bytes of a call's workspace: the caller's, or the cached one."""
+    if buf is not None:
+        return _ptr(buf, "workspace"), buf.numel() * buf.element_size()
+    hit = _ws_cache.get((device.index, raw))
+    if hit is None or hit[2] < nbytes:
+        buf = workspace(nbytes, device, stream)
+        return buf.data_ptr(), buf.numel()
+    return hit[1], hit[2]
+
+
 def _positions(t, T: int):
     if t is None:
         return None
@@ -637,6 +649,10 @@ def exl3_qkv_append_workspace_size() -> int:
     return lib().exl3_qkv_append_workspace_size()
 
 
+# (sizes of calls that a decode loop repeats)
+_append_workspace = functools.cache(exl3_qkv_append_workspace_size)
+
+
 def exl3_qkv_append(q, k, v, batch: PagedBatch, cache: KvCache, transform: HeadTransform, positions=None, q_out=None,
                     workspace_buf=None, stream=None) -> torch.Tensor:
     """Norm and rotate q [T, Hq, D], k and v [T, Hkv, D] (fp16 or fp32), write k and v to their
@@ -654,17 +670,18 @@ def exl3_qkv_append(q, k, v, batch: PagedBatch, cache: KvCache, transform: HeadT
     vp, vs = _rows(v, "v", cache.heads_kv, D, q.dtype)
     qop, pp = _out(q_out, "q_out", (T, Hq, D), torch.float16), _positions(positions, T)
     if T:
-        L = lib()
-        ws = workspace_buf if workspace_buf is not None else workspace(L.exl3_qkv_append_workspace_size(), q.device,
-                                                                       stream)
-        _check(L.exl3_qkv_append(qp, qs, kp, ks, vp, vs, in_dtype, T, Hq, ctypes.byref(transform), pp,
-                                 ctypes.byref(batch), ctypes.byref(cache), qop, _ptr(ws, "workspace"),
-                                 ws.numel() * ws.element_size(), _raw_stream(stream)))
+        raw = _raw_stream(stream)
+        wp, wn = _workspace_arg(workspace_buf, _append_workspace(), q.device, stream, raw)
+        _check(lib().exl3_qkv_append(qp, qs, kp, ks, vp, vs, in_dtype, T, Hq, ctypes.byref(transform), pp,
+                                     ctypes.byref(batch), ctypes.byref(cache), qop, wp, wn, raw))
     return q_out
 
 
 def exl3_paged_attention_workspace_size(T: int, heads_q: int, heads_kv: int, head_dim: int, batch: int) -> int:
     return lib().exl3_paged_attention_workspace_size(T, heads_q, heads_kv, head_dim, batch)
+
+
+_attention_workspace = functools.lru_cache(maxsize=4096)(exl3_paged_attention_workspace_size)
 
 
 def exl3_paged_attention(q, batch: PagedBatch, cache: KvCache, scale: float | None = None, causal: bool = True,
@@ -683,13 +700,10 @@ def exl3_paged_attention(q, batch: PagedBatch, cache: KvCache, scale: float | No
     yp = _out(y, "y", (T, Hq, D), odt)
     lp = None if lse is None else _out(lse, "lse", (T, Hq), torch.float32)
     if T:
-        L = lib()
-        ws = workspace_buf
-        if ws is None:
-            ws = workspace(L.exl3_paged_attention_workspace_size(T, Hq, cache.heads_kv, D, batch.batch), q.device,
-                           stream)
-        _check(L.exl3_paged_attention(qp, qs, T, Hq, ctypes.byref(batch), ctypes.byref(cache),
-                                      D ** -0.5 if scale is None else scale, 1 if causal else 0, window, yp, out_dtype,
-                                      lp, _ptr(ws, "workspace"), ws.numel() * ws.element_size(),
-                                      _raw_stream(stream)))
+        raw = _raw_stream(stream)
+        wp, wn = _workspace_arg(workspace_buf, _attention_workspace(T, Hq, cache.heads_kv, D, batch.batch), q.device,
+                                stream, raw)
+        _check(lib().exl3_paged_attention(qp, qs, T, Hq, ctypes.byref(batch), ctypes.byref(cache),
+                                          D ** -0.5 if scale is None else scale, 1 if causal else 0, window, yp,
+                                          out_dtype, lp, wp, wn, raw))
     return y
