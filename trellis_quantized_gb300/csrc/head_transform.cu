@@ -6,9 +6,12 @@
 //
 // Both calls are bound by memory: each input is read once and each output
 // written once, 2 to 4 bytes either way against about seven operations an
-// element.  A warp takes a token, or some of its heads where there are few
-// tokens, and nothing is shared between warps: no block-wide barrier, and 20
-// warps per SM with up to four loads in flight each cover the memory's latency.  A
+// element.  Nothing is shared between warps: no block-wide barrier, and 20
+// warps per SM with up to four loads in flight each cover the memory's latency
+// (9,310 tokens at 40/8 heads of 128, 267 MB: 53.9 us, 4.95 TB/s; what the
+// warps wait for is still mostly loads).  All warps take equal runs of the
+// tokens' passes, cutting tokens where they have to: whole tokens left most
+// warps without one in the last round (59.1 us).  A
 // lane holds eight neighbouring elements (16 bytes of fp16) of a head, so D / 8
 // lanes hold a head, the mean is a few shuffles, and the lane keeps its place
 // in the head while the warp walks over the token's heads: the norm weights
@@ -30,9 +33,10 @@ namespace ht {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kCtas = 5;   // per CTA, per SM
 // Passes whose data is under way beside the one at hand, and passes per turn
-// of the loop: fp32 rows are twice as long and need no more than one (at T =
-// 1777, 64-wide heads: 5.2 us; three ahead 5.6 us), fp16 rows gain from three
-// (append of 9310 tokens at 40/8 heads of 128: 59 us; one ahead 65 us).
+// of the loop: fp32 rows are twice as long and three ahead spill (1,777 tokens
+// at 24/8 heads of 64: 4.3 us with one, 6.8 with three), fp16 rows gain from
+// three (9,310 tokens appended: 54.4 us; two ahead 57.1, one 57.7).  Six CTAs
+// per SM (80 registers) take 56.8 us, four 58.1.
 template <bool F32>
 constexpr int kAhead = F32 ? 1 : 3;
 template <bool F32>
