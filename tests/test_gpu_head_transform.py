@@ -215,3 +215,60 @@ def test_append_past_two_gigabytes():
     assert_transform(kc[pages - 1, 7:10], *transform(k, kn, 1e-6, pos, f, False, 1.0), "k")
     assert torch.equal(vc[pages - 1, 7:10], v)
     assert math.isclose(float(kc[:pages - 1].abs().max()), 0.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+@pytest.mark.parametrize("Hq,Hkv,D,R", [(4, 4, 64, 64), (5, 3, 64, 20), (6, 1, 128, 128)])
+def test_append_more_tokens_than_warps(Hq, Hkv, D, R, dtype):
+    """Every warp goes through several tokens, and through the ends of sequences and pages."""
+    _append([1, 4001, 0, 5003, 17, 2], [30, 0, 9, 77, 15, 0], Hq, Hkv, D, R, 16, "tokens", dtype, pad=1100)
+
+
+def test_transform_of_more_tokens_than_warps():
+    T = 9001
+    q, k, _, qn, kn, f = _make(T, 5, 3, 64, 64, "both", torch.float16, _gen(4))
+    pos = torch.randint(-100, 1 << 20, (T,), generator=_gen(5), device="cuda", dtype=torch.int32)
+    qo, ko = tq.exl3_qk_norm_rope(q, k, pos, tq.head_transform(qn, kn, 1e-6, f))
+    assert_transform(qo, *transform(q, qn, 1e-6, pos, f, False, 1.0), "q")
+    assert_transform(ko, *transform(k, kn, 1e-6, pos, f, False, 1.0), "k")
+
+
+def test_append_rows_before_the_first_sequence():
+    first, new, page, D = 5002, 4500, 16, 64
+    T = first + new + 3
+    g = _gen(8)
+    q, k, v, qn, kn, f = _make(T, 4, 4, D, D, "both", torch.float16, g)
+    pages = (new + 40 + page - 1) // page
+    kc, vc = _cache(pages, page, 4, D, "tokens", g)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    # the first sequence has no rows
+    batch = tq.paged_batch(_i32([first, first, first + new]), _i32([3, new + 40]), torch.stack([table.flip(0), table]))
+    qo = tq.exl3_qkv_append(q, k, v, batch, tq.kv_cache(kc, vc), tq.head_transform(qn, kn, 1e-6, f), workspace_buf=ws)
+    assert tq.exl3_check_device_error(ws) == 0
+    mine = slice(first, first + new)
+    pos = torch.arange(40, 40 + new, device="cuda")
+    assert not qo[:first].any() and not qo[first + new:].any()
+    assert_transform(qo[mine], *transform(q[mine], qn, 1e-6, pos, f, False, 1.0), "q")
+    pg, off = table.long()[pos // page], pos % page
+    assert_transform(kc[pg, off], *transform(k[mine], kn, 1e-6, pos, f, False, 1.0), "k")
+    assert torch.equal(vc[pg, off], v[mine])
+
+
+def test_append_with_a_length_below_its_new_tokens():
+    """The tokens without a place are reported, the others are where they belong."""
+    new, n, page, D = 6000, 4000, 16, 64
+    g = _gen(12)
+    q, k, v, qn, kn, f = _make(new, 4, 4, D, D, "both", torch.float16, g)
+    kc, vc = _cache(n // page, page, 4, D, "tokens", g)
+    table = torch.randperm(n // page, generator=g, device="cuda").to(torch.int32)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    batch = tq.paged_batch(_i32([0, new]), _i32([n]), table[None].contiguous())
+    qo = tq.exl3_qkv_append(q, k, v, batch, tq.kv_cache(kc, vc), tq.head_transform(qn, kn, 1e-6, f), workspace_buf=ws)
+    assert tq.exl3_check_device_error(ws) != 0
+    pos = torch.arange(n, device="cuda")
+    pg, off = table.long()[pos // page], pos % page
+    assert not qo[:new - n].any()
+    assert_transform(qo[new - n:], *transform(q[new - n:], qn, 1e-6, pos, f, False, 1.0), "q")
+    assert_transform(kc[pg, off], *transform(k[new - n:], kn, 1e-6, pos, f, False, 1.0), "k")
+    assert torch.equal(vc[pg, off], v[new - n:])
