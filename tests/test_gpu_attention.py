@@ -265,3 +265,22 @@ def test_cache_past_two_gigabytes():
         q = torch.randn((n, 16, D), generator=gen, device="cuda").half()
         y = tq.exl3_paged_attention(q, tq.paged_batch(_i32([0, n]), _i32([L]), table), tq.kv_cache(k, v))
         _compare(y, None, q, [(kd[:L], vd[:L])], [n], [L - n], True, 0, D ** -0.5)
+
+
+@pytest.mark.parametrize("B", [32, 33, 530])
+@pytest.mark.parametrize("Hq,Hkv,D", [(10, 2, 128), (8, 1, 256)])
+@pytest.mark.parametrize("chunks", [False, True])
+def test_numbers_of_sequences(B, Hq, Hkv, D, chunks):
+    """The work is found with and without block barriers; some sequences have no row, some no history."""
+    old = [(i * 37) % 211 for i in range(B)]
+    new = [(i * 5 + 3) % 41 for i in range(B)] if chunks else [1 - (i % 7 == 3) for i in range(B)]
+    _run(new, old, Hq, Hkv, D, pad=3)
+
+
+@pytest.mark.parametrize("B", [5, 34])
+@pytest.mark.parametrize("rows", [1, 3, 9, 40, 41])
+def test_joins_of_short_tiles(B, rows):
+    """Long histories behind few rows: the units are cut, and their rows are spread over the join's blocks."""
+    old = [4000 + 900 * (i % 3) for i in range(B)]
+    _run([rows] * B, old, 16, 2, 256, page=64)
+    _run([rows] * B, old, 20, 4, 128, page=64)
