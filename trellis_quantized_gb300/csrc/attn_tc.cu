@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     }
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&q_full[s], C::QTM ? 4 : 1);
-      tc::mbar_init(&q_empty[s], 1);
+      tc::mbar_init(&q_empty[s], C::QTM ? 2 : 1);
     }
     abort_word = 0;
     tc::fence_mbar_init();
@@ -349,6 +349,10 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         const int n = w.nseg;
         const bool live = t == 0 || w.ntok > a.tile_tok;          // this unit has the tile
         if (live) wait(&q_full[t], units++ & 1);
+        // (q in TMEM: in a unit of one block only one of the two warps has scores
+        // to compute, so the next q is announced once both have seen this one's)
+        __syncwarp();
+        if (C::QTM && tc::elect_one()) tc::mbar_arrive(&q_empty[0]);
         for (int j = 0; j < n; ++j) {
           const int st = (it + j) % KST, c = c0 + j, slot = 2 * t + (c & 1);
           const bool mine = C::NQ == 2 ? live : (c & 1) == me;
@@ -442,8 +446,11 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     const uint32_t lanes = (uint32_t)(wl * 32) << 16;
     const int row = wl * 32 + lane;          // within the tile
     int c = 0;                               // blocks of this tile so far
+    int brought = 0;                         // units whose q is in TMEM
     // q of a unit to TMEM (256-wide heads): a thread brings its row, as the
-    // fp16 pairs that an A operand's columns hold
+    // fp16 pairs that an A operand's columns hold.  The place is free when the
+    // scores of the unit before have all been read; the barrier may go on to
+    // its next phase only when both score warps have seen the last.
     const auto bring_q = [&](const auto &u) {
       if (u.left <= 0) return;
       const int tok = row_token(a, row);
@@ -464,6 +471,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       }
       tc::tmem_st_wait();
       tc::tc_fence_before();
+      if (brought > 0) wait(&q_empty[0], (brought - 1) & 1);
+      ++brought;
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&q_full[0]);
     };
