@@ -3,8 +3,11 @@ scores, one key that outweighs a long history, batches whose sequences differ
 most.  Helpers and bounds are those of tests/test_gpu_attention.py and
 tests/attention_ref.py, unless a test derives a closer bound of its own."""
 import pytest
+import torch
 
-from test_gpu_attention import _run
+import trellis_quantized_gb300 as tq
+from attention_ref import U16
+from test_gpu_attention import _run, _setup
 
 pytestmark = pytest.mark.gpu
 
@@ -23,3 +26,56 @@ def test_short_units_among_long_ones(rows):
     """256-wide heads: units of one block between units that are cut."""
     old = [0, 9000, 1, 5, 20, 3000, 0, 0, 0, 15, 64, 2, 7000]
     _run([rows] * len(old), old, 8, 4, 256, page=32)
+
+
+def _signs(shape, size, gen):
+    return (torch.randint(0, 2, shape, generator=gen, device="cuda") * 2 - 1).half() * size
+
+
+def _sign_scores(new, old, Hq, Hkv, D, size, page=16):
+    """Attention with q and k of +-size in every element.  A score is then an
+    integer times size^2 with at most 24 significant bits, so every product and
+    sum of it is exact in fp32; scores that differ do so by 2 size^2 at least,
+    which leaves weights of zero: y is the mean of v over a row's largest keys.
+    Returns y, lse, the exact means, the keys of each mean and the exact lse."""
+    q, k, v, table, dense, q_start, kv_len = _setup([new], [old], Hq, Hkv, D, page, "tokens", seed=3)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(new + old + D)
+    q.copy_(_signs(q.shape, size, gen))
+    kd, vd = dense[0]
+    kd.copy_(_signs(kd.shape, size, gen))
+    p = torch.arange(new + old, device="cuda")
+    k[table[0].long()[p // page], p % page] = kd
+    lse = torch.empty((new, Hq), dtype=torch.float32, device="cuda")
+    ws = torch.zeros(tq.exl3_paged_attention_workspace_size(new, Hq, Hkv, D, 1), dtype=torch.uint8, device="cuda")
+    y = tq.exl3_paged_attention(q, tq.paged_batch(q_start, kv_len, table), tq.kv_cache(k, v), lse=lse, workspace_buf=ws)
+    assert tq.exl3_check_device_error(ws) == 0
+    G = Hq // Hkv
+    s = torch.einsum("tgd,jgd->tgj", q.double(), kd.double().repeat_interleave(G, 1))
+    s = torch.where(p[None, None, :] <= old + torch.arange(new, device="cuda")[:, None, None], s, -torch.inf)
+    top = s.amax(-1, keepdim=True)
+    largest = (s == top).double()
+    keys = largest.sum(-1)
+    mean = torch.einsum("tgj,jgd->tgd", largest, vd.double().repeat_interleave(G, 1)) / keys[..., None]
+    size_of_terms = torch.einsum("tgj,jgd->tgd", largest, vd.double().abs().repeat_interleave(G, 1)) / keys[..., None]
+    return y, lse, mean, size_of_terms, keys, top[..., 0] * D ** -0.5 + torch.log(keys)
+
+
+def _compare_means(y, lse, mean, terms, want_lse, rows):
+    """One rounding of y to fp16; sums of at most some tens of terms, the
+    division and the exponential of the weights within 2^-20 of the terms; an
+    lse within eight roundings of its size (scale, its product with the
+    maximum, the natural logarithm's factor, the sum)."""
+    assert torch.isfinite(y).all() and torch.isfinite(lse).all()
+    bound = U16 * mean.abs() + 2.0 ** -25 + 2.0 ** -20 * terms
+    assert ((y.double() - mean).abs() <= bound)[rows].all()
+    assert ((lse.double() - want_lse).abs() <= 2.0 ** -21 * want_lse.abs())[rows].all()
+
+
+@pytest.mark.parametrize("size", [8000.0, 32768.0])
+@pytest.mark.parametrize("Hq,Hkv,D", [(40, 8, 128), (16, 2, 256), (24, 8, 64)])
+@pytest.mark.parametrize("new,old", [(1, 700), (100, 700), (300, 0)])
+def test_scores_of_any_size(size, Hq, Hkv, D, new, old):
+    """Scores up to 2^37: rows with one largest key have its v, all rows are finite."""
+    y, lse, mean, terms, keys, want_lse = _sign_scores(new, old, Hq, Hkv, D, size)
+    _compare_means(y, lse, mean, terms, want_lse, keys == 1)
