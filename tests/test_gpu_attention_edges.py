@@ -79,3 +79,13 @@ def test_scores_of_any_size(size, Hq, Hkv, D, new, old):
     """Scores up to 2^37: rows with one largest key have its v, all rows are finite."""
     y, lse, mean, terms, keys, want_lse = _sign_scores(new, old, Hq, Hkv, D, size)
     _compare_means(y, lse, mean, terms, want_lse, keys == 1)
+
+
+@pytest.mark.parametrize("size", [8000.0, 32768.0])
+@pytest.mark.parametrize("Hq,Hkv,D", [(40, 8, 128), (16, 2, 256), (24, 8, 64)])
+@pytest.mark.parametrize("new,old", [(1, 700), (1, 5000), (100, 700)])
+def test_ties_at_scores_of_any_size(size, Hq, Hkv, D, new, old):
+    """Largest keys in several parts of a cut sequence, in different numbers: each counts once."""
+    y, lse, mean, terms, keys, want_lse = _sign_scores(new, old, Hq, Hkv, D, size)
+    assert (keys > 1).any()
+    _compare_means(y, lse, mean, terms, want_lse, keys >= 1)

@@ -144,7 +144,7 @@ int query_map(CUtensorMap *m, const void *q, int64_t stride, int T, int heads, i
 // ---- exl3_paged_attention workspace layout: a record per CTA of the unit
 // that it leaves unfinished, and two partial results per CTA
 struct AttnWs {
-  size_t cuts = 0, part_o = 0, part_lse = 0, total = 0;
+  size_t cuts = 0, part_o = 0, part_ml = 0, total = 0;
   int grid = 0, rows = 0;
 };
 
@@ -159,8 +159,8 @@ AttnWs attn_ws(int T, int G, int D, int batch) {
   off = align_up(off + sizeof(exl3::attn::Cut) * w.grid);
   w.part_o = off;
   off = align_up(off + sizeof(float) * rows * D);
-  w.part_lse = off;
-  off = align_up(off + sizeof(float) * rows);
+  w.part_ml = off;
+  off = align_up(off + sizeof(float2) * rows);
   w.total = off;
   return w;
 }
@@ -359,7 +359,7 @@ int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q
   a.y_aligned32 = (reinterpret_cast<uintptr_t>(y) & 31u) == 0;
   a.lse = lse;
   a.part_o = at<float>(workspace, L.part_o);
-  a.part_lse = at<float>(workspace, L.part_lse);
+  a.part_ml = at<float2>(workspace, L.part_ml);
   a.cuts = at<exl3::attn::Cut>(workspace, L.cuts);
   a.err = at<int>(workspace, 0);
   CUtensorMap mk, mv;

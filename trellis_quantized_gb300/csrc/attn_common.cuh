@@ -36,7 +36,7 @@ struct Args {
   int f32out, y_aligned32;
   float *lse;                // [T][Hq] or null
   float *part_o;             // partial results: [grid][2][rows][D] fp32
-  float *part_lse;           // [grid][2][rows], log2 of the sum
+  float2 *part_ml;           // [grid][2][rows]: maximum of the scaled scores (log2), sum of 2^(score - maximum)
   struct Cut *cuts;          // [grid] the unit that begins in a CTA and ends in a later one
   int *err;
 };
@@ -89,6 +89,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float((int)0xff800000u); }
+
+// ln of the sum of weights, from their maximum (log2) and the sum of 2^(score -
+// maximum).
+__device__ __forceinline__ float natural_lse(float m2, float l) {
+  return l == 0.0f ? neg_inf() : (m2 + log2f(l)) * 0.69314718055994530942f;
+}
 
 // Four neighbouring elements of the output, rounded once if it is fp16.
 __device__ __forceinline__ void store4(const Args &a, int64_t i, const float4 &v) {

@@ -1,19 +1,22 @@
 // attn_join.cu -- joins the parts of the units that the attention kernels
 // cut between CTAs:
 //
-//   y = sum_c 2^(lse_c - max) y_c / sum_c 2^(lse_c - max)
+//   w_c = l_c 2^(m_c - max_c m_c),  y = sum_c w_c y_c / sum_c w_c
+//
+// with the largest score m_c of a part and its sum of weights l_c, which are
+// kept apart: at scores past 2^20, log2(l_c) would be lost in their sum.
 //
 // A CTA leaves at most one unit unfinished for its successors: the blocks
 // (c, .) share the rows of the one that CTA c left, if there is one, up to 8
 // each after the tensor-core kernel and 2 after the step kernel.  A warp per
-// row turns the parts' lse into weights, then the block adds: a thread holds
+// row works out the parts' weights, then the block adds: a thread holds
 // four neighbouring elements of a row, and where the rows do not fill the
 // block several groups of threads share the parts (a single user's long
 // sequence is cut into up to 76 parts per key head) and are added at the end
 // in their order.  Bound by the latency of dependent reads of L2, where the
-// parts were just written: the record, then the lse together with the first
+// parts were just written: the record, then maxima and sums together with the first
 // eight parts of every thread (8 users x 5 tokens at 256-wide heads: the call
-// takes 37.4 us; 39.9 with 8 rows to a block and the parts read after the lse).
+// takes 37.4 us; 39.9 with 8 rows to a block and the parts read after them).
 //
 // Joining inside the attention kernel, by the CTA that arrived last, cost 115
 // us for eight sequences of up to 20,000 tokens at 256-wide heads against 66
@@ -59,32 +62,38 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
   float4 v[kRead];
   read(g, v);                                  // under way while the weights are worked out
   for (int r = warp; r < rows; r += kJoinThreads / 32) {
-    // (the first 128 parts' lse stay in registers between the two passes)
-    float ls[4], mx = neg_inf();
+    // (between the two passes the sums stay in the weights' places, the first
+    // 96 parts' maxima in registers)
+    const auto take = [&](int p) {
+      const float2 ml = __ldcg(a.part_ml + place(p, r));
+      weight[r][p] = ml.y;
+      return ml.x;
+    };
+    float m[3], mx = neg_inf();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      ls[k] = lane + 32 * k < parts ? __ldcg(a.part_lse + place(lane + 32 * k, r)) : neg_inf();
-      mx = fmaxf(mx, ls[k]);
+    for (int k = 0; k < 3; ++k) {
+      m[k] = lane + 32 * k < parts ? take(lane + 32 * k) : neg_inf();
+      mx = fmaxf(mx, m[k]);
     }
-    for (int p = lane + 128; p < parts; p += 32) mx = fmaxf(mx, __ldcg(a.part_lse + place(p, r)));
+    for (int p = lane + 96; p < parts; p += 32) mx = fmaxf(mx, take(p));
 #pragma unroll
     for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
     float sum = 0.0f;
-    const auto weigh = [&](int p, float l) {
-      const float f = l == neg_inf() ? 0.0f : exp2_approx(l - mx);
+    const auto weigh = [&](int p, float m_p) {
+      const float f = weight[r][p] * (m_p == neg_inf() ? 0.0f : exp2_approx(m_p - mx));   // (a NaN sum stays)
       weight[r][p] = f;
       sum += f;
     };
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (lane + 32 * k < parts) weigh(lane + 32 * k, ls[k]);
-    for (int p = lane + 128; p < parts; p += 32) weigh(p, __ldcg(a.part_lse + place(p, r)));
+    for (int k = 0; k < 3; ++k)
+      if (lane + 32 * k < parts) weigh(lane + 32 * k, m[k]);
+    for (int p = lane + 96; p < parts; p += 32) weigh(p, __ldcg(a.part_ml + place(p, r)).x);
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);  // (NaN stays)
     __syncwarp();
     for (int p = lane; p < parts; p += 32) weight[r][p] *= inv;
-    if (lane == 0) row_lse[r] = sum == 0.0f ? neg_inf() : (mx + log2f(sum)) * 0.69314718055994530942f;
+    if (lane == 0) row_lse[r] = natural_lse(mx, sum);
   }
   __syncthreads();
   for (int i0 = 0; i0 < items; i0 += kJoinThreads) {

@@ -385,15 +385,14 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
         const float4 u = *reinterpret_cast<const float4 *>(mb + r8 * C::MPITCH + c4);
         const float4 v = *reinterpret_cast<const float4 *>(mb + (8 + r8) * C::MPITCH + c4);
         const float4 res = make_float4((u.x + v.x) * inv, (u.y + v.y) * inv, (u.z + v.z) * inv, (u.w + v.w) * inv);
-        const float lse2 = l == 0.0f ? neg_inf() : mr + log2f(l);
         if (whole) {
           const int64_t head = out_head(a, w.s.t0 + w.i0, w.h, r);
           store4(a, head * D + c4, res);
-          if (a.lse && c4 == 0) a.lse[head] = lse2 * 0.69314718055994530942f;
+          if (a.lse && c4 == 0) a.lse[head] = natural_lse(mr, l);
         } else {
           const int64_t pr = ((int64_t)blockIdx.x * 2 + w.slot()) * kStepRows + r;
           *reinterpret_cast<float4 *>(a.part_o + pr * D + c4) = res;
-          if (c4 == 0) a.part_lse[pr] = lse2;
+          if (c4 == 0) a.part_ml[pr] = make_float2(mr, l);
         }
       }
       consumer_sync();

@@ -580,10 +580,14 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       const bool whole = w.whole();
       const bool aligned = !whole || a.y_aligned32;
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);      // (NaN stays)
-      const float lse2 = l == 0.0f ? neg_inf() : m * a.scale_log2 + log2f(l);
+      const float m2 = m * a.scale_log2;
       // (parts of a cut unit: the rows of its tiles one after the other)
       const int64_t head = out_head(a, w.s.t0 + i0, w.h, row);
       const int64_t pr = ((int64_t)blockIdx.x * 2 + w.slot()) * C::ROWS + t * a.tile_tok * a.G + row;
+      if (row < rows) {
+        if (!whole) a.part_ml[pr] = make_float2(m2, l);
+        else if (a.lse) a.lse[head] = natural_lse(m2, l);
+      }
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         float v[32];
@@ -616,10 +620,6 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
             }
           }
         }
-      }
-      if (row < rows) {
-        if (!whole) a.part_lse[pr] = lse2;
-        else if (a.lse) a.lse[head] = lse2 * 0.69314718055994530942f;
       }
       tc::tc_fence_before();
       if (tid == 0 && !whole && w.slot() == 1) a.cuts[blockIdx.x] = w.cut(share_mem);
