@@ -548,7 +548,9 @@ int exl3_qkv_append(const void *q, int64_t q_stride, const void *k, int64_t k_st
  *   workspace of exl3_paged_attention_workspace_size(T, heads_q, heads_kv,
  *   head_dim, batch) bytes; 0 for an unsupported shape.
  *   Products of fp16 values are accumulated in fp32; the weights exp(s - max)
- *   are rounded to fp16 before they multiply v.  What lies in the cache
+ *   are rounded to fp16 before they multiply v: 11 bits down to 2^-29 (few new
+ *   rows) or 2^-21 (many) of the largest, steps of 2^-39 or 2^-31 of it below.
+ *   Their sums and lse take them unrounded.  What lies in the cache
  *   outside the indexes the call's rows see is ignored, NaN and infinities
  *   included.  Values v_j seen by some rows of a sequence have to be finite:
  *   a non-finite one may also reach rows of that sequence that do not see it.

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import trellis_quantized_gb300 as tq
-from attention_ref import U16
+from attention_ref import U16, U32
 from test_gpu_attention import _run, _setup
 
 pytestmark = pytest.mark.gpu
@@ -89,3 +89,45 @@ def test_ties_at_scores_of_any_size(size, Hq, Hkv, D, new, old):
     y, lse, mean, terms, keys, want_lse = _sign_scores(new, old, Hq, Hkv, D, size)
     assert (keys > 1).any()
     _compare_means(y, lse, mean, terms, want_lse, keys >= 1)
+
+
+@pytest.mark.parametrize("D,G,new,B,smallest", [
+    (128, 4, 1, 700, 2.0 ** -40), (64, 7, 2, 900, 2.0 ** -40), (256, 8, 1, 300, 2.0 ** -40),
+    (128, 4, 8, 300, 2.0 ** -32), (64, 40, 7, 150, 2.0 ** -32), (256, 8, 5, 300, 2.0 ** -32)])
+def test_a_key_that_outweighs_a_long_history(D, G, new, B, smallest):
+    """A first key at weight 1 whose value is zero, 131,072 others at 2^-24 to
+    2^-25.5 of it: all of y is their share.  B sequences read the same pages, so
+    that most units stay whole.  Scores are single products, exact in fp32; the
+    bound has the terms of attention_ref without the dot product's, and takes
+    the smallest weight that is held (2^-25 fp16 steps below the largest,
+    which lies at 2^15 in the step kernel and at 2^7 or more in the other)."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(D + G + new)
+    page, L = 256, 131072 + 256
+    rand = lambda *shape: torch.rand(shape, generator=gen, device="cuda")
+    k = torch.zeros((L, 1, D), dtype=torch.float16, device="cuda")
+    k[:, 0, 0] = -(16.64 + 1.03 * rand(L)).half()
+    k[0, 0, 0] = 0
+    v = (0.5 + rand(L, 1, D)).half()
+    v[0] = 0
+    q = torch.zeros((B * new, G, D), dtype=torch.float16, device="cuda")
+    q[:, :, 0] = (0.97 + 0.03 * rand(B * new, G)).half()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    table = torch.arange(L // page, dtype=torch.int32, device="cuda").repeat(B, 1)
+    batch = tq.paged_batch(i32(range(0, B * new + 1, new)), i32([L] * B), table)
+    cache = tq.kv_cache(k.view(-1, page, 1, D), v.view(-1, page, 1, D))
+    lse = torch.empty((B * new, G), dtype=torch.float32, device="cuda")
+    y = tq.exl3_paged_attention(q, batch, cache, scale=1.0, out_dtype=tq.EXL3_OUT_F32, lse=lse)
+    rows = range(0, B * new, max(1, B * new // 60))
+    for t in rows:
+        n = L - new + t % new + 1
+        s = q[t, :, 0].double()[:, None] * k[:n, 0, 0].double()[None]
+        p = torch.exp(s)
+        l = p.sum(1, keepdim=True)
+        want = p @ v[:n, 0].double() / l
+        ds = 4 * U32 * 17.7 + 2.0 ** -20
+        bound = (2 * ds + U16 + (L / 16 + 64) * U32) * want + L * smallest * 1.5 / l + U32 * want
+        err = (y[t].double() - want).abs()
+        assert (err <= bound).all(), f"row {t}: worst error / bound {(err / bound).max().item():.3f}"
+        want_lse = torch.log(l[:, 0])
+        assert ((lse[t].double() - want_lse).abs() <= 2 * ds + (L / 16 + 64) * U32 + 2.0 ** -22 * want_lse.abs()).all()

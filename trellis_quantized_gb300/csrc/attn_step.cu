@@ -34,6 +34,10 @@ namespace attn {
 
 constexpr int kStepRows = 16, kStepKeys = 64;
 constexpr int kStepCost = 1;            // a unit's start and end, in blocks
+// Weights are 2^kStepTop at the maximum (off again in the sum that leaves the
+// kernel): fp16 then holds those down to 2^-29 of the largest in full and the
+// rest to 2^-40 of it, which counts where one key outweighs a long history.
+constexpr float kStepTop = 15.0f;
 constexpr int kStepThreads = 160;       // four consumer warps and the producer
 
 template <int D>
@@ -307,14 +311,15 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
         float p[2][4];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          p[n][0] = exp2_approx(sc[n][0] - base0);
-          p[n][1] = exp2_approx(sc[n][1] - base0);
-          p[n][2] = two ? exp2_approx(sc[n][2] - base1) : 0.0f;
-          p[n][3] = two ? exp2_approx(sc[n][3] - base1) : 0.0f;
+          // (two steps: at large scores the base itself cannot take the 15)
+          p[n][0] = exp2_approx((sc[n][0] - base0) + kStepTop);
+          p[n][1] = exp2_approx((sc[n][1] - base0) + kStepTop);
+          p[n][2] = two ? exp2_approx((sc[n][2] - base1) + kStepTop) : 0.0f;
+          p[n][3] = two ? exp2_approx((sc[n][3] - base1) + kStepTop) : 0.0f;
         }
         l0 += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
         l1 += (p[0][2] + p[0][3]) + (p[1][2] + p[1][3]);
-        // weights in [0, 1], rounded to fp16 for the second product
+        // weights in [0, 2^15], rounded to fp16 for the second product
         const uint32_t pf[4] = {pack_half2(p[0][0], p[0][1]), pack_half2(p[0][2], p[0][3]),
                                 pack_half2(p[1][0], p[1][1]), pack_half2(p[1][2], p[1][3])};
         // ---- o += p v; keys that no row sees may hold anything: 0 * NaN
@@ -382,6 +387,7 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
         for (int x = 0; x < 4; ++x)
           if (sm_m[x][r] != neg_inf()) l = fmaf(sm_l[x][r], exp2_approx(sm_m[x][r] - mr), l);
         const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);    // (NaN stays)
+        l *= 1.0f / (1 << (int)kStepTop);
         const float4 u = *reinterpret_cast<const float4 *>(mb + r8 * C::MPITCH + c4);
         const float4 v = *reinterpret_cast<const float4 *>(mb + (8 + r8) * C::MPITCH + c4);
         const float4 res = make_float4((u.x + v.x) * inv, (u.y + v.y) * inv, (u.z + v.z) * inv, (u.w + v.w) * inv);

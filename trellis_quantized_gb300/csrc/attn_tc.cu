@@ -1,7 +1,7 @@
 // attn_tc.cu -- attention of chunks of new tokens over a paged cache on the
 // 5th-generation tensor cores.
 //
-//   S = Q K^T,  P = exp2((S - m) scale_log2),  O += P V,  y = O / sum(P)
+//   S = Q K^T,  P = exp2((S - m) scale_log2 + 7),  O += P V,  y = O / sum(P)
 //
 // A unit holds up to 256 rows (D <= 128) or 128 rows (D = 256) of one key
 // head and walks over its keys in blocks of 64: 4 D operations per row and
@@ -35,8 +35,8 @@
 // 2^8 (in the weights; fp16 holds 2^15): then O is read, scaled and written
 // back, which is rare after the first blocks.  Sums, maxima, S and O are
 // fp32; the weights are rounded to fp16 once.  m is taken off before the scale
-// is multiplied on, so that the exponent of the largest key is exactly 0
-// whatever the scores' size: as fma(S, scale_log2, -m scale_log2) it would be
+// is multiplied on, so that the exponent of the largest key is exactly
+// 7 whatever the scores' size: as fma(S, scale_log2, -m scale_log2) it would add
 // the rounding error of the product, which from 2^28 on passes the range of
 // fp16 (that form took 1.3 % less on 8,192 tokens).
 //
@@ -56,6 +56,10 @@ namespace attn {
 constexpr int kTcKeys = 64;
 constexpr int kTcCost = 7;         // a unit's start and end, in blocks
 constexpr float kLazy = 8.0f;      // log2 of the growth that moves the maximum
+// Weights are 2^kTop at the maximum (off again in the sum that leaves the
+// kernel), so 2^15 at most, and fp16 holds those down to 2^-21 of the largest
+// in full and the rest to 2^-32 of it.
+constexpr float kTop = 7.0f;
 
 template <int D>
 struct TcCfg {
@@ -549,11 +553,12 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
           base = m == neg_inf() ? 0.0f : m;
         }
         const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nb2 = make_float2(-base, -base);
+        const float2 top2 = make_float2(kTop, kTop);
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         uint32_t pk[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float2 e = __fmul2_rn(__fadd2_rn(make_float2(s[2 * i], s[2 * i + 1]), nb2), sc2);
+          const float2 e = __ffma2_rn(__fadd2_rn(make_float2(s[2 * i], s[2 * i + 1]), nb2), sc2, top2);
           const float2 p = make_float2(exp2_approx(e.x), exp2_approx(e.y));
           sum[i & 1] = __fadd2_rn(sum[i & 1], p);
           const __half2 h = __floats2half2_rn(p.x, p.y);
@@ -581,6 +586,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       const bool aligned = !whole || a.y_aligned32;
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);      // (NaN stays)
       const float m2 = m * a.scale_log2;
+      l *= 1.0f / (1 << (int)kTop);
       // (parts of a cut unit: the rows of its tiles one after the other)
       const int64_t head = out_head(a, w.s.t0 + i0, w.h, row);
       const int64_t pr = ((int64_t)blockIdx.x * 2 + w.slot()) * C::ROWS + t * a.tile_tok * a.G + row;
