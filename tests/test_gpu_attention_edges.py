@@ -7,7 +7,7 @@ import torch
 
 import trellis_quantized_gb300 as tq
 from attention_ref import U16, U32
-from test_gpu_attention import _run, _setup
+from test_gpu_attention import _compare, _run, _setup
 
 pytestmark = pytest.mark.gpu
 
@@ -131,3 +131,33 @@ def test_a_key_that_outweighs_a_long_history(D, G, new, B, smallest):
         assert (err <= bound).all(), f"row {t}: worst error / bound {(err / bound).max().item():.3f}"
         want_lse = torch.log(l[:, 0])
         assert ((lse[t].double() - want_lse).abs() <= 2 * ds + (L / 16 + 64) * U32 + 2.0 ** -22 * want_lse.abs()).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 8, 128), (16, 2, 256), (24, 8, 64)])
+@pytest.mark.parametrize("new,old", [(1, 20), (1, 900), (2, 300), (60, 200)])
+def test_nan_stays_where_it_is_seen(Hq, Hkv, D, new, old):
+    """A NaN in a query makes its row's y and lse NaN and no other's; so do NaN
+    keys for the rows that see them, whole groups of 16 keys among them."""
+    q, k, v, table, dense, q_start, kv_len = _setup([new], [old], Hq, Hkv, D, 16, "tokens", seed=9)
+    args = (tq.paged_batch(q_start, kv_len, table), tq.kv_cache(k, v))
+    lse = torch.empty((new, Hq), dtype=torch.float32, device="cuda")
+    qn = q.clone()
+    qn[0, 1, 5] = torch.nan
+    y = tq.exl3_paged_attention(qn, *args, lse=lse)
+    assert torch.isnan(y[0, 1]).all() and torch.isnan(lse[0, 1])
+    y0 = tq.exl3_paged_attention(q, *args)
+    y[0, 1] = y0[0, 1]
+    _compare(y, None, q, dense, [new], [old], True, 0, D ** -0.5)
+    assert torch.isnan(lse).sum() == 1
+    for first, count in ((old, 1), (0, 16)):           # the first new key; a whole page of keys
+        p = torch.arange(first, first + count, device="cuda")
+        kn = k.clone()
+        kn[table[0].long()[p // 16], p % 16] = torch.nan
+        y = tq.exl3_paged_attention(q, args[0], tq.kv_cache(kn, v), lse=lse)
+        assert torch.isnan(y).all() and torch.isnan(lse).all()
+        if new > 1:                                    # a key that only the last row sees
+            kn = k.clone()
+            kn[table[0, (old + new - 1) // 16], (old + new - 1) % 16] = torch.nan
+            y = tq.exl3_paged_attention(q, args[0], tq.kv_cache(kn, v), lse=lse)
+            assert torch.isnan(y[-1]).all() and torch.isnan(lse[-1]).all()
+            assert not torch.isnan(y[:-1]).any() and not torch.isnan(lse[:-1]).any()

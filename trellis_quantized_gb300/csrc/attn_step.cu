@@ -384,8 +384,8 @@ __global__ void __launch_bounds__(kStepThreads, StepCfg<D>::CTAS)
         const float mr = fmaxf(fmaxf(sm_m[0][r], sm_m[1][r]), fmaxf(sm_m[2][r], sm_m[3][r]));
         float l = 0.0f;
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (sm_m[x][r] != neg_inf()) l = fmaf(sm_l[x][r], exp2_approx(sm_m[x][r] - mr), l);
+        for (int x = 0; x < 4; ++x)          // (a warp whose scores are all NaN has no maximum, but a sum)
+          l = fmaf(sm_l[x][r], sm_m[x][r] == neg_inf() ? 0.0f : exp2_approx(sm_m[x][r] - mr), l);
         const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);    // (NaN stays)
         l *= 1.0f / (1 << (int)kStepTop);
         const float4 u = *reinterpret_cast<const float4 *>(mb + r8 * C::MPITCH + c4);
