@@ -500,6 +500,15 @@ def exl3_noalloc_device_error(stream=None) -> int:
 
 # ------------------------------------------------------------------ attention
 
+_FP16_BITS = (torch.float16, torch.int16, torch.uint16)      # fp16 values, or their bits in integers
+
+
+def _check_fp16(t, name: str):
+    """bfloat16 is as wide as fp16 and would be read as other numbers."""
+    if isinstance(t, torch.Tensor) and t.dtype not in _FP16_BITS:
+        raise TypeError(f"{name} must be torch.float16 (or its bits in a 16-bit integer type), got {t.dtype}")
+
+
 def exl3_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = EXL3_ROPE_NONE, factor: float = 1.0,
                           original_len: int = 4096, low: float = 1.0, high: float = 32.0):
     """Rotary frequencies of a model, (inv_freq [rotary_dim / 2] fp32 host tensor, magnitude)."""
@@ -516,6 +525,8 @@ def head_transform(q_norm=None, k_norm=None, eps: float = 1e-6, inv_freq=None, l
     positions (inv_freq fp32 [rotary_dim / 2] or None); the tensors are kept alive with it."""
     if inv_freq is not None and inv_freq.dtype != torch.float32:
         raise TypeError(f"inv_freq must be torch.float32, got {inv_freq.dtype}")
+    _check_fp16(q_norm, "q_norm")
+    _check_fp16(k_norm, "k_norm")
     p = lambda t, name, size: None if t is None else _ptr(t, name, size).value
     d = HeadTransform(p(q_norm, "q_norm", 2), p(k_norm, "k_norm", 2), eps, p(inv_freq, "inv_freq", 4),
                       0 if inv_freq is None else 2 * inv_freq.numel(), layout, magnitude)
@@ -529,10 +540,9 @@ def kv_cache(k, v) -> KvCache:
     fp16: any strides with dense head elements, the same for both (head-major pages and one
     allocation for both are transposed or sliced views); the tensors are kept alive with it."""
     for t, name in ((k, "k"), (v, "v")):
+        _check_fp16(t, name)
         if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
             raise ValueError(f"{name} must be a CUDA tensor [pages, page_size, heads_kv, head_dim]")
-        if t.element_size() != 2:
-            raise TypeError(f"{name} must have 2-byte elements, got {t.dtype}")
         if t.stride(3) != 1:
             raise ValueError(f"{name}'s head elements must be dense")
     if k.shape != v.shape or k.stride() != v.stride():
