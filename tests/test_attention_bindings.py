@@ -26,3 +26,17 @@ def test_cache_of_two_types_is_refused():
         tq.head_transform(q_norm=torch.ones(128, dtype=torch.bfloat16, device="cuda"))
     tq.kv_cache(k.view(torch.int16), k.view(torch.int16))
     tq.head_transform(q_norm=torch.ones(128, dtype=torch.float16, device="cuda").view(torch.int16))
+
+
+def test_workspace_sizes_are_kept_by_device(monkeypatch):
+    """The size of a call's workspace goes by the device's number of SMs."""
+    sms = {0: 152, 1: 76}
+    current = [0]
+    monkeypatch.setattr(tq, "exl3_paged_attention_workspace_size", lambda *shape: sms[current[0]] * 1024)
+    tq._attention_workspace.cache_clear()
+    try:
+        for device in (0, 1, 0, 1):
+            current[0] = device
+            assert tq._attention_workspace(device, 1, 40, 8, 128, 1) == sms[device] * 1024
+    finally:
+        tq._attention_workspace.cache_clear()

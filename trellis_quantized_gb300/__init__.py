@@ -691,7 +691,10 @@ def exl3_paged_attention_workspace_size(T: int, heads_q: int, heads_kv: int, hea
     return lib().exl3_paged_attention_workspace_size(T, heads_q, heads_kv, head_dim, batch)
 
 
-_attention_workspace = functools.lru_cache(maxsize=4096)(exl3_paged_attention_workspace_size)
+@functools.lru_cache(maxsize=4096)
+def _attention_workspace(device: int, T: int, heads_q: int, heads_kv: int, head_dim: int, batch: int) -> int:
+    """The size depends on the current device's number of SMs too: `device` is its index."""
+    return exl3_paged_attention_workspace_size(T, heads_q, heads_kv, head_dim, batch)
 
 
 def exl3_paged_attention(q, batch: PagedBatch, cache: KvCache, scale: float | None = None, causal: bool = True,
@@ -711,8 +714,8 @@ def exl3_paged_attention(q, batch: PagedBatch, cache: KvCache, scale: float | No
     lp = None if lse is None else _out(lse, "lse", (T, Hq), torch.float32)
     if T:
         raw = _raw_stream(stream)
-        wp, wn = _workspace_arg(workspace_buf, _attention_workspace(T, Hq, cache.heads_kv, D, batch.batch), q.device,
-                                stream, raw)
+        need = _attention_workspace(torch.cuda.current_device(), T, Hq, cache.heads_kv, D, batch.batch)
+        wp, wn = _workspace_arg(workspace_buf, need, q.device, stream, raw)
         _check(lib().exl3_paged_attention(qp, qs, T, Hq, ctypes.byref(batch), ctypes.byref(cache),
                                           D ** -0.5 if scale is None else scale, 1 if causal else 0, window, yp,
                                           out_dtype, lp, wp, wn, raw))
