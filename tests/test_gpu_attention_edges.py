@@ -161,3 +161,15 @@ def test_nan_stays_where_it_is_seen(Hq, Hkv, D, new, old):
             y = tq.exl3_paged_attention(q, args[0], tq.kv_cache(kn, v), lse=lse)
             assert torch.isnan(y[-1]).all() and torch.isnan(lse[-1]).all()
             assert not torch.isnan(y[:-1]).any() and not torch.isnan(lse[:-1]).any()
+
+
+@pytest.mark.parametrize("B,at", [(30, 0), (30, 29), (64, 63), (150, 70)])
+@pytest.mark.parametrize("Hq,Hkv,D,chunk,behind", [(40, 8, 128, 141, 900), (8, 8, 128, 400, 300), (16, 2, 256, 60, 2000),
+                                                   (24, 8, 64, 333, 0)])
+def test_one_chunk_among_many_steps(B, at, Hq, Hkv, D, chunk, behind):
+    """One-token sequences before, around and behind a chunk of many units, with few
+    enough rows in all for the step kernel (where they are too many, on the tensor cores):
+    the chunk's units are counted, found and shared out."""
+    new, old = [1] * B, [(i * 29) % 150 for i in range(B)]
+    new[at], old[at] = chunk, behind
+    _run(new, old, Hq, Hkv, D)
