@@ -557,7 +557,10 @@ int exl3_qkv_append(const void *q, int64_t q_stride, const void *k, int64_t k_st
  *   A page outside [0, num_pages) and lengths that contradict one another
  *   (kv_len below the number of new tokens or past the page table, q_start
  *   outside 0 .. T or decreasing) are recorded in the device error word; such
- *   a page reads as zeros and such lengths are clamped.
+ *   a page reads as zeros and such lengths are clamped.  (The bit is the one
+ *   that a bounded wait sets when it runs out, as in the other calls.)
+ *   The kernel is chosen by the rows per sequence on average: many one-token
+ *   sequences and a long chunk are faster as two calls.
  *   The split of a sequence over the GPU depends on the call's other
  *   sequences, so bits may differ between batches (exl3_set_row_invariant
  *   does not apply).  The same call gives the same bits every time.

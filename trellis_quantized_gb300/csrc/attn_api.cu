@@ -120,7 +120,11 @@ int cache_map(CUtensorMap *m, const exl3_kv_cache *c, const void *base, int box,
 }
 
 // Few rows per sequence and key head take the step kernel (16 rows a unit),
-// more the tensor-core kernel (128 rows a tile).
+// more the tensor-core kernel (128 rows a tile): 64 sequences of 4 tokens (20
+// rows) behind 4,000 at 40/8 heads of 128 take 188 us there and 331 us in units
+// of 16, 3 tokens (15 rows) 181 us.  The host knows the average only: one chunk
+// among many steps runs in units of 16 as well (63 steps and 141 tokens behind
+// 30,000: 592 us, as two calls 118 and 89).
 bool few_rows(int T, int G, int batch) {
   return G <= exl3_attn_step_rows() && (int64_t)T * G <= (int64_t)exl3_attn_step_rows() * batch;
 }

@@ -12,11 +12,12 @@
 // row works out the parts' weights, then the block adds: a thread holds
 // four neighbouring elements of a row, and where the rows do not fill the
 // block several groups of threads share the parts (a single user's long
-// sequence is cut into up to 76 parts per key head) and are added at the end
-// in their order.  Bound by the latency of dependent reads of L2, where the
-// parts were just written: the record, then maxima and sums together with the first
-// eight parts of every thread (8 users x 5 tokens at 256-wide heads: the call
-// takes 37.4 us; 39.9 with 8 rows to a block and the parts read after them).
+// sequence is cut into one per CTA of its key head, up to the whole grid) and
+// are added at the end in their order.  After steps bound by the latency of
+// dependent reads of L2, where the parts were just written: the record, then
+// maxima and sums together with the first eight parts of every thread (8 users
+// x 5 tokens at 256-wide heads: the call takes 37.4 us; 39.9 with 8 rows to a
+// block and the parts read after them).
 //
 // Joining inside the attention kernel, by the CTA that arrived last, cost 115
 // us for eight sequences of up to 20,000 tokens at 256-wide heads against 66

@@ -18,8 +18,8 @@
 // operand registers without leaving the thread.
 //
 // Measured (40 query on 8 key heads of 128): one sequence of 131,001 tokens,
-// 537 MB, 89 us with the join, 83 without; 64 sequences of up to 8,000 tokens,
-// 875 MB, 145 us and 135.  Two CTAs on an SM with three stages each have 192 KB
+// 537 MB, 87 to 89 us with the join, 83 without; 64 sequences of up to 8,000
+// tokens, 875 MB, 143 to 148 us and 135.  Two CTAs on an SM with three stages each have 192 KB
 // of loads in flight; what is left to the memory's rate is the start (lengths,
 // pages, the first bytes) and the end of the longest part.
 #include <cudaTypedefs.h>

@@ -14,7 +14,8 @@
 // anywhere) into O, which stays in TMEM for the whole unit.  With 256-wide
 // heads q is an A operand in TMEM too: its 64 KB of shared memory go to the
 // rings and a score product reads K alone (16 on 2 heads, 2,047 tokens behind
-// 63,000: 1.66 to 1.76 ms with q in shared memory, 1.55 to 1.65 so).
+// 63,000, by graph replay: 1.66 to 1.76 ms with q in shared memory, 1.59 to 1.7
+// so, boards and their temperature differ).
 //
 // Every row tile of 128 has two slots that its blocks take in turn and a
 // softmax warpgroup: the scores of block j + 1 are computed while the weights
@@ -25,7 +26,8 @@
 // against 1.46.)  64-wide score products read 6 KB of shared memory each, 48
 // cycles where the arithmetic takes 32, which caps the pair of products at 80 %
 // of the tensor cores' rate.  At that rate the chip is also held by its power
-// limit: the same launch varies by 4 % between boards.
+// limit when the launch is repeated: 8,192 tokens take 529 us after a rest and
+// 565 us at the 1942 MHz that are left after seconds.
 //
 // Each MMA warp spends about as long on barriers, descriptors and commits as
 // its products take, so score products have two warps (a tile or a slot each)
@@ -34,7 +36,8 @@
 // The running maximum m moves only when it has grown by more than a factor of
 // 2^8 (in the weights; fp16 holds 2^15): then O is read, scaled and written
 // back, which is rare after the first blocks.  Sums, maxima, S and O are
-// fp32; the weights are rounded to fp16 once.  m is taken off before the scale
+// fp32; the weights are rounded to fp16 once, the type of V, which the second
+// product's operands have to share.  m is taken off before the scale
 // is multiplied on, so that the exponent of the largest key is exactly
 // 7 whatever the scores' size: as fma(S, scale_log2, -m scale_log2) it would add
 // the rounding error of the product, which from 2^28 on passes the range of
@@ -342,7 +345,9 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   }
 
   // (This branch first: with the softmax ahead of it in the code, the prompt of
-  // 8,192 tokens takes 596 us instead of 522.)
+  // 8,192 tokens took 596 us instead of 522.  Why is not known; the 64- and
+  // 128-wide kernels spill 336 bytes, all on account of the softmax loop, and
+  // are as sensitive to branches in it that are never taken.)
   if (warp >= C::SM_WARPS) {
     set_registers<C::REGS_IO>(false);
     if (warp == C::SM_WARPS || warp == C::SM_WARPS + 1) {

@@ -8,7 +8,7 @@
 // written once, 2 to 4 bytes either way against about seven operations an
 // element.  Nothing is shared between warps: no block-wide barrier, and 20
 // warps per SM with up to four loads in flight each cover the memory's latency
-// (9,310 tokens at 40/8 heads of 128, 267 MB: 53.9 us, 4.95 TB/s; what the
+// (9,310 tokens at 40/8 heads of 128, 267 MB: 54.4 us, 4.9 TB/s; what the
 // warps wait for is still mostly loads).  All warps take equal runs of the
 // tokens' passes, cutting tokens where they have to: whole tokens left most
 // warps without one in the last round (59.1 us).  A
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) head_transform_kernel(const A
         }
       }
     };
-    // Passes pa .. pb - 1 of one kind, two loads ahead of the arithmetic.
+    // Passes pa .. pb - 1 of one kind, kAhead loads ahead of the arithmetic.
     const auto walk = [&](int pa, int pb, int live, const char *src, Raw8<F32IN> raw, char *dst, int64_t step,
                           bool f32out, bool norm, bool zero, bool write) {
       const int end = min(pb, live);
