@@ -570,6 +570,142 @@ int exl3_paged_attention(const uint16_t *q, int64_t q_stride, int T, int heads_q
                          const exl3_kv_cache *cache, float scale, int causal, int window, void *y, int out_dtype,
                          float *lse, void *workspace, size_t ws_bytes, exl3_stream_t stream);
 
+/*
+ * Routing to experts (no counterpart on the source pages beyond the ids and
+ * weights that the routed experts take; an addition of this library): the
+ * router's product and the choice of experts, whose outputs are
+ * exl3_moe_grouped's topk_ids and topk_weights.
+ */
+
+/* A router: one row of weights per expert. */
+typedef struct {
+  const uint16_t *w;         /* [E][k] fp16, or [2][E][k] from exl3_router_pack */
+  const float *w_scale;      /* [E] from exl3_router_pack, or NULL: w is plain fp16 */
+  const float *bias;         /* [E] fp32 added to the logits, or NULL */
+  int E, k;                  /* 1 <= E <= 1024; k a multiple of 8 */
+} exl3_router;
+
+/*
+ * exl3_router_pack -- fp32 router weights as the two fp16 parts that
+ * exl3_router_logits multiplies with (once, at set-up):
+ *   w = scale (hi + 2^-11 lo), scale a power of two per expert that brings the
+ *   row's largest value into [2^14, 2^15).  The parts hold 22 bits of every
+ *   weight down to 2^-28 of its row's largest, and steps of 2^-49 of that below.
+ *   w [E][k] fp32 (16-byte aligned); packed [2][E][k] fp16; scale [E] fp32.
+ *   A row with an infinity or NaN gives NaN logits.
+ */
+int exl3_router_pack(const float *w, int E, int k, uint16_t *packed, float *scale, exl3_stream_t stream);
+
+/*
+ * exl3_router_logits -- logits[t][e] = x[t] . w[e] (+ bias[e])
+ *   x        [T][k] fp16, rows x_stride elements apart (a multiple of 8, >= k)
+ *   logits   dense [T][E] fp32; sums in fp32, nothing rounded before them
+ *   T        0 (enqueues nothing) .. 2^22
+ *   workspace of exl3_router_logits_workspace_size() bytes (its error word:
+ *   a bounded wait that ran out; the logits are then incomplete).
+ *   Up to 8 rows run on CUDA cores, more on the tensor cores; the split of k
+ *   depends on T, so a row's bits may differ between calls of different T.
+ *   The same call gives the same bits every time.
+ */
+size_t exl3_router_logits_workspace_size(void);
+int exl3_router_logits(const uint16_t *x, int64_t x_stride, int T, const exl3_router *router, float *logits,
+                       void *workspace, size_t ws_bytes, exl3_stream_t stream);
+
+typedef enum { EXL3_SCORE_SOFTMAX = 0, EXL3_SCORE_SIGMOID = 1 } exl3_route_score;
+typedef enum { EXL3_GROUP_MAX = 0, EXL3_GROUP_TOP2 = 1 } exl3_group_score;
+
+/* How experts are chosen. */
+typedef struct {
+  int score;                 /* exl3_route_score */
+  const float *bias;         /* [E] fp32 added to the scores for the choice only, or NULL */
+  int groups;                /* 1..32 groups of E / groups consecutive experts */
+  int groups_kept;           /* 1..groups; equal to groups: no choice of groups */
+  int group_score;           /* exl3_group_score: a group's largest c, or the sum of its two largest */
+  int topk;                  /* 1..32, at most groups_kept * (E / groups) */
+  int renormalise;           /* 1: weights divided by their sum */
+  float scale;               /* factor on the weights, finite */
+} exl3_route_rule;
+
+/*
+ * exl3_route -- experts and weights of each token from its logits:
+ *   s = softmax(l) over the E experts, or 1 / (1 + exp(-l));  c = s + bias
+ *   the groups_kept groups of largest group score; among their experts the
+ *   topk largest c, in falling order (equal: lower id, lower group);
+ *   weight = s (the bias is not in it), divided by the sum over the chosen if
+ *   renormalise, times scale.
+ *   logits   [T][E] fp32 or fp16 (in_dtype), rows `stride` ELEMENTS apart
+ *            (>= E), naturally aligned
+ *   ids      dense [T][topk] int32, always distinct and in [0, E)
+ *   weights  dense [T][topk] fp32
+ *   E        1..1024.  T = 0 enqueues nothing.  No workspace.
+ *   The choice is that of exact arithmetic on the given logits and bias: where
+ *   fp32 does not settle an order it is decided in 64 bits.  Weights are fp32.
+ *   A logit of -infinity has score 0; a row of nothing else has weights 0 and
+ *   the lowest ids.  A bias of -infinity bars an expert: it is chosen only when
+ *   nothing else is left, with weight 0.  NaN ranks below everything; weights
+ *   that depend on a NaN (or, under the softmax, on +infinity) are NaN.
+ */
+int exl3_route(const void *logits, int64_t stride, int in_dtype, int T, int E, const exl3_route_rule *rule,
+               int32_t *ids, float *weights, exl3_stream_t stream);
+
+/*
+ * Low-rank adapters of many requests beside one linear (no counterpart on
+ * the source pages; an addition of this library):
+ *   out[t] = y[t] + scale[i] (x[t] A_i^T) B_i^T     for the adapter i of row t
+ * with y the output of any linear above on the same x.
+ */
+
+/* A pool of adapters for one linear (device arrays). */
+typedef struct {
+  const uint16_t *a;         /* [count][max_rank][k] fp16 */
+  const uint16_t *b;         /* [count][n][max_rank] fp16 */
+  const float *scale;        /* [count] fp32 */
+  const int32_t *rank;       /* [count], or NULL: all of max_rank */
+  int count, max_rank;       /* 1..4096; a multiple of 8, 8..128 */
+  int k, n;                  /* multiples of 128 */
+} exl3_adapters;
+
+/*
+ * exl3_adapter_plan -- a step's rows in the order of their adapters, worked
+ * out on the device: once per step, for every linear of every layer.
+ *   q_start  [batch + 1] int32: sequence b is rows q_start[b] ..
+ *            q_start[b + 1] - 1 of a call's T rows (as in exl3_paged_batch;
+ *            sequences may be empty)
+ *   adapter  [batch] int32: its adapter, 0 .. count - 1, or -1 for none
+ *   plan     exl3_adapter_plan_size(T, batch, count) bytes, 256-byte aligned,
+ *            zero filled once before first use (exl3_workspace_clear)
+ *   An adapter outside [-1, count) is recorded in the plan's error word
+ *   (exl3_check_device_error on the plan) and its sequence treated as having
+ *   none.  Starts that decrease or leave 0 .. T are recorded, and nothing is
+ *   planned: calls with that plan write no row.
+ *   T 0..2^22, batch 1..2^20, count 1..4096.
+ */
+size_t exl3_adapter_plan_size(int T, int batch, int count);
+int exl3_adapter_plan(const int32_t *q_start, const int32_t *adapter, int T, int batch, int count, void *plan,
+                      size_t plan_bytes, exl3_stream_t stream);
+
+/*
+ * exl3_adapter_add -- the adapters' contribution added to a linear's output.
+ *   x        [T][k] fp16, y and out [T][n] fp16 or fp32 (dtype), rows x_stride,
+ *            y_stride and out_stride elements apart (multiples of 16 bytes, at
+ *            least k or n).  out may be y itself; otherwise it must overlap
+ *            neither y nor x.  Rows without an adapter are copied (nothing is
+ *            done when out is y); rows that belong to no sequence are left as
+ *            they were.
+ *   plan     filled for the same T, batch and count = adapters->count by a call
+ *            ahead on the stream (one made for others is recorded in its error
+ *            word and no row is written); it is only read (except for that
+ *            word), so several calls may use it at once
+ *   x A^T is summed in fp32 and enters the second product as two fp16 parts (22
+ *   bits); the sum with y is rounded once.  T = 0 enqueues nothing.  What lies in the pool past an
+ *   adapter's rank is not used, but in B it has to be finite up to the next
+ *   multiple of 16.  A row's bits do not depend on the other rows' contents.
+ *   No workspace.
+ */
+int exl3_adapter_add(const uint16_t *x, int64_t x_stride, const void *y, int64_t y_stride, void *out,
+                     int64_t out_stride, int dtype, const exl3_adapters *adapters, void *plan, int T, int batch,
+                     exl3_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

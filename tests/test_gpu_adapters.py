@@ -1,0 +1,283 @@
+"""exl3_adapter_plan and exl3_adapter_add against their definition in 64 bits."""
+import math
+
+import pytest
+import torch
+
+import trellis_quantized_gb300 as tq
+
+pytestmark = pytest.mark.gpu
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _pool(N, R, k, n, ranks=None, seed=0, junk=0.0):
+    """Adapters; past a rank lies `junk` in A and in B from the next multiple of 16 on, 9 before it."""
+    g = _gen(seed)
+    a = (torch.randn((N, R, k), generator=g, device="cuda") / math.sqrt(k)).half()
+    b = (torch.randn((N, n, R), generator=g, device="cuda") / math.sqrt(R)).half()
+    scale = torch.rand(N, generator=g, device="cuda") + 0.5
+    for i, r in enumerate(ranks or []):
+        a[i, r:] = junk
+        b[i, :, r:] = 9.0
+        b[i, :, (r + 15) // 16 * 16:] = junk
+    rank = None if ranks is None else torch.tensor(ranks, dtype=torch.int32, device="cuda")
+    return a, b, scale, rank
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _starts(rows, first=0):
+    out = [first]
+    for r in rows:
+        out.append(out[-1] + r)
+    return out
+
+
+def _reference(x, y, pool, rows, ids, first=0):
+    """out in 64 bits and a bound on what the kernels may be off by, before the output's own rounding.
+
+    h is a sum of k exact products in fp32 (k units of sum |x a|), enters the
+    second product with 22 bits (2^-22 of the row's largest at most), which has
+    2 R terms and as many roundings; one more each for the scale and the sum."""
+    a, b, scale, rank = pool
+    R, k = a.shape[1], a.shape[2]
+    want, tol = y.double().clone(), torch.zeros(y.shape, dtype=torch.float64, device="cuda")
+    t = first
+    for n, i in zip(rows, ids):
+        if i >= 0 and n:
+            r = R if rank is None else int(rank[i])
+            A, B, s = a[i, :r].double(), b[i, :, :r].double(), float(scale[i])
+            xd = x[t:t + n].double()
+            h, size = xd @ A.t(), xd.abs() @ A.abs().t()
+            err = size * (k * 2.0 ** -23) + h.abs().amax(1, keepdim=True) * 2.0 ** -22 if r else size
+            d = s * (h @ B.t())
+            bound = s * ((err + h.abs() * (2 * R + 2) * 2.0 ** -23) @ B.abs().t())
+            want[t:t + n] += d
+            tol[t:t + n] = bound + want[t:t + n].abs() * 2.0 ** -24
+        t += n
+    return want, tol
+
+
+def _check(out, want, tol):
+    assert torch.isfinite(out).all()
+    half_step = torch.finfo(out.dtype).eps / 2 if out.dtype == torch.float16 else 0.0
+    # fp16 below its normal range: half of its smallest step
+    tol = tol + (want.abs() + tol) * half_step + (2.0 ** -25 if out.dtype == torch.float16 else 0.0)
+    off = (out.double() - want).abs() - tol
+    assert (off <= 0).all(), f"{int((off > 0).sum())} off, by up to {float(off.max())}"
+
+
+def _run(rows, ids, N, R, k, n, fp32=False, ranks=None, in_place=False, seed=0, junk=0.0):
+    T = sum(rows)
+    g = _gen(seed + 100)
+    x = torch.randn((T, k), generator=g, device="cuda").half()
+    y = torch.randn((T, n), generator=g, device="cuda").to(torch.float32 if fp32 else torch.float16)
+    pool = _pool(N, R, k, n, ranks, seed, junk)
+    plan = tq.exl3_adapter_plan(_i32(_starts(rows)), _i32(ids), T, N)
+    want, tol = _reference(x, y, pool, rows, ids)
+    out = y if in_place else torch.full_like(y, math.nan)
+    tq.exl3_adapter_add(x, y, tq.adapters(*pool), plan, out=out)
+    assert tq.exl3_check_device_error(plan.data) == 0
+    _check(out, want, tol)
+    return out
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("R", [8, 16, 24, 32, 64, 104, 128])
+@pytest.mark.parametrize("k,n", [(128, 128), (1024, 640), (5120, 512)])
+def test_one_row(R, k, n, fp32):
+    _run([1], [1], 3, R, k, n, fp32)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("rows", [[16], [17], [1, 3, 15, 1], [1] * 40, [5, 0, 30, 1, 1, 2], [128], [129, 1], [100, 300]])
+def test_ragged_sequences(rows, fp32, in_place):
+    ids = [(3 * i + 1) % 5 for i in range(len(rows))]
+    _run(rows, ids, 5, 16, 512, 384, fp32, in_place=in_place)
+
+
+@pytest.mark.parametrize("R", [8, 16, 40, 64, 128])
+@pytest.mark.parametrize("rows", [[600], [200, 333, 1, 1, 1, 90], [127, 128, 129, 255, 257]])
+@pytest.mark.parametrize("fp32", [False, True])
+def test_prompts(rows, R, fp32):
+    _run(rows, [i % 3 for i in range(len(rows))], 3, R, 1024, 1152, fp32)
+
+
+@pytest.mark.parametrize("rows", [[1] * 30, [400, 1, 30, 200]])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_rows_without_an_adapter_keep_y(rows, in_place):
+    ids = [-1 if i % 3 else 2 for i in range(len(rows))]
+    _run(rows, ids, 4, 32, 256, 256, in_place=in_place)
+    _run(rows, [-1] * len(rows), 4, 32, 256, 256, in_place=in_place)
+
+
+@pytest.mark.parametrize("rows", [[1, 1, 2, 1, 1, 1], [300, 1, 5, 140, 200, 131]])
+@pytest.mark.parametrize("R,ranks", [(64, [8, 64, 16, 33, 0, 40]), (128, [128, 1, 64, 65, 100, 16])])
+def test_ranks_and_what_lies_past_them(rows, R, ranks):
+    """NaN past an adapter's rank in A, and in B past the next multiple of 16."""
+    _run(rows, list(range(6)), 6, R, 512, 512, True, ranks, junk=math.nan)
+
+
+@pytest.mark.parametrize("rows", [[1] * 8, [150, 20]])
+def test_rows_outside_the_sequences_are_left_alone(rows):
+    T, k, n = sum(rows) + 12, 256, 256
+    x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
+    y = torch.randn((T, n), generator=_gen(2), device="cuda").half()
+    x[:5], x[-7:] = math.nan, math.nan
+    pool = _pool(2, 16, k, n)
+    ids = [i % 2 for i in range(len(rows))]
+    plan = tq.exl3_adapter_plan(_i32(_starts(rows, 5)), _i32(ids), T, 2)
+    out = torch.full_like(y, 7.0)
+    tq.exl3_adapter_add(x, y, tq.adapters(*pool), plan, out=out)
+    want, tol = _reference(x, y, pool, rows, ids, 5)
+    _check(out[5:-7], want[5:-7], tol[5:-7])
+    assert (out[:5] == 7).all() and (out[-7:] == 7).all()
+
+
+@pytest.mark.parametrize("rows", [[2, 1], [180, 70]])
+def test_strided_rows(rows):
+    T, k, n = sum(rows), 256, 384
+    wx = torch.full((T, k + 64), math.nan, dtype=torch.float16, device="cuda")
+    wy = torch.full((T, 2 * n), math.nan, dtype=torch.float32, device="cuda")
+    wo = torch.full((T, n + 32), 7.0, dtype=torch.float32, device="cuda")
+    x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
+    y = torch.randn((T, n), generator=_gen(2), device="cuda")
+    wx[:, 64:], wy[:, n:] = x, y
+    pool = _pool(2, 24, k, n)
+    plan = tq.exl3_adapter_plan(_i32(_starts(rows)), _i32([1, 0]), T, 2)
+    tq.exl3_adapter_add(wx[:, 64:], wy[:, n:], tq.adapters(*pool), plan, out=wo[:, 16:n + 16])
+    _check(wo[:, 16:n + 16].contiguous(), *_reference(x, y, pool, rows, [1, 0]))
+    assert (wo[:, :16] == 7).all() and (wo[:, n + 16:] == 7).all()
+
+
+@pytest.mark.parametrize("size", [1e-6, 300.0])
+@pytest.mark.parametrize("rows", [[3, 2], [200, 60]])
+def test_h_outside_fp16(rows, size):
+    """x A^T of 1e-9 or of 1e6: its two parts are scaled by a power of two per row."""
+    T, k, n = sum(rows), 512, 256
+    x = (torch.randn((T, k), generator=_gen(1), device="cuda") * size).half()
+    y = torch.zeros((T, n), device="cuda")
+    a, b, scale, rank = _pool(2, 16, k, n)
+    a = (a.float() * (300.0 if size > 1 else 0.01)).half()
+    pool = (a, b, scale, rank)
+    plan = tq.exl3_adapter_plan(_i32(_starts(rows)), _i32([0, 1]), T, 2)
+    tq.exl3_adapter_add(x, y, tq.adapters(*pool), plan)
+    _check(y, *_reference(x, torch.zeros_like(y), pool, rows, [0, 1]))
+
+
+def test_a_row_does_not_depend_on_the_others():
+    """Infinities and NaN in one row of a tile stay there."""
+    for rows in ([9], [140]):
+        T = rows[0]
+        x = torch.randn((T, 256), generator=_gen(1), device="cuda").half()
+        y = torch.randn((T, 256), generator=_gen(2), device="cuda")
+        pool = tq.adapters(*_pool(1, 16, 256, 256))
+        plan = tq.exl3_adapter_plan(_i32([0, T]), _i32([0]), T, 1)
+        clean = tq.exl3_adapter_add(x, y, pool, plan, out=torch.empty_like(y))
+        x[3], x[5, 7] = math.nan, math.inf
+        got = tq.exl3_adapter_add(x, y, pool, plan, out=torch.empty_like(y))
+        keep = [t for t in range(T) if t not in (3, 5)]
+        assert torch.equal(got[keep], clean[keep]) and got[3].isnan().all()
+
+
+def test_bad_adapters_and_starts_are_recorded():
+    T, k, n = 6, 128, 128
+    x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
+    y = torch.randn((T, n), generator=_gen(2), device="cuda")
+    pool = _pool(2, 8, k, n)
+    for ids in ([0, 2, 1], [0, -2, 1]):                    # treated as none
+        plan = tq.exl3_adapter_plan(_i32([0, 2, 4, 6]), _i32(ids), T, 2)
+        out = tq.exl3_adapter_add(x, y, tq.adapters(*pool), plan, out=torch.zeros_like(y))
+        assert tq.exl3_check_device_error(plan.data) != 0
+        assert tq.exl3_check_device_error(plan.data) == 0
+        _check(out, *_reference(x, y, pool, [2, 2, 2], [0, -1, 1]))
+    for starts in ([0, 4, 2, 6], [-1, 2, 4, 6], [0, 2, 4, 7]):
+        plan = tq.exl3_adapter_plan(_i32(starts), _i32([0, 1, 1]), T, 2, plan=plan)
+        assert tq.exl3_check_device_error(plan.data) != 0
+        out = tq.exl3_adapter_add(x, y, tq.adapters(*pool), plan, out=torch.full_like(y, 7.0))
+        assert (out == 7).all()
+    # a plan that was never filled
+    empty = tq.AdapterPlan(T, 3, 2, x.device)
+    out = tq.exl3_adapter_add(x, y, tq.adapters(*pool), empty, out=torch.full_like(y, 7.0))
+    assert (out == 7).all() and tq.exl3_check_device_error(empty.data) != 0
+
+
+def test_many_adapters_and_sequences():
+    """Every row its own adapter out of 3000, and 3000 sequences of one."""
+    rows = [1] * 3000
+    _run(rows, [(7 * i) % 3000 for i in range(3000)], 3000, 8, 128, 128)
+    _run(rows, [1] * 3000, 2, 8, 128, 128)
+
+
+def test_plan_is_refilled_in_a_graph():
+    """One captured graph (plan and two linears' adapters) follows changed starts and adapters."""
+    T, k, n, N = 40, 256, 384, 4
+    x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
+    y = torch.randn((T, n), generator=_gen(2), device="cuda").half()
+    out, out2 = torch.empty_like(y), torch.empty_like(y)
+    pool, pool2 = _pool(N, 16, k, n), _pool(N, 64, k, n, seed=3)
+    ad, ad2 = tq.adapters(*pool), tq.adapters(*pool2)
+    q, ids = _i32([0, 10, 20, 40]), _i32([0, 1, 2])
+    plan = tq.exl3_adapter_plan(q, ids, T, N)
+
+    def step():
+        tq.exl3_adapter_plan(q, ids, T, N, plan=plan)
+        tq.exl3_adapter_add(x, y, ad, plan, out=out)
+        tq.exl3_adapter_add(x, y, ad2, plan, out=out2)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for rows, which in (([10, 10, 20], [0, 1, 2]), ([1, 38, 1], [3, 3, -1]), ([40, 0, 0], [2, 2, 1])):
+        q.copy_(_i32(_starts(rows)))
+        ids.copy_(_i32(which))
+        g.replay()
+        torch.cuda.synchronize()
+        _check(out, *_reference(x, y, pool, rows, which))
+        _check(out2, *_reference(x, y, pool2, rows, which))
+
+
+def test_one_plan_on_two_streams():
+    T, k, n, N = 24, 512, 1024, 3
+    x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
+    y = torch.randn((T, n), generator=_gen(2), device="cuda").half()
+    pools = [_pool(N, 16, k, n, seed=s) for s in (0, 1)]
+    ads = [tq.adapters(*p) for p in pools]
+    plan = tq.exl3_adapter_plan(_i32([0, 7, 24]), _i32([2, 0]), T, N)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ads]
+    outs = [torch.empty_like(y) for _ in ads]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for a, s, o in zip(ads, streams, outs):
+            with torch.cuda.stream(s):
+                tq.exl3_adapter_add(x, y, a, plan, out=o)
+    torch.cuda.synchronize()
+    for p, o in zip(pools, outs):
+        _check(o, *_reference(x, y, p, [7, 17], [2, 0]))
+
+
+def test_bindings_refuse_mismatches():
+    x, y = torch.zeros((4, 128), dtype=torch.float16, device="cuda"), torch.zeros((4, 256), device="cuda")
+    pool = tq.adapters(*_pool(2, 8, 128, 256))
+    plan = tq.exl3_adapter_plan(_i32([0, 4]), _i32([0]), 4, 2)
+    with pytest.raises(ValueError, match="rows"):
+        tq.exl3_adapter_add(x[:3], y, pool, plan)
+    with pytest.raises(ValueError, match="adapters"):
+        tq.exl3_adapter_add(x, y, tq.adapters(*_pool(3, 8, 128, 256)), plan)
+    with pytest.raises(TypeError, match="x must be"):
+        tq.exl3_adapter_add(x.float(), y, pool, plan)
+    with pytest.raises(TypeError, match="out must be"):
+        tq.exl3_adapter_add(x, y, pool, plan, out=y.half())
+    with pytest.raises(ValueError, match="plan was made"):
+        tq.exl3_adapter_plan(_i32([0, 4]), _i32([0]), 5, 2, plan=plan)

@@ -44,6 +44,11 @@ EXL3_ROPE_NTK = 2
 EXL3_ROPE_BANDS = 3
 EXL3_ROPE_YARN = 4
 
+EXL3_SCORE_SOFTMAX = 0
+EXL3_SCORE_SIGMOID = 1
+EXL3_GROUP_MAX = 0
+EXL3_GROUP_TOP2 = 1
+
 _lock = threading.Lock()
 _lib = None
 
@@ -81,6 +86,25 @@ class PagedBatch(ctypes.Structure):
     """exl3_paged_batch: the sequences of a call (device arrays)."""
     _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
                 ("batch", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
+class Router(ctypes.Structure):
+    """exl3_router: a row of weights per expert (device pointers)."""
+    _fields_ = [("w", ctypes.c_void_p), ("w_scale", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("E", ctypes.c_int),
+                ("k", ctypes.c_int)]
+
+
+class RouteRule(ctypes.Structure):
+    """exl3_route_rule: how experts are chosen from logits."""
+    _fields_ = [("score", ctypes.c_int), ("bias", ctypes.c_void_p), ("groups", ctypes.c_int),
+                ("groups_kept", ctypes.c_int), ("group_score", ctypes.c_int), ("topk", ctypes.c_int),
+                ("renormalise", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class Adapters(ctypes.Structure):
+    """exl3_adapters: a pool of low-rank adapters for one linear (device pointers)."""
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rank", ctypes.c_void_p),
+                ("count", ctypes.c_int), ("max_rank", ctypes.c_int), ("k", ctypes.c_int), ("n", ctypes.c_int)]
 
 
 class Exl3Error(RuntimeError):
@@ -146,6 +170,15 @@ def lib():
         L.exl3_paged_attention_workspace_size.argtypes = [I, I, I, I, I]
         L.exl3_paged_attention_workspace_size.restype = Z
         L.exl3_paged_attention.argtypes = [P, L64, I, I, P, P, ctypes.c_float, I, I, P, I, P, P, Z, P]
+        L.exl3_router_pack.argtypes = [P, I, I, P, P, P]
+        L.exl3_router_logits_workspace_size.argtypes = []
+        L.exl3_router_logits_workspace_size.restype = Z
+        L.exl3_router_logits.argtypes = [P, L64, I, P, P, P, Z, P]
+        L.exl3_route.argtypes = [P, L64, I, I, I, P, P, P, P]
+        L.exl3_adapter_plan_size.argtypes = [I, I, I]
+        L.exl3_adapter_plan_size.restype = Z
+        L.exl3_adapter_plan.argtypes = [P, P, I, I, I, P, Z, P]
+        L.exl3_adapter_add.argtypes = [P, L64, P, L64, P, L64, I, P, P, I, I, P]
         _lib = L
         return L
 
@@ -720,3 +753,210 @@ def exl3_paged_attention(q, batch: PagedBatch, cache: KvCache, scale: float | No
                                           D ** -0.5 if scale is None else scale, 1 if causal else 0, window, yp,
                                           out_dtype, lp, wp, wn, raw))
     return y
+
+
+# -------------------------------------------------------- routing to experts
+
+def _on_current(t, name: str):
+    """Kernels go to the current device's stream: a tensor of another device is refused."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _matrix(t, name: str, width: int, dtypes):
+    """Address and row stride of [rows, width] with dense rows."""
+    _on_current(t, name)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    shape, s = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != width:
+        raise ValueError(f"{name} must be [rows, {width}], got {tuple(shape)}")
+    if s[1] != 1 and width > 1:
+        raise ValueError(f"{name}'s rows must be dense")
+    return t.data_ptr(), (s[0] if shape[0] > 1 else width)
+
+
+def _vector(t, name: str, size: int, dtype):
+    """Address of a dense [size] tensor, or None."""
+    if t is None:
+        return None
+    _on_current(t, name)
+    if t.dtype != dtype or t.shape != (size,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {size}, got {tuple(t.shape)} {t.dtype}")
+    return t.data_ptr()
+
+
+def router(w, bias=None, stream=None) -> Router:
+    """Descriptor of a router: w [E, k] fp16, used as it is, or fp32, packed once into two fp16
+    parts (exl3_router_pack); bias fp32 [E] or None.  The tensors are kept alive with it."""
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.dtype not in (torch.float16, torch.float32):
+        raise TypeError("w must be a torch.float16 or torch.float32 tensor [E, k]")
+    E, k = w.shape
+    _on_current(w, "w")
+    parts, scale = w, None
+    if w.dtype == torch.float32:
+        parts = torch.empty((2, E, k), dtype=torch.float16, device=w.device)
+        scale = torch.empty(E, dtype=torch.float32, device=w.device)
+        _check(lib().exl3_router_pack(_ptr(w, "w"), E, k, _ptr(parts, "packed"), _ptr(scale, "scale"), _stream(stream)))
+    d = Router(_ptr(parts, "w").value, None if scale is None else scale.data_ptr(), _vector(bias, "bias", E, torch.float32),
+               E, k)
+    d._keep = (parts, scale, bias)
+    return d
+
+
+def exl3_router_pack(w, packed=None, scale=None, stream=None):
+    """fp32 router weights [E, k] as two fp16 parts [2, E, k] and powers of two [E]; returns both."""
+    E, k = w.shape
+    _on_current(w, "w")
+    if w.dtype != torch.float32:
+        raise TypeError(f"w must be torch.float32, got {w.dtype}")
+    if packed is None:
+        packed = torch.empty((2, E, k), dtype=torch.float16, device=w.device)
+    if scale is None:
+        scale = torch.empty(E, dtype=torch.float32, device=w.device)
+    _check(lib().exl3_router_pack(_ptr(w, "w"), E, k, _out(packed, "packed", (2, E, k), torch.float16),
+                                  _vector(scale, "scale", E, torch.float32), _raw_stream(stream)))
+    return packed, scale
+
+
+def exl3_router_logits_workspace_size() -> int:
+    return lib().exl3_router_logits_workspace_size()
+
+
+_logits_workspace = functools.cache(exl3_router_logits_workspace_size)
+
+
+def exl3_router_logits(x, router: Router, logits=None, workspace_buf=None, stream=None) -> torch.Tensor:
+    """logits [T, E] fp32 = x @ w^T (+ bias) for x [T, k] fp16 with dense rows."""
+    xp, xs = _matrix(x, "x", router.k, (torch.float16,))
+    T = x.shape[0]
+    if logits is None:
+        logits = torch.empty((T, router.E), dtype=torch.float32, device=x.device)
+    lp = _out(logits, "logits", (T, router.E), torch.float32)
+    _on_current(logits, "logits")
+    if T:
+        raw = _raw_stream(stream)
+        wp, wn = _workspace_arg(workspace_buf, _logits_workspace(), x.device, stream, raw)
+        _check(lib().exl3_router_logits(xp, xs, T, ctypes.byref(router), lp, wp, wn, raw))
+    return logits
+
+
+def route_rule(topk: int, score: int = EXL3_SCORE_SOFTMAX, bias=None, groups: int = 1, groups_kept: int | None = None,
+               group_score: int = EXL3_GROUP_MAX, renormalise: bool = True, scale: float = 1.0) -> RouteRule:
+    """Descriptor of how experts are chosen: softmax or sigmoid scores, a bias fp32 [E] (or None)
+    added for the choice only, groups of consecutive experts of which groups_kept stay, topk
+    experts, weights divided by their sum and multiplied by scale."""
+    bp = None
+    if bias is not None:
+        if not isinstance(bias, torch.Tensor) or bias.dim() != 1:
+            raise TypeError("bias must be a torch tensor [E]")
+        bp = _vector(bias, "bias", bias.shape[0], torch.float32)
+    d = RouteRule(score, bp, groups, groups if groups_kept is None else groups_kept, group_score, topk,
+                  1 if renormalise else 0, scale)
+    d._keep = (bias,)
+    d._experts = None if bias is None else bias.shape[0]
+    return d
+
+
+def exl3_route(logits, rule: RouteRule, ids=None, weights=None, stream=None):
+    """Experts and weights of each token from logits [T, E] (fp32 or fp16, dense rows): ids int32
+    and weights fp32, [T, topk], as exl3_moe_grouped takes them."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise TypeError("logits must be a torch tensor [T, E]")
+    T, E = logits.shape
+    lp, ls = _matrix(logits, "logits", E, (torch.float32, torch.float16))
+    if rule._experts is not None and rule._experts != E:
+        raise ValueError(f"the rule's bias has {rule._experts} experts, the logits {E}")
+    if ids is None:
+        ids = torch.empty((T, rule.topk), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, rule.topk), dtype=torch.float32, device=logits.device)
+    ip, wp = _out(ids, "ids", (T, rule.topk), torch.int32), _out(weights, "weights", (T, rule.topk), torch.float32)
+    _on_current(ids, "ids")
+    _on_current(weights, "weights")
+    if T:
+        _check(lib().exl3_route(lp, ls, _IO_DTYPES[logits.dtype], T, E, ctypes.byref(rule), ip, wp,
+                                _raw_stream(stream)))
+    return ids, weights
+
+
+# --------------------------------------------------------- low-rank adapters
+
+def adapters(a, b, scale, rank=None) -> Adapters:
+    """Descriptor of a pool of adapters for one linear: a [count, max_rank, k] and b [count, n,
+    max_rank] fp16, scale fp32 [count], rank int32 [count] or None (all of max_rank); the tensors
+    are kept alive with it."""
+    for t, name in ((a, "a"), (b, "b")):
+        _check_fp16(t, name)
+        _on_current(t, name)
+        if t.dim() != 3:
+            raise ValueError(f"{name} must have three dimensions, got {tuple(t.shape)}")
+    N, R, k = a.shape
+    n = b.shape[1]
+    if b.shape != (N, n, R):
+        raise ValueError(f"b must be [{N}, n, {R}] for a {tuple(a.shape)}, got {tuple(b.shape)}")
+    if scale is None:
+        raise TypeError("scale must be a torch tensor")
+    d = Adapters(_ptr(a, "a", 2).value, _ptr(b, "b", 2).value, _vector(scale, "scale", N, torch.float32),
+                 _vector(rank, "rank", N, torch.int32), N, R, k, n)
+    d._keep = (a, b, scale, rank)
+    return d
+
+
+class AdapterPlan:
+    """A step's rows in the order of their adapters (exl3_adapter_plan): the device buffer and what
+    it was made for."""
+    def __init__(self, T: int, batch: int, count: int, device, stream=None):
+        nbytes = exl3_adapter_plan_size(T, batch, count)
+        if nbytes == 0:
+            raise ValueError(f"T = {T}, batch = {batch} or count = {count} out of range")
+        self.T, self.batch, self.count = T, batch, count
+        self.data = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        exl3_workspace_clear(self.data, stream=stream)
+
+
+def exl3_adapter_plan_size(T: int, batch: int, count: int) -> int:
+    return lib().exl3_adapter_plan_size(T, batch, count)
+
+
+def exl3_adapter_plan(q_start, adapter, T: int, count: int, plan: AdapterPlan | None = None, stream=None) -> AdapterPlan:
+    """Plan of a step: sequence b is rows q_start[b] .. q_start[b + 1] - 1 of T and uses adapter[b]
+    of `count` (-1: none); int32 device tensors [B + 1] and [B].  `plan`, made for the same sizes,
+    is filled again."""
+    for t, name in ((q_start, "q_start"), (adapter, "adapter")):
+        _on_current(t, name)
+        if t.dtype != torch.int32 or t.dim() != 1:
+            raise TypeError(f"{name} must be a torch.int32 tensor of one dimension, got {t.dtype} {tuple(t.shape)}")
+    B = adapter.shape[0]
+    if q_start.shape[0] != B + 1:
+        raise ValueError(f"q_start must have {B + 1} elements for {B} adapters, got {q_start.shape[0]}")
+    if plan is None:
+        plan = AdapterPlan(T, B, count, adapter.device, stream)
+    elif (plan.T, plan.batch, plan.count) != (T, B, count):
+        raise ValueError(f"plan was made for T = {plan.T}, batch = {plan.batch}, count = {plan.count}")
+    _check(lib().exl3_adapter_plan(_ptr(q_start, "q_start"), _ptr(adapter, "adapter"), T, B, count,
+                                   plan.data.data_ptr(), plan.data.numel(), _raw_stream(stream)))
+    return plan
+
+
+def exl3_adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out=None, stream=None) -> torch.Tensor:
+    """y + scale (x A^T) B^T for each row's adapter: x [T, k] fp16, y [T, n] fp16 or fp32, dense
+    rows; written to `out`, or to y itself (rows of no sequence are left as they were)."""
+    xp, xs = _matrix(x, "x", adapters.k, (torch.float16,))
+    yp, ys = _matrix(y, "y", adapters.n, (torch.float16, torch.float32))
+    if out is None or out is y:
+        out, op, os_ = y, yp, ys
+    else:
+        op, os_ = _matrix(out, "out", adapters.n, (y.dtype,))
+    T = x.shape[0]
+    if y.shape[0] != T or out.shape[0] != T or plan.T != T:
+        raise ValueError(f"x has {T} rows, y {y.shape[0]}, out {out.shape[0]}, the plan {plan.T}")
+    if plan.count != adapters.count:
+        raise ValueError(f"the plan was made for {plan.count} adapters, the pool has {adapters.count}")
+    _check(lib().exl3_adapter_add(xp, xs, yp, ys, op, os_, _IO_DTYPES[y.dtype], ctypes.byref(adapters),
+                                  plan.data.data_ptr(), T, plan.batch, _raw_stream(stream)))
+    return out

@@ -1,0 +1,117 @@
+// adapter_api.cu -- the C entry points of the low-rank adapters: argument
+// checks and the choice of the kernel.
+#include "adapter.cuh"
+#include "api_util.cuh"
+
+// ---- kernels (other translation units)
+cudaError_t exl3_launch_adapter_plan(const exl3::ad::PlanArgs &p, cudaStream_t s);
+cudaError_t exl3_launch_adapter_step(const exl3::ad::Args &a, bool f32, cudaStream_t s);
+
+namespace {
+
+bool plan_shape_ok(int T, int batch, int count) {
+  return T >= 0 && T <= (1 << 22) && batch >= 1 && batch <= (1 << 20) && count >= 1 && count <= exl3::ad::kMaxCount;
+}
+
+int check_words(const void *p, const char *name, bool required = true) {
+  if (!p) return required ? exl3_fail(EXL3_ERR_ARG, "%s is NULL", name) : EXL3_OK;
+  if (reinterpret_cast<uintptr_t>(p) & 3u) return exl3_fail(EXL3_ERR_ARG, "%s is not 4-byte aligned", name);
+  return EXL3_OK;
+}
+
+int check_stride(const char *name, int64_t stride, int width, int per16) {
+  if (stride < width || stride % per16 || stride >= ((int64_t)1 << 38))
+    return exl3_fail(EXL3_ERR_SHAPE, "%s: stride %lld must be a multiple of 16 bytes, at least %d and below 2^38", name,
+                     (long long)stride, width);
+  return EXL3_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t exl3_adapter_plan_size(int T, int batch, int count) {
+  return plan_shape_ok(T, batch, count) ? exl3::ad::plan_layout(T, batch, count).total : 0;
+}
+
+int exl3_adapter_plan(const int32_t *q_start, const int32_t *adapter, int T, int batch, int count, void *plan,
+                      size_t plan_bytes, exl3_stream_t stream) {
+  exl3_clear_error();
+  if (!plan_shape_ok(T, batch, count))
+    return exl3_fail(EXL3_ERR_SHAPE, "T = %d (0..2^22), batch = %d (1..2^20) or count = %d (1..%d) out of range", T,
+                     batch, count, exl3::ad::kMaxCount);
+  EXL3_TRY(check_words(q_start, "q_start"));
+  EXL3_TRY(check_words(adapter, "adapter"));
+  const exl3::ad::PlanLayout L = exl3::ad::plan_layout(T, batch, count);
+  EXL3_TRY(check_workspace(plan, plan_bytes, L.total));
+  exl3::ad::PlanArgs p = {};
+  p.q_start = q_start;
+  p.adapter = adapter;
+  p.T = T;
+  p.B = batch;
+  p.N = count;
+  p.ctrl = at<int>(plan, 0);
+  p.base = at<int>(plan, L.base);
+  p.perm = at<int>(plan, L.perm);
+  p.step_tiles = at<int4>(plan, L.step_tiles);
+  p.tc_tiles = at<int4>(plan, L.tc_tiles);
+  p.max_step_tiles = L.max_step_tiles;
+  p.max_tc_tiles = L.max_tc_tiles;
+  return exl3_cuda_check(exl3_launch_adapter_plan(p, stream), "adapter plan launch");
+}
+
+int exl3_adapter_add(const uint16_t *x, int64_t x_stride, const void *y, int64_t y_stride, void *out,
+                     int64_t out_stride, int dtype, const exl3_adapters *ad, void *plan, int T, int batch,
+                     exl3_stream_t stream) {
+  exl3_clear_error();
+  if (!ad) return exl3_fail(EXL3_ERR_ARG, "adapters is NULL");
+  if (dtype != EXL3_OUT_F16 && dtype != EXL3_OUT_F32) return exl3_fail(EXL3_ERR_ARG, "dtype %d invalid", dtype);
+  if (!plan_shape_ok(T, batch, ad->count))
+    return exl3_fail(EXL3_ERR_SHAPE, "T = %d (0..2^22), batch = %d (1..2^20) or count = %d (1..%d) out of range", T,
+                     batch, ad->count, exl3::ad::kMaxCount);
+  if (ad->max_rank < 8 || ad->max_rank > exl3::ad::kMaxRank || ad->max_rank % 8)
+    return exl3_fail(EXL3_ERR_SHAPE, "max_rank = %d must be a multiple of 8 in 8..%d", ad->max_rank, exl3::ad::kMaxRank);
+  if (ad->k < 128 || ad->k % 128 || ad->n < 128 || ad->n % 128 || ad->k > (1 << 20) || ad->n > (1 << 20))
+    return exl3_fail(EXL3_ERR_SHAPE, "k = %d and n = %d must be multiples of 128 up to 2^20", ad->k, ad->n);
+  EXL3_TRY(check_ptr(ad->a, "adapters.a"));
+  EXL3_TRY(check_ptr(ad->b, "adapters.b"));
+  EXL3_TRY(check_words(ad->scale, "adapters.scale"));
+  EXL3_TRY(check_words(ad->rank, "adapters.rank", false));
+  EXL3_TRY(check_ptr(x, "x"));
+  EXL3_TRY(check_ptr(y, "y"));
+  EXL3_TRY(check_ptr(out, "out"));
+  const int per16 = dtype == EXL3_OUT_F32 ? 4 : 8;
+  EXL3_TRY(check_stride("x", x_stride, ad->k, 8));
+  EXL3_TRY(check_stride("y", y_stride, ad->n, per16));
+  EXL3_TRY(check_stride("out", out_stride, ad->n, per16));
+  if (out == y && out_stride != y_stride)
+    return exl3_fail(EXL3_ERR_SHAPE, "out is y, but their strides differ: %lld and %lld", (long long)out_stride,
+                     (long long)y_stride);
+  const exl3::ad::PlanLayout L = exl3::ad::plan_layout(T, batch, ad->count);
+  EXL3_TRY(check_workspace(plan, L.total, L.total));
+  if (T == 0) return EXL3_OK;
+  exl3::ad::Args a = {};
+  a.x = reinterpret_cast<const __half *>(x);
+  a.y = y;
+  a.out = out;
+  a.x_stride = x_stride;
+  a.y_stride = y_stride;
+  a.out_stride = out_stride;
+  a.a = reinterpret_cast<const __half *>(ad->a);
+  a.b = reinterpret_cast<const __half *>(ad->b);
+  a.scale = ad->scale;
+  a.rank = ad->rank;
+  a.N = ad->count;
+  a.R = ad->max_rank;
+  a.k = ad->k;
+  a.n = ad->n;
+  a.T = T;
+  a.B = batch;
+  a.ctrl = at<int>(plan, 0);
+  a.perm = at<int>(plan, L.perm);
+  a.tiles = at<int4>(plan, L.step_tiles);
+  a.max_tiles = L.max_step_tiles;
+  return exl3_cuda_check(exl3_launch_adapter_step(a, dtype == EXL3_OUT_F32, stream), "adapter launch");
+}
+
+}  // extern "C"

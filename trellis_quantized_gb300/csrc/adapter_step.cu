@@ -1,0 +1,253 @@
+// adapter_step.cu -- low-rank adapters on few rows:
+//
+//   out[t] = y[t] + scale (x[t] A^T) B^T
+//
+// A tile is up to 16 rows of one adapter; a cluster of S CTAs takes it.  First
+// each CTA forms h = x A^T over its share of k, the cluster adds the shares up
+// (distributed shared memory, in the order of the CTAs: no atomics, no second
+// launch), then each CTA adds h B^T to its share of the n columns.  What bounds
+// it is one read of A, B, y and one write of out; with one row, start-up and
+// the chain plan -> x, A -> h -> out.
+//
+// Products are mma.sync m16n8k16 on fragments loaded straight from global
+// memory: a sum does not depend on the order that its terms are named in, so a
+// lane takes eight neighbouring k of x and A (or eight ranks of h and B) and
+// feeds them to two products; every load is 16 bytes and nothing passes
+// through shared memory.  (tcgen05 wants 64 or 128 rows; these tiles have one to
+// 16.)  The columns of B are dealt out so that a lane ends up with eight
+// neighbouring outputs.
+//
+// h is an operand of the second product in two fp16 parts, hi + lo, after each
+// row is brought to [2^14, 2^15) by a power of two: 22 bits of every h, so that
+// an fp32 out is as good as its fp32 sums.
+#include "adapter.cuh"
+#include "tc_ptx.cuh"
+
+namespace exl3 {
+namespace ad {
+
+constexpr int kStepThreads = 256, kStepWarps = 8;
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two products over 32 values of the summed index, eight neighbours per lane.
+__device__ __forceinline__ void mma_pair(float (&d)[4], const uint4 &lo, const uint4 &hi, const uint4 &b) {
+  mma16816(d, lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+  mma16816(d, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+}
+
+__device__ __forceinline__ uint4 load16(const __half *p, bool ok) {
+  return ok ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0, 0, 0, 0);
+}
+
+// Rows without an adapter: out = y (if they are two buffers).
+template <bool F32>
+__device__ __forceinline__ void copy_rows(const Args &a, const int4 &tile, int split, int S, int threads) {
+  if (a.out == a.y) return;
+  constexpr int PER = F32 ? 4 : 8, SIZE = F32 ? 4 : 2;
+  const int quads = a.n / PER;
+  for (int r = 0; r < tile.z; ++r) {
+    const int64_t row = a.perm[tile.y + r];
+    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(a.y) + row * a.y_stride * SIZE);
+    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<char *>(a.out) + row * a.out_stride * SIZE);
+    for (int i = split * threads + threadIdx.x; i < quads; i += S * threads) dst[i] = src[i];
+  }
+}
+
+// RT: 8-wide tiles of ranks per warp; RG warps share the ranks (RT 8: up to 64 each).
+template <int RT, int RG, bool F32>
+__global__ void __launch_bounds__(kStepThreads) adapter_step_kernel(const Args a) {
+  constexpr int RMAX = RT * RG * 8, KW = kStepWarps / RG;       // warps that share k
+  constexpr int HP = RMAX + 8;                                  // halves between rows of h: other banks
+  __shared__ __align__(16) float part[KW][kStepRows][RMAX];     // each warp's sums
+  __shared__ __align__(16) float own[kStepRows][RMAX];          // this CTA's
+  // the cluster's, hi and lo, where the warps' sums were (read before the cluster's barrier)
+  __half(*hs)[kStepRows][HP] = reinterpret_cast<__half(*)[kStepRows][HP]>(&part[0][0][0]);
+  static_assert(2 * HP * 2 <= KW * RMAX * 4, "h in place of the warps' sums");
+  __shared__ float back[kStepRows];                             // scale 2^-p
+  const int S = gridDim.x, split = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, q = lane & 3;
+  pdl_trigger();
+  pdl_wait();
+  const int tiles = plan_tiles(a, kPlanStepTiles);
+  const int4 tile = a.tiles[blockIdx.y];                        // (inside the plan for every block)
+  if ((int)blockIdx.y >= tiles) return;                         // (the whole cluster)
+  if (tile.x < 0) {
+    copy_rows<F32>(a, tile, split, S, kStepThreads);
+    return;
+  }
+  const int rank = adapter_rank(a, tile.x), R8 = (rank + 7) / 8;
+  const __half *A = a.a + (int64_t)tile.x * a.R * a.k, *B = a.b + (int64_t)tile.x * a.n * a.R;
+  const bool ok0 = g < tile.z, ok1 = g + 8 < tile.z;
+  const int64_t t0 = ok0 ? a.perm[tile.y + g] : 0, t1 = ok1 ? a.perm[tile.y + g + 8] : 0;
+
+  {  // h over this CTA's share of k, 32 at a time
+    float acc[RT][4];
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+    const int rg = warp % RG, j0 = rg * RT, units = a.k / 32;
+    const int u0 = (int)((int64_t)units * split / S), u1 = (int)((int64_t)units * (split + 1) / S);
+    const __half *x0 = a.x + t0 * a.x_stride + q * 8, *x1 = a.x + t1 * a.x_stride + q * 8;
+    const __half *ar = A + (int64_t)(j0 * 8 + g) * a.k + q * 8;
+#pragma unroll 2
+    for (int u = u0 + warp / RG; u < u1; u += KW) {
+      const uint4 lo = load16(x0 + u * 32, ok0), hi = load16(x1 + u * 32, ok1);
+      uint4 w[RT];
+#pragma unroll
+      for (int j = 0; j < RT; ++j) w[j] = load16(ar + (int64_t)j * 8 * a.k + u * 32, j0 + j < R8);
+#pragma unroll
+      for (int j = 0; j < RT; ++j) mma_pair(acc[j], lo, hi, w[j]);
+    }
+    float *p = &part[warp / RG][0][0] + j0 * 8;
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+      *reinterpret_cast<float2 *>(p + g * RMAX + j * 8 + 2 * q) = make_float2(acc[j][0], acc[j][1]);
+      *reinterpret_cast<float2 *>(p + (g + 8) * RMAX + j * 8 + 2 * q) = make_float2(acc[j][2], acc[j][3]);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kStepRows * RMAX; i += kStepThreads) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) v += (&part[w][0][0])[i];
+    (&own[0][0])[i] = v;
+  }
+  cluster_arrive();
+  cluster_wait();
+  {  // the cluster's sum: 16 threads per row
+    const int r = threadIdx.x >> 4, c0 = threadIdx.x & 15;
+    constexpr int PER = (RMAX + 15) / 16;
+    float v[PER], top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = 0.0f;
+    for (int s = 0; s < S; ++s) {
+      const uint32_t at = map_rank(tc::smem_u32(&own[r][0]), s);
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (c0 + 16 * i < RMAX) v[i] += ld_cluster(at + (c0 + 16 * i) * 4);
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (c0 + 16 * i >= rank) v[i] = 0.0f;
+      top = fmaxf(top, fabsf(v[i]));
+    }
+#pragma unroll
+    for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int p = row_exponent(top);
+    const float f = scalbnf(1.0f, p);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (c0 + 16 * i < RMAX) {
+        const float z = v[i] * f;
+        const __half hi = __float2half_rn(z);
+        hs[0][r][c0 + 16 * i] = hi;
+        hs[1][r][c0 + 16 * i] = __float2half_rn(z - __half2float(hi));
+      }
+    if (c0 == 0) back[r] = __ldg(a.scale + tile.x) * scalbnf(1.0f, -p);
+  }
+  cluster_arrive();                                             // (its sums may go once the others have read them)
+  __syncthreads();
+
+  // this CTA's columns, 32 per warp and turn
+  const float f0 = back[g], f1 = back[g + 8];
+  const int units = a.n / 32, R32 = (rank + 31) / 32;
+  const int ncol = 8 * (g >> 1) + (g & 1);                      // column g of the j-th tile: ncol + 2 j
+  for (int u = split * kStepWarps + warp; u < units; u += S * kStepWarps) {
+    float d[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[j][i] = 0.0f;
+    const __half *br = B + (int64_t)(u * 32 + ncol) * a.R + q * 8;
+#pragma unroll 2
+    for (int c = 0; c < R32; ++c) {
+      uint4 w[4];
+      const bool ok = c * 4 + q < R8;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = load16(br + (int64_t)2 * j * a.R + c * 32, ok);
+      const int at = c * 32 + q * 8;
+      uint4 l0 = make_uint4(0, 0, 0, 0), h0 = l0, l1 = l0, h1 = l0;
+      if (ok) {
+        l0 = *reinterpret_cast<const uint4 *>(&hs[0][g][at]);
+        h0 = *reinterpret_cast<const uint4 *>(&hs[0][g + 8][at]);
+        l1 = *reinterpret_cast<const uint4 *>(&hs[1][g][at]);
+        h1 = *reinterpret_cast<const uint4 *>(&hs[1][g + 8][at]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mma_pair(d[j], l0, h0, w[j]);
+        mma_pair(d[j], l1, h1, w[j]);
+      }
+    }
+    const int col = u * 32 + q * 8;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (!(r ? ok1 : ok0)) continue;
+      const int64_t t = r ? t1 : t0;
+      const float f = r ? f1 : f0;
+      if (F32) {
+        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.y) + t * a.y_stride + col);
+        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + t * a.out_stride + col);
+        const float4 y0 = src[0], y1 = src[1];
+        dst[0] = make_float4(fmaf(f, d[0][2 * r], y0.x), fmaf(f, d[0][2 * r + 1], y0.y), fmaf(f, d[1][2 * r], y0.z),
+                             fmaf(f, d[1][2 * r + 1], y0.w));
+        dst[1] = make_float4(fmaf(f, d[2][2 * r], y1.x), fmaf(f, d[2][2 * r + 1], y1.y), fmaf(f, d[3][2 * r], y1.z),
+                             fmaf(f, d[3][2 * r + 1], y1.w));
+      } else {
+        uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(a.y) + t * a.y_stride + col);
+        __half2 *h = reinterpret_cast<__half2 *>(&v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 y = __half22float2(h[j]);
+          h[j] = __floats2half2_rn(fmaf(f, d[j][2 * r], y.x), fmaf(f, d[j][2 * r + 1], y.y));
+        }
+        *reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + t * a.out_stride + col) = v;
+      }
+    }
+  }
+  cluster_wait();
+}
+
+}  // namespace ad
+}  // namespace exl3
+
+using namespace exl3;
+
+namespace {
+
+template <int RT, int RG>
+cudaError_t launch_step(const ad::Args &a, bool f32, int S, cudaStream_t s) {
+  auto kfn = f32 ? ad::adapter_step_kernel<RT, RG, true> : ad::adapter_step_kernel<RT, RG, false>;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = S;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(S, a.max_tiles);
+  cfg.blockDim = dim3(ad::kStepThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kfn, a);
+}
+
+}  // namespace
+
+cudaError_t exl3_launch_adapter_step(const ad::Args &a, bool f32, cudaStream_t s) {
+  const int S = 8;
+  if (a.R <= 16) return launch_step<2, 1>(a, f32, S, s);
+  if (a.R <= 32) return launch_step<4, 1>(a, f32, S, s);
+  if (a.R <= 64) return launch_step<8, 1>(a, f32, S, s);
+  return launch_step<8, 2>(a, f32, S, s);
+}
