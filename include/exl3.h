@@ -639,7 +639,9 @@ typedef struct {
  *   weights  dense [T][topk] fp32
  *   E        1..1024.  T = 0 enqueues nothing.  No workspace.
  *   The choice is that of exact arithmetic on the given logits and bias: where
- *   fp32 does not settle an order it is decided in 64 bits.  Weights are fp32.
+ *   fp32 does not settle an order it is decided with 45 bits (scores below
+ *   exp(-69) of the softmax's largest, or of 1, then count as 0).  Weights are
+ *   fp32.
  *   A logit of -infinity has score 0; a row of nothing else has weights 0 and
  *   the lowest ids.  A bias of -infinity bars an expert: it is chosen only when
  *   nothing else is left, with weight 0.  NaN ranks below everything; weights

@@ -757,27 +757,39 @@ def exl3_paged_attention(q, batch: PagedBatch, cache: KvCache, scale: float | No
 
 # -------------------------------------------------------- routing to experts
 
-def _on_current(t, name: str):
-    """Kernels go to the current device's stream: a tensor of another device is refused."""
+# (As above: pointers as plain integers, each property asked for once.)
+
+def _on_current(t, name: str) -> int:
+    """The current device, on which t has to be: its stream gets the kernels."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
+    d = t.get_device()
+    if d < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != torch.cuda.current_device():
+    if d != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return d
 
 
 def _matrix(t, name: str, width: int, dtypes):
     """Address and row stride of [rows, width] with dense rows."""
-    _on_current(t, name)
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    shape, s = t.shape, t.stride()
+    shape = t.shape
     if len(shape) != 2 or shape[1] != width:
         raise ValueError(f"{name} must be [rows, {width}], got {tuple(shape)}")
-    if s[1] != 1 and width > 1:
+    s0, s1 = t.stride()
+    if s1 != 1 and width > 1:
         raise ValueError(f"{name}'s rows must be dense")
-    return t.data_ptr(), (s[0] if shape[0] > 1 else width)
+    return t.data_ptr(), (s0 if shape[0] > 1 else width)
+
+
+def _same_device(t, name: str, device: int):
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the other tensors' device cuda:{device}, got {t.device}")
+
+
+_F16, _F32, _F16_F32 = (torch.float16,), (torch.float32,), (torch.float16, torch.float32)
 
 
 def _vector(t, name: str, size: int, dtype):
@@ -804,7 +816,7 @@ def router(w, bias=None, stream=None) -> Router:
         _check(lib().exl3_router_pack(_ptr(w, "w"), E, k, _ptr(parts, "packed"), _ptr(scale, "scale"), _stream(stream)))
     d = Router(_ptr(parts, "w").value, None if scale is None else scale.data_ptr(), _vector(bias, "bias", E, torch.float32),
                E, k)
-    d._keep = (parts, scale, bias)
+    d._keep, d._address = (parts, scale, bias), ctypes.addressof(d)
     return d
 
 
@@ -832,16 +844,17 @@ _logits_workspace = functools.cache(exl3_router_logits_workspace_size)
 
 def exl3_router_logits(x, router: Router, logits=None, workspace_buf=None, stream=None) -> torch.Tensor:
     """logits [T, E] fp32 = x @ w^T (+ bias) for x [T, k] fp16 with dense rows."""
-    xp, xs = _matrix(x, "x", router.k, (torch.float16,))
+    device = _on_current(x, "x")
+    xp, xs = _matrix(x, "x", router.k, _F16)
     T = x.shape[0]
     if logits is None:
         logits = torch.empty((T, router.E), dtype=torch.float32, device=x.device)
     lp = _out(logits, "logits", (T, router.E), torch.float32)
-    _on_current(logits, "logits")
+    _same_device(logits, "logits", device)
     if T:
         raw = _raw_stream(stream)
         wp, wn = _workspace_arg(workspace_buf, _logits_workspace(), x.device, stream, raw)
-        _check(lib().exl3_router_logits(xp, xs, T, ctypes.byref(router), lp, wp, wn, raw))
+        _check(lib().exl3_router_logits(xp, xs, T, router._address, lp, wp, wn, raw))
     return logits
 
 
@@ -857,7 +870,7 @@ def route_rule(topk: int, score: int = EXL3_SCORE_SOFTMAX, bias=None, groups: in
         bp = _vector(bias, "bias", bias.shape[0], torch.float32)
     d = RouteRule(score, bp, groups, groups if groups_kept is None else groups_kept, group_score, topk,
                   1 if renormalise else 0, scale)
-    d._keep = (bias,)
+    d._keep, d._address = (bias,), ctypes.addressof(d)
     d._experts = None if bias is None else bias.shape[0]
     return d
 
@@ -868,19 +881,19 @@ def exl3_route(logits, rule: RouteRule, ids=None, weights=None, stream=None):
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise TypeError("logits must be a torch tensor [T, E]")
     T, E = logits.shape
-    lp, ls = _matrix(logits, "logits", E, (torch.float32, torch.float16))
+    device, topk = _on_current(logits, "logits"), rule.topk
+    lp, ls = _matrix(logits, "logits", E, _F16_F32)
     if rule._experts is not None and rule._experts != E:
         raise ValueError(f"the rule's bias has {rule._experts} experts, the logits {E}")
     if ids is None:
-        ids = torch.empty((T, rule.topk), dtype=torch.int32, device=logits.device)
+        ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
     if weights is None:
-        weights = torch.empty((T, rule.topk), dtype=torch.float32, device=logits.device)
-    ip, wp = _out(ids, "ids", (T, rule.topk), torch.int32), _out(weights, "weights", (T, rule.topk), torch.float32)
-    _on_current(ids, "ids")
-    _on_current(weights, "weights")
+        weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
+    ip, wp = _out(ids, "ids", (T, topk), torch.int32), _out(weights, "weights", (T, topk), torch.float32)
+    _same_device(ids, "ids", device)
+    _same_device(weights, "weights", device)
     if T:
-        _check(lib().exl3_route(lp, ls, _IO_DTYPES[logits.dtype], T, E, ctypes.byref(rule), ip, wp,
-                                _raw_stream(stream)))
+        _check(lib().exl3_route(lp, ls, _IO_DTYPES[logits.dtype], T, E, rule._address, ip, wp, _raw_stream(stream)))
     return ids, weights
 
 
@@ -903,7 +916,7 @@ def adapters(a, b, scale, rank=None) -> Adapters:
         raise TypeError("scale must be a torch tensor")
     d = Adapters(_ptr(a, "a", 2).value, _ptr(b, "b", 2).value, _vector(scale, "scale", N, torch.float32),
                  _vector(rank, "rank", N, torch.int32), N, R, k, n)
-    d._keep = (a, b, scale, rank)
+    d._keep, d._address = (a, b, scale, rank), ctypes.addressof(d)
     return d
 
 
@@ -916,6 +929,7 @@ class AdapterPlan:
             raise ValueError(f"T = {T}, batch = {batch} or count = {count} out of range")
         self.T, self.batch, self.count = T, batch, count
         self.data = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.address = self.data.data_ptr()
         exl3_workspace_clear(self.data, stream=stream)
 
 
@@ -939,24 +953,27 @@ def exl3_adapter_plan(q_start, adapter, T: int, count: int, plan: AdapterPlan | 
     elif (plan.T, plan.batch, plan.count) != (T, B, count):
         raise ValueError(f"plan was made for T = {plan.T}, batch = {plan.batch}, count = {plan.count}")
     _check(lib().exl3_adapter_plan(_ptr(q_start, "q_start"), _ptr(adapter, "adapter"), T, B, count,
-                                   plan.data.data_ptr(), plan.data.numel(), _raw_stream(stream)))
+                                   plan.address, plan.data.numel(), _raw_stream(stream)))
     return plan
 
 
 def exl3_adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out=None, stream=None) -> torch.Tensor:
     """y + scale (x A^T) B^T for each row's adapter: x [T, k] fp16, y [T, n] fp16 or fp32, dense
     rows; written to `out`, or to y itself (rows of no sequence are left as they were)."""
-    xp, xs = _matrix(x, "x", adapters.k, (torch.float16,))
-    yp, ys = _matrix(y, "y", adapters.n, (torch.float16, torch.float32))
+    device = _on_current(x, "x")
+    xp, xs = _matrix(x, "x", adapters.k, _F16)
+    yp, ys = _matrix(y, "y", adapters.n, _F16_F32)
+    _same_device(y, "y", device)
     if out is None or out is y:
         out, op, os_ = y, yp, ys
     else:
-        op, os_ = _matrix(out, "out", adapters.n, (y.dtype,))
+        op, os_ = _matrix(out, "out", adapters.n, _F16 if y.dtype == torch.float16 else _F32)
+        _same_device(out, "out", device)
     T = x.shape[0]
     if y.shape[0] != T or out.shape[0] != T or plan.T != T:
         raise ValueError(f"x has {T} rows, y {y.shape[0]}, out {out.shape[0]}, the plan {plan.T}")
     if plan.count != adapters.count:
         raise ValueError(f"the plan was made for {plan.count} adapters, the pool has {adapters.count}")
-    _check(lib().exl3_adapter_add(xp, xs, yp, ys, op, os_, _IO_DTYPES[y.dtype], ctypes.byref(adapters),
-                                  plan.data.data_ptr(), T, plan.batch, _raw_stream(stream)))
+    _check(lib().exl3_adapter_add(xp, xs, yp, ys, op, os_, _IO_DTYPES[y.dtype], adapters._address, plan.address, T,
+                                  plan.batch, _raw_stream(stream)))
     return out

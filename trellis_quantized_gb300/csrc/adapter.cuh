@@ -106,6 +106,20 @@ __device__ __forceinline__ int adapter_rank(const Args &a, int id) {
   return a.rank ? min(max(__ldg(a.rank + id), 0), a.R) : a.R;
 }
 
+// Rows without an adapter: out = y (if they are two buffers).
+template <bool F32>
+__device__ __forceinline__ void copy_rows(const Args &a, const int4 &tile, int split, int S, int threads) {
+  if (a.out == a.y) return;
+  constexpr int PER = F32 ? 4 : 8, SIZE = F32 ? 4 : 2;
+  const int quads = a.n / PER;
+  for (int r = 0; r < tile.z; ++r) {
+    const int64_t row = a.perm[tile.y + r];
+    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(a.y) + row * a.y_stride * SIZE);
+    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<char *>(a.out) + row * a.out_stride * SIZE);
+    for (int i = split * threads + threadIdx.x; i < quads; i += S * threads) dst[i] = src[i];
+  }
+}
+
 // The power of two that brings a row's largest |h| into [2^14, 2^15), as its
 // exponent; 0 for a row of zeros or one with infinities or NaN.
 __device__ __forceinline__ int row_exponent(float top) {

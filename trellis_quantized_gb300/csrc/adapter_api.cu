@@ -6,8 +6,11 @@
 // ---- kernels (other translation units)
 cudaError_t exl3_launch_adapter_plan(const exl3::ad::PlanArgs &p, cudaStream_t s);
 cudaError_t exl3_launch_adapter_step(const exl3::ad::Args &a, bool f32, cudaStream_t s);
+int exl3_launch_adapter_tc(const exl3::ad::Args &a, bool f32, cudaStream_t s);
 
 namespace {
+
+constexpr int kTcFrom = 256;   // rows from which tiles of 128 are used
 
 bool plan_shape_ok(int T, int batch, int count) {
   return T >= 0 && T <= (1 << 22) && batch >= 1 && batch <= (1 << 20) && count >= 1 && count <= exl3::ad::kMaxCount;
@@ -109,6 +112,11 @@ int exl3_adapter_add(const uint16_t *x, int64_t x_stride, const void *y, int64_t
   a.B = batch;
   a.ctrl = at<int>(plan, 0);
   a.perm = at<int>(plan, L.perm);
+  if (T >= kTcFrom) {
+    a.tiles = at<int4>(plan, L.tc_tiles);
+    a.max_tiles = L.max_tc_tiles;
+    return exl3_launch_adapter_tc(a, dtype == EXL3_OUT_F32, stream);
+  }
   a.tiles = at<int4>(plan, L.step_tiles);
   a.max_tiles = L.max_step_tiles;
   return exl3_cuda_check(exl3_launch_adapter_step(a, dtype == EXL3_OUT_F32, stream), "adapter launch");

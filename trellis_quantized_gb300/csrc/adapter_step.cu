@@ -47,20 +47,6 @@ __device__ __forceinline__ uint4 load16(const __half *p, bool ok) {
   return ok ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0, 0, 0, 0);
 }
 
-// Rows without an adapter: out = y (if they are two buffers).
-template <bool F32>
-__device__ __forceinline__ void copy_rows(const Args &a, const int4 &tile, int split, int S, int threads) {
-  if (a.out == a.y) return;
-  constexpr int PER = F32 ? 4 : 8, SIZE = F32 ? 4 : 2;
-  const int quads = a.n / PER;
-  for (int r = 0; r < tile.z; ++r) {
-    const int64_t row = a.perm[tile.y + r];
-    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const char *>(a.y) + row * a.y_stride * SIZE);
-    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<char *>(a.out) + row * a.out_stride * SIZE);
-    for (int i = split * threads + threadIdx.x; i < quads; i += S * threads) dst[i] = src[i];
-  }
-}
-
 // RT: 8-wide tiles of ranks per warp; RG warps share the ranks (RT 8: up to 64 each).
 template <int RT, int RG, bool F32>
 __global__ void __launch_bounds__(kStepThreads) adapter_step_kernel(const Args a) {

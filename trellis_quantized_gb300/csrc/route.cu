@@ -7,18 +7,21 @@
 //   chosen (equal values: the lower id); weights are the chosen s, divided by
 //   their sum if asked, times `scale`.
 //
-// A warp takes a token; lane l holds experts l, l + 32, ... as keys that order
-// as their values do (the float's bits, made monotone).  A pick is two warp
-// reductions (redux: the largest key, then the lowest id that has it) and one
-// pass over the owner's keys.  Softmax and the sigmoid are monotone, so without
-// a bias and without sums of two the keys are the logits themselves: exact, and
-// no exponential before the topk chosen ones.
+// A warp takes a token; lane l holds V neighbouring experts as keys that order
+// as their values do (the float's bits, made monotone).  A pick is one warp
+// reduction (redux: the largest key), a ballot (the lowest lane that has it has
+// the lowest id) and one pass over the owner's keys.  Softmax and the sigmoid
+// are monotone, so without a bias and without sums of two the keys are the
+// logits themselves: exact, and no exponential before the topk chosen ones.
 //
 // Otherwise values are computed in 32 bits, and every comparison that decides
 // something (neighbouring picks, the last group kept and the first left out) is
 // tested against a bound on their error.  A row with one that is closer than
-// that is done again in 64 bits, so that ids are those of exact arithmetic; with
-// random logits that is one row in a few hundred.
+// that, one in a few thousand with random logits, is done again on pairs of
+// floats (about 45 bits).  Not in 64-bit floats: this chip has so few units for
+// those that one such row took 15 us.  Neighbouring picks that are too close
+// are put in order among themselves, a lane each; only groups that are, and more
+// than 32 equal picks, take the whole row.
 #include <algorithm>
 #include <climits>
 
@@ -50,102 +53,256 @@ __device__ __forceinline__ float load_logit(const Args &a, int64_t row, int e) {
   return static_cast<const float *>(a.logits)[row * a.stride + e];
 }
 
+// V neighbouring logits from expert e0 on, of which `here` exist.
+template <int V, bool F16>
+__device__ __forceinline__ void load_row(const Args &a, int64_t row, int e0, int here, float (&l)[V]) {
+  constexpr int W = F16 ? (V < 8 ? V : 8) : (V < 4 ? V : 4);     // values of one wide load
+  if (a.wide && here == V) {
+    if (F16) {
+      const __half *src = static_cast<const __half *>(a.logits) + row * a.stride + e0;
+#pragma unroll
+      for (int i = 0; i < V; i += W) {
+        __align__(16) __half h[W];
+        if (W == 8) *reinterpret_cast<uint4 *>(h) = *reinterpret_cast<const uint4 *>(src + i);
+        if (W == 4) *reinterpret_cast<uint2 *>(h) = *reinterpret_cast<const uint2 *>(src + i);
+        if (W == 2) *reinterpret_cast<unsigned *>(h) = *reinterpret_cast<const unsigned *>(src + i);
+        if (W == 1) h[0] = src[i];
+#pragma unroll
+        for (int j = 0; j < W; ++j) l[i + j] = __half2float(h[j]);
+      }
+    } else {
+      const float *src = static_cast<const float *>(a.logits) + row * a.stride + e0;
+#pragma unroll
+      for (int i = 0; i < V; i += W) {
+        __align__(16) float f[W];
+        if (W == 4) *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(src + i);
+        if (W == 2) *reinterpret_cast<float2 *>(f) = *reinterpret_cast<const float2 *>(src + i);
+        if (W == 1) f[0] = src[i];
+#pragma unroll
+        for (int j = 0; j < W; ++j) l[i + j] = f[j];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = i < here ? load_logit<F16>(a, row, e0 + i) : neg_inf();
+  }
+}
+
 __device__ __forceinline__ float sigmoid(float l) {
   const float t = expf(-fabsf(l)), r = 1.0f / (1.0f + t);
   return l >= 0.0f ? r : t * r;
 }
 
-__device__ __forceinline__ double sigmoid(double l) {
-  const double t = exp(-fabs(l)), r = 1.0 / (1.0 + t);
-  return l >= 0.0 ? r : t * r;
-}
-
-// Sum and maximum over the warp (the same order of additions every time).
+// Sum over the warp (the same order of additions every time).
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
 }
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  return v;
-}
-
 // Does the order of two computed values (v above w) hold for the exact ones?
 // Infinities are exact; what is barred (-infinity) is never asked about.
 __device__ __forceinline__ bool uncertain(float v, float w, float tol) {
   return w > neg_inf() && !(v - w > tol + 0x1p-22f * fabsf(v));
 }
 
-// The whole selection in 64 bits, from the row's values in shared memory.
-// Lane j gets the j-th chosen expert.  Rare, so the simplest form.
-template <bool F16>
-__device__ __noinline__ int select_exact(const Args &a, int64_t row, int lane, double *c) {
-  double mx = -INFINITY, sum = 0.0;
-  if (a.score == EXL3_SCORE_SOFTMAX) {
-    for (int e = lane; e < a.E; e += 32) mx = fmax(mx, (double)load_logit<F16>(a, row, e));
+// ------------------------------------------------------ pairs of floats
+//
+// A value as the unevaluated sum of two floats, the second below half a unit of
+// the first (Dekker's and Knuth's error-free sums and products).
+
+struct Pair {
+  float h, l;
+};
+
+__device__ __forceinline__ Pair quick_sum(float a, float b) {      // |a| >= |b|
+  const float s = a + b;
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  Pair s = two_sum(a.h, b.h);
+  const Pair t = two_sum(a.l, b.l);
+  s = quick_sum(s.h, s.l + t.h);
+  return quick_sum(s.h, s.l + t.l);
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  const float p = __fmul_rn(a.h, b.h);
+  return quick_sum(p, fmaf(a.h, b.h, -p) + fmaf(a.h, b.l, a.l * b.h));
+}
+__device__ __forceinline__ Pair div(Pair a, Pair b) {
+  const float q = a.h / b.h;
+  const Pair p = mul({q, 0.0f}, b);
+  const Pair r = add(a, {-p.h, -p.l});
+  return quick_sum(q, (r.h + r.l) / b.h);
+}
+
+// 1 / k as a pair.
+template <int K>
+__device__ __forceinline__ Pair inverse() {
+  constexpr double v = 1.0 / K;
+  constexpr float h = (float)v;
+  return {h, (float)(v - (double)h)};
+}
+
+// 1 + r (1 + r / 2 (1 + r / 3 (...))): Taylor's series from its K-th factor on.
+template <int K>
+__device__ __forceinline__ Pair series(Pair r, Pair tail) {
+  return add({1.0f, 0.0f}, mul(mul(r, inverse<K>()), tail));
+}
+
+// exp(x) for x <= 0: x = n ln 2 + r with ln 2 in parts of which the first has
+// nine bits (n times it is exact; Cody and Waite), then the series.  From the
+// eighth factor on (below 2^-27 of the result) single floats do.  Zero from exp(-69) down.
+__device__ __forceinline__ Pair exp_pair(Pair x) {
+  if (!(x.h > -69.0f)) return {x.h == x.h ? 0.0f : x.h, 0.0f};
+  const float n = rintf(x.h * 1.44269504f);
+  constexpr double ln2 = 0.693147180559945309417;
+  constexpr float c1 = 0.693359375f, c2 = (float)(ln2 - c1), c3 = (float)(ln2 - c1 - c2);
+  const float p = __fmul_rn(n, c2);
+  Pair r = add({__fsub_rn(x.h, n * c1), x.l}, {-p, -fmaf(n, c2, -p)});
+  r = add(r, {-n * c3, 0.0f});
+  float t = 1.0f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmax(mx, __shfl_xor_sync(kFull, mx, o));
-    if (mx == -INFINITY) mx = 0.0;
-    for (int e = lane; e < a.E; e += 32) sum += exp((double)load_logit<F16>(a, row, e) - mx);
-    sum = warp_sum(sum);
+  for (int k = 13; k >= 8; --k) t = fmaf(r.h / (float)k, t, 1.0f);
+  Pair e = series<7>(r, {t, 0.0f});
+  e = series<6>(r, e);
+  e = series<5>(r, e);
+  e = series<4>(r, e);
+  e = series<3>(r, e);
+  e = series<2>(r, e);
+  e = series<1>(r, e);
+  const float f = scalbnf(1.0f, (int)n);
+  return {e.h * f, e.l * f};
+}
+
+// Order keys of a pair, high and low.
+__device__ __forceinline__ unsigned long long pair_key(Pair v) {
+  const unsigned hi = order_key(v.h);
+  return (unsigned long long)hi << 32 | (hi == 1u || isinf(v.h) ? 0u : order_key(v.l));
+}
+__device__ __forceinline__ Pair key_pair(unsigned long long k) {
+  const float h = key_value((unsigned)(k >> 32));
+  return {h, (unsigned)k ? key_value((unsigned)k) : 0.0f};
+}
+
+// The softmax's largest logit and sum of a row.
+template <bool F16>
+__device__ __forceinline__ void row_sum(const Args &a, int64_t row, int lane, float &mx, Pair &sum) {
+  mx = neg_inf();
+  for (int e = lane; e < a.E; e += 32) mx = fmaxf(mx, load_logit<F16>(a, row, e));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+  if (mx == neg_inf()) mx = 0.0f;
+  sum = {0.0f, 0.0f};
+#pragma unroll 2
+  for (int e = lane; e < a.E; e += 32) {
+    const float l = load_logit<F16>(a, row, e);
+    sum = add(sum, l == neg_inf() ? Pair{0.0f, 0.0f} : exp_pair(two_sum(l, -mx)));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum = add(sum, {__shfl_xor_sync(kFull, sum.h, o), __shfl_xor_sync(kFull, sum.l, o)});
+}
+
+// The key of expert e's c.
+template <bool F16>
+__device__ __forceinline__ unsigned long long value_key(const Args &a, int64_t row, int e, float mx, Pair sum) {
+  const bool soft = a.score == EXL3_SCORE_SOFTMAX;
+  const float l = load_logit<F16>(a, row, e);
+  const Pair t = exp_pair(soft ? two_sum(l, -mx) : Pair{-fabsf(l), 0.0f});
+  Pair v = div(soft || !(l >= 0.0f) ? t : Pair{1.0f, 0.0f}, soft ? sum : add({1.0f, 0.0f}, t));
+  if (l == neg_inf()) v = {0.0f, 0.0f};
+  if (a.bias) {
+    const float b = a.bias[e];
+    v = isfinite(b) ? add(v, {b, 0.0f}) : Pair{v.h + b, 0.0f};
+  }
+  return pair_key(v);
+}
+
+// A row with picks that are too close: lane j has the j-th of `count` experts,
+// of which everything else is known to be below; they are put in order.
+template <bool F16>
+__device__ __noinline__ int order_pairs(const Args &a, int64_t row, int lane, int id, int count, int *place) {
+  float mx = 0.0f;
+  Pair sum = {0.0f, 0.0f};
+  if (a.score == EXL3_SCORE_SOFTMAX) row_sum<F16>(a, row, lane, mx, sum);
+  const unsigned long long key = lane < count ? value_key<F16>(a, row, id, mx, sum) : 0;
+  int before = 0;
+  for (int o = 0; o < count; ++o) {
+    const unsigned long long v = __shfl_sync(kFull, key, o);
+    const int other = __shfl_sync(kFull, id, o);
+    before += v > key || (v == key && other < id);
   }
   __syncwarp();
-  for (int e = lane; e < a.E; e += 32) {
-    const double l = load_logit<F16>(a, row, e);
-    double v = a.score == EXL3_SCORE_SOFTMAX ? (sum == 0.0 ? 0.0 : exp(l - mx) / sum) : sigmoid(l);
-    if (a.bias) v += (double)a.bias[e];
-    // NaN ranks last, after what is barred (every finite value is above -1e300)
-    c[e] = v != v ? -INFINITY : v == -INFINITY ? -1e300 : v;
-  }
+  if (lane < count) place[before] = id;
+  __syncwarp();
+  return lane < count ? place[lane] : -1;
+}
+
+// The whole selection on pairs, the row's keys in shared memory: groups that are
+// too close, or too many equal picks.  Lane j gets the j-th chosen expert.  Rare,
+// so the simplest form.
+template <bool F16>
+__device__ __noinline__ int select_pairs(const Args &a, int64_t row, int lane, unsigned long long *c) {
+  float mx = 0.0f;
+  Pair sum = {0.0f, 0.0f};
+  if (a.score == EXL3_SCORE_SOFTMAX) row_sum<F16>(a, row, lane, mx, sum);
+  __syncwarp();
+#pragma unroll 2
+  for (int e = lane; e < a.E; e += 32) c[e] = value_key<F16>(a, row, e, mx, sum);
   __syncwarp();
   const int size = a.E / a.groups;
   unsigned keep = kFull;
   if (a.kept < a.groups) {
-    double g = -INFINITY;
+    unsigned long long g = 0;
     if (lane < a.groups) {
-      double first = -INFINITY, second = -INFINITY;
+      unsigned long long first = 0, second = 0;
       for (int i = 0; i < size; ++i) {
-        const double v = c[lane * size + i];
-        second = fmax(second, fmin(first, v));
-        first = fmax(first, v);
+        const unsigned long long v = c[lane * size + i];
+        second = max(second, min(first, v));
+        first = max(first, v);
       }
-      g = a.group_score == EXL3_GROUP_TOP2 && size > 1 ? first + second : first;
+      g = first;
+      if (a.group_score == EXL3_GROUP_TOP2 && size > 1) {
+        const Pair p = key_pair(first), q = key_pair(second);
+        g = first >> 32 == 1u || second >> 32 == 1u ? 1ull << 32
+            : isinf(p.h) || isinf(q.h)              ? pair_key({p.h + q.h, 0.0f})
+                                                    : pair_key(add(p, q));
+      }
     }
     // rank of a group: how many stand before it
     int before = 0;
     for (int o = 0; o < a.groups; ++o) {
-      const double v = __shfl_sync(kFull, g, o);
+      const unsigned long long v = __shfl_sync(kFull, g, o);
       before += v > g || (v == g && o < lane);
     }
     keep = __ballot_sync(kFull, lane < a.groups && before < a.kept);
   }
-  unsigned taken = 0;      // bit i: expert lane + 32 i is chosen or left out
-  for (int i = 0; lane + 32 * i < a.E; ++i)
-    if (a.kept < a.groups && !(keep >> ((lane + 32 * i) / size) & 1u)) taken |= 1u << i;
+  // left out: key 0, as what is chosen later
+  for (int e = lane; e < a.E; e += 32)
+    if (a.kept < a.groups && !(keep >> (e / size) & 1u)) c[e] = 0;
   int mine = -1;
   for (int j = 0; j < a.topk; ++j) {
-    double best = 0.0;
+    unsigned long long best = 0;
     int id = INT_MAX;
-    for (int i = 0; lane + 32 * i < a.E; ++i) {
-      const double v = c[lane + 32 * i];
-      if (!(taken >> i & 1u) && (id == INT_MAX || v > best)) {
-        best = v;
-        id = lane + 32 * i;
+    for (int e = lane; e < a.E; e += 32)
+      if (c[e] > best) {
+        best = c[e];
+        id = e;
       }
-    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-      const double v = __shfl_xor_sync(kFull, best, o);
+      const unsigned long long v = __shfl_xor_sync(kFull, best, o);
       const int other = __shfl_xor_sync(kFull, id, o);
-      if (other != INT_MAX && (id == INT_MAX || v > best || (v == best && other < id))) {
+      if (v > best || (v == best && other < id)) {
         best = v;
         id = other;
       }
     }
-    if (id == INT_MAX) break;
-    if ((id & 31) == lane) taken |= 1u << (id >> 5);
+    if (best == 0) break;
+    if ((id & 31) == lane) c[id] = 0;       // (that lane reads it again)
     if (j == lane) mine = id;
   }
   return mine;
@@ -163,50 +320,46 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const Args a) {
   if (row >= a.T) return;
   const bool soft = a.score == EXL3_SCORE_SOFTMAX;
 
+  const int e0 = lane * V, here = min(max(a.E - e0, 0), V);      // this lane's experts
   float l[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 32 * i;
-    l[i] = e < a.E ? load_logit<F16>(a, row, e) : neg_inf();
-  }
+  load_row<V, F16>(a, row, e0, here, l);
   // the whole row's softmax, where it is asked for
   float mx = 0.0f, inv = 1.0f;
   if (soft && (VALUE || !a.renormalise)) {
     unsigned top = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) top = max(top, lane + 32 * i < a.E ? order_key(l[i]) : 0u);
+    for (int i = 0; i < V; ++i) top = max(top, i < here ? order_key(l[i]) : 0u);
     top = __reduce_max_sync(kFull, top);
     mx = top > 1u ? key_value(top) : 0.0f;
     if (mx == neg_inf()) mx = 0.0f;              // a row that is masked throughout: scores of zero
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += lane + 32 * i < a.E ? expf(l[i] - mx) : 0.0f;
+    for (int i = 0; i < V; ++i) sum += i < here ? expf(l[i] - mx) : 0.0f;
     sum = warp_sum(sum);
     inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   }
   unsigned key[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = lane + 32 * i;
     float c = l[i];
     if (VALUE) {
       c = soft ? expf(l[i] - mx) * inv : sigmoid(l[i]);
-      if (a.bias && e < a.E) c += a.bias[e];
+      if (a.bias && i < here) c += a.bias[e0 + i];
     }
-    key[i] = e < a.E ? order_key(c) : 0u;
+    key[i] = i < here ? order_key(c) : 0u;
   }
   // Bound on the error of a computed c, apart from its last rounding: the
   // sigmoid is off by 3 roundings (2^-22), the softmax by its exponential's
   // and its sum's (32 + 5 additions: below 2^-18 of the largest score).
   const float tol = soft ? 0x1p-18f * inv : 0x1p-21f;
-  bool doubt = false;
+  bool doubt = false, again = false;       // picks or groups too close to call
 
   if (GROUPS) {
     // group values: `per` lanes to a group, every lane its share of the experts
     unsigned *keys = reinterpret_cast<unsigned *>(smem) + (size_t)warp * a.smem_per_warp / 4;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (lane + 32 * i < a.E) keys[lane + 32 * i] = key[i];
+      if (i < here) keys[e0 + i] = key[i];
     __syncwarp();
     const int size = a.E / a.groups, per = a.group_lanes, g = lane / per, sub = lane % per;
     unsigned first = 0, second = 0;
@@ -238,51 +391,74 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const Args a) {
       const int who = __ffs(__ballot_sync(kFull, left == top)) - 1;
       const float v = key_value(top);
       if (j == a.kept) {
-        if (VALUE) doubt = top > 1u && uncertain(last, v, 2.0f * tol);
+        if (VALUE) again = top > 1u && uncertain(last, v, 2.0f * tol);
       } else {
         keep |= 1u << (who / per);
         if (lane == who) left = 0;
         last = v;
       }
     }
+    int own = e0 / size, to = (own + 1) * size - e0;        // the group of expert e0 + i, and where it ends
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane + 32 * i < a.E && !(keep >> ((lane + 32 * i) / size) & 1u)) key[i] = 0;
+    for (int i = 0; i < V; ++i) {
+      if (i == to) {
+        ++own;
+        to += size;
+      }
+      if (!(keep >> (own & 31) & 1u)) key[i] = 0;
+    }
   }
 
-  int mine = -1;
+  int mine = -1, picks = 0;
   {
     unsigned best = 0;
+    int at = 0;                                            // this lane's best: its lowest place among equals
 #pragma unroll
-    for (int i = 0; i < V; ++i) best = max(best, key[i]);
-    const int picks = VALUE ? a.topk + 1 : a.topk;         // one more, to see how far off it is
+    for (int i = 0; i < V; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
+      }
     float last = 0.0f;
-    for (int j = 0; j < picks; ++j) {
+    for (int j = 0;; ++j) {
       const unsigned top = __reduce_max_sync(kFull, best);
       if (top == 0) break;                                 // (nothing behind the last pick)
-      int id = INT_MAX;
-#pragma unroll
-      for (int i = V - 1; i >= 0; --i)
-        if (key[i] == top) id = lane + 32 * i;
-      id = __reduce_min_sync(kFull, id);
-      if (VALUE) {
+      if (VALUE) {                                         // on until a pick is certainly below the topk-th
         const float v = key_value(top);
-        doubt |= j > 0 && top > 1u && uncertain(last, v, tol);
+        const bool close = j > 0 && top > 1u && uncertain(last, v, tol);
+        if (j >= a.topk && !close) break;
+        doubt |= close;
         last = v;
+        if (j == 32) {
+          again = true;
+          break;
+        }
+      } else if (j == a.topk) {
+        break;
       }
-      if (j == lane && j < a.topk) mine = id;
-      if ((id & 31) == lane) {
+      const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
+      const int id = __shfl_sync(kFull, e0 + at, owner);
+      if (j == lane) mine = id;
+      picks = j + 1;
+      if (lane == owner) {
+        const int gone = at;
         best = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          if (i == (id >> 5)) key[i] = 0;
-          best = max(best, key[i]);
+          key[i] = i == gone ? 0u : key[i];
+          if (key[i] > best) {
+            best = key[i];
+            at = i;
+          }
         }
       }
     }
   }
-  if (VALUE && doubt)
-    mine = select_exact<F16>(a, row, lane, reinterpret_cast<double *>(smem + (size_t)warp * a.smem_per_warp));
+  if (VALUE) {
+    unsigned char *mem = smem + (size_t)warp * a.smem_per_warp;
+    if (again) mine = select_pairs<F16>(a, row, lane, reinterpret_cast<unsigned long long *>(mem));
+    else if (doubt) mine = order_pairs<F16>(a, row, lane, mine, picks, reinterpret_cast<int *>(mem));
+  }
 
   // weights of the chosen
   const bool have = lane < a.topk && mine >= 0;
@@ -346,9 +522,11 @@ cudaError_t exl3_launch_route(const rt::Args &in, bool f16, cudaStream_t s) {
   rt::Args a = in;
   const bool groups = a.kept < a.groups;
   const bool value = a.bias || (groups && a.group_score == EXL3_GROUP_TOP2);
+  // wide loads: every row starts on 16 bytes (a lane's experts then start on their own size)
+  a.wide = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.stride % (f16 ? 8 : 4) == 0;
   a.group_lanes = 32;
   while (a.group_lanes * a.groups > 32) a.group_lanes /= 2;
-  // the row's values in 64 bits where a doubtful row is done again; 32-bit keys for groups
-  a.smem_per_warp = value ? (a.E * 8 + 15) / 16 * 16 : groups ? (a.E * 4 + 15) / 16 * 16 : 0;
+  // 64-bit keys where a doubtful row is done again, 32-bit keys for groups
+  a.smem_per_warp = value ? std::max(128, (a.E * 8 + 15) / 16 * 16) : groups ? (a.E * 4 + 15) / 16 * 16 : 0;
   return f16 ? launch_v<true>(a, value, groups, s) : launch_v<false>(a, value, groups, s);
 }

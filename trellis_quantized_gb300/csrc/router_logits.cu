@@ -168,6 +168,9 @@ __global__ void __launch_bounds__(kLogitThreads, 1) logits_tc_kernel(const __gri
     tc::prefetch_tmap(&mx);
     tc::prefetch_tmap(&mw);
   }
+  pdl_wait();
+  // TMEM only now: nobody ahead on the stream waits for it, and what comes next
+  // may start once all of this kernel has its own
   if (warp == 1) {
     tc::tmem_alloc(tmem_slot, a.tmem_cols);
     tc::tmem_relinquish();
@@ -176,8 +179,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) logits_tc_kernel(const __gri
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_trigger();                     // (after the allocation: the next kernel may want TMEM too)
-  pdl_wait();
+  pdl_trigger();
 
   if (warp == 0) {
     if (lane == 0) {
