@@ -695,18 +695,19 @@ int exl3_adapter_plan(const int32_t *q_start, const int32_t *adapter, int T, int
  *            done when out is y); rows that belong to no sequence are left as
  *            they were.
  *   plan     filled for the same T, batch and count = adapters->count by a call
- *            ahead on the stream (one made for others is recorded in its error
- *            word and no row is written); it is only read (except for that
- *            word), so several calls may use it at once
+ *            ahead on the stream (one made for others is recorded in the
+ *            workspace's error word and no row is written); it is only read, so
+ *            several calls may use it at once
+ *   workspace of exl3_adapter_add_workspace_size(T, max_rank) bytes
  *   x A^T is summed in fp32 and enters the second product as two fp16 parts (22
  *   bits); the sum with y is rounded once.  T = 0 enqueues nothing.  What lies in the pool past an
  *   adapter's rank is not used, but in B it has to be finite up to the next
  *   multiple of 16.  A row's bits do not depend on the other rows' contents.
- *   No workspace.
  */
+size_t exl3_adapter_add_workspace_size(int T, int max_rank);
 int exl3_adapter_add(const uint16_t *x, int64_t x_stride, const void *y, int64_t y_stride, void *out,
-                     int64_t out_stride, int dtype, const exl3_adapters *adapters, void *plan, int T, int batch,
-                     exl3_stream_t stream);
+                     int64_t out_stride, int dtype, const exl3_adapters *adapters, const void *plan, int T, int batch,
+                     void *workspace, size_t ws_bytes, exl3_stream_t stream);
 
 #ifdef __cplusplus
 }

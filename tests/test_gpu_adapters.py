@@ -83,8 +83,9 @@ def _run(rows, ids, N, R, k, n, fp32=False, ranks=None, in_place=False, seed=0, 
     plan = tq.exl3_adapter_plan(_i32(_starts(rows)), _i32(ids), T, N)
     want, tol = _reference(x, y, pool, rows, ids)
     out = y if in_place else torch.full_like(y, math.nan)
-    tq.exl3_adapter_add(x, y, tq.adapters(*pool), plan, out=out)
-    assert tq.exl3_check_device_error(plan.data) == 0
+    ws = torch.zeros(tq.exl3_adapter_add_workspace_size(T, R), dtype=torch.uint8, device="cuda")
+    tq.exl3_adapter_add(x, y, tq.adapters(*pool), plan, out=out, workspace_buf=ws)
+    assert tq.exl3_check_device_error(plan.data) == 0 and tq.exl3_check_device_error(ws) == 0
     _check(out, want, tol)
     return out
 
@@ -206,8 +207,9 @@ def test_bad_adapters_and_starts_are_recorded():
         assert (out == 7).all()
     # a plan that was never filled
     empty = tq.AdapterPlan(T, 3, 2, x.device)
-    out = tq.exl3_adapter_add(x, y, tq.adapters(*pool), empty, out=torch.full_like(y, 7.0))
-    assert (out == 7).all() and tq.exl3_check_device_error(empty.data) != 0
+    ws = torch.zeros(tq.exl3_adapter_add_workspace_size(T, 8), dtype=torch.uint8, device="cuda")
+    out = tq.exl3_adapter_add(x, y, tq.adapters(*pool), empty, out=torch.full_like(y, 7.0), workspace_buf=ws)
+    assert (out == 7).all() and tq.exl3_check_device_error(ws) != 0
 
 
 def test_many_adapters_and_sequences():

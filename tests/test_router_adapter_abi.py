@@ -54,7 +54,7 @@ def _add(p="default", **kw):
     g = lambda n, v: kw.pop(n, v)
     call = [g("x", FAKE), g("xs", 2048), g("y", FAKE), g("ys", 512), g("out", ctypes.c_void_p(0x20000)), g("os", 512),
             g("dt", 0)]
-    tail = [g("plan", FAKE), g("T", 3), g("batch", 2)]
+    tail = [g("plan", FAKE), g("T", 3), g("batch", 2), g("ws", FAKE), g("wsb", 256)]
     if p == "default":
         p = _fill(tq.Adapters, POOL, kw)
     return tq.lib().exl3_adapter_add(*call, ref(p), *tail, None)
@@ -105,7 +105,8 @@ def test_route_refuses(kw, code, text):
 
 @pytest.mark.parametrize("kw,code,text", [
     (dict(x=None), A, "x is NULL"), (dict(y=FAKE_MIS), A, "y is not"), (dict(out=None), A, "out"),
-    (dict(plan=None), W, "workspace"), (dict(plan=ctypes.c_void_p(0x10010)), W, "aligned"), (dict(dt=2), A, "dtype"),
+    (dict(plan=None), A, "plan"), (dict(plan=ctypes.c_void_p(0x10010)), A, "plan"), (dict(dt=2), A, "dtype"),
+    (dict(ws=None), W, "workspace"), (dict(wsb=255), W, "workspace"), (dict(T=1000, wsb=1000 * 16 * 4), W, "needed"),
     (dict(xs=2040), S, "x: stride"), (dict(xs=2052), S, "x: stride"), (dict(ys=508), S, "y: stride"),
     (dict(os=516), S, "out: stride"), (dict(os=520, out=FAKE), S, "strides differ"), (dict(a=None), A, "adapters.a"),
     (dict(b=FAKE_MIS.value), A, "adapters.b"), (dict(scale=None), A, "scale"), (dict(rank=FAKE_ODD.value), A, "rank"),

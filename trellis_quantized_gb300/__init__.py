@@ -178,7 +178,9 @@ def lib():
         L.exl3_adapter_plan_size.argtypes = [I, I, I]
         L.exl3_adapter_plan_size.restype = Z
         L.exl3_adapter_plan.argtypes = [P, P, I, I, I, P, Z, P]
-        L.exl3_adapter_add.argtypes = [P, L64, P, L64, P, L64, I, P, P, I, I, P]
+        L.exl3_adapter_add_workspace_size.argtypes = [I, I]
+        L.exl3_adapter_add_workspace_size.restype = Z
+        L.exl3_adapter_add.argtypes = [P, L64, P, L64, P, L64, I, P, P, I, I, P, Z, P]
         _lib = L
         return L
 
@@ -957,7 +959,17 @@ def exl3_adapter_plan(q_start, adapter, T: int, count: int, plan: AdapterPlan | 
     return plan
 
 
-def exl3_adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out=None, stream=None) -> torch.Tensor:
+def exl3_adapter_add_workspace_size(T: int, max_rank: int) -> int:
+    return lib().exl3_adapter_add_workspace_size(T, max_rank)
+
+
+@functools.lru_cache(maxsize=4096)
+def _adapter_workspace(T: int, max_rank: int) -> int:
+    return exl3_adapter_add_workspace_size(T, max_rank)
+
+
+def exl3_adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out=None, workspace_buf=None,
+                     stream=None) -> torch.Tensor:
     """y + scale (x A^T) B^T for each row's adapter: x [T, k] fp16, y [T, n] fp16 or fp32, dense
     rows; written to `out`, or to y itself (rows of no sequence are left as they were)."""
     device = _on_current(x, "x")
@@ -974,6 +986,8 @@ def exl3_adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out=None, stre
         raise ValueError(f"x has {T} rows, y {y.shape[0]}, out {out.shape[0]}, the plan {plan.T}")
     if plan.count != adapters.count:
         raise ValueError(f"the plan was made for {plan.count} adapters, the pool has {adapters.count}")
+    raw = _raw_stream(stream)
+    wp, wn = _workspace_arg(workspace_buf, _adapter_workspace(T, adapters.max_rank), x.device, stream, raw)
     _check(lib().exl3_adapter_add(xp, xs, yp, ys, op, os_, _IO_DTYPES[y.dtype], adapters._address, plan.address, T,
-                                  plan.batch, _raw_stream(stream)))
+                                  plan.batch, wp, wn, raw))
     return out

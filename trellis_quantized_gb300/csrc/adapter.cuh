@@ -15,12 +15,15 @@ constexpr int kMaxRank = 128;
 constexpr int kMaxCount = 4096;    // adapters of a plan
 
 // Words of a plan's control block (offset 0, 256 bytes; the error word first):
-// tiles of both sizes, then what the plan was made for.
-constexpr int kPlanErr = 0, kPlanStepTiles = 1, kPlanTcTiles = 2, kPlanT = 4, kPlanB = 5, kPlanN = 6;
+// tiles of both sizes, the large tiles' cost, then what the plan was made for.
+constexpr int kPlanErr = 0, kPlanStepTiles = 1, kPlanTcTiles = 2, kPlanCost = 3, kPlanT = 4, kPlanB = 5, kPlanN = 6;
+// A large tile's cost per column block, in rows, besides its rows: a block of B
+// and a product are taken whatever the rows.
+constexpr int kTileCost = 24;
 
 // A plan: control block, each sequence's place in the order, the rows in the
 // order of their adapters (rows without one last), and the tiles of both sizes
-// (adapter or -1, first place, rows, -).  Only what is known on the host goes
+// (adapter or -1, first place, rows, cost of the tiles before it).  Only what is known on the host goes
 // into the sizes.
 struct PlanLayout {
   size_t base, perm, step_tiles, tc_tiles, total;
@@ -60,10 +63,14 @@ struct Args {
   const int32_t *rank;                 // [N] or null: all R
   int N, R, k, n, T;
   int B;
-  int *ctrl;                           // the plan's control block
+  const int *ctrl;                     // the plan's control block
   const int *perm;
   const int4 *tiles;
   int max_tiles;
+  int *err;
+  // tensor cores: h of the rows in the plan's order, two parts, and scale 2^-p
+  __half *h;                           // [2][T][R]
+  float *back;                         // [T]
 };
 
 // Tiles of a plan (word `which` of its control block); none, and an error, if
@@ -72,7 +79,7 @@ __device__ __forceinline__ int plan_tiles(const Args &a, int which) {
   const int4 made = *reinterpret_cast<const int4 *>(a.ctrl + kPlanT);
   const int tiles = a.ctrl[which];
   if (made.x == a.T && made.y == a.B && made.z == a.N) return min(tiles, a.max_tiles);
-  if (threadIdx.x == 0) set_device_error(a.ctrl + kPlanErr, kErrBounds);
+  if (threadIdx.x == 0) set_device_error(a.err, kErrBounds);
   return 0;
 }
 

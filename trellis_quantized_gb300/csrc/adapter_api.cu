@@ -16,10 +16,26 @@ bool plan_shape_ok(int T, int batch, int count) {
   return T >= 0 && T <= (1 << 22) && batch >= 1 && batch <= (1 << 20) && count >= 1 && count <= exl3::ad::kMaxCount;
 }
 
+bool rank_ok(int R) { return R >= 8 && R <= exl3::ad::kMaxRank && R % 8 == 0; }
+
 int check_words(const void *p, const char *name, bool required = true) {
   if (!p) return required ? exl3_fail(EXL3_ERR_ARG, "%s is NULL", name) : EXL3_OK;
   if (reinterpret_cast<uintptr_t>(p) & 3u) return exl3_fail(EXL3_ERR_ARG, "%s is not 4-byte aligned", name);
   return EXL3_OK;
+}
+
+// ---- exl3_adapter_add workspace layout: h of all rows in two fp16 parts and
+// each row's factor, for the calls on large tiles
+struct AddWs {
+  size_t h = kCtrlBytes, back = 0, total = kCtrlBytes;
+};
+
+AddWs add_ws(int T, int R) {
+  AddWs w;
+  if (T < kTcFrom) return w;
+  w.back = align_up(w.h + (size_t)T * R * 4);
+  w.total = align_up(w.back + (size_t)T * 4);
+  return w;
 }
 
 int check_stride(const char *name, int64_t stride, int width, int per16) {
@@ -63,16 +79,21 @@ int exl3_adapter_plan(const int32_t *q_start, const int32_t *adapter, int T, int
   return exl3_cuda_check(exl3_launch_adapter_plan(p, stream), "adapter plan launch");
 }
 
+size_t exl3_adapter_add_workspace_size(int T, int max_rank) {
+  if (T < 0 || T > (1 << 22) || !rank_ok(max_rank)) return 0;
+  return add_ws(T, max_rank).total;
+}
+
 int exl3_adapter_add(const uint16_t *x, int64_t x_stride, const void *y, int64_t y_stride, void *out,
-                     int64_t out_stride, int dtype, const exl3_adapters *ad, void *plan, int T, int batch,
-                     exl3_stream_t stream) {
+                     int64_t out_stride, int dtype, const exl3_adapters *ad, const void *plan, int T, int batch,
+                     void *workspace, size_t ws_bytes, exl3_stream_t stream) {
   exl3_clear_error();
   if (!ad) return exl3_fail(EXL3_ERR_ARG, "adapters is NULL");
   if (dtype != EXL3_OUT_F16 && dtype != EXL3_OUT_F32) return exl3_fail(EXL3_ERR_ARG, "dtype %d invalid", dtype);
   if (!plan_shape_ok(T, batch, ad->count))
     return exl3_fail(EXL3_ERR_SHAPE, "T = %d (0..2^22), batch = %d (1..2^20) or count = %d (1..%d) out of range", T,
                      batch, ad->count, exl3::ad::kMaxCount);
-  if (ad->max_rank < 8 || ad->max_rank > exl3::ad::kMaxRank || ad->max_rank % 8)
+  if (!rank_ok(ad->max_rank))
     return exl3_fail(EXL3_ERR_SHAPE, "max_rank = %d must be a multiple of 8 in 8..%d", ad->max_rank, exl3::ad::kMaxRank);
   if (ad->k < 128 || ad->k % 128 || ad->n < 128 || ad->n % 128 || ad->k > (1 << 20) || ad->n > (1 << 20))
     return exl3_fail(EXL3_ERR_SHAPE, "k = %d and n = %d must be multiples of 128 up to 2^20", ad->k, ad->n);
@@ -91,7 +112,11 @@ int exl3_adapter_add(const uint16_t *x, int64_t x_stride, const void *y, int64_t
     return exl3_fail(EXL3_ERR_SHAPE, "out is y, but their strides differ: %lld and %lld", (long long)out_stride,
                      (long long)y_stride);
   const exl3::ad::PlanLayout L = exl3::ad::plan_layout(T, batch, ad->count);
-  EXL3_TRY(check_workspace(plan, L.total, L.total));
+  if (!plan) return exl3_fail(EXL3_ERR_ARG, "plan is NULL");
+  if (reinterpret_cast<uintptr_t>(plan) & (kAlign - 1))
+    return exl3_fail(EXL3_ERR_ARG, "plan is not %zu-byte aligned", kAlign);
+  const AddWs W = add_ws(T, ad->max_rank);
+  EXL3_TRY(check_workspace(workspace, ws_bytes, W.total));
   if (T == 0) return EXL3_OK;
   exl3::ad::Args a = {};
   a.x = reinterpret_cast<const __half *>(x);
@@ -110,14 +135,18 @@ int exl3_adapter_add(const uint16_t *x, int64_t x_stride, const void *y, int64_t
   a.n = ad->n;
   a.T = T;
   a.B = batch;
-  a.ctrl = at<int>(plan, 0);
-  a.perm = at<int>(plan, L.perm);
+  const auto in_plan = [&](size_t off) { return static_cast<const char *>(plan) + off; };
+  a.ctrl = reinterpret_cast<const int *>(in_plan(0));
+  a.perm = reinterpret_cast<const int *>(in_plan(L.perm));
+  a.err = at<int>(workspace, 0);
   if (T >= kTcFrom) {
-    a.tiles = at<int4>(plan, L.tc_tiles);
+    a.tiles = reinterpret_cast<const int4 *>(in_plan(L.tc_tiles));
     a.max_tiles = L.max_tc_tiles;
+    a.h = at<__half>(workspace, W.h);
+    a.back = at<float>(workspace, W.back);
     return exl3_launch_adapter_tc(a, dtype == EXL3_OUT_F32, stream);
   }
-  a.tiles = at<int4>(plan, L.step_tiles);
+  a.tiles = reinterpret_cast<const int4 *>(in_plan(L.step_tiles));
   a.max_tiles = L.max_step_tiles;
   return exl3_cuda_check(exl3_launch_adapter_step(a, dtype == EXL3_OUT_F32, stream), "adapter launch");
 }

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) adapter_plan_kernel(const PlanArgs p
   err = __syncthreads_or(err);      // (any thread's bits: told apart below)
   if (threadIdx.x == 0) p.ctrl[kPlanErr] |= bad ? kErrBounds : err ? kErrExpertId : 0;
 
-  int rows = 0, steps = 0, tcs = 0;                        // before this stretch of adapters
+  int rows = 0, steps = 0, tcs = 0, cost = 0;                        // before this stretch of adapters
   for (int i0 = 0; i0 < N1; i0 += kThreads) {
     const int i = i0 + threadIdx.x, c = i < N1 ? count[i] : 0;
     const int first = rows + block_scan(c, warp_sums, &total);
@@ -82,16 +82,21 @@ __global__ void __launch_bounds__(kThreads) adapter_plan_kernel(const PlanArgs p
     const int t0 = tcs + block_scan(nt, warp_sums, &total);
     tcs += total;
     __syncthreads();
+    const int w0 = cost + block_scan(c + nt * kTileCost, warp_sums, &total);
+    cost += total;
+    __syncthreads();
     for (int j = 0; j < ns; ++j)
       if (s0 + j < p.max_step_tiles)
         p.step_tiles[s0 + j] = make_int4(id, first + j * kStepRows, min(kStepRows, c - j * kStepRows), 0);
     for (int j = 0; j < nt; ++j)
       if (t0 + j < p.max_tc_tiles)
-        p.tc_tiles[t0 + j] = make_int4(id, first + j * kTcRows, min(kTcRows, c - j * kTcRows), 0);
+        p.tc_tiles[t0 + j] =
+            make_int4(id, first + j * kTcRows, min(kTcRows, c - j * kTcRows), w0 + j * (kTcRows + kTileCost));
   }
   if (threadIdx.x == 0) {
     p.ctrl[kPlanStepTiles] = min(steps, p.max_step_tiles);
     p.ctrl[kPlanTcTiles] = min(tcs, p.max_tc_tiles);
+    p.ctrl[kPlanCost] = cost;
     p.ctrl[kPlanT] = p.T;
     p.ctrl[kPlanB] = p.B;
     p.ctrl[kPlanN] = p.N;
