@@ -19,7 +19,7 @@ constexpr int kMaxCount = 4096;    // adapters of a plan
 constexpr int kPlanErr = 0, kPlanStepTiles = 1, kPlanTcTiles = 2, kPlanCost = 3, kPlanT = 4, kPlanB = 5, kPlanN = 6;
 // A large tile's cost per column block, in rows, besides its rows: a block of B
 // and a product are taken whatever the rows.
-constexpr int kTileCost = 24;
+constexpr int kTileCost = 96;
 
 // A plan: control block, each sequence's place in the order, the rows in the
 // order of their adapters (rows without one last), and the tiles of both sizes

@@ -128,6 +128,7 @@ __device__ __forceinline__ void store_chunk(char *p, const Chunk &c, bool wide) 
 // ------------------------------------------------------------------- h = x A^T
 
 __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_constant__ CUtensorMap mx,
+                                                                const __grid_constant__ CUtensorMap mt,
                                                                 const __grid_constant__ CUtensorMap ma,
                                                                 const InArgs g) {
   extern __shared__ uint8_t smem_raw[];
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
     *failed = 0;
     tc::fence_mbar_init();
     tc::prefetch_tmap(&mx);
+    tc::prefetch_tmap(&mt);
     tc::prefetch_tmap(&ma);
   }
   pdl_wait();
@@ -182,18 +184,26 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
       const int last = tile.z - 1, i = min(4 * lane, last);
       rows = make_int4(p[i], p[min(i + 1, last)], p[min(i + 2, last)], p[min(i + 3, last)]);
     }
+    // Rows that follow one another (a prompt's) come as one box, whose rows past the
+    // tile are somebody else's: 32 gathers take an SM a microsecond, a box a tenth.
+    const int at = __shfl_sync(0xffffffffu, rows.x, 0), n = min(4, tile.z - 4 * lane);
+    const bool box = __all_sync(0xffffffffu, lane >= quads ||
+                                                 (rows.x == at + 4 * lane && rows.y == rows.x + (n > 1) &&
+                                                  rows.z == rows.y + (n > 2) && rows.w == rows.z + (n > 3)));
     int st = 0;
     uint32_t phase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
       bool ok = true;
       if (lane == 0) {
         ok = tc::mbar_wait(&empty[st], phase ^ 1);
-        if (ok) tc::mbar_arrive_expect_tx(&full[st], quads * 512 + g.r16 * 128);
+        if (ok) tc::mbar_arrive_expect_tx(&full[st], (box ? kPanel : quads * 512) + g.r16 * 128);
         else *failed = 1;
       }
       if (!__all_sync(0xffffffffu, ok)) break;
       uint8_t *sx = ring + st * stage_bytes;
-      if (lane < quads) tma_gather4(sx + lane * 512, &mx, &full[st], kb * 64, rows);
+      if (box) {
+        if (lane == 0) tc::tma_load_2d(sx, &mt, &full[st], kb * 64, at);
+      } else if (lane < quads) tma_gather4(sx + lane * 512, &mx, &full[st], kb * 64, rows);
       if (lane == 0) tc::tma_load_3d(sx + kPanel, &ma, &full[st], kb * 64, 0, tile.x);
       if (++st == g.stages) { st = 0; phase ^= 1; }
     }
@@ -445,6 +455,9 @@ __global__ void __launch_bounds__(kOutThreads, CTAS) adapter_out_kernel(const __
     constexpr int SIZE = F32 ? 4 : 2, COLS = 32 / SIZE, GOES = 16 / COLS, CHUNKS = 2 * GOES;
     const int quarter = warp & 3, half = (warp - 2) >> 2, gr = lane >> 2, col = half * 64 + 16 * (lane & 3);
     const bool wide = g.wide;
+    const char *src = static_cast<const char *>(a.y) + col * SIZE;
+    char *dst = static_cast<char *>(a.out) + col * SIZE;
+    const int64_t y_bytes = a.y_stride * SIZE, out_bytes = a.out_stride * SIZE;
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
@@ -452,26 +465,21 @@ __global__ void __launch_bounds__(kOutThreads, CTAS) adapter_out_kernel(const __
       if (nb0 >= nb1) continue;
       const bool copy = tile.x < 0 || adapter_rank(a, tile.x) == 0;
       if (copy && a.out == a.y) continue;
-      const char *src[4];                                           // rows 16 m + g (2 m) and + 8 (2 m + 1)
-      char *dst[4];
+      int rows[4];                                                  // of m: 8 m + g; -1: none
       float f[4];
-      bool live[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const int r = 32 * quarter + 8 * m + gr;
-        live[m] = r < tile.z;
-        const int64_t row = live[m] ? a.perm[tile.y + r] : 0;
-        f[m] = live[m] && !copy ? a.back[tile.y + r] : 0.0f;
-        src[m] = static_cast<const char *>(a.y) + (row * a.y_stride + col) * SIZE;
-        dst[m] = static_cast<char *>(a.out) + (row * a.out_stride + col) * SIZE;
+        rows[m] = r < tile.z ? a.perm[tile.y + r] : -1;
+        f[m] = r < tile.z && !copy ? a.back[tile.y + r] : 0.0f;
       }
       Chunk y[2][2];
       // chunk c of a block: rows of m = c / GOES, columns COLS (c % GOES) on
       const auto load = [&](int nb, int c) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          if (live[2 * (c / GOES) + h])
-            load_chunk(y[c & 1][h], src[2 * (c / GOES) + h] + ((int64_t)nb * 128 + c % GOES * COLS) * SIZE, wide);
+          if (rows[2 * (c / GOES) + h] >= 0)
+            load_chunk(y[c & 1][h], src + rows[2 * (c / GOES) + h] * y_bytes + (nb * 128 + c % GOES * COLS) * SIZE, wide);
       };
       load(nb0, 0);
       load(nb0, 1);
@@ -496,7 +504,7 @@ __global__ void __launch_bounds__(kOutThreads, CTAS) adapter_out_kernel(const __
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int m = 2 * (c / GOES) + h;
-            if (!live[m]) continue;
+            if (rows[m] < 0) continue;
             Chunk &t = y[c & 1][h];
             if (!copy) {
 #pragma unroll
@@ -512,7 +520,7 @@ __global__ void __launch_bounds__(kOutThreads, CTAS) adapter_out_kernel(const __
                 }
               }
             }
-            store_chunk(dst[m] + ((int64_t)nb * 128 + c % GOES * COLS) * SIZE, t, wide);
+            store_chunk(dst + rows[m] * out_bytes + (nb * 128 + c % GOES * COLS) * SIZE, t, wide);
           }
           if (c + 2 < CHUNKS) load(nb, c + 2);
           else if (nb + 1 < nb1) load(nb + 1, c + 2 - CHUNKS);
@@ -562,11 +570,13 @@ int launch_in(const ad::Args &a, cudaStream_t s) {
   g.tmem_cols = 32;
   while ((int)g.tmem_cols < g.r16) g.tmem_cols *= 2;
   const size_t smem = 1024 + g.ring_bytes + 17 * 8 + 8;
-  CUtensorMap mx, ma;
+  CUtensorMap mx, mt, ma;      // x for gathers of rows and for boxes; A
   {
     const cuuint64_t dims[2] = {(cuuint64_t)a.k, (cuuint64_t)a.T}, stride[1] = {(cuuint64_t)a.x_stride * 2};
-    const cuuint32_t box[2] = {64, 1};
-    int rc = map_f16(&mx, a.x, 2, dims, stride, box);
+    const cuuint32_t row[2] = {64, 1}, box[2] = {64, ad::kTcRows};
+    int rc = map_f16(&mx, a.x, 2, dims, stride, row);
+    if (rc) return rc;
+    rc = map_f16(&mt, a.x, 2, dims, stride, box);
     if (rc) return rc;
   }
   {
@@ -593,7 +603,7 @@ int launch_in(const ad::Args &a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return exl3_cuda_check(cudaLaunchKernelEx(&cfg, ad::adapter_in_kernel, mx, ma, g), "adapter launch");
+  return exl3_cuda_check(cudaLaunchKernelEx(&cfg, ad::adapter_in_kernel, mx, mt, ma, g), "adapter launch");
 }
 
 template <bool F32, int CTAS>
