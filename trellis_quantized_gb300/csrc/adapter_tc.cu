@@ -23,9 +23,8 @@
 //
 // The accumulator is read in the layout of 16 x 256 bits: a lane gets two columns
 // of every eight for rows g and g + 8.  The copy of B permutes its rows (as a
-// tensor map of five dimensions) so that these are 16 neighbouring columns of out:
-// four lanes access one 128-byte line of y or out, and no transposition is needed.
-// (With a row to a lane, 32 lines an access, y and out ran at 3 TB/s.)
+// tensor map of five dimensions) so that these are 32 neighbouring bytes of out:
+// four lanes write one 128-byte line, and no transposition is needed.
 #include "adapter.cuh"
 #include "tc_ptx.cuh"
 
@@ -34,8 +33,8 @@ namespace ad {
 
 constexpr int kPanel = kTcRows * 128;           // bytes of 128 rows of 64 fp16
 constexpr int kInThreads = 192;                 // producer, issuer, four warps for the sums
-constexpr int kOutThreads = 320;                // producer, issuer, eight warps for the output
 constexpr int kEpiWarps = 8;
+constexpr int kOutThreads = (3 + kEpiWarps) * 32;   // producers of h and B, and of y; issuer; output
 constexpr uint32_t kOutCols = 256;              // TMEM: two accumulators
 
 struct InArgs {
@@ -48,8 +47,8 @@ struct InArgs {
 struct OutArgs {
   Args a;
   int panels;             // panels of 64 ranks
-  int stages;
-  int wide;               // y and out may be accessed 32 bytes at a time
+  int stages, y_stages;   // blocks of B; pieces of y
+  int wide;               // out may be written 32 bytes at a time
 };
 
 // Four rows of a tensor map (its box is one row), 64 columns each.
@@ -62,7 +61,7 @@ __device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *m, uin
       : "memory");
 }
 
-// 128 columns of B by 64 ranks from block z of 64 columns on, in the order that its map gives.
+// 128 columns of B by 64 ranks, from place z on in the order that its map gives.
 __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *m, uint64_t *bar, int x, int z) {
   asm volatile(
       "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %4, %4, %5}], "
@@ -98,22 +97,10 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 32 bytes of y or out: one access where the rows allow it.
+// 32 bytes of out: one store where the rows allow it.
 struct Chunk {
   uint32_t w[8];
 };
-__device__ __forceinline__ void load_chunk(Chunk &c, const char *p, bool wide) {
-  if (wide) {
-    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
-                 : "=r"(c.w[0]), "=r"(c.w[1]), "=r"(c.w[2]), "=r"(c.w[3]), "=r"(c.w[4]), "=r"(c.w[5]), "=r"(c.w[6]),
-                   "=r"(c.w[7])
-                 : "l"(p)
-                 : "memory");
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p), v = *reinterpret_cast<const uint4 *>(p + 16);
-    c = {{u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w}};
-  }
-}
 __device__ __forceinline__ void store_chunk(char *p, const Chunk &c, bool wide) {
   if (wide) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(c.w[0]), "r"(c.w[1]),
@@ -124,6 +111,37 @@ __device__ __forceinline__ void store_chunk(char *p, const Chunk &c, bool wide) 
     *reinterpret_cast<uint4 *>(p + 16) = make_uint4(c.w[4], c.w[5], c.w[6], c.w[7]);
   }
 }
+
+// The rows of a tile as one warp's copies of 128-byte pieces see them: one box
+// where they follow one another and are most of a tile (a prompt's; the box's rows
+// past the tile are somebody else's), else gathers of four, lane i rows 4 i .. 4 i
+// + 3 (past the last row: that one again).  32 gathers take an SM a microsecond, a
+// box a tenth.
+struct TileRows {
+  int4 rows;
+  int at, quads;
+  bool box;
+  __device__ __forceinline__ void load(const Args &a, const int4 &tile, int lane) {
+    const int *p = a.perm + tile.y;
+    const int last = tile.z - 1, i = min(4 * lane, last), n = min(4, tile.z - 4 * lane);
+    rows = make_int4(p[i], p[min(i + 1, last)], p[min(i + 2, last)], p[min(i + 3, last)]);
+    quads = (tile.z + 3) / 4;
+    at = __shfl_sync(0xffffffffu, rows.x, 0);
+    box = __all_sync(0xffffffffu, lane >= quads || (rows.x == at + 4 * lane && rows.y == rows.x + (n > 1) &&
+                                                    rows.z == rows.y + (n > 2) && rows.w == rows.z + (n > 3)));
+    box = box && tile.z > kTcRows / 2;
+  }
+  __device__ __forceinline__ int bytes() const { return box ? kPanel : quads * 512; }
+  // the piece at column x: `box_map` has boxes of 128 rows, `row_map` of one
+  __device__ __forceinline__ void copy(uint8_t *dst, const CUtensorMap *box_map, const CUtensorMap *row_map, uint64_t *bar,
+                                       int x, int lane) const {
+    if (box) {
+      if (lane == 0) tc::tma_load_2d(dst, box_map, bar, x, at);
+    } else if (lane < quads) {
+      tma_gather4(dst + lane * 512, row_map, bar, x, rows);
+    }
+  }
+};
 
 // ------------------------------------------------------------------- h = x A^T
 
@@ -176,34 +194,20 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
   const int stage_bytes = kPanel + g.r16 * 128;
   const int pitch = g.r16 + 4;                                      // floats between rows of sums
   if (warp == 0) {
-    // lane i gathers rows 4 i .. 4 i + 3 (past the last row: that one again)
-    const int quads = (tile.z + 3) / 4;
-    int4 rows;
-    {
-      const int *p = a.perm + tile.y;
-      const int last = tile.z - 1, i = min(4 * lane, last);
-      rows = make_int4(p[i], p[min(i + 1, last)], p[min(i + 2, last)], p[min(i + 3, last)]);
-    }
-    // Rows that follow one another (a prompt's) come as one box, whose rows past the
-    // tile are somebody else's: 32 gathers take an SM a microsecond, a box a tenth.
-    const int at = __shfl_sync(0xffffffffu, rows.x, 0), n = min(4, tile.z - 4 * lane);
-    const bool box = __all_sync(0xffffffffu, lane >= quads ||
-                                                 (rows.x == at + 4 * lane && rows.y == rows.x + (n > 1) &&
-                                                  rows.z == rows.y + (n > 2) && rows.w == rows.z + (n > 3)));
+    TileRows rows;
+    rows.load(a, tile, lane);
     int st = 0;
     uint32_t phase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
       bool ok = true;
       if (lane == 0) {
         ok = tc::mbar_wait(&empty[st], phase ^ 1);
-        if (ok) tc::mbar_arrive_expect_tx(&full[st], (box ? kPanel : quads * 512) + g.r16 * 128);
+        if (ok) tc::mbar_arrive_expect_tx(&full[st], rows.bytes() + g.r16 * 128);
         else *failed = 1;
       }
       if (!__all_sync(0xffffffffu, ok)) break;
       uint8_t *sx = ring + st * stage_bytes;
-      if (box) {
-        if (lane == 0) tc::tma_load_2d(sx, &mt, &full[st], kb * 64, at);
-      } else if (lane < quads) tma_gather4(sx + lane * 512, &mx, &full[st], kb * 64, rows);
+      rows.copy(sx, &mt, &mx, &full[st], kb * 64, lane);
       if (lane == 0) tc::tma_load_3d(sx + kPanel, &ma, &full[st], kb * 64, 0, tile.x);
       if (++st == g.stages) { st = 0; phase ^= 1; }
     }
@@ -327,16 +331,29 @@ struct Run {
   }
 };
 
-template <bool F32, int CTAS>
-__global__ void __launch_bounds__(kOutThreads, CTAS) adapter_out_kernel(const __grid_constant__ CUtensorMap mh,
-                                                                        const __grid_constant__ CUtensorMap mb,
-                                                                        const OutArgs g) {
+// A tile whose rows keep y.
+__device__ __forceinline__ bool copies(const Args &a, const int4 &tile) {
+  return tile.x < 0 || adapter_rank(a, tile.x) == 0;
+}
+
+// Warp 0 brings h and B, warp 1 issues the products, warps 2 to 9 add y and write
+// out, warp 10 brings y: pieces of 128 rows by 128 bytes, a ring of 80 to 128 KB
+// of them (loads into registers, 64 KB of them in flight, ran at 2.2 TB/s).
+template <bool F32>
+__global__ void __launch_bounds__(kOutThreads, 1) adapter_out_kernel(const __grid_constant__ CUtensorMap mh,
+                                                                     const __grid_constant__ CUtensorMap mb,
+                                                                     const __grid_constant__ CUtensorMap my,
+                                                                     const __grid_constant__ CUtensorMap mr,
+                                                                     const OutArgs g) {
+  constexpr int SIZE = F32 ? 4 : 2, PIECES = F32 ? 4 : 2, PCOLS = 128 / SIZE;   // pieces of 128 columns
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = tc::smem_u32(smem_raw);
   uint8_t *hs = smem_raw + (((raw + 1023u) & ~1023u) - raw);        // [2][panels]: hi, lo
   uint8_t *ring = hs + 2 * g.panels * kPanel;                       // B
-  uint64_t *full = reinterpret_cast<uint64_t *>(ring + g.stages * g.panels * kPanel);
-  uint64_t *empty = full + 8, *h_full = empty + 8, *h_empty = h_full + 1, *t_full = h_empty + 1, *t_empty = t_full + 2;
+  uint8_t *ys = ring + g.stages * g.panels * kPanel;                // y
+  uint64_t *full = reinterpret_cast<uint64_t *>(ys + g.y_stages * kPanel), *empty = full + 8;
+  uint64_t *y_full = empty + 8, *y_empty = y_full + 8;
+  uint64_t *h_full = y_empty + 8, *h_empty = h_full + 1, *t_full = h_empty + 1, *t_empty = t_full + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(t_empty + 2);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *first = failed + 1;
@@ -347,6 +364,8 @@ __global__ void __launch_bounds__(kOutThreads, CTAS) adapter_out_kernel(const __
     for (int s = 0; s < 8; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
+      tc::mbar_init(&y_full[s], 1);
+      tc::mbar_init(&y_empty[s], 4);
     }
     tc::mbar_init(h_full, 1);
     tc::mbar_init(h_empty, 1);
@@ -359,6 +378,8 @@ __global__ void __launch_bounds__(kOutThreads, CTAS) adapter_out_kernel(const __
     tc::fence_mbar_init();
     tc::prefetch_tmap(&mh);
     tc::prefetch_tmap(&mb);
+    tc::prefetch_tmap(&my);
+    tc::prefetch_tmap(&mr);
   }
   pdl_wait();
   if (warp == 1) {                                                  // (after the wait, as above)
@@ -389,14 +410,14 @@ __global__ void __launch_bounds__(kOutThreads, CTAS) adapter_out_kernel(const __
 
   int4 tile;
   int nb0, nb1;
+  bool ok = true;
   if (warp == 0) {
     if (lane == 0) {
       const int bytes = g.panels * kPanel;
       int st = 0;
       uint32_t phase = 0, h_phase = 0;
-      bool ok = true;
       for (int i = run.first; ok && run.part(a, i, tile, nb0, nb1); ++i) {
-        if (tile.x < 0 || nb0 >= nb1 || adapter_rank(a, tile.x) == 0) continue;
+        if (nb0 >= nb1 || copies(a, tile)) continue;
         ok = tc::mbar_wait(h_empty, h_phase ^ 1);
         if (!ok) break;
         h_phase ^= 1;
@@ -408,11 +429,10 @@ __global__ void __launch_bounds__(kOutThreads, CTAS) adapter_out_kernel(const __
           if (!ok) break;
           tc::mbar_arrive_expect_tx(&full[st], bytes);
           for (int p = 0; p < g.panels; ++p)
-            tma_load_5d(ring + st * bytes + p * kPanel, &mb, &full[st], p * 64, tile.x * (a.n / 64) + 2 * nb);
+            tma_load_5d(ring + st * bytes + p * kPanel, &mb, &full[st], p * 64, (tile.x * run.NB + nb) * (F32 ? 4 : 2));
           if (++st == g.stages) { st = 0; phase ^= 1; }
         }
       }
-      if (!ok) *failed = 1;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -420,11 +440,9 @@ __global__ void __launch_bounds__(kOutThreads, CTAS) adapter_out_kernel(const __
     const uint64_t hd = tc::sdesc_k_sw128(hs);
     int st = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0, h_phase = 0;
-    bool ok = true;
     for (int i = run.first; ok && run.part(a, i, tile, nb0, nb1); ++i) {
-      if (tile.x < 0 || nb0 >= nb1) continue;
+      if (nb0 >= nb1 || copies(a, tile)) continue;
       const int kr = (adapter_rank(a, tile.x) + 15) / 16;
-      if (kr == 0) continue;
       ok = __all_sync(0xffffffffu, tc::mbar_wait(h_full, h_phase));
       h_phase ^= 1;
       for (int nb = nb0; ok && nb < nb1; ++nb) {
@@ -440,30 +458,45 @@ __global__ void __launch_bounds__(kOutThreads, CTAS) adapter_out_kernel(const __
                           part || kk ? 1u : 0u);
             }
           tc::mma_commit(&empty[st]);
-          tc::mma_commit(&t_full[acc]);
           if (nb + 1 == nb1) tc::mma_commit(h_empty);
+          tc::mma_commit(&t_full[acc]);                             // (last: what waits for it ends the kernel)
         }
         __syncwarp();
         if (++st == g.stages) { st = 0; phase ^= 1; }
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
       }
     }
-    if (!ok) *failed = 1;
+  } else if (warp == 2 + kEpiWarps) {
+    int st = 0;
+    uint32_t phase = 0;
+    for (int i = run.first; ok && run.part(a, i, tile, nb0, nb1); ++i) {
+      if (nb0 >= nb1 || (a.out == a.y && copies(a, tile))) continue;
+      TileRows rows;
+      rows.load(a, tile, lane);
+      for (int p = nb0 * PIECES; p < nb1 * PIECES; ++p) {
+        if (lane == 0) {
+          ok = tc::mbar_wait(&y_empty[st], phase ^ 1);
+          if (ok) tc::mbar_arrive_expect_tx(&y_full[st], rows.bytes());
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        rows.copy(ys + st * kPanel, &my, &mr, &y_full[st], p * PCOLS, lane);
+        if (++st == g.y_stages) { st = 0; phase ^= 1; }
+      }
+    }
   } else {
-    // warps 2-9: 32 rows by 64 columns each, 16 rows at a time; lane: rows g and
-    // g + 8, 16 columns (fp32: eight, in two goes)
-    constexpr int SIZE = F32 ? 4 : 2, COLS = 32 / SIZE, GOES = 16 / COLS, CHUNKS = 2 * GOES;
-    const int quarter = warp & 3, half = (warp - 2) >> 2, gr = lane >> 2, col = half * 64 + 16 * (lane & 3);
+    // 32 rows by 64 columns per block and warp, 16 rows at a time; a lane: rows g
+    // and g + 8, 16 neighbouring columns (fp32: eight, in two pieces)
+    constexpr int COLS = 32 / SIZE, GOES = PIECES / 2;
+    const int quarter = warp & 3, half = (warp - 2) >> 2, gr = lane >> 2, t = lane & 3;
     const bool wide = g.wide;
-    const char *src = static_cast<const char *>(a.y) + col * SIZE;
-    char *dst = static_cast<char *>(a.out) + col * SIZE;
-    const int64_t y_bytes = a.y_stride * SIZE, out_bytes = a.out_stride * SIZE;
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    bool ok = true;
+    char *dst = static_cast<char *>(a.out) + (half * 64 + COLS * t) * SIZE;
+    const int64_t out_bytes = a.out_stride * SIZE;
+    int acc = 0, st = half * GOES;                                  // this half's first piece
+    uint32_t acc_phase = 0, phase = 0;
     for (int i = run.first; ok && run.part(a, i, tile, nb0, nb1); ++i) {
       if (nb0 >= nb1) continue;
-      const bool copy = tile.x < 0 || adapter_rank(a, tile.x) == 0;
+      const bool copy = copies(a, tile);
       if (copy && a.out == a.y) continue;
       int rows[4];                                                  // of m: 8 m + g; -1: none
       float f[4];
@@ -473,16 +506,6 @@ __global__ void __launch_bounds__(kOutThreads, CTAS) adapter_out_kernel(const __
         rows[m] = r < tile.z ? a.perm[tile.y + r] : -1;
         f[m] = r < tile.z && !copy ? a.back[tile.y + r] : 0.0f;
       }
-      Chunk y[2][2];
-      // chunk c of a block: rows of m = c / GOES, columns COLS (c % GOES) on
-      const auto load = [&](int nb, int c) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (rows[2 * (c / GOES) + h] >= 0)
-            load_chunk(y[c & 1][h], src + rows[2 * (c / GOES) + h] * y_bytes + (nb * 128 + c % GOES * COLS) * SIZE, wide);
-      };
-      load(nb0, 0);
-      load(nb0, 1);
       for (int nb = nb0; nb < nb1; ++nb) {
         if (!copy) {
           ok = __all_sync(0xffffffffu, tc::mbar_wait(&t_full[acc], acc_phase));
@@ -490,46 +513,58 @@ __global__ void __launch_bounds__(kOutThreads, CTAS) adapter_out_kernel(const __
           tc::tc_fence_after();
         }
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) {
-          float v[2 * COLS];
+        for (int go = 0; go < GOES; ++go) {
+          float v[2][2 * COLS];
           if (!copy) {
-            tmem_ld_rows(tmem + ((uint32_t)(32 * quarter + 16 * (c / GOES)) << 16) + acc * 128 + half * 64 + c % GOES * 32, v);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+              tmem_ld_rows(tmem + ((uint32_t)(32 * quarter + 16 * m) << 16) + acc * 128 + half * 64 + go * 32, v[m]);
             tc::tmem_ld_wait();
-            if (c + 1 == CHUNKS) {
+            if (go + 1 == GOES) {
               tc::tc_fence_before();
               __syncwarp();
               if (lane == 0) tc::mbar_arrive(&t_empty[acc]);
             }
           }
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(&y_full[st], phase));
+          if (!ok) break;
+          const uint8_t *piece = ys + st * kPanel;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int m = 2 * (c / GOES) + h;
-            if (rows[m] < 0) continue;
-            Chunk &t = y[c & 1][h];
+          for (int m = 0; m < 4; ++m) {
+            // 128-byte swizzle; a row's 16-byte places 2 t and 2 t + 1
+            const int r = 32 * quarter + 8 * m + gr;
+            const uint8_t *row = piece + r * 128;
+            const uint4 lo = *reinterpret_cast<const uint4 *>(row + (((2 * t) ^ (r & 7)) << 4));
+            const uint4 hi = *reinterpret_cast<const uint4 *>(row + (((2 * t + 1) ^ (r & 7)) << 4));
+            Chunk c = {{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
             if (!copy) {
 #pragma unroll
               for (int j = 0; j < COLS / 2; ++j) {
-                const float d0 = v[4 * j + 2 * h], d1 = v[4 * j + 2 * h + 1];
+                const float d0 = v[m / 2][4 * j + 2 * (m & 1)], d1 = v[m / 2][4 * j + 2 * (m & 1) + 1];
                 if (F32) {
-                  t.w[(2 * j) % 8] = __float_as_uint(fmaf(f[m], d0, __uint_as_float(t.w[(2 * j) % 8])));
-                  t.w[(2 * j + 1) % 8] = __float_as_uint(fmaf(f[m], d1, __uint_as_float(t.w[(2 * j + 1) % 8])));
+                  c.w[(2 * j) % 8] = __float_as_uint(fmaf(f[m], d0, __uint_as_float(c.w[(2 * j) % 8])));
+                  c.w[(2 * j + 1) % 8] = __float_as_uint(fmaf(f[m], d1, __uint_as_float(c.w[(2 * j + 1) % 8])));
                 } else {
-                  const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&t.w[j]));
+                  const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&c.w[j]));
                   const __half2 o = __floats2half2_rn(fmaf(f[m], d0, z.x), fmaf(f[m], d1, z.y));
-                  t.w[j] = *reinterpret_cast<const uint32_t *>(&o);
+                  c.w[j] = *reinterpret_cast<const uint32_t *>(&o);
                 }
               }
             }
-            store_chunk(dst + rows[m] * out_bytes + (nb * 128 + c % GOES * COLS) * SIZE, t, wide);
+            if (rows[m] >= 0) store_chunk(dst + rows[m] * out_bytes + (nb * 128 + go * 32) * SIZE, c, wide);
           }
-          if (c + 2 < CHUNKS) load(nb, c + 2);
-          else if (nb + 1 < nb1) load(nb + 1, c + 2 - CHUNKS);
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&y_empty[st]);
+          const int step = go + 1 < GOES ? 1 : PIECES - GOES + 1;    // over the other half's pieces
+          st += step;
+          if (st >= g.y_stages) { st -= g.y_stages; phase ^= 1; }
         }
+        if (!ok) break;
         if (!copy && ++acc == 2) { acc = 0; acc_phase ^= 1; }
       }
     }
-    if (!ok) *failed = 1;
   }
+  if (!ok) *failed = 1;
   tc::tc_fence_before();
   __syncthreads();
   if (*failed && threadIdx.x == 0) set_device_error(a.err, kErrBounds);
@@ -546,16 +581,21 @@ using namespace exl3;
 
 namespace {
 
-int map_f16(CUtensorMap *m, const void *base, int dims, const cuuint64_t *size, const cuuint64_t *stride,
-            const cuuint32_t *box) {
+int map_rows(CUtensorMap *m, const void *base, int dims, const cuuint64_t *size, const cuuint64_t *stride,
+             const cuuint32_t *box, bool f32) {
   auto fn = exl3_tmap_encode_fn();
   if (!fn) return exl3_fail(EXL3_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims, const_cast<void *>(base), size, stride, box, estr,
+  CUresult r = fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims, const_cast<void *>(base), size, stride, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return exl3_fail(EXL3_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return EXL3_OK;
+}
+
+int map_f16(CUtensorMap *m, const void *base, int dims, const cuuint64_t *size, const cuuint64_t *stride,
+            const cuuint32_t *box) {
+  return map_rows(m, base, dims, size, stride, box, false);
 }
 
 int launch_in(const ad::Args &a, cudaStream_t s) {
@@ -563,10 +603,10 @@ int launch_in(const ad::Args &a, cudaStream_t s) {
   g.a = a;
   g.r16 = (a.R + 15) / 16 * 16;
   const int stage = ad::kPanel + g.r16 * 128;
-  // a ring of 72 KB: at most three CTAs on an SM, whose 128 TMEM columns each fit
+  // Three CTAs on an SM, two above rank 64: never more than TMEM has columns for
   // (a CTA that waited for TMEM while its cluster waits for it could wait for ever)
-  g.stages = 72 * 1024 / stage;
-  g.ring_bytes = 72 * 1024;
+  g.ring_bytes = (a.R <= 64 ? 72 : 104) * 1024;
+  g.stages = std::min(8, g.ring_bytes / stage);
   g.tmem_cols = 32;
   while ((int)g.tmem_cols < g.r16) g.tmem_cols *= 2;
   const size_t smem = 1024 + g.ring_bytes + 17 * 8 + 8;
@@ -606,10 +646,10 @@ int launch_in(const ad::Args &a, cudaStream_t s) {
   return exl3_cuda_check(cudaLaunchKernelEx(&cfg, ad::adapter_in_kernel, mx, mt, ma, g), "adapter launch");
 }
 
-template <bool F32, int CTAS>
+template <bool F32>
 int launch_out(const ad::OutArgs &g, cudaStream_t s) {
   const ad::Args &a = g.a;
-  CUtensorMap mh, mb;
+  CUtensorMap mh, mb, my, mr;
   {
     const cuuint64_t dims[3] = {(cuuint64_t)a.R, (cuuint64_t)a.T, 2};
     const cuuint64_t stride[2] = {(cuuint64_t)a.R * 2, (cuuint64_t)a.T * a.R * 2};
@@ -618,19 +658,29 @@ int launch_out(const ad::OutArgs &g, cudaStream_t s) {
     if (rc) return rc;
   }
   {
-    // column 16 t + 2 j + b of 64 goes to row 8 j + 2 t + b of the operand
-    const cuuint64_t R = a.R, dims[5] = {R, 2, 4, 8, (cuuint64_t)a.n / 64 * a.N};
-    const cuuint64_t stride[4] = {R * 2, R * 32, R * 4, R * 128};
-    const cuuint32_t box[5] = {64, 2, 4, 8, 2};
+    // fp16: column 16 t + 2 j + b of 64 goes to row 8 j + 2 t + b of the operand,
+    // fp32: column 8 t + 2 j + b of 32 (32 bytes a lane either way)
+    const cuuint64_t R = a.R, J = F32 ? 4 : 8;
+    const cuuint64_t dims[5] = {R, 2, 4, J, (cuuint64_t)a.n / (8 * J) * a.N};
+    const cuuint64_t stride[4] = {R * 2, R * 2 * J * 2, R * 4, R * 8 * J * 2};
+    const cuuint32_t box[5] = {64, 2, 4, (cuuint32_t)J, F32 ? 4u : 2u};
     int rc = map_f16(&mb, a.b, 5, dims, stride, box);
     if (rc) return rc;
   }
-  const size_t smem = 1024 + (2 + g.stages) * (size_t)g.panels * ad::kPanel + 22 * 8 + 16;
-  auto kfn = ad::adapter_out_kernel<F32, CTAS>;
+  {
+    const cuuint64_t dims[2] = {(cuuint64_t)a.n, (cuuint64_t)a.T}, stride[1] = {(cuuint64_t)a.y_stride * (F32 ? 4 : 2)};
+    const cuuint32_t box[2] = {F32 ? 32u : 64u, ad::kTcRows}, row[2] = {F32 ? 32u : 64u, 1};
+    int rc = map_rows(&my, a.y, 2, dims, stride, box, F32);
+    if (rc) return rc;
+    rc = map_rows(&mr, a.y, 2, dims, stride, row, F32);
+    if (rc) return rc;
+  }
+  const size_t smem = 1024 + ((2 + g.stages) * (size_t)g.panels + g.y_stages) * ad::kPanel + 38 * 8 + 16;
+  auto kfn = ad::adapter_out_kernel<F32>;
   static std::atomic<size_t> given[kMaxDevices];
   int rc = exl3_cuda_check(exl3_ensure_smem(reinterpret_cast<const void *>(kfn), smem, given), "adapter attribute");
   if (rc) return rc;
-  return exl3_cuda_check(launch_pdl(kfn, dim3(exl3_sm_count() * CTAS), dim3(ad::kOutThreads), smem, s, mh, mb, g),
+  return exl3_cuda_check(launch_pdl(kfn, dim3(exl3_sm_count()), dim3(ad::kOutThreads), smem, s, mh, mb, my, mr, g),
                          "adapter launch");
 }
 
@@ -642,13 +692,11 @@ int exl3_launch_adapter_tc(const ad::Args &a, bool f32, cudaStream_t s) {
   ad::OutArgs g = {};
   g.a = a;
   g.panels = (a.R + 63) / 64;
-  // Up to rank 64 two CTAs on an SM (operands of 32 KB, a ring of 64), above it one
-  g.stages = g.panels == 1 ? 4 : 3;
-  const int size = f32 ? 4 : 2;
-  const auto on32 = [&](const void *p, int64_t stride) {
-    return reinterpret_cast<uintptr_t>(p) % 32 == 0 && stride * size % 32 == 0;
-  };
-  g.wide = on32(a.y, a.y_stride) && on32(a.out, a.out_stride);
-  if (g.panels == 1) return f32 ? launch_out<true, 2>(g, s) : launch_out<false, 2>(g, s);
-  return f32 ? launch_out<true, 1>(g, s) : launch_out<false, 1>(g, s);
+  // 192 to 224 KB: h, blocks of B, pieces of y.  The places for pieces are a multiple
+  // of a block's pieces, so that a place always serves the same four warps: a
+  // warp that did not see each of its phases could not tell them apart.
+  g.stages = g.panels == 1 ? 3 : 2;
+  g.y_stages = g.panels == 1 ? 8 : f32 ? 4 : 6;
+  g.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride * (f32 ? 4 : 2) % 32 == 0;
+  return f32 ? launch_out<true>(g, s) : launch_out<false>(g, s);
 }
