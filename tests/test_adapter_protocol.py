@@ -84,10 +84,11 @@ def _fault(blocks, pieces, places, b_stages=2):
     return None
 
 
+@pytest.mark.parametrize("b_stages", [1, 2])
 @pytest.mark.parametrize("pieces,places,blocks", [(2, 4, 5), (2, 6, 4), (4, 4, 4)])
-def test_every_wait_sees_its_own_phase(pieces, places, blocks):
+def test_every_wait_sees_its_own_phase(pieces, places, blocks, b_stages):
     """fp16 (two pieces to a block) and fp32 (four), rings that are whole blocks."""
-    assert _fault(blocks, pieces, places) is None
+    assert _fault(blocks, pieces, places, b_stages) is None
 
 
 def test_places_that_change_hands_can_be_passed_early():

@@ -47,11 +47,47 @@ __device__ __forceinline__ uint4 load16(const __half *p, bool ok) {
   return ok ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0, 0, 0, 0);
 }
 
+// Eight neighbouring elements of y, and out = y + v.
+template <bool F32>
+struct Out;
+template <>
+struct Out<false> {
+  uint4 y;
+  __device__ __forceinline__ void load(const void *p, int64_t at) {
+    y = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(p) + at);
+  }
+  __device__ __forceinline__ void add_store(const float (&v)[8], void *p, int64_t at) const {
+    uint4 o = y;
+    __half2 *h = reinterpret_cast<__half2 *>(&o);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 t = __half22float2(h[j]);
+      h[j] = __floats2half2_rn(t.x + v[2 * j], t.y + v[2 * j + 1]);
+    }
+    *reinterpret_cast<uint4 *>(static_cast<__half *>(p) + at) = o;
+  }
+};
+template <>
+struct Out<true> {
+  float4 y0, y1;
+  __device__ __forceinline__ void load(const void *p, int64_t at) {
+    const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
+    y0 = src[0];
+    y1 = src[1];
+  }
+  __device__ __forceinline__ void add_store(const float (&v)[8], void *p, int64_t at) const {
+    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
+    dst[0] = make_float4(y0.x + v[0], y0.y + v[1], y0.z + v[2], y0.w + v[3]);
+    dst[1] = make_float4(y1.x + v[4], y1.y + v[5], y1.z + v[6], y1.w + v[7]);
+  }
+};
+
 // RT: 8-wide tiles of ranks per warp; RG warps share the ranks (RT 8: up to 64 each).
 template <int RT, int RG, bool F32>
 __global__ void __launch_bounds__(kStepThreads) adapter_step_kernel(const Args a) {
   constexpr int RMAX = RT * RG * 8, KW = kStepWarps / RG;       // warps that share k
   constexpr int HP = RMAX + 8;                                  // halves between rows of h: other banks
+  constexpr int NC = RMAX > 32 ? 2 : 1;                         // blocks of 32 ranks of B held ahead
   __shared__ __align__(16) float part[KW][kStepRows][RMAX];     // each warp's sums
   __shared__ __align__(16) float own[kStepRows][RMAX];          // this CTA's
   // the cluster's, hi and lo, where the warps' sums were (read before the cluster's barrier)
@@ -84,7 +120,8 @@ __global__ void __launch_bounds__(kStepThreads) adapter_step_kernel(const Args a
     const int u0 = (int)((int64_t)units * split / S), u1 = (int)((int64_t)units * (split + 1) / S);
     const __half *x0 = a.x + t0 * a.x_stride + q * 8, *x1 = a.x + t1 * a.x_stride + q * 8;
     const __half *ar = A + (int64_t)(j0 * 8 + g) * a.k + q * 8;
-#pragma unroll 2
+    // (all of a warp's loads on their way at once where the registers allow it)
+#pragma unroll(RT <= 2 ? 4 : 2)
     for (int u = u0 + warp / RG; u < u1; u += KW) {
       const uint4 lo = load16(x0 + u * 32, ok0), hi = load16(x1 + u * 32, ok1);
       uint4 w[RT];
@@ -100,6 +137,25 @@ __global__ void __launch_bounds__(kStepThreads) adapter_step_kernel(const Args a
       *reinterpret_cast<float2 *>(p + (g + 8) * RMAX + j * 8 + 2 * q) = make_float2(acc[j][2], acc[j][3]);
     }
   }
+  // the first columns' B and y, on their way while h is put together
+  const int units = a.n / 32, R32 = (rank + 31) / 32, ustep = S * kStepWarps;
+  const int ncol = 8 * (g >> 1) + (g & 1);                      // column g of the j-th tile: ncol + 2 j
+  const auto load_b = [&](int u, int c, uint4 (&w)[4]) {
+    const __half *br = B + (int64_t)(u * 32 + ncol) * a.R + c * 32 + q * 8;
+    const bool ok = u < units && c * 4 + q < R8;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = load16(br + (int64_t)2 * j * a.R, ok);
+  };
+  const auto load_y = [&](int u, Out<F32> (&y)[2]) {
+    if (u < units && ok0) y[0].load(a.y, t0 * a.y_stride + u * 32 + q * 8);
+    if (u < units && ok1) y[1].load(a.y, t1 * a.y_stride + u * 32 + q * 8);
+  };
+  int u = split * kStepWarps + warp;
+  uint4 w_next[NC][4];
+  Out<F32> y_next[2] = {};
+#pragma unroll
+  for (int c = 0; c < NC; ++c) load_b(u, c, w_next[c]);
+  load_y(u, y_next);
   __syncthreads();
   for (int i = threadIdx.x; i < kStepRows * RMAX; i += kStepThreads) {
     float v = 0.0f;
@@ -115,6 +171,7 @@ __global__ void __launch_bounds__(kStepThreads) adapter_step_kernel(const Args a
     float v[PER], top = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) v[i] = 0.0f;
+#pragma unroll 4
     for (int s = 0; s < S; ++s) {
       const uint32_t at = map_rank(tc::smem_u32(&own[r][0]), s);
 #pragma unroll
@@ -145,24 +202,25 @@ __global__ void __launch_bounds__(kStepThreads) adapter_step_kernel(const Args a
 
   // this CTA's columns, 32 per warp and turn
   const float f0 = back[g], f1 = back[g + 8];
-  const int units = a.n / 32, R32 = (rank + 31) / 32;
-  const int ncol = 8 * (g >> 1) + (g & 1);                      // column g of the j-th tile: ncol + 2 j
-  for (int u = split * kStepWarps + warp; u < units; u += S * kStepWarps) {
+  for (; u < units; u += ustep) {
     float d[4][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) d[j][i] = 0.0f;
-    const __half *br = B + (int64_t)(u * 32 + ncol) * a.R + q * 8;
-#pragma unroll 2
-    for (int c = 0; c < R32; ++c) {
-      uint4 w[4];
-      const bool ok = c * 4 + q < R8;
+    uint4 w[NC][4];
+    Out<F32> y[2] = {y_next[0], y_next[1]};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = load16(br + (int64_t)2 * j * a.R + c * 32, ok);
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[c][j] = w_next[c][j];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) load_b(u + ustep, c, w_next[c]);
+    load_y(u + ustep, y_next);
+    const auto product = [&](int c, const uint4 (&b)[4]) {
       const int at = c * 32 + q * 8;
       uint4 l0 = make_uint4(0, 0, 0, 0), h0 = l0, l1 = l0, h1 = l0;
-      if (ok) {
+      if (c * 4 + q < R8) {
         l0 = *reinterpret_cast<const uint4 *>(&hs[0][g][at]);
         h0 = *reinterpret_cast<const uint4 *>(&hs[0][g + 8][at]);
         l1 = *reinterpret_cast<const uint4 *>(&hs[1][g][at]);
@@ -170,35 +228,31 @@ __global__ void __launch_bounds__(kStepThreads) adapter_step_kernel(const Args a
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        mma_pair(d[j], l0, h0, w[j]);
-        mma_pair(d[j], l1, h1, w[j]);
+        mma_pair(d[j], l0, h0, b[j]);
+        mma_pair(d[j], l1, h1, b[j]);
+      }
+    };
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      if (c < R32) product(c, w[c]);
+    if (RMAX > 64) {
+      for (int c = NC; c < R32; ++c) {
+        load_b(u, c, w[0]);
+        product(c, w[0]);
       }
     }
-    const int col = u * 32 + q * 8;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      if (!(r ? ok1 : ok0)) continue;
-      const int64_t t = r ? t1 : t0;
-      const float f = r ? f1 : f0;
-      if (F32) {
-        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.y) + t * a.y_stride + col);
-        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + t * a.out_stride + col);
-        const float4 y0 = src[0], y1 = src[1];
-        dst[0] = make_float4(fmaf(f, d[0][2 * r], y0.x), fmaf(f, d[0][2 * r + 1], y0.y), fmaf(f, d[1][2 * r], y0.z),
-                             fmaf(f, d[1][2 * r + 1], y0.w));
-        dst[1] = make_float4(fmaf(f, d[2][2 * r], y1.x), fmaf(f, d[2][2 * r + 1], y1.y), fmaf(f, d[3][2 * r], y1.z),
-                             fmaf(f, d[3][2 * r + 1], y1.w));
-      } else {
-        uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(a.y) + t * a.y_stride + col);
-        __half2 *h = reinterpret_cast<__half2 *>(&v);
+    for (int r = 0; r < 2; ++r)
+      if (r ? ok1 : ok0) {
+        const float f = r ? f1 : f0;
+        float v[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 y = __half22float2(h[j]);
-          h[j] = __floats2half2_rn(fmaf(f, d[j][2 * r], y.x), fmaf(f, d[j][2 * r + 1], y.y));
+          v[2 * j] = f * d[j][2 * r];
+          v[2 * j + 1] = f * d[j][2 * r + 1];
         }
-        *reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + t * a.out_stride + col) = v;
+        y[r].add_store(v, a.out, (r ? t1 : t0) * a.out_stride + u * 32 + q * 8);
       }
-    }
   }
   cluster_wait();
 }
@@ -213,6 +267,18 @@ namespace {
 template <int RT, int RG>
 cudaError_t launch_step(const ad::Args &a, bool f32, int S, cudaStream_t s) {
   auto kfn = f32 ? ad::adapter_step_kernel<RT, RG, true> : ad::adapter_step_kernel<RT, RG, false>;
+  if (S > 8) {
+    // (sixteen CTAs are more than every device has to grant: asked for per function and device)
+    static std::atomic<bool> granted[2][kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= kMaxDevices || !granted[f32][dev].load(std::memory_order_acquire)) {
+      e = cudaFuncSetAttribute(kfn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      if (dev < kMaxDevices) granted[f32][dev].store(true, std::memory_order_release);
+    }
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -231,7 +297,8 @@ cudaError_t launch_step(const ad::Args &a, bool f32, int S, cudaStream_t s) {
 }  // namespace
 
 cudaError_t exl3_launch_adapter_step(const ad::Args &a, bool f32, cudaStream_t s) {
-  const int S = 8;
+  // a cluster of sixteen while that is at most one CTA per SM, else of eight
+  const int S = (int64_t)a.max_tiles * 16 <= exl3_sm_count() ? 16 : 8;
   if (a.R <= 16) return launch_step<2, 1>(a, f32, S, s);
   if (a.R <= 32) return launch_step<4, 1>(a, f32, S, s);
   if (a.R <= 64) return launch_step<8, 1>(a, f32, S, s);

@@ -33,9 +33,11 @@ namespace ad {
 
 constexpr int kPanel = kTcRows * 128;           // bytes of 128 rows of 64 fp16
 constexpr int kInThreads = 192;                 // producer, issuer, four warps for the sums
+constexpr int kSplit = 8;                       // CTAs of a cluster: shares of k
 constexpr int kEpiWarps = 8;
 constexpr int kOutThreads = (3 + kEpiWarps) * 32;   // producers of h and B, and of y; issuer; output
 constexpr uint32_t kOutCols = 256;              // TMEM: two accumulators
+constexpr int kYPlaces = 10;                    // at most, for pieces of y
 
 struct InArgs {
   Args a;
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const Args &a = g.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, S = gridDim.x, split = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, split = blockIdx.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 8; ++s) {
@@ -173,11 +175,28 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
   pdl_wait();
   const int tiles = plan_tiles(a, kPlanTcTiles);
   const int4 tile = a.tiles[blockIdx.y];
-  const int rank = (int)blockIdx.y < tiles && tile.x >= 0 ? adapter_rank(a, tile.x) : 0;
+  const bool some = (int)blockIdx.y < tiles && tile.x >= 0;
+  TileRows rows;
+  if (some && warp == 0) rows.load(a, tile, lane);                  // (beside the rank's load)
+  const int rank = some ? adapter_rank(a, tile.x) : 0;
   if (rank == 0) {                                                  // (the whole cluster)
     pdl_trigger();
     return;
   }
+  const int KB = a.k / 64, kb0 = KB * split / kSplit, kb1 = KB * (split + 1) / kSplit;
+  const int stage_bytes = kPanel + g.r16 * 128;
+  const int pitch = g.r16 + 4;                                      // floats between rows of sums
+  const auto bring = [&](int st, int kb) {                          // (warp 0)
+    if (lane == 0) tc::mbar_arrive_expect_tx(&full[st], rows.bytes() + g.r16 * 128);
+    __syncwarp();
+    uint8_t *sx = ring + st * stage_bytes;
+    rows.copy(sx, &mt, &mx, &full[st], kb * 64, lane);
+    if (lane == 0) tc::tma_load_3d(sx + kPanel, &ma, &full[st], kb * 64, 0, tile.x);
+  };
+  const int ahead = min(kb1, kb0 + g.stages);
+  __syncwarp();
+  if (warp == 0)                                                    // the ring's first round
+    for (int kb = kb0; kb < ahead; ++kb) bring(kb - kb0, kb);
   // TMEM only now: nobody ahead on the stream waits for it, and what comes next
   // may start once all of this kernel has its own
   if (warp == 1) {
@@ -190,25 +209,16 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
   const uint32_t tmem = *tmem_slot;
   pdl_trigger();
 
-  const int KB = a.k / 64, kb0 = KB * split / S, kb1 = KB * (split + 1) / S;
-  const int stage_bytes = kPanel + g.r16 * 128;
-  const int pitch = g.r16 + 4;                                      // floats between rows of sums
   if (warp == 0) {
-    TileRows rows;
-    rows.load(a, tile, lane);
     int st = 0;
     uint32_t phase = 0;
-    for (int kb = kb0; kb < kb1; ++kb) {
-      bool ok = true;
-      if (lane == 0) {
-        ok = tc::mbar_wait(&empty[st], phase ^ 1);
-        if (ok) tc::mbar_arrive_expect_tx(&full[st], rows.bytes() + g.r16 * 128);
-        else *failed = 1;
+    for (int kb = ahead; kb < kb1; ++kb) {
+      const bool ok = __all_sync(0xffffffffu, lane != 0 || tc::mbar_wait(&empty[st], phase));
+      if (!ok) {
+        *failed = 1;
+        break;
       }
-      if (!__all_sync(0xffffffffu, ok)) break;
-      uint8_t *sx = ring + st * stage_bytes;
-      rows.copy(sx, &mt, &mx, &full[st], kb * 64, lane);
-      if (lane == 0) tc::tma_load_3d(sx + kPanel, &ma, &full[st], kb * 64, 0, tile.x);
+      bring(st, kb);
       if (++st == g.stages) { st = 0; phase ^= 1; }
     }
   } else if (warp == 1) {
@@ -258,7 +268,8 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
 
   // 16 threads to a row, eight ranks each (a half-warp stays whole: a CTA's rows are a multiple of 16)
   if (warp >= 2) {
-    const int per = kTcRows / S, t = threadIdx.x - 64, c = 8 * (t & 15);
+    constexpr int per = kTcRows / kSplit;
+    const int t = threadIdx.x - 64, c = 8 * (t & 15);
     for (int r0 = t >> 4; r0 < per; r0 += 8) {
       const int r = split * per + r0;
       float v[8];
@@ -266,11 +277,17 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
       for (int i = 0; i < 8; ++i) v[i] = 0.0f;
       if (c < g.r16) {
         const uint32_t at = tc::smem_u32(ring) + (uint32_t)(r * pitch + c) * 4;
-        for (int s = 0; s < S; ++s) {
+        float4 p[kSplit], q[kSplit];                                // (all on their way at once)
+#pragma unroll
+        for (int s = 0; s < kSplit; ++s) {
           const uint32_t from = map_rank(at, s);
-          const float4 p = ld_cluster4(from), q = ld_cluster4(from + 16);
-          v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
-          v[4] += q.x; v[5] += q.y; v[6] += q.z; v[7] += q.w;
+          p[s] = ld_cluster4(from);
+          q[s] = ld_cluster4(from + 16);
+        }
+#pragma unroll
+        for (int s = 0; s < kSplit; ++s) {
+          v[0] += p[s].x; v[1] += p[s].y; v[2] += p[s].z; v[3] += p[s].w;
+          v[4] += q[s].x; v[5] += q[s].y; v[6] += q[s].z; v[7] += q[s].w;
         }
       }
       float top = 0.0f;
@@ -337,8 +354,8 @@ __device__ __forceinline__ bool copies(const Args &a, const int4 &tile) {
 }
 
 // Warp 0 brings h and B, warp 1 issues the products, warps 2 to 9 add y and write
-// out, warp 10 brings y: pieces of 128 rows by 128 bytes, a ring of 80 to 128 KB
-// of them (loads into registers, 64 KB of them in flight, ran at 2.2 TB/s).
+// out, warp 10 brings y: pieces of 128 rows by 128 bytes, a ring of 128 or 160
+// KB of them (loads into registers, 64 KB of them in flight, ran at 2.2 TB/s).
 template <bool F32>
 __global__ void __launch_bounds__(kOutThreads, 1) adapter_out_kernel(const __grid_constant__ CUtensorMap mh,
                                                                      const __grid_constant__ CUtensorMap mb,
@@ -351,9 +368,9 @@ __global__ void __launch_bounds__(kOutThreads, 1) adapter_out_kernel(const __gri
   uint8_t *hs = smem_raw + (((raw + 1023u) & ~1023u) - raw);        // [2][panels]: hi, lo
   uint8_t *ring = hs + 2 * g.panels * kPanel;                       // B
   uint8_t *ys = ring + g.stages * g.panels * kPanel;                // y
-  uint64_t *full = reinterpret_cast<uint64_t *>(ys + g.y_stages * kPanel), *empty = full + 8;
-  uint64_t *y_full = empty + 8, *y_empty = y_full + 8;
-  uint64_t *h_full = y_empty + 8, *h_empty = h_full + 1, *t_full = h_empty + 1, *t_empty = t_full + 2;
+  uint64_t *full = reinterpret_cast<uint64_t *>(ys + g.y_stages * kPanel), *empty = full + 2;
+  uint64_t *y_full = empty + 2, *y_empty = y_full + kYPlaces;
+  uint64_t *h_full = y_empty + kYPlaces, *h_empty = h_full + 1, *t_full = h_empty + 1, *t_empty = t_full + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(t_empty + 2);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *first = failed + 1;
@@ -361,9 +378,11 @@ __global__ void __launch_bounds__(kOutThreads, 1) adapter_out_kernel(const __gri
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 8; ++s) {
+    for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kYPlaces; ++s) {
       tc::mbar_init(&y_full[s], 1);
       tc::mbar_init(&y_empty[s], 4);
     }
@@ -634,10 +653,10 @@ int launch_in(const ad::Args &a, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 8;
+  attr[1].val.clusterDim.x = ad::kSplit;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(8, a.max_tiles);
+  cfg.gridDim = dim3(ad::kSplit, a.max_tiles);
   cfg.blockDim = dim3(ad::kInThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -675,7 +694,7 @@ int launch_out(const ad::OutArgs &g, cudaStream_t s) {
     rc = map_rows(&mr, a.y, 2, dims, stride, row, F32);
     if (rc) return rc;
   }
-  const size_t smem = 1024 + ((2 + g.stages) * (size_t)g.panels + g.y_stages) * ad::kPanel + 38 * 8 + 16;
+  const size_t smem = 1024 + ((2 + g.stages) * (size_t)g.panels + g.y_stages) * ad::kPanel + (10 + 2 * ad::kYPlaces) * 8 + 16;
   auto kfn = ad::adapter_out_kernel<F32>;
   static std::atomic<size_t> given[kMaxDevices];
   int rc = exl3_cuda_check(exl3_ensure_smem(reinterpret_cast<const void *>(kfn), smem, given), "adapter attribute");
@@ -692,11 +711,12 @@ int exl3_launch_adapter_tc(const ad::Args &a, bool f32, cudaStream_t s) {
   ad::OutArgs g = {};
   g.a = a;
   g.panels = (a.R + 63) / 64;
-  // 192 to 224 KB: h, blocks of B, pieces of y.  The places for pieces are a multiple
+  // 224 or 208 KB: h, blocks of B (the next one comes while this one's products are
+  // written out), pieces of y.  The places for pieces are a multiple
   // of a block's pieces, so that a place always serves the same four warps: a
   // warp that did not see each of its phases could not tell them apart.
-  g.stages = g.panels == 1 ? 3 : 2;
-  g.y_stages = g.panels == 1 ? 8 : f32 ? 4 : 6;
+  g.stages = g.panels == 1 ? 2 : 1;
+  g.y_stages = g.panels == 1 && !f32 ? 10 : 8;
   g.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride * (f32 ? 4 : 2) % 32 == 0;
   return f32 ? launch_out<true>(g, s) : launch_out<false>(g, s);
 }

@@ -169,6 +169,16 @@ __global__ void __launch_bounds__(kLogitThreads, 1) logits_tc_kernel(const __gri
     tc::prefetch_tmap(&mw);
   }
   pdl_wait();
+  const auto bring = [&](int st, int kb) {                  // (one thread)
+    uint8_t *sa = smem + st * stage_bytes, *sb = sa + BM * BK * 2;
+    tc::mbar_arrive_expect_tx(&full[st], stage_bytes);
+    tc::tma_load_2d(sa, &mx, &full[st], kb * BK, m0);
+    tc::tma_load_2d(sb, &mw, &full[st], kb * BK, n0);
+    if (PACKED) tc::tma_load_2d(sb + a.bn * BK * 2, &mw, &full[st], kb * BK, a.E + n0);
+  };
+  const int ahead = min(kb1, kb0 + a.stages);
+  if (threadIdx.x == 0)                                     // the ring's first round
+    for (int kb = kb0; kb < ahead; ++kb) bring(kb - kb0, kb);
   // TMEM only now: nobody ahead on the stream waits for it, and what comes next
   // may start once all of this kernel has its own
   if (warp == 1) {
@@ -185,16 +195,12 @@ __global__ void __launch_bounds__(kLogitThreads, 1) logits_tc_kernel(const __gri
     if (lane == 0) {
       int st = 0;
       uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!tc::mbar_wait(&empty[st], phase ^ 1)) {
+      for (int kb = ahead; kb < kb1; ++kb) {
+        if (!tc::mbar_wait(&empty[st], phase)) {
           *failed = 1;
           break;
         }
-        uint8_t *sa = smem + st * stage_bytes, *sb = sa + BM * BK * 2;
-        tc::mbar_arrive_expect_tx(&full[st], stage_bytes);
-        tc::tma_load_2d(sa, &mx, &full[st], kb * BK, m0);
-        tc::tma_load_2d(sb, &mw, &full[st], kb * BK, n0);
-        if (PACKED) tc::tma_load_2d(sb + a.bn * BK * 2, &mw, &full[st], kb * BK, a.E + n0);
+        bring(st, kb);
         if (++st == a.stages) { st = 0; phase ^= 1; }
       }
     }
@@ -254,14 +260,19 @@ __global__ void __launch_bounds__(kLogitThreads, 1) logits_tc_kernel(const __gri
       if (t >= a.T || e >= a.E) continue;
       const uint32_t at = base + (uint32_t)(r * a.pitch + c) * 4;
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f), lo = v;
-      for (int s = 0; s < S; ++s) {
-        const float4 p = ld_cluster4(at, s);
-        v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
-        if (PACKED) {
-          const float4 q = ld_cluster4(at + a.bn * 4, s);
-          lo.x += q.x; lo.y += q.y; lo.z += q.z; lo.w += q.w;
+      float4 p[8], q[8];                                    // (all on their way at once)
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s < S) {
+          p[s] = ld_cluster4(at, s);
+          if (PACKED) q[s] = ld_cluster4(at + a.bn * 4, s);
         }
-      }
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s < S) {
+          v.x += p[s].x; v.y += p[s].y; v.z += p[s].z; v.w += p[s].w;
+          if (PACKED) { lo.x += q[s].x; lo.y += q[s].y; lo.z += q[s].z; lo.w += q[s].w; }
+        }
       float o[4] = {v.x, v.y, v.z, v.w};
       const float l[4] = {lo.x, lo.y, lo.z, lo.w};
       float *dst = a.logits + (int64_t)t * a.E + e;
