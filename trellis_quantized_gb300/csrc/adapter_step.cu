@@ -84,7 +84,7 @@ struct Out<true> {
 
 // RT: 8-wide tiles of ranks per warp; RG warps share the ranks (RT 8: up to 64 each).
 template <int RT, int RG, bool F32>
-__global__ void __launch_bounds__(kStepThreads) adapter_step_kernel(const Args a) {
+__global__ void __launch_bounds__(kStepThreads, 2) adapter_step_kernel(const Args a) {
   constexpr int RMAX = RT * RG * 8, KW = kStepWarps / RG;       // warps that share k
   constexpr int HP = RMAX + 8;                                  // halves between rows of h: other banks
   constexpr int NC = RMAX > 32 ? 2 : 1;                         // blocks of 32 ranks of B held ahead

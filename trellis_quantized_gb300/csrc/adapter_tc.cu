@@ -33,11 +33,10 @@ namespace ad {
 
 constexpr int kPanel = kTcRows * 128;           // bytes of 128 rows of 64 fp16
 constexpr int kInThreads = 192;                 // producer, issuer, four warps for the sums
-constexpr int kSplit = 8;                       // CTAs of a cluster: shares of k
 constexpr int kEpiWarps = 8;
 constexpr int kOutThreads = (3 + kEpiWarps) * 32;   // producers of h and B, and of y; issuer; output
 constexpr uint32_t kOutCols = 256;              // TMEM: two accumulators
-constexpr int kYPlaces = 10;                    // at most, for pieces of y
+constexpr int kBStages = 6, kYPlaces = 10;      // at most: blocks of B, pieces of y
 
 struct InArgs {
   Args a;
@@ -147,6 +146,8 @@ struct TileRows {
 
 // ------------------------------------------------------------------- h = x A^T
 
+// S: CTAs of a cluster, shares of k.
+template <int S>
 __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_constant__ CUtensorMap mx,
                                                                 const __grid_constant__ CUtensorMap mt,
                                                                 const __grid_constant__ CUtensorMap ma,
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
     pdl_trigger();
     return;
   }
-  const int KB = a.k / 64, kb0 = KB * split / kSplit, kb1 = KB * (split + 1) / kSplit;
+  const int KB = a.k / 64, kb0 = KB * split / S, kb1 = KB * (split + 1) / S;
   const int stage_bytes = kPanel + g.r16 * 128;
   const int pitch = g.r16 + 4;                                      // floats between rows of sums
   const auto bring = [&](int st, int kb) {                          // (warp 0)
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
 
   // 16 threads to a row, eight ranks each (a half-warp stays whole: a CTA's rows are a multiple of 16)
   if (warp >= 2) {
-    constexpr int per = kTcRows / kSplit;
+    constexpr int per = kTcRows / S;
     const int t = threadIdx.x - 64, c = 8 * (t & 15);
     for (int r0 = t >> 4; r0 < per; r0 += 8) {
       const int r = split * per + r0;
@@ -277,15 +278,15 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
       for (int i = 0; i < 8; ++i) v[i] = 0.0f;
       if (c < g.r16) {
         const uint32_t at = tc::smem_u32(ring) + (uint32_t)(r * pitch + c) * 4;
-        float4 p[kSplit], q[kSplit];                                // (all on their way at once)
+        float4 p[S], q[S];                                // (all on their way at once)
 #pragma unroll
-        for (int s = 0; s < kSplit; ++s) {
+        for (int s = 0; s < S; ++s) {
           const uint32_t from = map_rank(at, s);
           p[s] = ld_cluster4(from);
           q[s] = ld_cluster4(from + 16);
         }
 #pragma unroll
-        for (int s = 0; s < kSplit; ++s) {
+        for (int s = 0; s < S; ++s) {
           v[0] += p[s].x; v[1] += p[s].y; v[2] += p[s].z; v[3] += p[s].w;
           v[4] += q[s].x; v[5] += q[s].y; v[6] += q[s].z; v[7] += q[s].w;
         }
@@ -368,8 +369,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) adapter_out_kernel(const __gri
   uint8_t *hs = smem_raw + (((raw + 1023u) & ~1023u) - raw);        // [2][panels]: hi, lo
   uint8_t *ring = hs + 2 * g.panels * kPanel;                       // B
   uint8_t *ys = ring + g.stages * g.panels * kPanel;                // y
-  uint64_t *full = reinterpret_cast<uint64_t *>(ys + g.y_stages * kPanel), *empty = full + 2;
-  uint64_t *y_full = empty + 2, *y_empty = y_full + kYPlaces;
+  uint64_t *full = reinterpret_cast<uint64_t *>(ys + g.y_stages * kPanel), *empty = full + kBStages;
+  uint64_t *y_full = empty + kBStages, *y_empty = y_full + kYPlaces;
   uint64_t *h_full = y_empty + kYPlaces, *h_empty = h_full + 1, *t_full = h_empty + 1, *t_empty = t_full + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(t_empty + 2);
   volatile int *failed = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) adapter_out_kernel(const __gri
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kBStages; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
     }
@@ -617,6 +618,29 @@ int map_f16(CUtensorMap *m, const void *base, int dims, const cuuint64_t *size, 
   return map_rows(m, base, dims, size, stride, box, false);
 }
 
+template <int S>
+int launch_clusters(const CUtensorMap &mx, const CUtensorMap &mt, const CUtensorMap &ma, const ad::InArgs &g,
+                    size_t smem, cudaStream_t s) {
+  auto kfn = ad::adapter_in_kernel<S>;
+  static std::atomic<size_t> given[kMaxDevices];
+  int rc = exl3_cuda_check(exl3_ensure_smem(reinterpret_cast<const void *>(kfn), smem, given), "adapter attribute");
+  if (rc) return rc;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = S;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(S, g.a.max_tiles);
+  cfg.blockDim = dim3(ad::kInThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return exl3_cuda_check(cudaLaunchKernelEx(&cfg, kfn, mx, mt, ma, g), "adapter launch");
+}
+
 int launch_in(const ad::Args &a, cudaStream_t s) {
   ad::InArgs g = {};
   g.a = a;
@@ -645,24 +669,12 @@ int launch_in(const ad::Args &a, cudaStream_t s) {
     int rc = map_f16(&ma, a.a, 3, dims, stride, box);
     if (rc) return rc;
   }
-  static std::atomic<size_t> given[kMaxDevices];
-  int rc = exl3_cuda_check(exl3_ensure_smem(reinterpret_cast<const void *>(ad::adapter_in_kernel), smem, given),
-                           "adapter attribute");
-  if (rc) return rc;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ad::kSplit;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ad::kSplit, a.max_tiles);
-  cfg.blockDim = dim3(ad::kInThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return exl3_cuda_check(cudaLaunchKernelEx(&cfg, ad::adapter_in_kernel, mx, mt, ma, g), "adapter launch");
+  // The largest split whose clusters all run at once (as for the router's product:
+  // 15, 36 or 76 clusters of eight, four or two at one CTA per SM)
+  const int sms = exl3_sm_count() * (a.R <= 64 ? 3 : 2);
+  if (a.max_tiles <= sms * 15 / 152) return launch_clusters<8>(mx, mt, ma, g, smem, s);
+  if (a.max_tiles <= sms * 36 / 152) return launch_clusters<4>(mx, mt, ma, g, smem, s);
+  return launch_clusters<2>(mx, mt, ma, g, smem, s);
 }
 
 template <bool F32>
@@ -694,7 +706,7 @@ int launch_out(const ad::OutArgs &g, cudaStream_t s) {
     rc = map_rows(&mr, a.y, 2, dims, stride, row, F32);
     if (rc) return rc;
   }
-  const size_t smem = 1024 + ((2 + g.stages) * (size_t)g.panels + g.y_stages) * ad::kPanel + (10 + 2 * ad::kYPlaces) * 8 + 16;
+  const size_t smem = 1024 + ((2 + g.stages) * (size_t)g.panels + g.y_stages) * ad::kPanel + (6 + 2 * ad::kBStages + 2 * ad::kYPlaces) * 8 + 16;
   auto kfn = ad::adapter_out_kernel<F32>;
   static std::atomic<size_t> given[kMaxDevices];
   int rc = exl3_cuda_check(exl3_ensure_smem(reinterpret_cast<const void *>(kfn), smem, given), "adapter attribute");
@@ -715,8 +727,8 @@ int exl3_launch_adapter_tc(const ad::Args &a, bool f32, cudaStream_t s) {
   // written out), pieces of y.  The places for pieces are a multiple
   // of a block's pieces, so that a place always serves the same four warps: a
   // warp that did not see each of its phases could not tell them apart.
-  g.stages = g.panels == 1 ? 2 : 1;
-  g.y_stages = g.panels == 1 && !f32 ? 10 : 8;
+  g.stages = g.panels == 1 ? 4 : f32 ? 3 : 2;
+  g.y_stages = g.panels == 1 ? 8 : f32 ? 4 : 6;
   g.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride * (f32 ? 4 : 2) % 32 == 0;
   return f32 ? launch_out<true>(g, s) : launch_out<false>(g, s);
 }

@@ -332,10 +332,16 @@ int launch_logits(rt::LogitArgs a, cudaStream_t s) {
   }
   const int sms = exl3_sm_count(), MT = (a.T + rt::BM - 1) / rt::BM, KB = (a.k + rt::BK - 1) / rt::BK;
   const int most = PACKED ? 128 : 256;                      // experts of one tile
-  int NT = (a.E + most - 1) / most, S = 1;
-  while (S < 8 && 2 * S <= KB && (int64_t)MT * NT * 2 * S <= sms) S *= 2;
-  // still SMs to spare: smaller tiles of experts
-  while (S == 8 && (int64_t)MT * NT * 2 * S <= sms && a.E / (2 * NT) >= 16) NT *= 2;
+  int NT = (a.E + most - 1) / most;
+  // Clusters that run at once at one CTA per SM, by the parts that the SMs come in:
+  // 76 of two CTAs, 36 of four, 15 of eight (of 152 SMs; one more cluster is a
+  // second round: 48 tokens took 9.2 us as 16 clusters of eight and 5.2 as 8).
+  // Smaller tiles of experts while clusters of four are to be had (32 experts at
+  // least), then the largest split that fits.
+  while ((int64_t)MT * 2 * NT <= sms * 36 / 152 && a.E / (2 * NT) >= 32) NT *= 2;
+  const int64_t clusters = (int64_t)MT * NT;
+  int S = clusters <= sms * 15 / 152 ? 8 : clusters <= sms * 36 / 152 ? 4 : clusters <= sms / 2 ? 2 : 1;
+  while (S > KB) S /= 2;
   a.bn = ((a.E + NT - 1) / NT + 15) / 16 * 16;
   NT = (a.E + a.bn - 1) / a.bn;
   const int cols = PACKED ? 2 * a.bn : a.bn, stage = (rt::BM + cols) * rt::BK * 2;
