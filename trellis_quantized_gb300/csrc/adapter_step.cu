@@ -19,7 +19,10 @@
 //
 // h is an operand of the second product in two fp16 parts, hi + lo, after each
 // row is brought to [2^14, 2^15) by a power of two: 22 bits of every h, so that
-// an fp32 out is as good as its fp32 sums.
+// an fp32 out is as good as its fp32 sums.  Up to eight rows (most tiles of a step)
+// hi takes the upper half of the product's 16 rows and lo the lower, and the lane
+// that holds both results adds them: one product where 9 to 16 rows take two, which
+// at rank 64 are a quarter of the time (64 users: 20 us against 15 with one).
 #include "adapter.cuh"
 #include "tc_ptx.cuh"
 
@@ -90,9 +93,10 @@ __global__ void __launch_bounds__(kStepThreads, 2) adapter_step_kernel(const Arg
   constexpr int NC = RMAX > 32 ? 2 : 1;                         // blocks of 32 ranks of B held ahead
   __shared__ __align__(16) float part[KW][kStepRows][RMAX];     // each warp's sums
   __shared__ __align__(16) float own[kStepRows][RMAX];          // this CTA's
-  // the cluster's, hi and lo, where the warps' sums were (read before the cluster's barrier)
-  __half(*hs)[kStepRows][HP] = reinterpret_cast<__half(*)[kStepRows][HP]>(&part[0][0][0]);
-  static_assert(2 * HP * 2 <= KW * RMAX * 4, "h in place of the warps' sums");
+  // the cluster's, and its hi and lo, where the warps' sums were (read before the cluster's barrier)
+  float(*sum)[RMAX] = part[0];
+  __half(*hs)[kStepRows][HP] = reinterpret_cast<__half(*)[kStepRows][HP]>(&part[1][0][0]);
+  static_assert(2 * HP * 2 <= (KW - 1) * RMAX * 4, "h in place of the warps' sums");
   __shared__ float back[kStepRows];                             // scale 2^-p
   const int S = gridDim.x, split = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
@@ -165,22 +169,38 @@ __global__ void __launch_bounds__(kStepThreads, 2) adapter_step_kernel(const Arg
   }
   cluster_arrive();
   cluster_wait();
-  {  // the cluster's sum: 16 threads per row
+  {  // the cluster's sum of the tile's rows, four ranks at a time
+    const int R4 = (R8 * 8) / 4, items = tile.z * R4;
+    const auto total = [&](int i) {
+      const uint32_t at = tc::smem_u32(&own[i / R4][i % R4 * 4]);
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+      for (int s = 0; s < S; ++s) {
+        const float4 p = ld_cluster4(map_rank(at, s));
+        v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+      }
+      return v;
+    };
+    if (S * items <= 4096) {                                    // everybody adds up everything,
+      for (int i = threadIdx.x; i < items; i += kStepThreads) *reinterpret_cast<float4 *>(&sum[i / R4][i % R4 * 4]) = total(i);
+    } else {                                                    // or its share, and hands it out
+      for (int i = items * split / S + threadIdx.x; i < items * (split + 1) / S; i += kStepThreads) {
+        const float4 v = total(i);
+        const uint32_t at = tc::smem_u32(&sum[i / R4][i % R4 * 4]);
+        for (int s = 0; s < S; ++s) st_cluster4(map_rank(at, s), v);
+      }
+      cluster_arrive();
+      cluster_wait();
+    }
+    __syncthreads();
+  }
+  {  // as two fp16 parts: 16 threads per row
     const int r = threadIdx.x >> 4, c0 = threadIdx.x & 15;
     constexpr int PER = (RMAX + 15) / 16;
     float v[PER], top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = 0.0f;
-#pragma unroll 4
-    for (int s = 0; s < S; ++s) {
-      const uint32_t at = map_rank(tc::smem_u32(&own[r][0]), s);
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (c0 + 16 * i < RMAX) v[i] += ld_cluster(at + (c0 + 16 * i) * 4);
-    }
-#pragma unroll
     for (int i = 0; i < PER; ++i) {
-      if (c0 + 16 * i >= rank) v[i] = 0.0f;
+      v[i] = r < tile.z && c0 + 16 * i < rank ? sum[r][c0 + 16 * i] : 0.0f;
       top = fmaxf(top, fabsf(v[i]));
     }
 #pragma unroll
@@ -201,6 +221,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) adapter_step_kernel(const Arg
   __syncthreads();
 
   // this CTA's columns, 32 per warp and turn
+  const bool few = tile.z <= 8;                                 // hi and lo in one product
   const float f0 = back[g], f1 = back[g + 8];
   for (; u < units; u += ustep) {
     float d[4][4];
@@ -219,17 +240,21 @@ __global__ void __launch_bounds__(kStepThreads, 2) adapter_step_kernel(const Arg
     load_y(u + ustep, y_next);
     const auto product = [&](int c, const uint4 (&b)[4]) {
       const int at = c * 32 + q * 8;
-      uint4 l0 = make_uint4(0, 0, 0, 0), h0 = l0, l1 = l0, h1 = l0;
-      if (c * 4 + q < R8) {
-        l0 = *reinterpret_cast<const uint4 *>(&hs[0][g][at]);
-        h0 = *reinterpret_cast<const uint4 *>(&hs[0][g + 8][at]);
-        l1 = *reinterpret_cast<const uint4 *>(&hs[1][g][at]);
-        h1 = *reinterpret_cast<const uint4 *>(&hs[1][g + 8][at]);
-      }
+      const bool ok = c * 4 + q < R8;
+      const auto part_of = [&](int part, int row) {
+        return ok ? *reinterpret_cast<const uint4 *>(&hs[part][row][at]) : make_uint4(0, 0, 0, 0);
+      };
+      if (few) {
+        const uint4 hi = part_of(0, g), lo = part_of(1, g);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        mma_pair(d[j], l0, h0, b[j]);
-        mma_pair(d[j], l1, h1, b[j]);
+        for (int j = 0; j < 4; ++j) mma_pair(d[j], hi, lo, b[j]);
+      } else {
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const uint4 upper = part_of(part, g), lower = part_of(part, g + 8);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma_pair(d[j], upper, lower, b[j]);
+        }
       }
     };
 #pragma unroll
@@ -241,6 +266,12 @@ __global__ void __launch_bounds__(kStepThreads, 2) adapter_step_kernel(const Arg
         product(c, w[0]);
       }
     }
+    if (few)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        d[j][0] += d[j][2];
+        d[j][1] += d[j][3];
+      }
 #pragma unroll
     for (int r = 0; r < 2; ++r)
       if (r ? ok1 : ok0) {
@@ -297,8 +328,12 @@ cudaError_t launch_step(const ad::Args &a, bool f32, int S, cudaStream_t s) {
 }  // namespace
 
 cudaError_t exl3_launch_adapter_step(const ad::Args &a, bool f32, cudaStream_t s) {
-  // a cluster of sixteen while that is at most one CTA per SM, else of eight
-  const int S = (int64_t)a.max_tiles * 16 <= exl3_sm_count() ? 16 : 8;
+  // The largest cluster of which all run at once at two CTAs per SM (30 of eight and
+  // 72 of four on 152 SMs; 128 users on 48 adapters: 12.5 us in clusters of eight, 9.0 in
+  // fours); sixteen pay for single tiles only (one of rank 64, 17408 columns: 12.8 and 15
+  // us, eight of rank 16: 6.8 and 6.1)
+  const int sms = exl3_sm_count();
+  const int S = a.max_tiles <= 4 ? 16 : a.max_tiles <= sms * 30 / 152 ? 8 : a.max_tiles <= sms * 72 / 152 ? 4 : 2;
   if (a.R <= 16) return launch_step<2, 1>(a, f32, S, s);
   if (a.R <= 32) return launch_step<4, 1>(a, f32, S, s);
   if (a.R <= 64) return launch_step<8, 1>(a, f32, S, s);
