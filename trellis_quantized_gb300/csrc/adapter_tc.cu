@@ -267,16 +267,18 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
   cluster_arrive();
   cluster_wait();
 
-  // 16 threads to a row, eight ranks each (a half-warp stays whole: a CTA's rows are a multiple of 16)
+  // `per_row` threads to a row, eight ranks each (a warp stays whole: a CTA's rows are a multiple of 16)
   if (warp >= 2) {
     constexpr int per = kTcRows / S;
-    const int t = threadIdx.x - 64, c = 8 * (t & 15);
-    for (int r0 = t >> 4; r0 < per; r0 += 8) {
+    int per_row = 2;
+    while (per_row * 8 < g.r16) per_row *= 2;
+    const int t = threadIdx.x - 64, c = 8 * (t & (per_row - 1));
+    for (int r0 = t / per_row; r0 < per; r0 += 128 / per_row) {
       const int r = split * per + r0;
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-      if (c < g.r16) {
+      if (c < rank && r < tile.z) {
         const uint32_t at = tc::smem_u32(ring) + (uint32_t)(r * pitch + c) * 4;
         float4 p[S], q[S];                                // (all on their way at once)
 #pragma unroll
@@ -298,7 +300,10 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
         top = fmaxf(top, fabsf(v[i]));
       }
 #pragma unroll
-      for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = 8; o; o >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, top, o);
+        if (o < per_row) top = fmaxf(top, other);
+      }
       const int p = row_exponent(top);
       const float f = scalbnf(1.0f, p);
       uint32_t hi[4], lo[4];
