@@ -773,22 +773,32 @@ def _on_current(t, name: str) -> int:
     return d
 
 
-def _matrix(t, name: str, width: int, dtypes):
-    """Address and row stride of [rows, width] with dense rows."""
+def _matrix(t, name: str, width: int, dtypes, device: int):
+    """Address and row stride of [rows, width] with dense rows on the given device."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     shape = t.shape
     if len(shape) != 2 or shape[1] != width:
         raise ValueError(f"{name} must be [rows, {width}], got {tuple(shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the other tensors' device cuda:{device}, got {t.device}")
     s0, s1 = t.stride()
     if s1 != 1 and width > 1:
         raise ValueError(f"{name}'s rows must be dense")
     return t.data_ptr(), (s0 if shape[0] > 1 else width)
 
 
-def _same_device(t, name: str, device: int):
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on the other tensors' device cuda:{device}, got {t.device}")
+def _dense(t, name: str, shape, dtype, device: int) -> int:
+    """Address of a dense output of the given shape and type on the given device."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor {shape} {dtype} on cuda:{device}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _stream_of(stream, device: int) -> int:
+    """The given stream's handle, or that of the device's current one."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 _F16, _F32, _F16_F32 = (torch.float16,), (torch.float32,), (torch.float16, torch.float32)
@@ -818,7 +828,7 @@ def router(w, bias=None, stream=None) -> Router:
         _check(lib().exl3_router_pack(_ptr(w, "w"), E, k, _ptr(parts, "packed"), _ptr(scale, "scale"), _stream(stream)))
     d = Router(_ptr(parts, "w").value, None if scale is None else scale.data_ptr(), _vector(bias, "bias", E, torch.float32),
                E, k)
-    d._keep, d._address = (parts, scale, bias), ctypes.addressof(d)
+    d._keep, d._address, d._device, d._shape = (parts, scale, bias), ctypes.addressof(d), w.get_device(), (E, k)
     return d
 
 
@@ -847,16 +857,20 @@ _logits_workspace = functools.cache(exl3_router_logits_workspace_size)
 def exl3_router_logits(x, router: Router, logits=None, workspace_buf=None, stream=None) -> torch.Tensor:
     """logits [T, E] fp32 = x @ w^T (+ bias) for x [T, k] fp16 with dense rows."""
     device = _on_current(x, "x")
-    xp, xs = _matrix(x, "x", router.k, _F16)
+    E, k = router._shape
+    xp, xs = _matrix(x, "x", k, _F16, device)
     T = x.shape[0]
+    if router._device != device:
+        raise ValueError(f"the router is on cuda:{router._device}, x on cuda:{device}")
     if logits is None:
-        logits = torch.empty((T, router.E), dtype=torch.float32, device=x.device)
-    lp = _out(logits, "logits", (T, router.E), torch.float32)
-    _same_device(logits, "logits", device)
+        logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
+    lp = _dense(logits, "logits", (T, E), torch.float32, device)
     if T:
-        raw = _raw_stream(stream)
+        raw = _stream_of(stream, device)
         wp, wn = _workspace_arg(workspace_buf, _logits_workspace(), x.device, stream, raw)
-        _check(lib().exl3_router_logits(xp, xs, T, router._address, lp, wp, wn, raw))
+        rc = lib().exl3_router_logits(xp, xs, T, router._address, lp, wp, wn, raw)
+        if rc:
+            _check(rc)
     return logits
 
 
@@ -872,30 +886,32 @@ def route_rule(topk: int, score: int = EXL3_SCORE_SOFTMAX, bias=None, groups: in
         bp = _vector(bias, "bias", bias.shape[0], torch.float32)
     d = RouteRule(score, bp, groups, groups if groups_kept is None else groups_kept, group_score, topk,
                   1 if renormalise else 0, scale)
-    d._keep, d._address = (bias,), ctypes.addressof(d)
-    d._experts = None if bias is None else bias.shape[0]
+    d._keep, d._address, d._topk = (bias,), ctypes.addressof(d), topk
+    d._experts, d._device = (None, None) if bias is None else (bias.shape[0], bias.get_device())
     return d
 
 
 def exl3_route(logits, rule: RouteRule, ids=None, weights=None, stream=None):
     """Experts and weights of each token from logits [T, E] (fp32 or fp16, dense rows): ids int32
     and weights fp32, [T, topk], as exl3_moe_grouped takes them."""
-    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
-        raise TypeError("logits must be a torch tensor [T, E]")
-    T, E = logits.shape
-    device, topk = _on_current(logits, "logits"), rule.topk
-    lp, ls = _matrix(logits, "logits", E, _F16_F32)
-    if rule._experts is not None and rule._experts != E:
-        raise ValueError(f"the rule's bias has {rule._experts} experts, the logits {E}")
+    device = _on_current(logits, "logits")
+    shape, topk, bias = logits.shape, rule._topk, rule._experts
+    if len(shape) != 2:
+        raise ValueError(f"logits must be [T, E], got {tuple(shape)}")
+    T, E = shape
+    lp, ls = _matrix(logits, "logits", E, _F16_F32, device)
+    if bias is not None and (bias != E or rule._device != device):
+        raise ValueError(f"the rule's bias has {bias} experts on cuda:{rule._device}, the logits {E} on cuda:{device}")
     if ids is None:
         ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
     if weights is None:
         weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
-    ip, wp = _out(ids, "ids", (T, topk), torch.int32), _out(weights, "weights", (T, topk), torch.float32)
-    _same_device(ids, "ids", device)
-    _same_device(weights, "weights", device)
+    out = (T, topk)
+    ip, wp = _dense(ids, "ids", out, torch.int32, device), _dense(weights, "weights", out, torch.float32, device)
     if T:
-        _check(lib().exl3_route(lp, ls, _IO_DTYPES[logits.dtype], T, E, rule._address, ip, wp, _raw_stream(stream)))
+        rc = lib().exl3_route(lp, ls, _IO_DTYPES[logits.dtype], T, E, rule._address, ip, wp, _stream_of(stream, device))
+        if rc:
+            _check(rc)
     return ids, weights
 
 
@@ -918,7 +934,7 @@ def adapters(a, b, scale, rank=None) -> Adapters:
         raise TypeError("scale must be a torch tensor")
     d = Adapters(_ptr(a, "a", 2).value, _ptr(b, "b", 2).value, _vector(scale, "scale", N, torch.float32),
                  _vector(rank, "rank", N, torch.int32), N, R, k, n)
-    d._keep, d._address = (a, b, scale, rank), ctypes.addressof(d)
+    d._keep, d._address, d._device, d._shape = (a, b, scale, rank), ctypes.addressof(d), a.get_device(), (N, R, k, n)
     return d
 
 
@@ -931,7 +947,7 @@ class AdapterPlan:
             raise ValueError(f"T = {T}, batch = {batch} or count = {count} out of range")
         self.T, self.batch, self.count = T, batch, count
         self.data = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        self.address = self.data.data_ptr()
+        self.address, self.device = self.data.data_ptr(), self.data.get_device()
         exl3_workspace_clear(self.data, stream=stream)
 
 
@@ -972,22 +988,25 @@ def exl3_adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out=None, work
                      stream=None) -> torch.Tensor:
     """y + scale (x A^T) B^T for each row's adapter: x [T, k] fp16, y [T, n] fp16 or fp32, dense
     rows; written to `out`, or to y itself (rows of no sequence are left as they were)."""
-    device = _on_current(x, "x")
-    xp, xs = _matrix(x, "x", adapters.k, _F16)
-    yp, ys = _matrix(y, "y", adapters.n, _F16_F32)
-    _same_device(y, "y", device)
+    device, dtype = _on_current(x, "x"), y.dtype
+    N, R, k, n = adapters._shape
+    xp, xs = _matrix(x, "x", k, _F16, device)
+    yp, ys = _matrix(y, "y", n, _F16_F32, device)
     if out is None or out is y:
         out, op, os_ = y, yp, ys
     else:
-        op, os_ = _matrix(out, "out", adapters.n, _F16 if y.dtype == torch.float16 else _F32)
-        _same_device(out, "out", device)
+        op, os_ = _matrix(out, "out", n, _F16 if dtype is torch.float16 else _F32, device)
     T = x.shape[0]
     if y.shape[0] != T or out.shape[0] != T or plan.T != T:
         raise ValueError(f"x has {T} rows, y {y.shape[0]}, out {out.shape[0]}, the plan {plan.T}")
-    if plan.count != adapters.count:
-        raise ValueError(f"the plan was made for {plan.count} adapters, the pool has {adapters.count}")
-    raw = _raw_stream(stream)
-    wp, wn = _workspace_arg(workspace_buf, _adapter_workspace(T, adapters.max_rank), x.device, stream, raw)
-    _check(lib().exl3_adapter_add(xp, xs, yp, ys, op, os_, _IO_DTYPES[y.dtype], adapters._address, plan.address, T,
-                                  plan.batch, wp, wn, raw))
+    if plan.device != device or adapters._device != device:
+        raise ValueError(f"x is on cuda:{device}, the plan on cuda:{plan.device}, the pool on cuda:{adapters._device}")
+    if plan.count != N:
+        raise ValueError(f"the plan was made for {plan.count} adapters, the pool has {N}")
+    raw = _stream_of(stream, device)
+    wp, wn = _workspace_arg(workspace_buf, _adapter_workspace(T, R), x.device, stream, raw)
+    rc = lib().exl3_adapter_add(xp, xs, yp, ys, op, os_, _IO_DTYPES[dtype], adapters._address, plan.address, T,
+                                plan.batch, wp, wn, raw)
+    if rc:
+        _check(rc)
     return out
