@@ -7,10 +7,10 @@
 //   chosen (equal values: the lower id); weights are the chosen s, divided by
 //   their sum if asked, times `scale`.
 //
-// A warp takes a token; lane l holds V neighbouring experts as keys that order
-// as their values do (the float's bits, made monotone).  A pick is one warp
-// reduction (redux: the largest key), a ballot (the lowest lane that has it has
-// the lowest id) and one pass over the owner's keys.  Softmax and the sigmoid
+// A warp takes a token; lane l holds experts l, l + 32, ... as keys that order as
+// their values do (the float's bits, made monotone).  A pick is one warp reduction
+// (redux: the largest key), a ballot (its lane) and a subtraction and a maximum
+// over the owner's keys.  Softmax and the sigmoid
 // are monotone, so without a bias and without sums of two the keys are the
 // logits themselves: exact, and no exponential before the topk chosen ones.
 //
@@ -36,12 +36,13 @@ constexpr int kWarps = 4;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float((int)0xff800000u); }
 
-// A key that orders as the value does (-0 as 0); NaN below everything.  Keys
-// start at 1: 0 is a place without an expert, or one that is gone.
+// A key that orders as the value does (-0 as 0); NaN below everything (-infinity
+// has 0x007fffff).  0 is a place without an expert, or one that is gone.
+constexpr unsigned kNanKey = 64;
 __device__ __forceinline__ unsigned order_key(float v) {
   const unsigned b = __float_as_uint(v + 0.0f);
-  const unsigned k = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return v != v ? 1u : k;
+  const unsigned k = b ^ ((unsigned)((int)b >> 31) | 0x80000000u);
+  return v != v ? kNanKey : k;
 }
 __device__ __forceinline__ float key_value(unsigned k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
@@ -51,41 +52,6 @@ template <bool F16>
 __device__ __forceinline__ float load_logit(const Args &a, int64_t row, int e) {
   if (F16) return __half2float(static_cast<const __half *>(a.logits)[row * a.stride + e]);
   return static_cast<const float *>(a.logits)[row * a.stride + e];
-}
-
-// V neighbouring logits from expert e0 on, of which `here` exist.
-template <int V, bool F16>
-__device__ __forceinline__ void load_row(const Args &a, int64_t row, int e0, int here, float (&l)[V]) {
-  constexpr int W = F16 ? (V < 8 ? V : 8) : (V < 4 ? V : 4);     // values of one wide load
-  if (a.wide && here == V) {
-    if (F16) {
-      const __half *src = static_cast<const __half *>(a.logits) + row * a.stride + e0;
-#pragma unroll
-      for (int i = 0; i < V; i += W) {
-        __align__(16) __half h[W];
-        if (W == 8) *reinterpret_cast<uint4 *>(h) = *reinterpret_cast<const uint4 *>(src + i);
-        if (W == 4) *reinterpret_cast<uint2 *>(h) = *reinterpret_cast<const uint2 *>(src + i);
-        if (W == 2) *reinterpret_cast<unsigned *>(h) = *reinterpret_cast<const unsigned *>(src + i);
-        if (W == 1) h[0] = src[i];
-#pragma unroll
-        for (int j = 0; j < W; ++j) l[i + j] = __half2float(h[j]);
-      }
-    } else {
-      const float *src = static_cast<const float *>(a.logits) + row * a.stride + e0;
-#pragma unroll
-      for (int i = 0; i < V; i += W) {
-        __align__(16) float f[W];
-        if (W == 4) *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(src + i);
-        if (W == 2) *reinterpret_cast<float2 *>(f) = *reinterpret_cast<const float2 *>(src + i);
-        if (W == 1) f[0] = src[i];
-#pragma unroll
-        for (int j = 0; j < W; ++j) l[i + j] = f[j];
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = i < here ? load_logit<F16>(a, row, e0 + i) : neg_inf();
-  }
 }
 
 __device__ __forceinline__ float sigmoid(float l) {
@@ -99,10 +65,11 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
 }
-// Does the order of two computed values (v above w) hold for the exact ones?
-// Infinities are exact; what is barred (-infinity) is never asked about.
-__device__ __forceinline__ bool uncertain(float v, float w, float tol) {
-  return w > neg_inf() && !(v - w > tol + 0x1p-22f * fabsf(v));
+// Does the order of two computed values (v above w) hold for the exact ones?  They
+// are off by tol together, and by `rel` of themselves.  Infinities are exact;
+// what is barred (-infinity) is never asked about.
+__device__ __forceinline__ bool uncertain(float v, float w, float tol, float rel) {
+  return w > neg_inf() && !(v - w > tol + rel * fabsf(v));
 }
 
 // ------------------------------------------------------ pairs of floats
@@ -181,7 +148,7 @@ __device__ __forceinline__ Pair exp_pair(Pair x) {
 // Order keys of a pair, high and low.
 __device__ __forceinline__ unsigned long long pair_key(Pair v) {
   const unsigned hi = order_key(v.h);
-  return (unsigned long long)hi << 32 | (hi == 1u || isinf(v.h) ? 0u : order_key(v.l));
+  return (unsigned long long)hi << 32 | (hi == kNanKey || isinf(v.h) ? 0u : order_key(v.l));
 }
 __device__ __forceinline__ Pair key_pair(unsigned long long k) {
   const float h = key_value((unsigned)(k >> 32));
@@ -206,11 +173,12 @@ __device__ __forceinline__ void row_sum(const Args &a, int64_t row, int lane, fl
   for (int o = 16; o; o >>= 1) sum = add(sum, {__shfl_xor_sync(kFull, sum.h, o), __shfl_xor_sync(kFull, sum.l, o)});
 }
 
-// The key of expert e's c.
-template <bool F16>
+// The key of expert e's c, or (VALUE false) of its logit.
+template <bool F16, bool VALUE>
 __device__ __forceinline__ unsigned long long value_key(const Args &a, int64_t row, int e, float mx, Pair sum) {
   const bool soft = a.score == EXL3_SCORE_SOFTMAX;
   const float l = load_logit<F16>(a, row, e);
+  if (!VALUE) return (unsigned long long)order_key(l) << 32;
   const Pair t = exp_pair(soft ? two_sum(l, -mx) : Pair{-fabsf(l), 0.0f});
   Pair v = div(soft || !(l >= 0.0f) ? t : Pair{1.0f, 0.0f}, soft ? sum : add({1.0f, 0.0f}, t));
   if (l == neg_inf()) v = {0.0f, 0.0f};
@@ -223,12 +191,12 @@ __device__ __forceinline__ unsigned long long value_key(const Args &a, int64_t r
 
 // A row with picks that are too close: lane j has the j-th of `count` experts,
 // of which everything else is known to be below; they are put in order.
-template <bool F16>
+template <bool F16, bool VALUE>
 __device__ __noinline__ int order_pairs(const Args &a, int64_t row, int lane, int id, int count, int *place) {
   float mx = 0.0f;
   Pair sum = {0.0f, 0.0f};
-  if (a.score == EXL3_SCORE_SOFTMAX) row_sum<F16>(a, row, lane, mx, sum);
-  const unsigned long long key = lane < count ? value_key<F16>(a, row, id, mx, sum) : 0;
+  if (VALUE && a.score == EXL3_SCORE_SOFTMAX) row_sum<F16>(a, row, lane, mx, sum);
+  const unsigned long long key = lane < count ? value_key<F16, VALUE>(a, row, id, mx, sum) : 0;
   int before = 0;
   for (int o = 0; o < count; ++o) {
     const unsigned long long v = __shfl_sync(kFull, key, o);
@@ -244,14 +212,14 @@ __device__ __noinline__ int order_pairs(const Args &a, int64_t row, int lane, in
 // The whole selection on pairs, the row's keys in shared memory: groups that are
 // too close, or too many equal picks.  Lane j gets the j-th chosen expert.  Rare,
 // so the simplest form.
-template <bool F16>
+template <bool F16, bool VALUE>
 __device__ __noinline__ int select_pairs(const Args &a, int64_t row, int lane, unsigned long long *c) {
   float mx = 0.0f;
   Pair sum = {0.0f, 0.0f};
-  if (a.score == EXL3_SCORE_SOFTMAX) row_sum<F16>(a, row, lane, mx, sum);
+  if (VALUE && a.score == EXL3_SCORE_SOFTMAX) row_sum<F16>(a, row, lane, mx, sum);
   __syncwarp();
 #pragma unroll 2
-  for (int e = lane; e < a.E; e += 32) c[e] = value_key<F16>(a, row, e, mx, sum);
+  for (int e = lane; e < a.E; e += 32) c[e] = value_key<F16, VALUE>(a, row, e, mx, sum);
   __syncwarp();
   const int size = a.E / a.groups;
   unsigned keep = kFull;
@@ -267,7 +235,7 @@ __device__ __noinline__ int select_pairs(const Args &a, int64_t row, int lane, u
       g = first;
       if (a.group_score == EXL3_GROUP_TOP2 && size > 1) {
         const Pair p = key_pair(first), q = key_pair(second);
-        g = first >> 32 == 1u || second >> 32 == 1u ? 1ull << 32
+        g = first >> 32 == kNanKey || second >> 32 == kNanKey ? (unsigned long long)kNanKey << 32
             : isinf(p.h) || isinf(q.h)              ? pair_key({p.h + q.h, 0.0f})
                                                     : pair_key(add(p, q));
       }
@@ -320,38 +288,42 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const Args a) {
   if (row >= a.T) return;
   const bool soft = a.score == EXL3_SCORE_SOFTMAX;
 
-  const int e0 = lane * V, here = min(max(a.E - e0, 0), V);      // this lane's experts
   float l[V];
-  load_row<V, F16>(a, row, e0, here, l);
+#pragma unroll
+  for (int i = 0; i < V; ++i) l[i] = lane + 32 * i < a.E ? load_logit<F16>(a, row, lane + 32 * i) : neg_inf();
   // the whole row's softmax, where it is asked for
   float mx = 0.0f, inv = 1.0f;
   if (soft && (VALUE || !a.renormalise)) {
     unsigned top = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) top = max(top, i < here ? order_key(l[i]) : 0u);
+    for (int i = 0; i < V; ++i) top = max(top, lane + 32 * i < a.E ? order_key(l[i]) : 0u);
     top = __reduce_max_sync(kFull, top);
-    mx = top > 1u ? key_value(top) : 0.0f;
+    mx = top > kNanKey ? key_value(top) : 0.0f;
     if (mx == neg_inf()) mx = 0.0f;              // a row that is masked throughout: scores of zero
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += i < here ? expf(l[i] - mx) : 0.0f;
+    for (int i = 0; i < V; ++i) sum += lane + 32 * i < a.E ? expf(l[i] - mx) : 0.0f;
     sum = warp_sum(sum);
     inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   }
   unsigned key[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
+    const int e = lane + 32 * i;
     float c = l[i];
     if (VALUE) {
-      c = soft ? expf(l[i] - mx) * inv : sigmoid(l[i]);
-      if (a.bias && i < here) c += a.bias[e0 + i];
+      // (the fast exponential: both forms stay well within the bound below; the
+      // sigmoid's may be too large to divide by)
+      c = soft ? __expf(l[i] - mx) * inv : l[i] < -80.0f ? 0.0f : __fdividef(1.0f, 1.0f + __expf(-l[i]));
+      if (a.bias && e < a.E) c += __ldg(a.bias + e);
     }
-    key[i] = i < here ? order_key(c) : 0u;
+    key[i] = e < a.E ? order_key(c) : 0u;
   }
-  // Bound on the error of a computed c, apart from its last rounding: the
-  // sigmoid is off by 3 roundings (2^-22), the softmax by its exponential's
-  // and its sum's (32 + 5 additions: below 2^-18 of the largest score).
-  const float tol = soft ? 0x1p-18f * inv : 0x1p-21f;
+  // Bound on the error of two computed c together, apart from their own rounding.
+  // Sigmoid: the exponential's units times s (1 - s) 0.7, the division 2, the sum
+  // half a unit, of 2^-23 each.  Softmax: its exponential's and its sum's (32 + 5
+  // additions), below 2^-18 of the largest score.
+  const float tol = soft ? 0x1p-17f * inv : 0x1p-20f;
   bool doubt = false, again = false;       // picks or groups too close to call
 
   if (GROUPS) {
@@ -359,7 +331,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const Args a) {
     unsigned *keys = reinterpret_cast<unsigned *>(smem) + (size_t)warp * a.smem_per_warp / 4;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i < here) keys[e0 + i] = key[i];
+      if (lane + 32 * i < a.E) keys[lane + 32 * i] = key[i];
     __syncwarp();
     const int size = a.E / a.groups, per = a.group_lanes, g = lane / per, sub = lane % per;
     unsigned first = 0, second = 0;
@@ -380,7 +352,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const Args a) {
     unsigned value = first;
     if (VALUE && a.group_score == EXL3_GROUP_TOP2 && size > 1) {
       const float p = key_value(first), q = key_value(second);
-      value = first > 1u && second > 1u ? order_key(p + q) : 1u;
+      value = first > kNanKey && second > kNanKey ? order_key(p + q) : kNanKey;
     }
     if (g >= a.groups || sub) value = 0;
     // the rank of each group among all of them
@@ -391,73 +363,79 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const Args a) {
       const int who = __ffs(__ballot_sync(kFull, left == top)) - 1;
       const float v = key_value(top);
       if (j == a.kept) {
-        if (VALUE) again = top > 1u && uncertain(last, v, 2.0f * tol);
+        if (VALUE) again = top > kNanKey && uncertain(last, v, 2.0f * tol, 0x1p-21f);
       } else {
         keep |= 1u << (who / per);
         if (lane == who) left = 0;
         last = v;
       }
     }
-    int own = e0 / size, to = (own + 1) * size - e0;        // the group of expert e0 + i, and where it ends
+    const int inv_size = ((1 << 20) + size - 1) / size;     // (exact below 2^10)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (i == to) {
-        ++own;
-        to += size;
-      }
-      if (!(keep >> (own & 31) & 1u)) key[i] = 0;
-    }
+    for (int i = 0; i < V; ++i)
+      if (!(keep >> ((lane + 32 * i) * inv_size >> 20 & 31) & 1u)) key[i] = 0;
   }
 
+  // Picks: a key's lowest bits give way to the place within the lane (the first place
+  // the largest; equal keys in one place go to the lower lane: the order of their
+  // ids).  The owner's next key is its largest below the one that it gave: the one
+  // for which key - top is largest modulo 2^32.
+  constexpr unsigned LOW = V - 1;
   int mine = -1, picks = 0;
   {
     unsigned best = 0;
-    int at = 0;                                            // this lane's best: its lowest place among equals
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-      }
-    float last = 0.0f;
+    for (int i = 0; i < V; ++i) {
+      key[i] = key[i] ? (key[i] & ~LOW) | (LOW - i) : 0u;
+      best = max(best, key[i]);
+    }
+    unsigned last = 0, seen = 0;                           // `seen`: keys equal but for their lowest bits, looked at
+    bool mixed = false;                                    // and not all equal
     for (int j = 0;; ++j) {
       const unsigned top = __reduce_max_sync(kFull, best);
       if (top == 0) break;                                 // (nothing behind the last pick)
-      if (VALUE) {                                         // on until a pick is certainly below the topk-th
-        const float v = key_value(top);
-        const bool close = j > 0 && top > 1u && uncertain(last, v, tol);
-        if (j >= a.topk && !close) break;
-        doubt |= close;
-        last = v;
-        if (j == 32) {
-          again = true;
-          break;
+      // on until a pick is certainly below the topk-th
+      bool close = false;
+      if (VALUE) {
+        close = j > 0 && top > (kNanKey | LOW) &&
+                uncertain(key_value(last | LOW), key_value(top & ~LOW), tol, 0x1p-22f + 0x1p-22f * V);
+      } else if (!F16 && j > 0 && (last | LOW) == (top | LOW)) {   // (fp16 has no bits there)
+        if (seen != (top | LOW)) {
+          seen = top | LOW;
+          unsigned high = 0, low = 0xffffffffu;
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if ((key[i] | LOW) == seen) {
+              high = max(high, order_key(l[i]));
+              low = min(low, order_key(l[i]));
+            }
+          mixed = __reduce_max_sync(kFull, high) != __reduce_min_sync(kFull, low);
         }
-      } else if (j == a.topk) {
+        close = mixed;
+      }
+      if (j >= a.topk && !close) break;
+      doubt |= close;
+      last = top;
+      if (j == 32) {
+        again = true;
         break;
       }
       const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
-      const int id = __shfl_sync(kFull, e0 + at, owner);
-      if (j == lane) mine = id;
+      if (j == lane) mine = owner + 32 * (int)(LOW - (top & LOW));
       picks = j + 1;
       if (lane == owner) {
-        const int gone = at;
-        best = 0;
+        unsigned rest = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          key[i] = i == gone ? 0u : key[i];
-          if (key[i] > best) {
-            best = key[i];
-            at = i;
-          }
-        }
+        for (int i = 0; i < V; ++i) rest = max(rest, key[i] - top);
+        best = rest + top;                                 // (of keys that are gone: 0)
+        if (best >= top) best = 0;                         // (nothing below, only what it gave before)
       }
     }
   }
-  if (VALUE) {
+  if (VALUE || !F16) {
     unsigned char *mem = smem + (size_t)warp * a.smem_per_warp;
-    if (again) mine = select_pairs<F16>(a, row, lane, reinterpret_cast<unsigned long long *>(mem));
-    else if (doubt) mine = order_pairs<F16>(a, row, lane, mine, picks, reinterpret_cast<int *>(mem));
+    if (again) mine = select_pairs<F16, VALUE>(a, row, lane, reinterpret_cast<unsigned long long *>(mem));
+    else if (doubt) mine = order_pairs<F16, VALUE>(a, row, lane, mine, picks, reinterpret_cast<int *>(mem));
   }
 
   // weights of the chosen
@@ -522,11 +500,9 @@ cudaError_t exl3_launch_route(const rt::Args &in, bool f16, cudaStream_t s) {
   rt::Args a = in;
   const bool groups = a.kept < a.groups;
   const bool value = a.bias || (groups && a.group_score == EXL3_GROUP_TOP2);
-  // wide loads: every row starts on 16 bytes (a lane's experts then start on their own size)
-  a.wide = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.stride % (f16 ? 8 : 4) == 0;
   a.group_lanes = 32;
   while (a.group_lanes * a.groups > 32) a.group_lanes /= 2;
   // 64-bit keys where a doubtful row is done again, 32-bit keys for groups
-  a.smem_per_warp = value ? std::max(128, (a.E * 8 + 15) / 16 * 16) : groups ? (a.E * 4 + 15) / 16 * 16 : 0;
+  a.smem_per_warp = value || !f16 ? std::max(128, (a.E * 8 + 15) / 16 * 16) : groups ? (a.E * 4 + 15) / 16 * 16 : 0;
   return f16 ? launch_v<true>(a, value, groups, s) : launch_v<false>(a, value, groups, s);
 }

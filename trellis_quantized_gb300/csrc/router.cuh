@@ -17,7 +17,6 @@ struct Args {
   int32_t *ids;             // [T][topk]
   float *weights;           // [T][topk]
   int group_lanes;          // lanes per group: the largest power of two with groups * lanes <= 32
-  int wide;                 // rows may be read 16 bytes at a time
   int smem_per_warp;
 };
 
