@@ -1003,8 +1003,11 @@ def exl3_adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out=None, work
         raise ValueError(f"x is on cuda:{device}, the plan on cuda:{plan.device}, the pool on cuda:{adapters._device}")
     if plan.count != N:
         raise ValueError(f"the plan was made for {plan.count} adapters, the pool has {N}")
-    raw = _stream_of(stream, device)
-    wp, wn = _workspace_arg(workspace_buf, _adapter_workspace(T, R), x.device, stream, raw)
+    raw, need = _stream_of(stream, device), _adapter_workspace(T, R)
+    if need > 256 and workspace_buf is None and stream is None and torch._C._cuda_isCurrentStreamCapturing():
+        # a graph gets memory of its own: two that share the stream's would race when they run at once
+        workspace_buf = torch.empty(need, dtype=torch.uint8, device=x.device)
+    wp, wn = _workspace_arg(workspace_buf, need, x.device, stream, raw)
     rc = lib().exl3_adapter_add(xp, xs, yp, ys, op, os_, _IO_DTYPES[dtype], adapters._address, plan.address, T,
                                 plan.batch, wp, wn, raw)
     if rc:

@@ -25,9 +25,10 @@ int check_words(const void *p, const char *name, bool required = true) {
 }
 
 // ---- exl3_adapter_add workspace layout: h of all rows in two fp16 parts and
-// each row's factor, for the calls on large tiles
+// each row's factor, for the calls on large tiles (behind the counters, which
+// the linears that share a workspace have to find at zero)
 struct AddWs {
-  size_t h = kCtrlBytes, back = 0, total = kCtrlBytes;
+  size_t h = kDataOff, back = 0, total = kCtrlBytes;
 };
 
 AddWs add_ws(int T, int R) {
