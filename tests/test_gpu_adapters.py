@@ -29,6 +29,11 @@ def _pool(N, R, k, n, ranks=None, seed=0, junk=0.0):
     return a, b, scale, rank
 
 
+def _large(T, R, k, n):
+    """Calls on tiles of 128 rows (the library's rule; smaller ones run on tiles of 16)."""
+    return T >= 48 and T * R * (k + n) >= 1 << 28
+
+
 def _i32(v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
 
@@ -112,28 +117,53 @@ def test_prompts(rows, R, fp32):
     _run(rows, [i % 3 for i in range(len(rows))], 3, R, 1024, 1152, fp32)
 
 
-@pytest.mark.parametrize("rows", [[1] * 30, [400, 1, 30, 200]])
 @pytest.mark.parametrize("in_place", [False, True])
-def test_rows_without_an_adapter_keep_y(rows, in_place):
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("R,k,n", [(8, 128, 60032), (16, 17408, 12288), (24, 19200, 384), (40, 512, 12288),
+                                   (64, 256, 8320), (72, 8192, 128), (128, 4096, 512), (128, 128, 5120)])
+@pytest.mark.parametrize("rows", [[600], [200, 333, 1, 1, 1, 90], [127, 128, 129, 255, 1, 0, 11, 12, 13, 50]])
+def test_large_tiles(rows, R, k, n, fp32, in_place):
+    assert _large(sum(rows), R, k, n)
+    _run(rows, [i % 3 for i in range(len(rows))], 3, R, k, n, fp32, in_place=in_place)
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+def test_large_tiles_of_scattered_rows(fp32):
+    """Sequences of one to five rows of five adapters and none: every tile gathers."""
+    rows = [1 + i % 5 for i in range(300)]
+    ids = [(i * 7) % 6 - 1 for i in range(300)]
+    assert _large(sum(rows), 64, 512, 4224)
+    _run(rows, ids, 5, 64, 512, 4224, fp32)
+    _run(rows, ids, 5, 64, 512, 4224, fp32, in_place=True)
+
+
+@pytest.mark.parametrize("rows,R,n", [([1] * 30, 32, 256), ([400, 1, 30, 200], 32, 256), ([400, 1, 30, 200], 64, 8192)])
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_rows_without_an_adapter_keep_y(rows, R, n, fp32, in_place):
     ids = [-1 if i % 3 else 2 for i in range(len(rows))]
-    _run(rows, ids, 4, 32, 256, 256, in_place=in_place)
-    _run(rows, [-1] * len(rows), 4, 32, 256, 256, in_place=in_place)
+    assert _large(sum(rows), R, 256, n) == (n > 256)
+    _run(rows, ids, 4, R, 256, n, fp32, in_place=in_place)
+    _run(rows, [-1] * len(rows), 4, R, 256, n, fp32, in_place=in_place)
 
 
-@pytest.mark.parametrize("rows", [[1, 1, 2, 1, 1, 1], [300, 1, 5, 140, 200, 131]])
+@pytest.mark.parametrize("rows,n", [([1, 1, 2, 1, 1, 1], 512), ([300, 1, 5, 140, 200, 131], 512),
+                                    ([300, 1, 5, 140, 200, 131], 8192)])
 @pytest.mark.parametrize("R,ranks", [(64, [8, 64, 16, 33, 0, 40]), (128, [128, 1, 64, 65, 100, 16])])
-def test_ranks_and_what_lies_past_them(rows, R, ranks):
+def test_ranks_and_what_lies_past_them(rows, n, R, ranks):
     """NaN past an adapter's rank in A, and in B past the next multiple of 16."""
-    _run(rows, list(range(6)), 6, R, 512, 512, True, ranks, junk=math.nan)
+    assert _large(sum(rows), R, 512, n) == (n > 512)
+    _run(rows, list(range(6)), 6, R, 512, n, True, ranks, junk=math.nan)
 
 
-@pytest.mark.parametrize("rows", [[1] * 8, [150, 20]])
-def test_rows_outside_the_sequences_are_left_alone(rows):
-    T, k, n = sum(rows) + 12, 256, 256
+@pytest.mark.parametrize("rows,R,n", [([1] * 8, 16, 256), ([150, 20], 16, 256), ([150, 20], 128, 12288)])
+def test_rows_outside_the_sequences_are_left_alone(rows, R, n):
+    T, k = sum(rows) + 12, 256
+    assert _large(T, R, k, n) == (n > 256)
     x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
     y = torch.randn((T, n), generator=_gen(2), device="cuda").half()
     x[:5], x[-7:] = math.nan, math.nan
-    pool = _pool(2, 16, k, n)
+    pool = _pool(2, R, k, n)
     ids = [i % 2 for i in range(len(rows))]
     plan = tq.exl3_adapter_plan(_i32(_starts(rows, 5)), _i32(ids), T, 2)
     out = torch.full_like(y, 7.0)
@@ -143,16 +173,17 @@ def test_rows_outside_the_sequences_are_left_alone(rows):
     assert (out[:5] == 7).all() and (out[-7:] == 7).all()
 
 
-@pytest.mark.parametrize("rows", [[2, 1], [180, 70]])
-def test_strided_rows(rows):
-    T, k, n = sum(rows), 256, 384
+@pytest.mark.parametrize("rows,R,n", [([2, 1], 24, 384), ([180, 70], 24, 384), ([180, 70], 128, 8448)])
+def test_strided_rows(rows, R, n):
+    T, k = sum(rows), 256
+    assert _large(T, R, k, n) == (n > 384)
     wx = torch.full((T, k + 64), math.nan, dtype=torch.float16, device="cuda")
     wy = torch.full((T, 2 * n), math.nan, dtype=torch.float32, device="cuda")
     wo = torch.full((T, n + 32), 7.0, dtype=torch.float32, device="cuda")
     x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
     y = torch.randn((T, n), generator=_gen(2), device="cuda")
     wx[:, 64:], wy[:, n:] = x, y
-    pool = _pool(2, 24, k, n)
+    pool = _pool(2, R, k, n)
     plan = tq.exl3_adapter_plan(_i32(_starts(rows)), _i32([1, 0]), T, 2)
     tq.exl3_adapter_add(wx[:, 64:], wy[:, n:], tq.adapters(*pool), plan, out=wo[:, 16:n + 16])
     _check(wo[:, 16:n + 16].contiguous(), *_reference(x, y, pool, rows, [1, 0]))
@@ -160,13 +191,14 @@ def test_strided_rows(rows):
 
 
 @pytest.mark.parametrize("size", [1e-6, 300.0])
-@pytest.mark.parametrize("rows", [[3, 2], [200, 60]])
-def test_h_outside_fp16(rows, size):
+@pytest.mark.parametrize("rows,R,n", [([3, 2], 16, 256), ([200, 60], 16, 256), ([200, 60], 128, 8192)])
+def test_h_outside_fp16(rows, R, n, size):
     """x A^T of 1e-9 or of 1e6: its two parts are scaled by a power of two per row."""
-    T, k, n = sum(rows), 512, 256
+    T, k = sum(rows), 512
+    assert _large(T, R, k, n) == (n > 256)
     x = (torch.randn((T, k), generator=_gen(1), device="cuda") * size).half()
     y = torch.zeros((T, n), device="cuda")
-    a, b, scale, rank = _pool(2, 16, k, n)
+    a, b, scale, rank = _pool(2, R, k, n)
     a = (a.float() * (300.0 if size > 1 else 0.01)).half()
     pool = (a, b, scale, rank)
     plan = tq.exl3_adapter_plan(_i32(_starts(rows)), _i32([0, 1]), T, 2)
@@ -176,11 +208,11 @@ def test_h_outside_fp16(rows, size):
 
 def test_a_row_does_not_depend_on_the_others():
     """Infinities and NaN in one row of a tile stay there."""
-    for rows in ([9], [140]):
-        T = rows[0]
+    for T, R, n in ((9, 16, 256), (140, 16, 256), (140, 128, 16384)):
+        assert _large(T, R, 256, n) == (n > 256)
         x = torch.randn((T, 256), generator=_gen(1), device="cuda").half()
-        y = torch.randn((T, 256), generator=_gen(2), device="cuda")
-        pool = tq.adapters(*_pool(1, 16, 256, 256))
+        y = torch.randn((T, n), generator=_gen(2), device="cuda")
+        pool = tq.adapters(*_pool(1, R, 256, n))
         plan = tq.exl3_adapter_plan(_i32([0, T]), _i32([0]), T, 1)
         clean = tq.exl3_adapter_add(x, y, pool, plan, out=torch.empty_like(y))
         x[3], x[5, 7] = math.nan, math.inf
@@ -217,17 +249,22 @@ def test_many_adapters_and_sequences():
     rows = [1] * 3000
     _run(rows, [(7 * i) % 3000 for i in range(3000)], 3000, 8, 128, 128)
     _run(rows, [1] * 3000, 2, 8, 128, 128)
+    assert _large(3000, 8, 128, 11136)
+    _run(rows, [(7 * i) % 3000 for i in range(3000)], 3000, 8, 128, 11136)
+    _run(rows, [1] * 3000, 2, 8, 128, 11136)
 
 
-def test_plan_is_refilled_in_a_graph():
+@pytest.mark.parametrize("T,R,n", [(40, 16, 384), (300, 128, 8192)])
+def test_plan_is_refilled_in_a_graph(T, R, n):
     """One captured graph (plan and two linears' adapters) follows changed starts and adapters."""
-    T, k, n, N = 40, 256, 384, 4
+    k, N = 256, 4
+    assert _large(T, R, k, n) == (T > 40)
     x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
     y = torch.randn((T, n), generator=_gen(2), device="cuda").half()
     out, out2 = torch.empty_like(y), torch.empty_like(y)
-    pool, pool2 = _pool(N, 16, k, n), _pool(N, 64, k, n, seed=3)
+    pool, pool2 = _pool(N, R, k, n), _pool(N, 64, k, n, seed=3)
     ad, ad2 = tq.adapters(*pool), tq.adapters(*pool2)
-    q, ids = _i32([0, 10, 20, 40]), _i32([0, 1, 2])
+    q, ids = _i32([0, 10, 20, T]), _i32([0, 1, 2])
     plan = tq.exl3_adapter_plan(q, ids, T, N)
 
     def step():
@@ -240,7 +277,7 @@ def test_plan_is_refilled_in_a_graph():
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         step()
-    for rows, which in (([10, 10, 20], [0, 1, 2]), ([1, 38, 1], [3, 3, -1]), ([40, 0, 0], [2, 2, 1])):
+    for rows, which in (([10, 10, T - 20], [0, 1, 2]), ([1, T - 2, 1], [3, 3, -1]), ([T, 0, 0], [2, 2, 1])):
         q.copy_(_i32(_starts(rows)))
         ids.copy_(_i32(which))
         g.replay()
@@ -249,13 +286,14 @@ def test_plan_is_refilled_in_a_graph():
         _check(out2, *_reference(x, y, pool2, rows, which))
 
 
-def test_one_plan_on_two_streams():
-    T, k, n, N = 24, 512, 1024, 3
+@pytest.mark.parametrize("T,R,n", [(24, 16, 1024), (300, 128, 8192)])
+def test_one_plan_on_two_streams(T, R, n):
+    k, N = 512, 3
     x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
     y = torch.randn((T, n), generator=_gen(2), device="cuda").half()
-    pools = [_pool(N, 16, k, n, seed=s) for s in (0, 1)]
+    pools = [_pool(N, R, k, n, seed=s) for s in (0, 1)]
     ads = [tq.adapters(*p) for p in pools]
-    plan = tq.exl3_adapter_plan(_i32([0, 7, 24]), _i32([2, 0]), T, N)
+    plan = tq.exl3_adapter_plan(_i32([0, 7, T]), _i32([2, 0]), T, N)
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in ads]
     outs = [torch.empty_like(y) for _ in ads]
@@ -266,7 +304,7 @@ def test_one_plan_on_two_streams():
                 tq.exl3_adapter_add(x, y, a, plan, out=o)
     torch.cuda.synchronize()
     for p, o in zip(pools, outs):
-        _check(o, *_reference(x, y, p, [7, 17], [2, 0]))
+        _check(o, *_reference(x, y, p, [7, T - 7], [2, 0]))
 
 
 def test_bindings_refuse_mismatches():

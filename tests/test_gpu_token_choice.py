@@ -10,7 +10,7 @@ import exl3_synth as synth
 import oracle
 import trellis_quantized_gb300 as tq
 from gpu_util import assert_close, dev, host
-from test_gpu_adapters import _check, _i32, _pool, _reference, _starts
+from test_gpu_adapters import _check, _i32, _large, _pool, _reference, _starts
 from test_gpu_router import W_TOL, _check_logits, _route_exact
 
 pytestmark = pytest.mark.gpu
@@ -23,8 +23,9 @@ class Layer:
     layer's own: the linear's outputs have a magnitude of sqrt(512), whose products in
     the experts pass fp16's range.)"""
 
-    def __init__(self, T, seed=0, R=24):
-        self.T = T
+    def __init__(self, T, seed=0):
+        self.T, self.R = T, 24 if T < 2000 else 128
+        assert _large(T, self.R, HIDDEN, HIDDEN) == (T > 2000)
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
         self.moe = synth.moe_case(60, seed, T, E=E, topk=TOPK, hidden=HIDDEN, inter=INTER, K=4)
@@ -35,7 +36,7 @@ class Layer:
         self.lin = synth.linear_case(61, seed, T, HIDDEN, HIDDEN, 4)
         self.x = dev(self.lin.x)
         self.weights = [dev(a) for a in (self.lin.trellis, self.lin.suh, self.lin.svh)]
-        self.pool = _pool(4, R, HIDDEN, HIDDEN, seed=seed)
+        self.pool = _pool(4, self.R, HIDDEN, HIDDEN, seed=seed)
         self.adapters = tq.adapters(*self.pool)
         self.rows = [T] if T < 3 else [T // 3, 1, T - T // 3 - 1]
         self.users = [2, -1, 0][:len(self.rows)]
@@ -82,7 +83,7 @@ def test_a_layers_choices(T):
     assert_close(host(l.z), ref, "experts")
 
 
-@pytest.mark.parametrize("T", [1, 12, 300])
+@pytest.mark.parametrize("T", [1, 12, 300, 2100])
 def test_a_graph_gives_the_same_bits(T):
     l = Layer(T)
     l.step()
@@ -104,7 +105,7 @@ def test_a_graph_gives_the_same_bits(T):
             assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("T", [40, 300])
+@pytest.mark.parametrize("T", [40, 300, 2100])
 def test_two_graphs_at_once(T):
     """Two captured layers replayed on two streams: nothing of one shows in the other.
     (The linears and experts take the stream's workspace, which graphs would share: here only what is new runs.)"""
@@ -138,14 +139,14 @@ def test_two_graphs_at_once(T):
             assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("T", [12, 300])
+@pytest.mark.parametrize("T", [12, 300, 2100])
 def test_one_workspace_for_all_calls(T):
     """Every operator in one workspace, whose counters the linears and experts find at zero."""
     l = Layer(T)
     l.step()
     torch.cuda.synchronize()
     want = l.outputs()
-    need = max(tq.exl3_linear_workspace_size(T, HIDDEN, HIDDEN, 4), tq.exl3_adapter_add_workspace_size(T, 24),
+    need = max(tq.exl3_linear_workspace_size(T, HIDDEN, HIDDEN, 4), tq.exl3_adapter_add_workspace_size(T, l.R),
                tq.exl3_router_logits_workspace_size(), tq.exl3_moe_workspace_size(T, TOPK, E, l.w13, l.w2))
     ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
     kw = dict(workspace_buf=ws)

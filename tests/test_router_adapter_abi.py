@@ -54,7 +54,7 @@ def _add(p="default", **kw):
     g = lambda n, v: kw.pop(n, v)
     call = [g("x", FAKE), g("xs", 2048), g("y", FAKE), g("ys", 512), g("out", ctypes.c_void_p(0x20000)), g("os", 512),
             g("dt", 0)]
-    tail = [g("plan", FAKE), g("T", 3), g("batch", 2), g("ws", FAKE), g("wsb", 256)]
+    tail = [g("plan", FAKE), g("T", 3), g("batch", 2), g("ws", FAKE), g("wsb", 1 << 30)]
     if p == "default":
         p = _fill(tq.Adapters, POOL, kw)
     return tq.lib().exl3_adapter_add(*call, ref(p), *tail, None)

@@ -1004,7 +1004,7 @@ def exl3_adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out=None, work
     if plan.count != N:
         raise ValueError(f"the plan was made for {plan.count} adapters, the pool has {N}")
     raw, need = _stream_of(stream, device), _adapter_workspace(T, R)
-    if need > 256 and workspace_buf is None and stream is None and torch._C._cuda_isCurrentStreamCapturing():
+    if workspace_buf is None and stream is None and torch._C._cuda_isCurrentStreamCapturing():
         # a graph gets memory of its own: two that share the stream's would race when they run at once
         workspace_buf = torch.empty(need, dtype=torch.uint8, device=x.device)
     wp, wn = _workspace_arg(workspace_buf, need, x.device, stream, raw)

@@ -10,7 +10,11 @@ int exl3_launch_adapter_tc(const exl3::ad::Args &a, bool f32, cudaStream_t s);
 
 namespace {
 
-constexpr int kTcFrom = 256;   // rows from which tiles of 128 are used
+// Tiles of 128 rows from here on, of 16 before: the small tiles read A and B once for
+// every 16 rows, the large ones start two kernels.  At k = 5120, in us, small and large:
+// rank 16, n 5120: 1024 rows 10.8 and 16.1; rank 64, n 5120: 512 rows 18.4 and 17.2;
+// rank 64, n 17408: 128 rows 20.7 and 16.0; rank 128, n 17408: 64 rows 25.9 and 21.5.
+bool large_tiles(int T, int R, int k, int n) { return T >= 48 && (int64_t)T * R * (k + n) >= (int64_t)1 << 28; }
 
 bool plan_shape_ok(int T, int batch, int count) {
   return T >= 0 && T <= (1 << 22) && batch >= 1 && batch <= (1 << 20) && count >= 1 && count <= exl3::ad::kMaxCount;
@@ -25,7 +29,7 @@ int check_words(const void *p, const char *name, bool required = true) {
 }
 
 // ---- exl3_adapter_add workspace layout: h of all rows in two fp16 parts and
-// each row's factor, for the calls on large tiles (behind the counters, which
+// each row's factor, for calls on large tiles (behind the counters, which
 // the linears that share a workspace have to find at zero)
 struct AddWs {
   size_t h = kDataOff, back = 0, total = kCtrlBytes;
@@ -33,7 +37,6 @@ struct AddWs {
 
 AddWs add_ws(int T, int R) {
   AddWs w;
-  if (T < kTcFrom) return w;
   w.back = align_up(w.h + (size_t)T * R * 4);
   w.total = align_up(w.back + (size_t)T * 4);
   return w;
@@ -140,7 +143,7 @@ int exl3_adapter_add(const uint16_t *x, int64_t x_stride, const void *y, int64_t
   a.ctrl = reinterpret_cast<const int *>(in_plan(0));
   a.perm = reinterpret_cast<const int *>(in_plan(L.perm));
   a.err = at<int>(workspace, 0);
-  if (T >= kTcFrom) {
+  if (large_tiles(T, ad->max_rank, ad->k, ad->n)) {
     a.tiles = reinterpret_cast<const int4 *>(in_plan(L.tc_tiles));
     a.max_tiles = L.max_tc_tiles;
     a.h = at<__half>(workspace, W.h);

@@ -113,31 +113,36 @@ __device__ __forceinline__ void store_chunk(char *p, const Chunk &c, bool wide) 
   }
 }
 
-// The rows of a tile as one warp's copies of 128-byte pieces see them: one box
-// where they follow one another and are most of a tile (a prompt's; the box's rows
-// past the tile are somebody else's), else gathers of four, lane i rows 4 i .. 4 i
-// + 3 (past the last row: that one again).  32 gathers take an SM a microsecond, a
-// box a tenth.
+// The rows of a tile as one warp's copies of 128-byte pieces see them, 32 at a time:
+// one box where they follow one another (a prompt's; rows of the box past the tile
+// are somebody else's), else gathers of four, lane i rows 4 i .. 4 i + 3 (past the
+// last row: that one again).  32 gathers take an SM a microsecond, a box of as many
+// rows a tenth.
 struct TileRows {
   int4 rows;
-  int at, quads;
-  bool box;
+  int quads, total;
+  bool boxed;             // this lane's 32 rows
   __device__ __forceinline__ void load(const Args &a, const int4 &tile, int lane) {
     const int *p = a.perm + tile.y;
     const int last = tile.z - 1, i = min(4 * lane, last), n = min(4, tile.z - 4 * lane);
     rows = make_int4(p[i], p[min(i + 1, last)], p[min(i + 2, last)], p[min(i + 3, last)]);
     quads = (tile.z + 3) / 4;
-    at = __shfl_sync(0xffffffffu, rows.x, 0);
-    box = __all_sync(0xffffffffu, lane >= quads || (rows.x == at + 4 * lane && rows.y == rows.x + (n > 1) &&
-                                                    rows.z == rows.y + (n > 2) && rows.w == rows.z + (n > 3)));
-    box = box && tile.z > kTcRows / 2;
+    const int first = __shfl_sync(0xffffffffu, rows.x, lane & 24);
+    const bool next = rows.x == first + 4 * (lane & 7) && rows.y == rows.x + (n > 1) && rows.z == rows.y + (n > 2) &&
+                      rows.w == rows.z + (n > 3);
+    const unsigned apart = __ballot_sync(0xffffffffu, lane < quads && !next);
+    // (fewer than twelve rows: three gathers at most)
+    boxed = !(apart >> (lane & 24) & 0xffu) && tile.z - 4 * (lane & 24) >= 12;
+    total = __popc(__ballot_sync(0xffffffffu, boxed && (lane & 7) == 0)) * 4096 +
+            __popc(__ballot_sync(0xffffffffu, !boxed && lane < quads)) * 512;
   }
-  __device__ __forceinline__ int bytes() const { return box ? kPanel : quads * 512; }
-  // the piece at column x: `box_map` has boxes of 128 rows, `row_map` of one
+  // Bytes that a piece's copies bring.
+  __device__ __forceinline__ int bytes() const { return total; }
+  // The piece at column x: `box_map` has boxes of 32 rows, `row_map` of one.
   __device__ __forceinline__ void copy(uint8_t *dst, const CUtensorMap *box_map, const CUtensorMap *row_map, uint64_t *bar,
                                        int x, int lane) const {
-    if (box) {
-      if (lane == 0) tc::tma_load_2d(dst, box_map, bar, x, at);
+    if (boxed) {
+      if ((lane & 7) == 0) tc::tma_load_2d(dst + lane * 512, box_map, bar, x, rows.x);
     } else if (lane < quads) {
       tma_gather4(dst + lane * 512, row_map, bar, x, rows);
     }
@@ -661,7 +666,7 @@ int launch_in(const ad::Args &a, cudaStream_t s) {
   CUtensorMap mx, mt, ma;      // x for gathers of rows and for boxes; A
   {
     const cuuint64_t dims[2] = {(cuuint64_t)a.k, (cuuint64_t)a.T}, stride[1] = {(cuuint64_t)a.x_stride * 2};
-    const cuuint32_t row[2] = {64, 1}, box[2] = {64, ad::kTcRows};
+    const cuuint32_t row[2] = {64, 1}, box[2] = {64, 32};
     int rc = map_f16(&mx, a.x, 2, dims, stride, row);
     if (rc) return rc;
     rc = map_f16(&mt, a.x, 2, dims, stride, box);
@@ -705,7 +710,7 @@ int launch_out(const ad::OutArgs &g, cudaStream_t s) {
   }
   {
     const cuuint64_t dims[2] = {(cuuint64_t)a.n, (cuuint64_t)a.T}, stride[1] = {(cuuint64_t)a.y_stride * (F32 ? 4 : 2)};
-    const cuuint32_t box[2] = {F32 ? 32u : 64u, ad::kTcRows}, row[2] = {F32 ? 32u : 64u, 1};
+    const cuuint32_t box[2] = {F32 ? 32u : 64u, 32}, row[2] = {F32 ? 32u : 64u, 1};
     int rc = map_rows(&my, a.y, 2, dims, stride, box, F32);
     if (rc) return rc;
     rc = map_rows(&mr, a.y, 2, dims, stride, row, F32);
