@@ -774,7 +774,7 @@ def _on_current(t, name: str) -> int:
 
 
 def _matrix(t, name: str, width: int, dtypes, device: int):
-    """Address and row stride of [rows, width] with dense rows on the given device."""
+    """Address, row stride and number of rows of [rows, width] with dense rows on the given device."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     shape = t.shape
@@ -785,7 +785,8 @@ def _matrix(t, name: str, width: int, dtypes, device: int):
     s0, s1 = t.stride()
     if s1 != 1 and width > 1:
         raise ValueError(f"{name}'s rows must be dense")
-    return t.data_ptr(), (s0 if shape[0] > 1 else width)
+    rows = shape[0]
+    return t.data_ptr(), (s0 if rows > 1 else width), rows
 
 
 def _dense(t, name: str, shape, dtype, device: int) -> int:
@@ -858,8 +859,7 @@ def exl3_router_logits(x, router: Router, logits=None, workspace_buf=None, strea
     """logits [T, E] fp32 = x @ w^T (+ bias) for x [T, k] fp16 with dense rows."""
     device = _on_current(x, "x")
     E, k = router._shape
-    xp, xs = _matrix(x, "x", k, _F16, device)
-    T = x.shape[0]
+    xp, xs, T = _matrix(x, "x", k, _F16, device)
     if router._device != device:
         raise ValueError(f"the router is on cuda:{router._device}, x on cuda:{device}")
     if logits is None:
@@ -899,7 +899,7 @@ def exl3_route(logits, rule: RouteRule, ids=None, weights=None, stream=None):
     if len(shape) != 2:
         raise ValueError(f"logits must be [T, E], got {tuple(shape)}")
     T, E = shape
-    lp, ls = _matrix(logits, "logits", E, _F16_F32, device)
+    lp, ls, _ = _matrix(logits, "logits", E, _F16_F32, device)
     if bias is not None and (bias != E or rule._device != device):
         raise ValueError(f"the rule's bias has {bias} experts on cuda:{rule._device}, the logits {E} on cuda:{device}")
     if ids is None:
@@ -988,24 +988,23 @@ def exl3_adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out=None, work
                      stream=None) -> torch.Tensor:
     """y + scale (x A^T) B^T for each row's adapter: x [T, k] fp16, y [T, n] fp16 or fp32, dense
     rows; written to `out`, or to y itself (rows of no sequence are left as they were)."""
-    device, dtype = _on_current(x, "x"), y.dtype
+    device, dtype, T = _on_current(x, "x"), y.dtype, plan.T
     N, R, k, n = adapters._shape
-    xp, xs = _matrix(x, "x", k, _F16, device)
-    yp, ys = _matrix(y, "y", n, _F16_F32, device)
+    xp, xs, xr = _matrix(x, "x", k, _F16, device)
+    yp, ys, yr = _matrix(y, "y", n, _F16_F32, device)
     if out is None or out is y:
-        out, op, os_ = y, yp, ys
+        out, op, os_, rows = y, yp, ys, yr
     else:
-        op, os_ = _matrix(out, "out", n, _F16 if dtype is torch.float16 else _F32, device)
-    T = x.shape[0]
-    if y.shape[0] != T or out.shape[0] != T or plan.T != T:
-        raise ValueError(f"x has {T} rows, y {y.shape[0]}, out {out.shape[0]}, the plan {plan.T}")
-    if plan.device != device or adapters._device != device:
-        raise ValueError(f"x is on cuda:{device}, the plan on cuda:{plan.device}, the pool on cuda:{adapters._device}")
-    if plan.count != N:
-        raise ValueError(f"the plan was made for {plan.count} adapters, the pool has {N}")
+        op, os_, rows = _matrix(out, "out", n, _F16 if dtype is torch.float16 else _F32, device)
+    if not xr == yr == rows == T:
+        raise ValueError(f"x has {xr} rows, y {yr}, out {rows}, the plan {T}")
+    if plan.device != device or adapters._device != device or plan.count != N:
+        raise ValueError(f"x is on cuda:{device}; the plan is for {plan.count} adapters on cuda:{plan.device}, the pool has "
+                         f"{N} on cuda:{adapters._device}")
     raw, need = _stream_of(stream, device), _adapter_workspace(T, R)
-    if workspace_buf is None and stream is None and torch._C._cuda_isCurrentStreamCapturing():
-        # a graph gets memory of its own: two that share the stream's would race when they run at once
+    if workspace_buf is None and stream is None and T >= 48 and torch._C._cuda_isCurrentStreamCapturing():
+        # (fewer rows keep nothing there) a graph gets memory of its own: two that share the stream's would race
+        # when they run at once
         workspace_buf = torch.empty(need, dtype=torch.uint8, device=x.device)
     wp, wn = _workspace_arg(workspace_buf, need, x.device, stream, raw)
     rc = lib().exl3_adapter_add(xp, xs, yp, ys, op, os_, _IO_DTYPES[dtype], adapters._address, plan.address, T,
