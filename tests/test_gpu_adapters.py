@@ -254,6 +254,34 @@ def test_many_adapters_and_sequences():
     _run(rows, [1] * 3000, 2, 8, 128, 11136)
 
 
+@pytest.mark.parametrize("rows,R,n", [([1] * 50, 16, 512), ([3, 1, 1, 30, 2, 9] * 7, 24, 256), ([1, 200, 3, 70, 1, 1], 128, 8192)])
+def test_the_same_call_gives_the_same_bits(rows, R, n):
+    """Plans made again, for sequences whose rows fall into tiles of different sizes."""
+    T, k = sum(rows), 512
+    x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
+    y = torch.randn((T, n), generator=_gen(2), device="cuda")
+    ad, q, ids = tq.adapters(*_pool(2, R, k, n)), _i32(_starts(rows)), _i32([i % 2 for i in range(len(rows))])
+    first = None
+    for _ in range(8):
+        plan = tq.exl3_adapter_plan(q, ids, T, 2)
+        out = tq.exl3_adapter_add(x, y, ad, plan, out=torch.empty_like(y))
+        first = out if first is None else first
+        assert torch.equal(out, first)
+
+
+def test_more_sequences_than_threads():
+    """2500 sequences of zero to three rows: places counted in several stretches."""
+    rows = [i % 4 for i in range(2500)]
+    _run(rows, [(i * 5) % 7 - 1 for i in range(2500)], 6, 16, 128, 128)
+
+
+def test_no_rows():
+    plan = tq.exl3_adapter_plan(_i32([0, 0]), _i32([0]), 0, 1)
+    y = torch.empty((0, 128), device="cuda")
+    x = torch.empty((0, 128), dtype=torch.float16, device="cuda")
+    assert tq.exl3_adapter_add(x, y, tq.adapters(*_pool(1, 8, 128, 128)), plan) is y
+
+
 @pytest.mark.parametrize("T,R,n", [(40, 16, 384), (300, 128, 8192)])
 def test_plan_is_refilled_in_a_graph(T, R, n):
     """One captured graph (plan and two linears' adapters) follows changed starts and adapters."""

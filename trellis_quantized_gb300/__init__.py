@@ -998,6 +998,8 @@ def exl3_adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out=None, work
         op, os_, rows = _matrix(out, "out", n, _F16 if dtype is torch.float16 else _F32, device)
     if not xr == yr == rows == T:
         raise ValueError(f"x has {xr} rows, y {yr}, out {rows}, the plan {T}")
+    if T == 0:
+        return out
     if plan.device != device or adapters._device != device or plan.count != N:
         raise ValueError(f"x is on cuda:{device}; the plan is for {plan.count} adapters on cuda:{plan.device}, the pool has "
                          f"{N} on cuda:{adapters._device}")

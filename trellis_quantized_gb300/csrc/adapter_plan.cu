@@ -4,9 +4,9 @@
 // counted by adapter, each gets its place behind the earlier ones of its
 // adapter, and every adapter's run of rows is cut into tiles.  Rows without an
 // adapter come last, as tiles of adapter -1.  One CTA: a step's batch is small,
-// and one plan serves every linear of every layer.  The order of sequences
-// within an adapter comes from atomics and may differ between runs; no result
-// depends on it (a row's sums do not involve the other rows of its tile).
+// and one plan serves every linear of every layer.  Sequences of one adapter keep
+// their order, so the same batch makes the same tiles every time (a row's last
+// bits go by how many rows its tile has).
 #include "adapter.cuh"
 
 namespace exl3 {
@@ -102,13 +102,27 @@ __global__ void __launch_bounds__(kThreads) adapter_plan_kernel(const PlanArgs p
     p.ctrl[kPlanN] = p.N;
   }
   __syncthreads();
-  // each sequence's place
-  for (int b = threadIdx.x; b < B; b += kThreads) {
-    int a = p.adapter[b];
-    if (a < 0 || a >= p.N) a = p.N;
-    p.base[b] = atomicAdd(&next[a], p.q_start[b + 1] - p.q_start[b]);
+  // each sequence's place: behind its adapter's earlier ones, 1024 at a time
+  __shared__ int ids[kThreads], sizes[kThreads];
+  for (int b0 = 0; b0 < B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x, here = min(kThreads, B - b0);
+    int a = -1, n = 0;
+    if (b < B) {
+      a = p.adapter[b];
+      if (a < 0 || a >= p.N) a = p.N;
+      n = p.q_start[b + 1] - p.q_start[b];
+    }
+    ids[threadIdx.x] = a;
+    sizes[threadIdx.x] = n;
+    __syncthreads();
+    int before = 0;
+    for (int j = 0; j < here; ++j)                         // (every thread reads the same one)
+      if (j < (int)threadIdx.x && ids[j] == a) before += sizes[j];
+    if (b < B) p.base[b] = next[a] + before;
+    __syncthreads();
+    if (b < B) atomicAdd(&next[a], n);                     // (sums of integers: any order)
+    __syncthreads();
   }
-  __syncthreads();
   // each row's place: its sequence is the last one that starts at or before it
   const int lo0 = B ? p.q_start[0] : 0, hi0 = B ? p.q_start[B] : 0;
   for (int t = lo0 + threadIdx.x; t < hi0; t += kThreads) {
