@@ -333,15 +333,18 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const Args a) {
     for (int i = 0; i < V; ++i)
       if (lane + 32 * i < a.E) keys[lane + 32 * i] = key[i];
     __syncwarp();
-    const int size = a.E / a.groups, per = a.group_lanes, g = lane / per, sub = lane % per;
+    const int size = a.group_size, per = 1 << a.group_shift, g = lane >> a.group_shift, sub = lane & (per - 1);
     unsigned first = 0, second = 0;
     if (g < a.groups) {
-      const int n = (size - sub + per - 1) / per;          // this lane's experts: sub, sub + per, ...
-      for (int i = 0, at = n ? g % n : 0; i < n; ++i) {    // (started at different places: other banks)
-        const unsigned k = keys[g * size + sub + per * at];
+      const unsigned *own = keys + g * size;
+      int e = sub + ((g & 7) << a.group_shift);            // (started at different places: other banks)
+      if (e >= size) e = sub;
+      for (int i = sub; i < size; i += per) {
+        const unsigned k = own[e];
         second = max(second, min(first, k));
         first = max(first, k);
-        at = at + 1 == n ? 0 : at + 1;
+        e += per;
+        if (e >= size) e = sub;
       }
     }
     for (int o = per / 2; o; o >>= 1) {
@@ -354,26 +357,23 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const Args a) {
       const float p = key_value(first), q = key_value(second);
       value = first > kNanKey && second > kNanKey ? order_key(p + q) : kNanKey;
     }
-    if (g >= a.groups || sub) value = 0;
-    // the rank of each group among all of them
-    unsigned left = value, keep = 0;
-    float last = 0.0f;
-    for (int j = 0; j <= a.kept; ++j) {                    // (kept < groups: one more than stays)
-      const unsigned top = __reduce_max_sync(kFull, left);
-      const int who = __ffs(__ballot_sync(kFull, left == top)) - 1;
-      const float v = key_value(top);
-      if (j == a.kept) {
-        if (VALUE) again = top > kNanKey && uncertain(last, v, 2.0f * tol, 0x1p-21f);
-      } else {
-        keep |= 1u << (who / per);
-        if (lane == who) left = 0;
-        last = v;
-      }
+    // how many groups stand before each (its first lane speaks for it)
+    const bool speaks = g < a.groups && sub == 0;
+    int before = 0;
+    for (int o = 0; o < a.groups; ++o) {
+      const unsigned v = __shfl_sync(kFull, value, o << a.group_shift);
+      before += v > value || (v == value && o < g);
     }
-    const int inv_size = ((1 << 20) + size - 1) / size;     // (exact below 2^10)
+    const unsigned keep = __ballot_sync(kFull, speaks && before < a.kept);
+    if (VALUE) {                                           // the last that stays and the first that does not
+      const int in = __ffs(__ballot_sync(kFull, speaks && before == a.kept - 1)) - 1;
+      const int out = __ffs(__ballot_sync(kFull, speaks && before == a.kept)) - 1;
+      const unsigned v = __shfl_sync(kFull, value, in), w = __shfl_sync(kFull, value, out);
+      again = w > kNanKey && uncertain(key_value(v), key_value(w), 2.0f * tol, 0x1p-21f);
+    }
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (!(keep >> ((lane + 32 * i) * inv_size >> 20 & 31) & 1u)) key[i] = 0;
+    for (int i = 0; i < V; ++i)                            // (the product's upper bits: e / size for e below 2^10)
+      if (!(keep >> (((lane + 32 * i) * a.group_inverse >> 20) << a.group_shift & 31) & 1u)) key[i] = 0;
   }
 
   // Picks: a key's lowest bits give way to the place within the lane (the first place
@@ -381,57 +381,67 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const Args a) {
   // ids).  The owner's next key is its largest below the one that it gave: the one
   // for which key - top is largest modulo 2^32.
   constexpr unsigned LOW = V - 1;
-  int mine = -1, picks = 0;
-  {
-    unsigned best = 0;
+  unsigned best = 0, top = 0, given = 0;                   // `given`: lane j's, the j-th pick's key,
+  int from = 0, picks = a.topk;                            // and its lane
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      key[i] = key[i] ? (key[i] & ~LOW) | (LOW - i) : 0u;
-      best = max(best, key[i]);
+  for (int i = 0; i < V; ++i) {
+    key[i] = key[i] ? (key[i] & ~LOW) | (LOW - i) : 0u;
+    best = max(best, key[i]);
+  }
+  const auto pick = [&](int j) {
+    top = __reduce_max_sync(kFull, best);
+    const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
+    if (j == lane) {
+      given = top;
+      from = owner;
     }
-    unsigned last = 0, seen = 0;                           // `seen`: keys equal but for their lowest bits, looked at
-    bool mixed = false;                                    // and not all equal
-    for (int j = 0;; ++j) {
-      const unsigned top = __reduce_max_sync(kFull, best);
-      if (top == 0) break;                                 // (nothing behind the last pick)
-      // on until a pick is certainly below the topk-th
-      bool close = false;
-      if (VALUE) {
-        close = j > 0 && top > (kNanKey | LOW) &&
-                uncertain(key_value(last | LOW), key_value(top & ~LOW), tol, 0x1p-22f + 0x1p-22f * V);
-      } else if (!F16 && j > 0 && (last | LOW) == (top | LOW)) {   // (fp16 has no bits there)
-        if (seen != (top | LOW)) {
-          seen = top | LOW;
-          unsigned high = 0, low = 0xffffffffu;
+    if (lane == owner) {
+      unsigned rest = 0;
 #pragma unroll
-          for (int i = 0; i < V; ++i)
-            if ((key[i] | LOW) == seen) {
-              high = max(high, order_key(l[i]));
-              low = min(low, order_key(l[i]));
-            }
-          mixed = __reduce_max_sync(kFull, high) != __reduce_min_sync(kFull, low);
-        }
-        close = mixed;
+      for (int i = 0; i < V; ++i) rest = max(rest, key[i] - top);
+      best = rest + top;                                   // (of keys that are gone: 0)
+      if (best >= top) best = 0;                           // (nothing below, only what it gave before)
+    }
+  };
+  for (int j = 0; j < a.topk; ++j) pick(j);                // (there are as many)
+
+  if (VALUE || !F16) {                                     // (an fp16 logit has no bits where the place went)
+    // Could the exact values of two neighbouring picks stand in another order?
+    const auto close = [&](unsigned upper, unsigned lower) {
+      if (!VALUE) return (upper | LOW) == (lower | LOW);
+      return lower > (kNanKey | LOW) &&
+             uncertain(key_value(upper | LOW), key_value(lower & ~LOW), tol, 0x1p-22f + 0x1p-22f * V);
+    };
+    const unsigned next = __shfl_down_sync(kFull, given, 1);
+    doubt = __any_sync(kFull, lane + 1 < a.topk && close(given, next));
+    if (!VALUE && doubt) {                                 // (equal logits are in order)
+      const unsigned k = order_key(load_logit<F16>(a, row, lane < a.topk ? from + 32 * (int)(LOW - (given & LOW)) : 0));
+      const unsigned n = __shfl_down_sync(kFull, k, 1);
+      doubt = __any_sync(kFull, lane + 1 < a.topk && close(given, next) && k != n);
+    }
+    // on until a pick is certainly below the topk-th
+    for (;;) {
+      const unsigned below = __reduce_max_sync(kFull, best);
+      if (below == 0 || !close(top, below)) break;
+      if (!VALUE) {                                        // all equal: the lower ids come first as they are
+        unsigned high = 0, low = 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if ((key[i] | LOW) == (top | LOW)) {
+            high = max(high, order_key(l[i]));
+            low = min(low, order_key(l[i]));
+          }
+        if (__reduce_max_sync(kFull, high) == __reduce_min_sync(kFull, low)) break;
       }
-      if (j >= a.topk && !close) break;
-      doubt |= close;
-      last = top;
-      if (j == 32) {
+      doubt = true;
+      if (picks == 32) {
         again = true;
         break;
       }
-      const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
-      if (j == lane) mine = owner + 32 * (int)(LOW - (top & LOW));
-      picks = j + 1;
-      if (lane == owner) {
-        unsigned rest = 0;
-#pragma unroll
-        for (int i = 0; i < V; ++i) rest = max(rest, key[i] - top);
-        best = rest + top;                                 // (of keys that are gone: 0)
-        if (best >= top) best = 0;                         // (nothing below, only what it gave before)
-      }
+      pick(picks++);
     }
   }
+  int mine = lane < picks ? from + 32 * (int)(LOW - (given & LOW)) : -1;
   if (VALUE || !F16) {
     unsigned char *mem = smem + (size_t)warp * a.smem_per_warp;
     if (again) mine = select_pairs<F16, VALUE>(a, row, lane, reinterpret_cast<unsigned long long *>(mem));
@@ -500,8 +510,10 @@ cudaError_t exl3_launch_route(const rt::Args &in, bool f16, cudaStream_t s) {
   rt::Args a = in;
   const bool groups = a.kept < a.groups;
   const bool value = a.bias || (groups && a.group_score == EXL3_GROUP_TOP2);
-  a.group_lanes = 32;
-  while (a.group_lanes * a.groups > 32) a.group_lanes /= 2;
+  a.group_shift = 5;
+  while ((a.groups << a.group_shift) > 32) --a.group_shift;
+  a.group_size = a.E / a.groups;
+  a.group_inverse = ((1 << 20) + a.group_size - 1) / a.group_size;
   // 64-bit keys where a doubtful row is done again, 32-bit keys for groups
   a.smem_per_warp = value || !f16 ? std::max(128, (a.E * 8 + 15) / 16 * 16) : groups ? (a.E * 4 + 15) / 16 * 16 : 0;
   return f16 ? launch_v<true>(a, value, groups, s) : launch_v<false>(a, value, groups, s);

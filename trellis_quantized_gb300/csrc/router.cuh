@@ -16,7 +16,8 @@ struct Args {
   float scale;
   int32_t *ids;             // [T][topk]
   float *weights;           // [T][topk]
-  int group_lanes;          // lanes per group: the largest power of two with groups * lanes <= 32
+  int group_shift;          // lanes per group, as a power of two: the most with groups * lanes <= 32
+  int group_size, group_inverse;   // E / groups; 2^20 over it, rounded up
   int smem_per_warp;
 };
 
