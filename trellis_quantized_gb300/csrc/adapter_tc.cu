@@ -13,8 +13,9 @@
 //
 // x, y, A and B are read once and out is written once; h goes through L2.  Up to
 // 4 R / 3 operations per byte: HBM bounds it at every rank, mostly by y and out.
-// One launch (the cluster keeps h and splits the columns too) was measured at
-// 228 us where this takes a third: 46 tiles are two rounds of clusters, one of
+// Four prompts of 6301 tokens, rank 16, 5120 -> 17408, take 99 us: 21 and 78, the
+// second 439 MB of y and out at 0.8 of the copy rate.  One launch (the cluster keeps h
+// and splits the columns too) took 228: 50 tiles are two rounds of clusters, one of
 // them almost empty.
 //
 // h: each row is brought to [2^14, 2^15) by a power of two and then hi + lo, 22
@@ -36,7 +37,7 @@ constexpr int kInThreads = 192;                 // producer, issuer, four warps 
 constexpr int kEpiWarps = 8;
 constexpr int kOutThreads = (3 + kEpiWarps) * 32;   // producers of h and B, and of y; issuer; output
 constexpr uint32_t kOutCols = 256;              // TMEM: two accumulators
-constexpr int kBStages = 6, kYPlaces = 10;      // at most: blocks of B, pieces of y
+constexpr int kBStages = 4, kYPlaces = 8;       // at most: blocks of B, pieces of y
 
 struct InArgs {
   Args a;
@@ -365,8 +366,8 @@ __device__ __forceinline__ bool copies(const Args &a, const int4 &tile) {
 }
 
 // Warp 0 brings h and B, warp 1 issues the products, warps 2 to 9 add y and write
-// out, warp 10 brings y: pieces of 128 rows by 128 bytes, a ring of 128 or 160
-// KB of them (loads into registers, 64 KB of them in flight, ran at 2.2 TB/s).
+// out, warp 10 brings y: pieces of 128 rows by 128 bytes, a ring of 64 to
+// 128 KB of them (loads into registers, 64 KB of them in flight, ran at 2.2 TB/s).
 template <bool F32>
 __global__ void __launch_bounds__(kOutThreads, 1) adapter_out_kernel(const __grid_constant__ CUtensorMap mh,
                                                                      const __grid_constant__ CUtensorMap mb,
@@ -733,8 +734,8 @@ int exl3_launch_adapter_tc(const ad::Args &a, bool f32, cudaStream_t s) {
   ad::OutArgs g = {};
   g.a = a;
   g.panels = (a.R + 63) / 64;
-  // 224 or 208 KB: h, blocks of B (the next one comes while this one's products are
-  // written out), pieces of y.  The places for pieces are a multiple
+  // 224 KB: h, blocks of B (as far ahead as y, behind whose copies theirs queue: two
+  // blocks and ten pieces took 109 us on the prompts above), pieces of y.  The places for pieces are a multiple
   // of a block's pieces, so that a place always serves the same four warps: a
   // warp that did not see each of its phases could not tell them apart.
   g.stages = g.panels == 1 ? 4 : f32 ? 3 : 2;
