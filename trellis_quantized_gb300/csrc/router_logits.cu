@@ -235,14 +235,22 @@ __global__ void __launch_bounds__(kLogitThreads, 1) logits_tc_kernel(const __gri
     tc::tc_fence_after();
     if (!*failed) {
       const int row = 32 * (warp & 3) + lane;
+      const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
       float *dst = reinterpret_cast<float *>(smem) + row * a.pitch;
-      for (int c = 0; c < cols; c += 32) {
+      for (int c = 0; c < a.bn; c += 32) {
         float v[32];
-        tc::tmem_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c, v);
+        tc::tmem_ld32(from + c, v);
+        if (PACKED) {                                       // (half as much to exchange)
+          float lo[32];
+          tc::tmem_ld32(from + a.bn + c, lo);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = fmaf(lo[i], kLoScale, v[i]);
+        }
         tc::tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; i += 4)
-          if (c + i < cols) *reinterpret_cast<float4 *>(dst + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          if (c + i < a.bn) *reinterpret_cast<float4 *>(dst + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
     }
   }
@@ -259,28 +267,22 @@ __global__ void __launch_bounds__(kLogitThreads, 1) logits_tc_kernel(const __gri
       const int r = split * rows + i / quads, c = i % quads * 4, t = m0 + r, e = n0 + c;
       if (t >= a.T || e >= a.E) continue;
       const uint32_t at = base + (uint32_t)(r * a.pitch + c) * 4;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f), lo = v;
-      float4 p[8], q[8];                                    // (all on their way at once)
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f), p[8];   // (all on their way at once)
 #pragma unroll
       for (int s = 0; s < 8; ++s)
-        if (s < S) {
-          p[s] = ld_cluster4(at, s);
-          if (PACKED) q[s] = ld_cluster4(at + a.bn * 4, s);
-        }
+        if (s < S) p[s] = ld_cluster4(at, s);
 #pragma unroll
       for (int s = 0; s < 8; ++s)
         if (s < S) {
           v.x += p[s].x; v.y += p[s].y; v.z += p[s].z; v.w += p[s].w;
-          if (PACKED) { lo.x += q[s].x; lo.y += q[s].y; lo.z += q[s].z; lo.w += q[s].w; }
         }
       float o[4] = {v.x, v.y, v.z, v.w};
-      const float l[4] = {lo.x, lo.y, lo.z, lo.w};
       float *dst = a.logits + (int64_t)t * a.E + e;
       const int n = min(4, a.E - e);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (j < n) {
-          if (PACKED) o[j] = fmaf(l[j], kLoScale, o[j]) * __ldg(a.w_scale + e + j);
+          if (PACKED) o[j] *= __ldg(a.w_scale + e + j);
           if (a.bias) o[j] += __ldg(a.bias + e + j);
         }
       if ((a.E & 3) == 0) {
@@ -346,10 +348,10 @@ int launch_logits(rt::LogitArgs a, cudaStream_t s) {
   NT = (a.E + a.bn - 1) / a.bn;
   const int cols = PACKED ? 2 * a.bn : a.bn, stage = (rt::BM + cols) * rt::BK * 2;
   a.stages = std::min((KB + S - 1) / S, std::min(8, 200 * 1024 / stage));
-  a.pitch = cols + 4;                                       // (a float4 apart: rows start in different banks)
+  a.pitch = a.bn + 4;                                       // (a float4 apart: rows start in different banks)
   a.data_bytes = (int)((std::max<size_t>((size_t)a.stages * stage, (size_t)rt::BM * a.pitch * 4) + 15) / 16 * 16);
-  a.tmem_cols = 32;
-  while ((int)a.tmem_cols < cols) a.tmem_cols *= 2;
+  a.tmem_cols = 32;                                         // (read 32 at a time: lo from bn on)
+  while ((int)a.tmem_cols < cols + (PACKED && a.bn % 32 ? 16 : 0)) a.tmem_cols *= 2;
   // One CTA per SM whatever the ring needs: a CTA that waited for TMEM held by
   // another cluster's, which waits for its own members, could wait for ever.
   const size_t smem = std::max<size_t>(1024 + a.data_bytes + (2 * a.stages + 1) * 8 + 16, 120 * 1024);
