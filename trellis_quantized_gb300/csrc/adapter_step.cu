@@ -154,12 +154,17 @@ __global__ void __launch_bounds__(kStepThreads, 2) adapter_step_kernel(const Arg
     if (u < units && ok0) y[0].load(a.y, t0 * a.y_stride + u * 32 + q * 8);
     if (u < units && ok1) y[1].load(a.y, t1 * a.y_stride + u * 32 + q * 8);
   };
-  int u = split * kStepWarps + warp;
-  uint4 w_next[NC][4];
-  Out<F32> y_next[2] = {};
+  // (two column blocks in flight per warp, each taken up where it was loaded)
+  uint4 w[2][NC][4];
+  Out<F32> y[2][2] = {};
+  const auto load = [&](int u, int at) {
 #pragma unroll
-  for (int c = 0; c < NC; ++c) load_b(u, c, w_next[c]);
-  load_y(u, y_next);
+    for (int c = 0; c < NC; ++c) load_b(u, c, w[at][c]);
+    load_y(u, y[at]);
+  };
+  int u = split * kStepWarps + warp;
+  load(u, 0);
+  load(u + ustep, 1);
   __syncthreads();
   for (int i = threadIdx.x; i < kStepRows * RMAX; i += kStepThreads) {
     float v = 0.0f;
@@ -223,26 +228,17 @@ __global__ void __launch_bounds__(kStepThreads, 2) adapter_step_kernel(const Arg
   // this CTA's columns, 32 per warp and turn
   const bool few = tile.z <= 8;                                 // hi and lo in one product
   const float f0 = back[g], f1 = back[g + 8];
-  for (; u < units; u += ustep) {
+  const auto block = [&](int at) {
     float d[4][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) d[j][i] = 0.0f;
-    uint4 w[NC][4];
-    Out<F32> y[2] = {y_next[0], y_next[1]};
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[c][j] = w_next[c][j];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) load_b(u + ustep, c, w_next[c]);
-    load_y(u + ustep, y_next);
     const auto product = [&](int c, const uint4 (&b)[4]) {
-      const int at = c * 32 + q * 8;
+      const int k = c * 32 + q * 8;
       const bool ok = c * 4 + q < R8;
       const auto part_of = [&](int part, int row) {
-        return ok ? *reinterpret_cast<const uint4 *>(&hs[part][row][at]) : make_uint4(0, 0, 0, 0);
+        return ok ? *reinterpret_cast<const uint4 *>(&hs[part][row][k]) : make_uint4(0, 0, 0, 0);
       };
       if (few) {
         const uint4 hi = part_of(0, g), lo = part_of(1, g);
@@ -259,13 +255,12 @@ __global__ void __launch_bounds__(kStepThreads, 2) adapter_step_kernel(const Arg
     };
 #pragma unroll
     for (int c = 0; c < NC; ++c)
-      if (c < R32) product(c, w[c]);
-    if (RMAX > 64) {
+      if (c < R32) product(c, w[at][c]);
+    if (RMAX > 64)
       for (int c = NC; c < R32; ++c) {
-        load_b(u, c, w[0]);
-        product(c, w[0]);
+        load_b(u, c, w[at][0]);
+        product(c, w[at][0]);
       }
-    }
     if (few)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -282,8 +277,15 @@ __global__ void __launch_bounds__(kStepThreads, 2) adapter_step_kernel(const Arg
           v[2 * j] = f * d[j][2 * r];
           v[2 * j + 1] = f * d[j][2 * r + 1];
         }
-        y[r].add_store(v, a.out, (r ? t1 : t0) * a.out_stride + u * 32 + q * 8);
+        y[at][r].add_store(v, a.out, (r ? t1 : t0) * a.out_stride + u * 32 + q * 8);
       }
+    load(u + 2 * ustep, at);
+    u += ustep;
+  };
+  while (u < units) {
+    block(0);
+    if (u >= units) break;
+    block(1);
   }
   cluster_wait();
 }
