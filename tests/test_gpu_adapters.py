@@ -190,6 +190,46 @@ def test_strided_rows(rows, R, n):
     assert (wo[:, :16] == 7).all() and (wo[:, n + 16:] == 7).all()
 
 
+@pytest.mark.parametrize("fp32", [False, True])
+def test_out_on_16_bytes(fp32):
+    """Large tiles whose output rows start on 16 bytes, not on 32."""
+    T, R, k, n = 250, 128, 256, 8448
+    assert _large(T, R, k, n)
+    at = 4 if fp32 else 8
+    x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
+    y = torch.randn((T, n), generator=_gen(2), device="cuda").to(torch.float32 if fp32 else torch.float16)
+    wide = torch.full((T, n + 2 * at), 7.0, dtype=y.dtype, device="cuda")
+    pool = _pool(2, R, k, n)
+    plan = tq.exl3_adapter_plan(_i32([0, 33, T]), _i32([1, 0]), T, 2)
+    tq.exl3_adapter_add(x, y, tq.adapters(*pool), plan, out=wide[:, at:n + at])
+    _check(wide[:, at:n + at].contiguous(), *_reference(x, y, pool, [33, T - 33], [1, 0]))
+    assert (wide[:, :at] == 7).all() and (wide[:, n + at:] == 7).all()
+
+
+@pytest.mark.parametrize("T,R,k,n,N", [(130000, 8, 128, 17408, 2), (130000, 8, 17408, 128, 2), (2, 128, 128, 17408, 1000),
+                                       (200, 128, 128, 17408, 1000)])
+def test_offsets_past_32_bits(T, R, k, n, N):
+    """x, y and out, or a pool, of more than 2^31 elements: the last rows and the last adapter."""
+    assert max(T * k, T * n, N * R * n) > 1 << 31
+    tail = min(T, 70)
+    x = torch.zeros((T, k), dtype=torch.float16, device="cuda")
+    y = torch.zeros((T, n), dtype=torch.float16, device="cuda")
+    x[-tail:] = torch.randn((tail, k), generator=_gen(1), device="cuda").half()
+    y[-tail:] = torch.randn((tail, n), generator=_gen(2), device="cuda").half()
+    a = torch.zeros((N, R, k), dtype=torch.float16, device="cuda")
+    b = torch.zeros((N, n, R), dtype=torch.float16, device="cuda")
+    small = _pool(1, R, k, n)
+    a[-1], b[-1] = small[0][0], small[1][0]
+    scale = torch.zeros(N, device="cuda")
+    scale[-1] = small[2][0]
+    out = torch.empty_like(y)
+    plan = tq.exl3_adapter_plan(_i32([0, T - tail, T]), _i32([-1 if T == tail else 0, N - 1]), T, N)
+    tq.exl3_adapter_add(x, y, tq.adapters(a, b, scale), plan, out=out)
+    _check(out[-tail:], *_reference(x[-tail:], y[-tail:], small, [tail], [0]))
+    if T > tail:
+        assert (out[:T - tail:1009] == 0).all()
+
+
 @pytest.mark.parametrize("size", [1e-6, 300.0])
 @pytest.mark.parametrize("rows,R,n", [([3, 2], 16, 256), ([200, 60], 16, 256), ([200, 60], 128, 8192)])
 def test_h_outside_fp16(rows, R, n, size):

@@ -90,6 +90,21 @@ def test_packed_weights_keep_22_bits(T):
     assert ((got - want).abs() <= tol).all()
 
 
+def test_rows_past_32_bits():
+    """x and logits of more than 2^31 elements: the last rows."""
+    k, E, tail = 17408, 8, 100
+    x = torch.zeros((130000, k), dtype=torch.float16, device="cuda")
+    xs, w = _inputs(tail, k, E, False)
+    x[-tail:] = xs
+    _check_logits(xs, w, None, tq.exl3_router_logits(x, tq.router(w))[-tail:])
+    del x
+    l = torch.zeros((2200000, 1024), dtype=torch.float16, device="cuda")
+    l[-tail:] = _rand_logits(tail, 1024, seed=20, half=True)
+    ids, got = tq.exl3_route(l, tq.route_rule(4))
+    want_ids, want = _route_exact(l[-tail:], 4, "softmax", None, 1, 1, "max", True, 1.0)
+    assert torch.equal(ids[-tail:].long(), want_ids) and torch.allclose(got[-tail:].double(), want, rtol=W_TOL)
+
+
 def test_logits_repeat_bit_for_bit():
     x, w = _inputs(700, 2048, 256, True)
     r = tq.router(w)

@@ -827,8 +827,8 @@ def router(w, bias=None, stream=None) -> Router:
         parts = torch.empty((2, E, k), dtype=torch.float16, device=w.device)
         scale = torch.empty(E, dtype=torch.float32, device=w.device)
         _check(lib().exl3_router_pack(_ptr(w, "w"), E, k, _ptr(parts, "packed"), _ptr(scale, "scale"), _stream(stream)))
-    d = Router(_ptr(parts, "w").value, None if scale is None else scale.data_ptr(), _vector(bias, "bias", E, torch.float32),
-               E, k)
+    d = Router(_ptr(parts, "w").value, None if scale is None else scale.data_ptr(),
+               _vector(bias, "bias", E, torch.float32), E, k)
     d._keep, d._address, d._device, d._shape = (parts, scale, bias), ctypes.addressof(d), w.get_device(), (E, k)
     return d
 
@@ -1001,8 +1001,8 @@ def exl3_adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out=None, work
     if T == 0:
         return out
     if plan.device != device or adapters._device != device or plan.count != N:
-        raise ValueError(f"x is on cuda:{device}; the plan is for {plan.count} adapters on cuda:{plan.device}, the pool has "
-                         f"{N} on cuda:{adapters._device}")
+        raise ValueError(f"x is on cuda:{device}; the plan is for {plan.count} adapters on cuda:{plan.device}, the pool "
+                         f"has {N} on cuda:{adapters._device}")
     raw, need = _stream_of(stream, device), _adapter_workspace(T, R)
     if workspace_buf is None and stream is None and T >= 48 and torch._C._cuda_isCurrentStreamCapturing():
         # (fewer rows keep nothing there) a graph gets memory of its own: two that share the stream's would race

@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(kStepThreads, 2) adapter_step_kernel(const Arg
       return v;
     };
     if (S * items <= 4096) {                                    // everybody adds up everything,
-      for (int i = threadIdx.x; i < items; i += kStepThreads) *reinterpret_cast<float4 *>(&sum[i / R4][i % R4 * 4]) = total(i);
+      for (int i = threadIdx.x; i < items; i += kStepThreads)
+        *reinterpret_cast<float4 *>(&sum[i / R4][i % R4 * 4]) = total(i);
     } else {                                                    // or its share, and hands it out
       for (int i = items * split / S + threadIdx.x; i < items * (split + 1) / S; i += kStepThreads) {
         const float4 v = total(i);

@@ -140,8 +140,8 @@ struct TileRows {
   // Bytes that a piece's copies bring.
   __device__ __forceinline__ int bytes() const { return total; }
   // The piece at column x: `box_map` has boxes of 32 rows, `row_map` of one.
-  __device__ __forceinline__ void copy(uint8_t *dst, const CUtensorMap *box_map, const CUtensorMap *row_map, uint64_t *bar,
-                                       int x, int lane) const {
+  __device__ __forceinline__ void copy(uint8_t *dst, const CUtensorMap *box_map, const CUtensorMap *row_map,
+                                       uint64_t *bar, int x, int lane) const {
     if (boxed) {
       if ((lane & 7) == 0) tc::tma_load_2d(dst + lane * 512, box_map, bar, x, rows.x);
     } else if (lane < quads) {
@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
       const uint64_t bd = tc::sdesc_k_sw128(ring + st * stage_bytes + kPanel);
       if (tc::elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) tc::mma_f16(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (kb != kb0 || kk != 0) ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk)
+          tc::mma_f16(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (kb != kb0 || kk != 0) ? 1u : 0u);
         tc::mma_commit(&empty[st]);
       }
       __syncwarp();
@@ -617,7 +618,8 @@ int map_rows(CUtensorMap *m, const void *base, int dims, const cuuint64_t *size,
   auto fn = exl3_tmap_encode_fn();
   if (!fn) return exl3_fail(EXL3_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  CUresult r = fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims, const_cast<void *>(base), size, stride, box, estr,
+  CUresult r = fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims,
+                  const_cast<void *>(base), size, stride, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return exl3_fail(EXL3_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
@@ -717,7 +719,8 @@ int launch_out(const ad::OutArgs &g, cudaStream_t s) {
     rc = map_rows(&mr, a.y, 2, dims, stride, row, F32);
     if (rc) return rc;
   }
-  const size_t smem = 1024 + ((2 + g.stages) * (size_t)g.panels + g.y_stages) * ad::kPanel + (6 + 2 * ad::kBStages + 2 * ad::kYPlaces) * 8 + 16;
+  const size_t smem = 1024 + ((2 + g.stages) * (size_t)g.panels + g.y_stages) * ad::kPanel +
+                      (6 + 2 * ad::kBStages + 2 * ad::kYPlaces) * 8 + 16;
   auto kfn = ad::adapter_out_kernel<F32>;
   static std::atomic<size_t> given[kMaxDevices];
   int rc = exl3_cuda_check(exl3_ensure_smem(reinterpret_cast<const void *>(kfn), smem, given), "adapter attribute");
@@ -735,9 +738,10 @@ int exl3_launch_adapter_tc(const ad::Args &a, bool f32, cudaStream_t s) {
   g.a = a;
   g.panels = (a.R + 63) / 64;
   // 224 KB: h, blocks of B (as far ahead as y, behind whose copies theirs queue: two
-  // blocks and ten pieces took 109 us on the prompts above), pieces of y.  The places for pieces are a multiple
-  // of a block's pieces, so that a place always serves the same four warps: a
-  // warp that did not see each of its phases could not tell them apart.
+  // blocks and ten pieces took 109 us on the prompts above), pieces of y.  The places
+  // for pieces are a multiple of a block's pieces, so that a place always serves the
+  // same four warps: a warp that did not see each of its phases could not tell them
+  // apart.
   g.stages = g.panels == 1 ? 4 : f32 ? 3 : 2;
   g.y_stages = g.panels == 1 ? 8 : f32 ? 4 : 6;
   g.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride * (f32 ? 4 : 2) % 32 == 0;
