@@ -29,9 +29,9 @@ def _pool(N, R, k, n, ranks=None, seed=0, junk=0.0):
     return a, b, scale, rank
 
 
-def _large(T, R, k, n):
+def _large(T, R, n):
     """Calls on tiles of 128 rows (the library's rule; smaller ones run on tiles of 16)."""
-    return T >= 48 and T * R * (k + n) >= 1 << 28
+    return T >= 48 and T * (R + 16) ** 2 * n >= 3 << 33
 
 
 def _i32(v):
@@ -119,12 +119,28 @@ def test_prompts(rows, R, fp32):
 
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("fp32", [False, True])
-@pytest.mark.parametrize("R,k,n", [(8, 128, 60032), (16, 17408, 12288), (24, 19200, 384), (40, 512, 12288),
-                                   (64, 256, 8320), (72, 8192, 128), (128, 4096, 512), (128, 128, 5120)])
+@pytest.mark.parametrize("R,k,n", [(8, 128, 76800), (16, 17408, 43008), (24, 19200, 27008), (40, 512, 13696),
+                                   (64, 256, 8320), (72, 8192, 5632), (128, 4096, 2176), (128, 128, 5120)])
 @pytest.mark.parametrize("rows", [[600], [200, 333, 1, 1, 1, 90], [127, 128, 129, 255, 1, 0, 11, 12, 13, 50]])
 def test_large_tiles(rows, R, k, n, fp32, in_place):
-    assert _large(sum(rows), R, k, n)
+    assert _large(sum(rows), R, n)
     _run(rows, [i % 3 for i in range(len(rows))], 3, R, k, n, fp32, in_place=in_place)
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("R,k,n", [(128, 384, 128), (104, 640, 256)])
+def test_large_tiles_of_few_columns(R, k, n, fp32):
+    rows = [9000, 1, 0, 900, 30]
+    assert _large(sum(rows), R, n)
+    _run(rows, [0, 1, 2, 1, -1], 3, R, k, n, fp32)
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("rows", [[4000], [1, 2100, 7, 900, 16, 17]])
+def test_many_small_tiles(rows, fp32):
+    """Prompts of a small rank: hundreds of tiles of 16 rows, in clusters of two."""
+    assert not _large(sum(rows), 16, 1280)
+    _run(rows, [i % 3 for i in range(len(rows))], 3, 16, 1024, 1280, fp32)
 
 
 @pytest.mark.parametrize("fp32", [False, True])
@@ -132,9 +148,9 @@ def test_large_tiles_of_scattered_rows(fp32):
     """Sequences of one to five rows of five adapters and none: every tile gathers."""
     rows = [1 + i % 5 for i in range(300)]
     ids = [(i * 7) % 6 - 1 for i in range(300)]
-    assert _large(sum(rows), 64, 512, 4224)
-    _run(rows, ids, 5, 64, 512, 4224, fp32)
-    _run(rows, ids, 5, 64, 512, 4224, fp32, in_place=True)
+    assert _large(sum(rows), 64, 4608)
+    _run(rows, ids, 5, 64, 512, 4608, fp32)
+    _run(rows, ids, 5, 64, 512, 4608, fp32, in_place=True)
 
 
 @pytest.mark.parametrize("rows,R,n", [([1] * 30, 32, 256), ([400, 1, 30, 200], 32, 256), ([400, 1, 30, 200], 64, 8192)])
@@ -142,7 +158,7 @@ def test_large_tiles_of_scattered_rows(fp32):
 @pytest.mark.parametrize("in_place", [False, True])
 def test_rows_without_an_adapter_keep_y(rows, R, n, fp32, in_place):
     ids = [-1 if i % 3 else 2 for i in range(len(rows))]
-    assert _large(sum(rows), R, 256, n) == (n > 256)
+    assert _large(sum(rows), R, n) == (n > 256)
     _run(rows, ids, 4, R, 256, n, fp32, in_place=in_place)
     _run(rows, [-1] * len(rows), 4, R, 256, n, fp32, in_place=in_place)
 
@@ -152,14 +168,14 @@ def test_rows_without_an_adapter_keep_y(rows, R, n, fp32, in_place):
 @pytest.mark.parametrize("R,ranks", [(64, [8, 64, 16, 33, 0, 40]), (128, [128, 1, 64, 65, 100, 16])])
 def test_ranks_and_what_lies_past_them(rows, n, R, ranks):
     """NaN past an adapter's rank in A, and in B past the next multiple of 16."""
-    assert _large(sum(rows), R, 512, n) == (n > 512)
+    assert _large(sum(rows), R, n) == (n > 512)
     _run(rows, list(range(6)), 6, R, 512, n, True, ranks, junk=math.nan)
 
 
 @pytest.mark.parametrize("rows,R,n", [([1] * 8, 16, 256), ([150, 20], 16, 256), ([150, 20], 128, 12288)])
 def test_rows_outside_the_sequences_are_left_alone(rows, R, n):
     T, k = sum(rows) + 12, 256
-    assert _large(T, R, k, n) == (n > 256)
+    assert _large(T, R, n) == (n > 256)
     x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
     y = torch.randn((T, n), generator=_gen(2), device="cuda").half()
     x[:5], x[-7:] = math.nan, math.nan
@@ -176,7 +192,7 @@ def test_rows_outside_the_sequences_are_left_alone(rows, R, n):
 @pytest.mark.parametrize("rows,R,n", [([2, 1], 24, 384), ([180, 70], 24, 384), ([180, 70], 128, 8448)])
 def test_strided_rows(rows, R, n):
     T, k = sum(rows), 256
-    assert _large(T, R, k, n) == (n > 384)
+    assert _large(T, R, n) == (n > 384)
     wx = torch.full((T, k + 64), math.nan, dtype=torch.float16, device="cuda")
     wy = torch.full((T, 2 * n), math.nan, dtype=torch.float32, device="cuda")
     wo = torch.full((T, n + 32), 7.0, dtype=torch.float32, device="cuda")
@@ -194,7 +210,7 @@ def test_strided_rows(rows, R, n):
 def test_out_on_16_bytes(fp32):
     """Large tiles whose output rows start on 16 bytes, not on 32."""
     T, R, k, n = 250, 128, 256, 8448
-    assert _large(T, R, k, n)
+    assert _large(T, R, n)
     at = 4 if fp32 else 8
     x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
     y = torch.randn((T, n), generator=_gen(2), device="cuda").to(torch.float32 if fp32 else torch.float16)
@@ -206,7 +222,8 @@ def test_out_on_16_bytes(fp32):
     assert (wide[:, :at] == 7).all() and (wide[:, n + at:] == 7).all()
 
 
-@pytest.mark.parametrize("T,R,k,n,N", [(130000, 8, 128, 17408, 2), (130000, 8, 17408, 128, 2), (2, 128, 128, 17408, 1000),
+@pytest.mark.parametrize("T,R,k,n,N", [(130000, 8, 128, 17408, 2), (130000, 8, 17408, 128, 2),
+                                       (130000, 64, 17408, 128, 2), (2, 128, 128, 17408, 1000),
                                        (200, 128, 128, 17408, 1000)])
 def test_offsets_past_32_bits(T, R, k, n, N):
     """x, y and out, or a pool, of more than 2^31 elements: the last rows and the last adapter."""
@@ -235,7 +252,7 @@ def test_offsets_past_32_bits(T, R, k, n, N):
 def test_h_outside_fp16(rows, R, n, size):
     """x A^T of 1e-9 or of 1e6: its two parts are scaled by a power of two per row."""
     T, k = sum(rows), 512
-    assert _large(T, R, k, n) == (n > 256)
+    assert _large(T, R, n) == (n > 256)
     x = (torch.randn((T, k), generator=_gen(1), device="cuda") * size).half()
     y = torch.zeros((T, n), device="cuda")
     a, b, scale, rank = _pool(2, R, k, n)
@@ -249,7 +266,7 @@ def test_h_outside_fp16(rows, R, n, size):
 def test_a_row_does_not_depend_on_the_others():
     """Infinities and NaN in one row of a tile stay there."""
     for T, R, n in ((9, 16, 256), (140, 16, 256), (140, 128, 16384)):
-        assert _large(T, R, 256, n) == (n > 256)
+        assert _large(T, R, n) == (n > 256)
         x = torch.randn((T, 256), generator=_gen(1), device="cuda").half()
         y = torch.randn((T, n), generator=_gen(2), device="cuda")
         pool = tq.adapters(*_pool(1, R, 256, n))
@@ -289,9 +306,9 @@ def test_many_adapters_and_sequences():
     rows = [1] * 3000
     _run(rows, [(7 * i) % 3000 for i in range(3000)], 3000, 8, 128, 128)
     _run(rows, [1] * 3000, 2, 8, 128, 128)
-    assert _large(3000, 8, 128, 11136)
-    _run(rows, [(7 * i) % 3000 for i in range(3000)], 3000, 8, 128, 11136)
-    _run(rows, [1] * 3000, 2, 8, 128, 11136)
+    assert _large(3000, 8, 14976)
+    _run(rows, [(7 * i) % 3000 for i in range(3000)], 3000, 8, 128, 14976)
+    _run(rows, [1] * 3000, 2, 8, 128, 14976)
 
 
 @pytest.mark.parametrize("rows,R,n", [([1] * 50, 16, 512), ([3, 1, 1, 30, 2, 9] * 7, 24, 256), ([1, 200, 3, 70, 1, 1], 128, 8192)])
@@ -326,7 +343,7 @@ def test_no_rows():
 def test_plan_is_refilled_in_a_graph(T, R, n):
     """One captured graph (plan and two linears' adapters) follows changed starts and adapters."""
     k, N = 256, 4
-    assert _large(T, R, k, n) == (T > 40)
+    assert _large(T, R, n) == (T > 40)
     x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
     y = torch.randn((T, n), generator=_gen(2), device="cuda").half()
     out, out2 = torch.empty_like(y), torch.empty_like(y)

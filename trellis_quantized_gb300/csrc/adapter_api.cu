@@ -11,10 +11,17 @@ int exl3_launch_adapter_tc(const exl3::ad::Args &a, bool f32, cudaStream_t s);
 namespace {
 
 // Tiles of 128 rows from here on, of 16 before: the small tiles read A and B once for
-// every 16 rows, the large ones start two kernels.  At k = 5120, in us, small and large:
-// rank 16, n 5120: 1024 rows 10.8 and 16.1; rank 64, n 5120: 512 rows 18.4 and 17.2;
-// rank 64, n 17408: 128 rows 20.7 and 16.0; rank 128, n 17408: 64 rows 25.9 and 21.5.
-bool large_tiles(int T, int R, int k, int n) { return T >= 48 && (int64_t)T * R * (k + n) >= (int64_t)1 << 28; }
+// every 16 rows and their time grows with rank and columns, the large ones start two
+// kernels and pass over y at the copy rate.  One prompt, us on small and large tiles:
+//   k 5120, n 5120:  rank 16: 2048 rows 16 and 20, 4096 38 and 30;
+//                    rank 64: 768 rows 18 and 19, 1536 29 and 21;
+//   k 5120, n 17408: rank 16: 768 rows 20 and 20, 1536 43 and 29;
+//                    rank 64: 64 rows 15 and 16, 192 23 and 19; rank 128: 64 rows 28 and 18;
+//   k 17408, n 5120: rank 16: 4096 rows 56 and 50; rank 128: 256 rows 30 and 36, 512 45 and 37.
+// Rows of many short sequences gather, which costs the large tiles up to twice as much
+// (768 rows of rank 16, n 17408: 22 and 36).  Over 1200 such calls the time is 1.03 of
+// the better side's.  (The small tiles' grid stays within 2^15 tiles: T < 2^19 here.)
+bool large_tiles(int T, int R, int n) { return T >= 48 && (int64_t)T * (R + 16) * (R + 16) * n >= (int64_t)3 << 33; }
 
 bool plan_shape_ok(int T, int batch, int count) {
   return T >= 0 && T <= (1 << 22) && batch >= 1 && batch <= (1 << 20) && count >= 1 && count <= exl3::ad::kMaxCount;
@@ -143,7 +150,7 @@ int exl3_adapter_add(const uint16_t *x, int64_t x_stride, const void *y, int64_t
   a.ctrl = reinterpret_cast<const int *>(in_plan(0));
   a.perm = reinterpret_cast<const int *>(in_plan(L.perm));
   a.err = at<int>(workspace, 0);
-  if (large_tiles(T, ad->max_rank, ad->k, ad->n)) {
+  if (large_tiles(T, ad->max_rank, ad->n)) {
     a.tiles = reinterpret_cast<const int4 *>(in_plan(L.tc_tiles));
     a.max_tiles = L.max_tc_tiles;
     a.h = at<__half>(workspace, W.h);

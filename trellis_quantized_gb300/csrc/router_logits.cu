@@ -337,7 +337,7 @@ int launch_logits(rt::LogitArgs a, cudaStream_t s) {
   int NT = (a.E + most - 1) / most;
   // Clusters that run at once at one CTA per SM, by the parts that the SMs come in:
   // 76 of two CTAs, 36 of four, 15 of eight (of 152 SMs; one more cluster is a
-  // second round: 48 tokens took 9.2 us as 16 clusters of eight and 5.2 as 8).
+  // second round: 48 tokens took 9.2 us as 16 clusters of eight and 5.1 as 8).
   // Smaller tiles of experts while clusters of four are to be had (32 experts at
   // least), then the largest split that fits.
   while ((int64_t)MT * 2 * NT <= sms * 36 / 152 && a.E / (2 * NT) >= 32) NT *= 2;
