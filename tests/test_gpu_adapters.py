@@ -31,7 +31,7 @@ def _pool(N, R, k, n, ranks=None, seed=0, junk=0.0):
 
 def _large(T, R, n):
     """Calls on tiles of 128 rows (the library's rule; smaller ones run on tiles of 16)."""
-    return T >= 48 and T * (R + 16) ** 2 * n >= 3 << 33
+    return T >= 48 and T * (R + 16) ** 2 * n >= 1 << 34
 
 
 def _i32(v):

@@ -13,15 +13,15 @@ namespace {
 // Tiles of 128 rows from here on, of 16 before: the small tiles read A and B once for
 // every 16 rows and their time grows with rank and columns, the large ones start two
 // kernels and pass over y at the copy rate.  One prompt, us on small and large tiles:
-//   k 5120, n 5120:  rank 16: 2048 rows 16 and 20, 4096 38 and 30;
-//                    rank 64: 768 rows 18 and 19, 1536 29 and 21;
-//   k 5120, n 17408: rank 16: 768 rows 20 and 20, 1536 43 and 29;
-//                    rank 64: 64 rows 15 and 16, 192 23 and 19; rank 128: 64 rows 28 and 18;
-//   k 17408, n 5120: rank 16: 4096 rows 56 and 50; rank 128: 256 rows 30 and 36, 512 45 and 37.
+//   k 5120, n 5120:  rank 16: 2048 rows 16 and 19, 4096 38 and 30;
+//                    rank 64: 512 rows 18 and 16, 1536 29 and 19;
+//   k 5120, n 17408: rank 16: 768 rows 20 and 18, 1536 43 and 28;
+//                    rank 64: 64 rows 15 and 13, 192 23 and 17; rank 128: 64 rows 28 and 15;
+//   k 17408, n 5120: rank 16: 1536 rows 24 and 25, 4096 56 and 49; rank 128: 256 rows 30 and 25.
 // Rows of many short sequences gather, which costs the large tiles up to twice as much
 // (768 rows of rank 16, n 17408: 22 and 36).  Over 1200 such calls the time is 1.03 of
-// the better side's.  (The small tiles' grid stays within 2^15 tiles: T < 2^19 here.)
-bool large_tiles(int T, int R, int n) { return T >= 48 && (int64_t)T * (R + 16) * (R + 16) * n >= (int64_t)3 << 33; }
+// the better side's.  (The small tiles' grid stays within 2^15 tiles: T < 2^18 here.)
+bool large_tiles(int T, int R, int n) { return T >= 48 && (int64_t)T * (R + 16) * (R + 16) * n >= (int64_t)1 << 34; }
 
 bool plan_shape_ok(int T, int batch, int count) {
   return T >= 0 && T <= (1 << 22) && batch >= 1 && batch <= (1 << 20) && count >= 1 && count <= exl3::ad::kMaxCount;

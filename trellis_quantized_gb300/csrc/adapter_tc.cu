@@ -13,7 +13,7 @@
 //
 // x, y, A and B are read once and out is written once; h goes through L2.  Up to
 // 4 R / 3 operations per byte: HBM bounds it at every rank, mostly by y and out.
-// Four prompts of 6301 tokens, rank 16, 5120 -> 17408, take 99 us: 21 and 78, the
+// Four prompts of 6301 tokens, rank 16, 5120 -> 17408, take 100 us: 21 and 79, the
 // second 439 MB of y and out at 0.8 of the copy rate.  One launch (the cluster keeps h
 // and splits the columns too) took 228: 50 tiles are two rounds of clusters, one of
 // them almost empty.
@@ -118,34 +118,47 @@ __device__ __forceinline__ void store_chunk(char *p, const Chunk &c, bool wide) 
 // one box where they follow one another (a prompt's; rows of the box past the tile
 // are somebody else's), else gathers of four, lane i rows 4 i .. 4 i + 3 (past the
 // last row: that one again).  32 gathers take an SM a microsecond, a box of as many
-// rows a tenth.
+// rows a tenth.  One elected lane starts the boxes and a vote skips the gathers: copies
+// under conditions that the compiler cannot tell to be one lane's took the warp 1100
+// cycles a piece, 600 of them for a branch that no lane took.
 struct TileRows {
   int4 rows;
   int quads, total;
-  bool boxed;             // this lane's 32 rows
+  int first[4];           // rows of the boxes
+  unsigned boxes;         // a bit for each that is one
+  bool gather;            // this lane's rows
   __device__ __forceinline__ void load(const Args &a, const int4 &tile, int lane) {
     const int *p = a.perm + tile.y;
     const int last = tile.z - 1, i = min(4 * lane, last), n = min(4, tile.z - 4 * lane);
     rows = make_int4(p[i], p[min(i + 1, last)], p[min(i + 2, last)], p[min(i + 3, last)]);
     quads = (tile.z + 3) / 4;
-    const int first = __shfl_sync(0xffffffffu, rows.x, lane & 24);
-    const bool next = rows.x == first + 4 * (lane & 7) && rows.y == rows.x + (n > 1) && rows.z == rows.y + (n > 2) &&
+    const int start = __shfl_sync(0xffffffffu, rows.x, lane & 24);
+    const bool next = rows.x == start + 4 * (lane & 7) && rows.y == rows.x + (n > 1) && rows.z == rows.y + (n > 2) &&
                       rows.w == rows.z + (n > 3);
     const unsigned apart = __ballot_sync(0xffffffffu, lane < quads && !next);
-    // (fewer than twelve rows: three gathers at most)
-    boxed = !(apart >> (lane & 24) & 0xffu) && tile.z - 4 * (lane & 24) >= 12;
-    total = __popc(__ballot_sync(0xffffffffu, boxed && (lane & 7) == 0)) * 4096 +
-            __popc(__ballot_sync(0xffffffffu, !boxed && lane < quads)) * 512;
+    boxes = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      first[b] = __shfl_sync(0xffffffffu, rows.x, 8 * b);
+      // (fewer than twelve rows: three gathers at most)
+      if (!(apart >> (8 * b) & 0xffu) && tile.z - 32 * b >= 12) boxes |= 1u << b;
+    }
+    gather = lane < quads && !(boxes >> (lane >> 3) & 1u);
+    total = __popc(boxes) * 4096 + __popc(__ballot_sync(0xffffffffu, gather)) * 512;
   }
   // Bytes that a piece's copies bring.
   __device__ __forceinline__ int bytes() const { return total; }
   // The piece at column x: `box_map` has boxes of 32 rows, `row_map` of one.
   __device__ __forceinline__ void copy(uint8_t *dst, const CUtensorMap *box_map, const CUtensorMap *row_map,
                                        uint64_t *bar, int x, int lane) const {
-    if (boxed) {
-      if ((lane & 7) == 0) tc::tma_load_2d(dst + lane * 512, box_map, bar, x, rows.x);
-    } else if (lane < quads) {
-      tma_gather4(dst + lane * 512, row_map, bar, x, rows);
+    if (tc::elect_one()) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (boxes >> b & 1u) tc::tma_load_2d(dst + b * 4096, box_map, bar, x, first[b]);
+    }
+    if (__any_sync(0xffffffffu, gather)) {
+      if (gather) tma_gather4(dst + lane * 512, row_map, bar, x, rows);
+      __syncwarp();
     }
   }
 };
@@ -194,11 +207,13 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
   const int stage_bytes = kPanel + g.r16 * 128;
   const int pitch = g.r16 + 4;                                      // floats between rows of sums
   const auto bring = [&](int st, int kb) {                          // (warp 0)
-    if (lane == 0) tc::mbar_arrive_expect_tx(&full[st], rows.bytes() + g.r16 * 128);
-    __syncwarp();
     uint8_t *sx = ring + st * stage_bytes;
+    if (tc::elect_one()) {
+      tc::mbar_arrive_expect_tx(&full[st], rows.bytes() + g.r16 * 128);
+      tc::tma_load_3d(sx + kPanel, &ma, &full[st], kb * 64, 0, tile.x);
+    }
+    __syncwarp();
     rows.copy(sx, &mt, &mx, &full[st], kb * 64, lane);
-    if (lane == 0) tc::tma_load_3d(sx + kPanel, &ma, &full[st], kb * 64, 0, tile.x);
   };
   const int ahead = min(kb1, kb0 + g.stages);
   __syncwarp();
@@ -506,12 +521,10 @@ __global__ void __launch_bounds__(kOutThreads, 1) adapter_out_kernel(const __gri
       TileRows rows;
       rows.load(a, tile, lane);
       for (int p = nb0 * PIECES; p < nb1 * PIECES; ++p) {
-        if (lane == 0) {
-          ok = tc::mbar_wait(&y_empty[st], phase ^ 1);
-          if (ok) tc::mbar_arrive_expect_tx(&y_full[st], rows.bytes());
-        }
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&y_empty[st], phase ^ 1));
         if (!ok) break;
+        if (tc::elect_one()) tc::mbar_arrive_expect_tx(&y_full[st], rows.bytes());
+        __syncwarp();
         rows.copy(ys + st * kPanel, &my, &mr, &y_full[st], p * PCOLS, lane);
         if (++st == g.y_stages) { st = 0; phase ^= 1; }
       }
@@ -660,8 +673,10 @@ int launch_in(const ad::Args &a, cudaStream_t s) {
   g.r16 = (a.R + 15) / 16 * 16;
   const int stage = ad::kPanel + g.r16 * 128;
   // Three CTAs on an SM, two above rank 64: never more than TMEM has columns for
-  // (a CTA that waited for TMEM while its cluster waits for it could wait for ever)
-  g.ring_bytes = (a.R <= 64 ? 72 : 104) * 1024;
+  // (a CTA that waited for TMEM while its cluster waits for it could wait for ever).
+  // Few tiles leave a CTA an SM: as deep a ring as fits.
+  const bool few = a.max_tiles <= exl3_sm_count() * 15 / 152;
+  g.ring_bytes = (few ? 192 : a.R <= 64 ? 72 : 104) * 1024;
   g.stages = std::min(8, g.ring_bytes / stage);
   g.tmem_cols = 32;
   while ((int)g.tmem_cols < g.r16) g.tmem_cols *= 2;
