@@ -695,9 +695,10 @@ int exl3_adapter_plan(const int32_t *q_start, const int32_t *adapter, int T, int
  *            done when out is y); rows that belong to no sequence are left as
  *            they were.
  *   plan     filled for the same T, batch and count = adapters->count by a call
- *            ahead on the stream (one made for others is recorded in the
- *            workspace's error word and no row is written); it is only read, so
- *            several calls may use it at once
+ *            ahead on the stream (one made for others, whose first 256 bytes are
+ *            then all that is read, is recorded in the workspace's error word and
+ *            no row is written); it is only read, so several calls may use it at
+ *            once
  *   workspace of exl3_adapter_add_workspace_size(T, max_rank) bytes
  *   x A^T is summed in fp32 and enters the second product as two fp16 parts (22
  *   bits); the sum with y is rounded once.  T = 0 enqueues nothing.  What lies in the pool past an

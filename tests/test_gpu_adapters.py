@@ -406,3 +406,20 @@ def test_bindings_refuse_mismatches():
         tq.exl3_adapter_add(x, y, pool, plan, out=y.half())
     with pytest.raises(ValueError, match="plan was made"):
         tq.exl3_adapter_plan(_i32([0, 4]), _i32([0]), 5, 2, plan=plan)
+
+
+@pytest.mark.parametrize("T,batch,R,n", [(100000, 1, 8, 128), (40, 2, 8, 128), (70000, 1, 128, 256), (300, 3000, 128, 8192)])
+def test_a_plan_of_another_call_is_recorded(T, batch, R, n):
+    """The C entry point gets a plan that was made for six rows and is as long as these need: behind
+    its control block nothing of it may be read by the sizes of this call."""
+    k, L = 128, tq.lib()
+    x = torch.zeros((T, k), dtype=torch.float16, device="cuda")
+    y, out = torch.zeros((T, n), device="cuda"), torch.full((T, n), 7.0, device="cuda")
+    pool = tq.adapters(*_pool(2, R, k, n))
+    plan = tq.exl3_adapter_plan(_i32([0, 6]), _i32([1]), 6, 2)
+    ws = torch.zeros(tq.exl3_adapter_add_workspace_size(T, R), dtype=torch.uint8, device="cuda")
+    assert plan.data.numel() <= tq.exl3_adapter_plan_size(T, batch, 2)    # (whole blocks of 256 bytes)
+    assert L.exl3_adapter_add(x.data_ptr(), k, y.data_ptr(), n, out.data_ptr(), n, tq.EXL3_OUT_F32, pool._address,
+                              plan.address, T, batch, ws.data_ptr(), ws.numel(), None) == 0
+    torch.cuda.synchronize()
+    assert (out == 7).all() and tq.exl3_check_device_error(ws) != 0

@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(kStepThreads, 2) adapter_step_kernel(const Arg
   pdl_trigger();
   pdl_wait();
   const int tiles = plan_tiles(a, kPlanStepTiles);
-  const int4 tile = a.tiles[blockIdx.y];                        // (inside the plan for every block)
   if ((int)blockIdx.y >= tiles) return;                         // (the whole cluster)
+  const int4 tile = a.tiles[blockIdx.y];                        // (not before: another call's plan may be shorter)
   if (tile.x < 0) {
     copy_rows<F32>(a, tile, split, S, kStepThreads);
     return;

@@ -194,8 +194,9 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
   }
   pdl_wait();
   const int tiles = plan_tiles(a, kPlanTcTiles);
-  const int4 tile = a.tiles[blockIdx.y];
-  const bool some = (int)blockIdx.y < tiles && tile.x >= 0;
+  int4 tile = make_int4(-1, 0, 0, 0);
+  if ((int)blockIdx.y < tiles) tile = a.tiles[blockIdx.y];          // (else it may lie behind another call's plan)
+  const bool some = tile.x >= 0;
   TileRows rows;
   if (some && warp == 0) rows.load(a, tile, lane);                  // (beside the rank's load)
   const int rank = some ? adapter_rank(a, tile.x) : 0;
