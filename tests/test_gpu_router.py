@@ -295,3 +295,28 @@ def test_empty_calls():
     assert tq.exl3_route(torch.empty((0, 8), device="cuda"), tq.route_rule(2))[0].shape == (0, 2)
     w = torch.zeros((8, 64), dtype=torch.float16, device="cuda")
     assert tq.exl3_router_logits(torch.empty((0, 64), dtype=torch.float16, device="cuda"), tq.router(w)).shape == (0, 8)
+
+
+def test_a_rule_changed_after_it_was_made():
+    """The rule's fields are read at the call: outputs are as wide as its topk then."""
+    l = _rand_logits(30, 64, seed=17)
+    rule = tq.route_rule(4)
+    for topk in (4, 12, 2):
+        rule.topk = topk
+        ids, w = tq.exl3_route(l, rule)
+        want_ids, want_w = tq.exl3_route(l, tq.route_rule(topk))
+        assert ids.shape == (30, topk) and torch.equal(ids, want_ids) and torch.equal(w, want_w)
+    rule.topk = 12
+    with pytest.raises(ValueError, match="ids must be"):
+        tq.exl3_route(l, rule, ids=torch.empty((30, 4), dtype=torch.int32, device="cuda"))
+    rule.scale = 2.5
+    assert torch.equal(tq.exl3_route(l, rule)[1], tq.exl3_route(l, tq.route_rule(12, scale=2.5))[1])
+
+
+def test_sizes_of_a_router_stay():
+    x, w = _inputs(3, 64, 16, False)
+    r = tq.router(w)
+    for name in ("E", "k"):
+        with pytest.raises(AttributeError, match="size"):
+            setattr(r, name, 128)
+    _check_logits(x, w, None, tq.exl3_router_logits(x, r))

@@ -167,3 +167,20 @@ def test_bindings_refuse_other_types():
         tq.exl3_route(torch.zeros(2, 8), tq.route_rule(2))
     with pytest.raises(ValueError, match="CUDA"):
         tq.exl3_adapter_plan(torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), 1, 1)
+
+
+def test_descriptors_keep_the_sizes_of_their_tensors():
+    """Kernels go by the descriptor's sizes, a call's checks by the tensors': they must not part.
+    (Descriptors as router() and adapters() leave them, of addresses that nothing reads.)"""
+    router, pool = tq.Router(FAKE.value, None, None, 16, 64), tq.Adapters(FAKE.value, FAKE.value, FAKE.value, None, 2, 8, 128, 256)
+    for d in (router, pool):
+        d.k = d.k                                          # (not made yet)
+        d._address = ctypes.addressof(d)
+    for d, names in ((router, "E k"), (pool, "count max_rank k n")):
+        for name in names.split():
+            before = getattr(d, name)
+            with pytest.raises(AttributeError, match="size"):
+                setattr(d, name, before + 128)
+            assert getattr(d, name) == before
+    router.bias = FAKE.value                               # an address may be set
+    assert router.bias == FAKE.value

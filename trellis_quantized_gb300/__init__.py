@@ -88,8 +88,20 @@ class PagedBatch(ctypes.Structure):
                 ("batch", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
-class Router(ctypes.Structure):
+class _Made(ctypes.Structure):
+    """A descriptor made for tensors of certain sizes: those fields stay as they are, since the
+    kernels go by them and the checks of a call by the tensors' shapes."""
+    _sizes: tuple = ()
+
+    def __setattr__(self, name, value):
+        if name in self._sizes and "_address" in self.__dict__:
+            raise AttributeError(f"{name} is a size of the {type(self).__name__}'s tensors: make another one")
+        super().__setattr__(name, value)
+
+
+class Router(_Made):
     """exl3_router: a row of weights per expert (device pointers)."""
+    _sizes = ("E", "k")
     _fields_ = [("w", ctypes.c_void_p), ("w_scale", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("E", ctypes.c_int),
                 ("k", ctypes.c_int)]
 
@@ -101,8 +113,9 @@ class RouteRule(ctypes.Structure):
                 ("renormalise", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
-class Adapters(ctypes.Structure):
+class Adapters(_Made):
     """exl3_adapters: a pool of low-rank adapters for one linear (device pointers)."""
+    _sizes = ("count", "max_rank", "k", "n")
     _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rank", ctypes.c_void_p),
                 ("count", ctypes.c_int), ("max_rank", ctypes.c_int), ("k", ctypes.c_int), ("n", ctypes.c_int)]
 
@@ -886,7 +899,7 @@ def route_rule(topk: int, score: int = EXL3_SCORE_SOFTMAX, bias=None, groups: in
         bp = _vector(bias, "bias", bias.shape[0], torch.float32)
     d = RouteRule(score, bp, groups, groups if groups_kept is None else groups_kept, group_score, topk,
                   1 if renormalise else 0, scale)
-    d._keep, d._address, d._topk = (bias,), ctypes.addressof(d), topk
+    d._keep, d._address = (bias,), ctypes.addressof(d)
     d._experts, d._device = (None, None) if bias is None else (bias.shape[0], bias.get_device())
     return d
 
@@ -895,7 +908,7 @@ def exl3_route(logits, rule: RouteRule, ids=None, weights=None, stream=None):
     """Experts and weights of each token from logits [T, E] (fp32 or fp16, dense rows): ids int32
     and weights fp32, [T, topk], as exl3_moe_grouped takes them."""
     device = _on_current(logits, "logits")
-    shape, topk, bias = logits.shape, rule._topk, rule._experts
+    shape, topk, bias = logits.shape, rule.topk, rule._experts
     if len(shape) != 2:
         raise ValueError(f"logits must be [T, E], got {tuple(shape)}")
     T, E = shape
