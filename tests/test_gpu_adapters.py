@@ -423,3 +423,12 @@ def test_a_plan_of_another_call_is_recorded(T, batch, R, n):
                               plan.address, T, batch, ws.data_ptr(), ws.numel(), None) == 0
     torch.cuda.synchronize()
     assert (out == 7).all() and tq.exl3_check_device_error(ws) != 0
+
+
+def test_a_plan_of_another_device_is_refused():
+    """(With one GPU: a plan that says so.)"""
+    q, ids = _i32([0, 4]), _i32([0])
+    plan = tq.exl3_adapter_plan(q, ids, 4, 2)
+    plan.device += 1
+    with pytest.raises(ValueError, match="plan is on"):
+        tq.exl3_adapter_plan(q, ids, 4, 2, plan=plan)

@@ -184,3 +184,18 @@ def test_descriptors_keep_the_sizes_of_their_tensors():
             assert getattr(d, name) == before
     router.bias = FAKE.value                               # an address may be set
     assert router.bias == FAKE.value
+
+
+def test_workspaces_of_another_device_are_refused():
+    class Elsewhere:                                       # what a tensor on the second GPU says of itself
+        device = torch.device("cuda", 1)
+        numel = element_size = lambda self: 256
+        get_device = lambda self: 1
+
+    tq_ptr, tq._ptr = tq._ptr, lambda t, name: FAKE
+    try:
+        assert tq._workspace_arg(Elsewhere(), 256, torch.device("cuda", 1), None, 0) == (FAKE, 256 * 256)
+        with pytest.raises(ValueError, match="workspace is on cuda:1"):
+            tq._workspace_arg(Elsewhere(), 256, torch.device("cuda", 0), None, 0)
+    finally:
+        tq._ptr = tq_ptr

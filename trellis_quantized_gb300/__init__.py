@@ -655,7 +655,10 @@ def _out(t, name: str, shape, dtype) -> int:
 def _workspace_arg(buf, nbytes: int, device, stream, raw: int):
     """Address and bytes of a call's workspace: the caller's, or the cached one."""
     if buf is not None:
-        return _ptr(buf, "workspace"), buf.numel() * buf.element_size()
+        address = _ptr(buf, "workspace")
+        if buf.get_device() != device.index:
+            raise ValueError(f"the workspace is on {buf.device}, the call's tensors on {device}")
+        return address, buf.numel() * buf.element_size()
     hit = _ws_cache.get((device.index, raw))
     if hit is None or hit[2] < nbytes:
         buf = workspace(nbytes, device, stream)
@@ -983,6 +986,8 @@ def exl3_adapter_plan(q_start, adapter, T: int, count: int, plan: AdapterPlan | 
         plan = AdapterPlan(T, B, count, adapter.device, stream)
     elif (plan.T, plan.batch, plan.count) != (T, B, count):
         raise ValueError(f"plan was made for T = {plan.T}, batch = {plan.batch}, count = {plan.count}")
+    elif plan.device != adapter.get_device():
+        raise ValueError(f"plan is on cuda:{plan.device}, q_start and adapter on {adapter.device}")
     _check(lib().exl3_adapter_plan(_ptr(q_start, "q_start"), _ptr(adapter, "adapter"), T, B, count,
                                    plan.address, plan.data.numel(), _raw_stream(stream)))
     return plan
