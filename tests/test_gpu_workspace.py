@@ -1,0 +1,46 @@
+"""The binding's own workspaces: kept by device and stream, and what captured graphs hold of them."""
+import gc
+
+import pytest
+import torch
+
+import trellis_quantized_gb300 as tq
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture
+def stream():
+    """A stream that no workspace was asked for on (streams come from a pool and return)."""
+    s = torch.cuda.Stream()
+    for key in [k for k in tq._ws_cache if k[1] == s.cuda_stream]:
+        del tq._ws_cache[key]
+    return s
+
+
+@pytest.mark.parametrize("named", [False, True])
+def test_a_graphs_workspace_outlives_a_larger_one(stream, named):
+    """A larger call takes the cached buffer's place; the graph's address stays allocated."""
+    kw = dict(stream=stream) if named else {}
+    with torch.cuda.stream(stream):
+        address = tq.workspace(1 << 20, **kw).data_ptr()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            assert tq.workspace(1 << 20, **kw).data_ptr() == address
+            torch.zeros(1, device="cuda")
+        assert tq.workspace(3 << 20, **kw).data_ptr() != address
+        gc.collect()
+        again = [torch.empty(1 << 20, dtype=torch.uint8, device="cuda") for _ in range(64)]
+        assert address not in [t.data_ptr() for t in again]
+
+
+def test_outgrown_workspaces_are_bounded(stream):
+    """Sizes that grow by little: each buffer is twice the one before it, and all before it no more than the last."""
+    with torch.cuda.stream(stream):
+        seen = {}
+        for i in range(1, 200):
+            ws = tq.workspace(4096 * i)
+            assert ws.numel() >= 4096 * i and not ws.any()
+            seen[ws.data_ptr()] = ws.numel()
+        sizes = list(seen.values())
+        assert len(sizes) < 10 and sum(sizes[:-1]) <= sizes[-1] < 4 * 4096 * 199

@@ -242,13 +242,18 @@ def _stream(stream=None):
 
 
 _ws_cache: dict = {}                      # (device, stream): (buffer, address, bytes)
+_ws_outgrown: list = []                   # buffers that captured graphs may go on using
 
 
 def workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
     """A zero-initialised workspace of at least nbytes, cached per (device, stream).
 
     Every libexl3 call leaves its counters at zero again, so one cleared
-    workspace serves any number of calls made in stream order."""
+    workspace serves any number of calls made in stream order.  A buffer whose
+    place a larger one takes stays alive, since a captured graph may hold its
+    address; its successor is at least twice as large, so that all that are
+    kept are no more than the present one.  (Nothing is captured on the default
+    stream: its buffers grow as asked and go.)"""
     if device is None:
         index = torch.cuda.current_device()
     else:
@@ -259,6 +264,9 @@ def workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
     buf, _, size = _ws_cache.get(key, (None, 0, -1))
     if size < nbytes:
         dev = torch.device("cuda", index)
+        if buf is not None and raw:
+            _ws_outgrown.append(buf)
+            nbytes = max(nbytes, 2 * size)
         buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
         exl3_workspace_clear(buf, stream=stream if stream is not None else torch.cuda.current_stream(dev))
         _ws_cache[key] = (buf, buf.data_ptr(), buf.numel())
