@@ -44,3 +44,29 @@ def test_outgrown_workspaces_are_bounded(stream):
             seen[ws.data_ptr()] = ws.numel()
         sizes = list(seen.values())
         assert len(sizes) < 10 and sum(sizes[:-1]) <= sizes[-1] < 4 * 4096 * 199
+
+
+def test_memory_of_a_workspace_is_its_streams(stream):
+    """What the current stream has freed, and may still be using, does not become another stream's workspace."""
+    size = 5 << 20
+    freed = torch.empty(size, dtype=torch.uint8, device="cuda")
+    address = freed.data_ptr()
+    del freed
+    assert tq.workspace(size, stream=stream).data_ptr() != address
+    again = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert again.data_ptr() == address                     # (it was there to be had)
+
+
+def test_memory_of_plans_and_packed_weights_is_their_streams(stream):
+    q, ids = torch.tensor([0, 900000], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    w = torch.randn((1024, 2048), device="cuda")
+    for make, state in ((lambda: tq.exl3_adapter_plan(q, ids, 900000, 1, stream=stream), lambda p: p.data),
+                        (lambda: tq.router(w, stream=stream), lambda r: r._keep[0])):
+        torch.cuda.synchronize()
+        held = state(make())                               # (of the same size: what is freed next would fit)
+        size = held.numel() * held.element_size()
+        freed = torch.empty(size, dtype=torch.uint8, device="cuda")
+        address = freed.data_ptr()
+        del freed
+        assert state(make()).data_ptr() != address
+        torch.cuda.synchronize()

@@ -267,8 +267,10 @@ def workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
         if buf is not None and raw:
             _ws_outgrown.append(buf)
             nbytes = max(nbytes, 2 * size)
-        buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        exl3_workspace_clear(buf, stream=stream if stream is not None else torch.cuda.current_stream(dev))
+        on = stream if stream is not None else torch.cuda.current_stream(dev)
+        with torch.cuda.stream(on):      # (memory that another stream freed may still be in use there)
+            buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        exl3_workspace_clear(buf, stream=on)
         _ws_cache[key] = (buf, buf.data_ptr(), buf.numel())
     return buf
 
@@ -848,8 +850,9 @@ def router(w, bias=None, stream=None) -> Router:
     _on_current(w, "w")
     parts, scale = w, None
     if w.dtype == torch.float32:
-        parts = torch.empty((2, E, k), dtype=torch.float16, device=w.device)
-        scale = torch.empty(E, dtype=torch.float32, device=w.device)
+        with torch.cuda.stream(stream):
+            parts = torch.empty((2, E, k), dtype=torch.float16, device=w.device)
+            scale = torch.empty(E, dtype=torch.float32, device=w.device)
         _check(lib().exl3_router_pack(_ptr(w, "w"), E, k, _ptr(parts, "packed"), _ptr(scale, "scale"), _stream(stream)))
     d = Router(_ptr(parts, "w").value, None if scale is None else scale.data_ptr(),
                _vector(bias, "bias", E, torch.float32), E, k)
@@ -970,7 +973,8 @@ class AdapterPlan:
         if nbytes == 0:
             raise ValueError(f"T = {T}, batch = {batch} or count = {count} out of range")
         self.T, self.batch, self.count = T, batch, count
-        self.data = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        with torch.cuda.stream(stream):      # (the memory of the stream that fills it)
+            self.data = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.address, self.device = self.data.data_ptr(), self.data.get_device()
         exl3_workspace_clear(self.data, stream=stream)
 
