@@ -100,6 +100,12 @@ int exl3_copy_in(const void *src, void *dst, size_t bytes, exl3_stream_t stream)
  * workspace is first used). */
 int exl3_workspace_clear(void *workspace, size_t ws_bytes, exl3_stream_t stream);
 
+/* A caller that has to allocate or wait on another stream while one is being
+ * captured (for a workspace that is first needed then: its fill belongs in no
+ * graph) may not do so in the capture's own mode.  relaxed 1: the calling thread
+ * may from here on, and its mode so far goes to *previous; 0: back to *previous. */
+int exl3_relax_capture(int relaxed, int *previous);
+
 /* Test helper: waits for `stream`, then copies the device error word of a
  * workspace to *err_out (0 = no violation recorded) and clears it. */
 int exl3_check_device_error(void *workspace, size_t ws_bytes, exl3_stream_t stream, int *err_out);

@@ -70,3 +70,52 @@ def test_memory_of_plans_and_packed_weights_is_their_streams(stream):
         del freed
         assert state(make()).data_ptr() != address
         torch.cuda.synchronize()
+
+
+def test_a_workspace_first_asked_for_in_a_capture_is_cleared(stream):
+    """Zero for everyone, though nothing of the graph has run, and of memory that no graph's temporaries are written to."""
+    size, g = 1 << 20, torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        used = torch.empty(size, dtype=torch.uint8, device="cuda")
+        used.fill_(0x55)
+        del used
+    g.replay()
+    torch.cuda.synchronize()
+    g2 = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g2, pool=g.pool(), stream=stream):
+        temporary = torch.full((2 * size,), 0x55, dtype=torch.uint8, device="cuda")
+        del temporary
+        ws = tq.workspace(size)
+        y = ws[:16].clone()
+    with torch.cuda.stream(stream):
+        assert tq.workspace(size).data_ptr() == ws.data_ptr()
+    assert not ws.any()
+    for graph in (g, g2, g):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert not ws.any()
+        if graph is g2:                                    # (y shares its memory with the first graph's temporary)
+            assert not y.any()
+
+
+def test_a_linear_captured_without_a_call_before(stream):
+    """Its counters are zero in the graph and for a call outside of it."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    k, n, K = 2048, 2048, 4
+    t = torch.randint(-2**15, 2**15, (k // 16, n // 16, 16 * K), generator=g, device="cuda").to(torch.int16)
+    suh, svh = (torch.ones(d, dtype=torch.float16, device="cuda") for d in (k, n))
+    x = torch.randn((5, k), generator=g, device="cuda").half()
+    want = tq.exl3_linear(x, t, suh, svh, K)
+    torch.cuda.synchronize()
+    graph, y = torch.cuda.CUDAGraph(), torch.empty_like(want)
+    with torch.cuda.graph(graph, stream=stream):
+        tq.exl3_linear(x, t, suh, svh, K, y=y)
+    with torch.cuda.stream(stream):
+        assert torch.equal(tq.exl3_linear(x, t, suh, svh, K), want)
+        ws = tq.workspace(1)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+    assert tq.exl3_check_device_error(ws) == 0

@@ -199,3 +199,7 @@ def test_workspaces_of_another_device_are_refused():
             tq._workspace_arg(Elsewhere(), 256, torch.device("cuda", 0), None, 0)
     finally:
         tq._ptr = tq_ptr
+
+
+def test_relaxing_captures_wants_a_place_for_the_mode():
+    assert tq.lib().exl3_relax_capture(1, None) == A and "previous" in _err()

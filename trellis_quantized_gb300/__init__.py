@@ -13,6 +13,7 @@ device.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import threading
@@ -144,6 +145,7 @@ def lib():
         L.exl3_last_error.restype = ctypes.c_char_p
         L.exl3_version.restype = I
         L.exl3_workspace_clear.argtypes = [P, Z, P]
+        L.exl3_relax_capture.argtypes = [I, ctypes.POINTER(I)]
         L.exl3_copy_in.argtypes = [P, P, Z, P]
         L.exl3_check_device_error.argtypes = [P, Z, P, ctypes.POINTER(I)]
         L.exl3_decode_tile.argtypes = [P, I, I, I, I, I, I, I, I, P, L64, P]
@@ -269,10 +271,30 @@ def workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
             nbytes = max(nbytes, 2 * size)
         on = stream if stream is not None else torch.cuda.current_stream(dev)
         with torch.cuda.stream(on):      # (memory that another stream freed may still be in use there)
-            buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        exl3_workspace_clear(buf, stream=on)
+            captured = torch.cuda.is_current_stream_capturing()
+            if not captured:
+                buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        if captured:
+            buf = _outside_captures(max(nbytes, 256), dev)
+        else:
+            exl3_workspace_clear(buf, stream=on)
         _ws_cache[key] = (buf, buf.data_ptr(), buf.numel())
     return buf
+
+
+def _outside_captures(nbytes: int, device) -> torch.Tensor:
+    """A workspace first needed during a capture: cleared now, for all who will use it, and of
+    memory that is no graph's (a graph's temporaries take turns in theirs, at every replay)."""
+    with exl3_relax_capture():
+        for _ in range(64):              # (streams come from a pool; one of them is being captured)
+            s = torch.cuda.Stream(device)
+            with torch.cuda.stream(s):
+                if not torch.cuda.is_current_stream_capturing():
+                    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+                    exl3_workspace_clear(buf, stream=s)
+                    s.synchronize()
+                    return buf
+    raise RuntimeError("every stream is being captured: make a first call before the capture")
 
 
 # ------------------------------------------------------------------ entry points
@@ -283,6 +305,17 @@ def exl3_version() -> int:
 
 def exl3_workspace_clear(ws: torch.Tensor, stream=None):
     _check(lib().exl3_workspace_clear(_ptr(ws, "workspace"), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+@contextlib.contextmanager
+def exl3_relax_capture():
+    """The calling thread may allocate and wait on streams that no capture under way includes."""
+    previous = ctypes.c_int(0)
+    _check(lib().exl3_relax_capture(1, ctypes.byref(previous)))
+    try:
+        yield
+    finally:
+        _check(lib().exl3_relax_capture(0, ctypes.byref(previous)))
 
 
 def exl3_copy_in(src: torch.Tensor, dst: torch.Tensor, stream=None) -> torch.Tensor:

@@ -452,6 +452,16 @@ int exl3_workspace_clear(void *workspace, size_t ws_bytes, exl3_stream_t stream)
   return exl3_cuda_check(cudaMemsetAsync(workspace, 0, ws_bytes, stream), "cudaMemsetAsync(workspace)");
 }
 
+int exl3_relax_capture(int relaxed, int *previous) {
+  g_last_error.clear();
+  if (!previous) return exl3_fail(EXL3_ERR_ARG, "previous is NULL");
+  cudaStreamCaptureMode mode = static_cast<cudaStreamCaptureMode>(*previous);
+  if (relaxed) mode = cudaStreamCaptureModeRelaxed;
+  EXL3_TRY(exl3_cuda_check(cudaThreadExchangeStreamCaptureMode(&mode), "cudaThreadExchangeStreamCaptureMode"));
+  if (relaxed) *previous = mode;
+  return EXL3_OK;
+}
+
 int exl3_check_device_error(void *workspace, size_t ws_bytes, exl3_stream_t stream, int *err_out) {
   g_last_error.clear();
   if (!err_out) return exl3_fail(EXL3_ERR_ARG, "err_out is NULL");
