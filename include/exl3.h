@@ -717,6 +717,20 @@ int exl3_adapter_add(const uint16_t *x, int64_t x_stride, const void *y, int64_t
                      int64_t out_stride, int dtype, const exl3_adapters *adapters, const void *plan, int T, int batch,
                      void *workspace, size_t ws_bytes, exl3_stream_t stream);
 
+/*
+ * exl3_adapter_add_scratch -- the same call with what it keeps between its two
+ * kernels apart from the error word: calls that may run at once (in graphs
+ * captured on one stream) share the workspace, of 256 bytes at least, but not the
+ * scratch.
+ *   scratch  exl3_adapter_scratch_size(T, max_rank, n) bytes, 256-byte aligned, of
+ *            any content; NULL where that is 0 (calls of one kernel)
+ */
+size_t exl3_adapter_scratch_size(int T, int max_rank, int n);
+int exl3_adapter_add_scratch(const uint16_t *x, int64_t x_stride, const void *y, int64_t y_stride, void *out,
+                             int64_t out_stride, int dtype, const exl3_adapters *adapters, const void *plan, int T,
+                             int batch, void *workspace, size_t ws_bytes, void *scratch, size_t scratch_bytes,
+                             exl3_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

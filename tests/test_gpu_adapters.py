@@ -432,3 +432,95 @@ def test_a_plan_of_another_device_is_refused():
     plan.device += 1
     with pytest.raises(ValueError, match="plan is on"):
         tq.exl3_adapter_plan(q, ids, 4, 2, plan=plan)
+
+
+def _captured(T, R, n, stream, named, plan=None, seed=1):
+    """A captured call's graph, inputs and output."""
+    k, N = 256, 2
+    x = torch.randn((T, k), generator=_gen(seed), device="cuda").half()
+    y = torch.randn((T, n), generator=_gen(seed + 1), device="cuda").half()
+    pool = _pool(N, R, k, n, seed=seed)
+    plan = plan or tq.exl3_adapter_plan(_i32([0, 7, T]), _i32([1, 0]), T, N)
+    ad, out = tq.adapters(*pool), torch.empty_like(y)
+    kw = dict(stream=stream) if named else {}
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        tq.exl3_adapter_add(x, y, ad, plan, out=out, **kw)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        for _ in range(3):
+            tq.exl3_adapter_add(x, y, ad, plan, out=out, **kw)
+    return g, (x, y, ad, plan, pool), out
+
+
+@pytest.mark.parametrize("named", [False, True])
+@pytest.mark.parametrize("T,R,n", [(24, 16, 1024), (300, 128, 8192)])
+def test_a_graph_keeps_nothing_in_the_streams_workspace(T, R, n, named):
+    """Two graphs captured on one stream would race there when they run at once: what a graph
+    leaves in the stream's workspace is an error word at most."""
+    s = torch.cuda.Stream()
+    assert _large(T, R, n) == (tq.exl3_adapter_scratch_size(T, R, n) > 0) == (T > 24)
+    g, (x, y, _, _, pool), out = _captured(T, R, n, s, named)
+    with torch.cuda.stream(s):
+        ws = tq.workspace(1)
+    used = ws.clone()
+    ws[33024:] = 0x77                                      # (all but the counters)
+    g.replay()
+    torch.cuda.synchronize()
+    assert (ws[33024:] == 0x77).all() and not ws[:33024].any()
+    ws.copy_(used)
+    _check(out, *_reference(x, y, pool, [7, T - 7], [1, 0]))
+
+
+@pytest.mark.parametrize("named", [False, True])
+@pytest.mark.parametrize("T,R,n", [(300, 128, 8192), (2500, 64, 2048)])
+def test_two_graphs_of_one_stream_at_once(T, R, n, named):
+    s = torch.cuda.Stream()
+    made = [_captured(T, R, n, s, named, seed=seed) for seed in (1, 5)]
+    streams = [torch.cuda.Stream() for _ in made]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (g, _, _), on in zip(made, streams):
+            with torch.cuda.stream(on):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, (x, y, _, _, pool), out in made:
+        _check(out, *_reference(x, y, pool, [7, T - 7], [1, 0]))
+
+
+@pytest.mark.parametrize("named", [False, True])
+@pytest.mark.parametrize("T,R,n", [(24, 16, 1024), (300, 128, 8192)])
+def test_errors_of_a_graph_are_found_in_its_streams_workspace(T, R, n, named):
+    """A plan that was never filled, found when the graph runs."""
+    s = torch.cuda.Stream()
+    g, _, out = _captured(T, R, n, s, named, plan=tq.AdapterPlan(T, 2, 2, "cuda"))
+    with torch.cuda.stream(s):
+        ws = tq.workspace(1)
+        assert tq.exl3_check_device_error(ws) != 0         # (the call before the capture)
+        assert tq.exl3_check_device_error(ws) == 0
+        out.fill_(7.0)
+        g.replay()
+        assert tq.exl3_check_device_error(ws) != 0
+    assert (out == 7).all()
+
+
+@pytest.mark.parametrize("T,R,n", [(24, 16, 1024), (300, 128, 8192)])
+def test_scratch_apart_from_the_error_word(T, R, n):
+    k, need = 256, tq.exl3_adapter_scratch_size(T, R, n)
+    x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
+    y = torch.randn((T, n), generator=_gen(2), device="cuda")
+    pool = _pool(2, R, k, n)
+    ad, plan = tq.adapters(*pool), tq.exl3_adapter_plan(_i32([0, 7, T]), _i32([1, 0]), T, 2)
+    ws = torch.zeros(512, dtype=torch.uint8, device="cuda")
+    buf = torch.full((need + 512,), 0x77, dtype=torch.uint8, device="cuda")
+    out = tq.exl3_adapter_add_scratch(x, y, ad, plan, buf[:need] if need else None, out=torch.empty_like(y),
+                                      workspace_buf=ws)
+    _check(out, *_reference(x, y, pool, [7, T - 7], [1, 0]))
+    assert (buf[need:] == 0x77).all() and not ws.any()
+    assert torch.equal(out, tq.exl3_adapter_add(x, y, ad, plan, out=torch.empty_like(y)))
+    if need:
+        with pytest.raises(tq.Exl3Error, match="needed"):
+            tq.exl3_adapter_add_scratch(x, y, ad, plan, buf[:need - 1], out=out, workspace_buf=ws)
+        with pytest.raises(tq.Exl3Error, match="scratch is NULL"):
+            tq.exl3_adapter_add_scratch(x, y, ad, plan, None, out=out, workspace_buf=ws)

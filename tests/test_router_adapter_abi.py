@@ -203,3 +203,34 @@ def test_workspaces_of_another_device_are_refused():
 
 def test_relaxing_captures_wants_a_place_for_the_mode():
     assert tq.lib().exl3_relax_capture(1, None) == A and "previous" in _err()
+
+
+def _add_scratch(**kw):
+    d = dict(T=3, k=2048, n=512, R=16, ws=FAKE, wsb=256, scratch=None, sb=0, plan=FAKE)
+    d.update(kw)
+    p = _fill(tq.Adapters, POOL, dict(k=d["k"], n=d["n"], max_rank=d["R"]))
+    return tq.lib().exl3_adapter_add_scratch(FAKE, d["k"], FAKE, d["n"], ctypes.c_void_p(0x20000), d["n"], 0, ref(p), d["plan"],
+                                             d["T"], 2, d["ws"], d["wsb"], d["scratch"], d["sb"], None)
+
+
+@pytest.mark.parametrize("kw,code,text", [
+    (dict(ws=None), W, "workspace"), (dict(wsb=255), W, "workspace"), (dict(plan=None), A, "plan"),
+    (dict(T=2000, R=128, n=4096), W, "scratch is NULL"), (dict(T=2000, R=128, n=4096, scratch=FAKE), W, "scratch has"),
+    (dict(T=2000, R=128, n=4096, scratch=FAKE_MIS, sb=1 << 30), W, "aligned"), (dict(k=100), S, "k ="),
+])
+def test_adapter_add_scratch_refuses(kw, code, text):
+    assert _add_scratch(**kw) == code and text in _err()
+
+
+@pytest.mark.parametrize("T,R,n", [(47, 128, 17408), (48, 128, 17408), (63, 64, 41984), (2000, 16, 8448), (200, 8, 128),
+                                   (1 << 22, 128, 1 << 20), (0, 16, 128)])
+def test_scratch_sizes(T, R, n):
+    """h of every row in two fp16 parts and a factor, where h passes from one kernel to another."""
+    large = T >= 48 and T * (R + 16) ** 2 * n >= 1 << 34
+    size, whole = tq.exl3_adapter_scratch_size(T, R, n), tq.exl3_adapter_add_workspace_size(T, R)
+    assert (T * (4 * R + 4) <= size <= whole - 33024 < size + 256) if large else size == 0
+
+
+def test_scratch_sizes_of_refused_shapes_are_zero():
+    assert all(tq.exl3_adapter_scratch_size(*s) == 0 for s in ((-1, 16, 128), (1 << 23, 16, 128), (4096, 12, 4096), (4096, 128, 0)))
+    assert _add_scratch(T=0) == 0

@@ -196,6 +196,9 @@ def lib():
         L.exl3_adapter_add_workspace_size.argtypes = [I, I]
         L.exl3_adapter_add_workspace_size.restype = Z
         L.exl3_adapter_add.argtypes = [P, L64, P, L64, P, L64, I, P, P, I, I, P, Z, P]
+        L.exl3_adapter_scratch_size.argtypes = [I, I, I]
+        L.exl3_adapter_scratch_size.restype = Z
+        L.exl3_adapter_add_scratch.argtypes = [P, L64, P, L64, P, L64, I, P, P, I, I, P, Z, P, Z, P]
         _lib = L
         return L
 
@@ -1042,15 +1045,40 @@ def exl3_adapter_add_workspace_size(T: int, max_rank: int) -> int:
     return lib().exl3_adapter_add_workspace_size(T, max_rank)
 
 
+def exl3_adapter_scratch_size(T: int, max_rank: int, n: int) -> int:
+    return lib().exl3_adapter_scratch_size(T, max_rank, n)
+
+
 @functools.lru_cache(maxsize=4096)
-def _adapter_workspace(T: int, max_rank: int) -> int:
-    return exl3_adapter_add_workspace_size(T, max_rank)
+def _adapter_sizes(T: int, max_rank: int, n: int):
+    return exl3_adapter_add_workspace_size(T, max_rank), exl3_adapter_scratch_size(T, max_rank, n)
+
+
+def _capturing(stream, raw: int, device: int) -> bool:
+    """Is the stream of a call being captured?  (Never the default one; asking takes the driver 0.4 us.)"""
+    if raw == 0:
+        return False
+    if stream is None or raw == torch._C._cuda_getCurrentRawStream(device):
+        return torch._C._cuda_isCurrentStreamCapturing()
+    with torch.cuda.stream(stream):
+        return torch._C._cuda_isCurrentStreamCapturing()
 
 
 def exl3_adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out=None, workspace_buf=None,
                      stream=None) -> torch.Tensor:
     """y + scale (x A^T) B^T for each row's adapter: x [T, k] fp16, y [T, n] fp16 or fp32, dense
     rows; written to `out`, or to y itself (rows of no sequence are left as they were)."""
+    return _adapter_add(x, y, adapters, plan, out, workspace_buf, stream, None, False)
+
+
+def exl3_adapter_add_scratch(x, y, adapters: Adapters, plan: AdapterPlan, scratch, out=None, workspace_buf=None,
+                             stream=None) -> torch.Tensor:
+    """exl3_adapter_add with a buffer of exl3_adapter_scratch_size(T, max_rank, n) bytes that no call
+    running at once shares, or None where that is 0; the workspace holds the error word only."""
+    return _adapter_add(x, y, adapters, plan, out, workspace_buf, stream, scratch, True)
+
+
+def _adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out, workspace_buf, stream, scratch, apart: bool):
     device, dtype, T = _on_current(x, "x"), y.dtype, plan.T
     N, R, k, n = adapters._shape
     xp, xs, xr = _matrix(x, "x", k, _F16, device)
@@ -1066,14 +1094,24 @@ def exl3_adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out=None, work
     if plan.device != device or adapters._device != device or plan.count != N:
         raise ValueError(f"x is on cuda:{device}; the plan is for {plan.count} adapters on cuda:{plan.device}, the pool "
                          f"has {N} on cuda:{adapters._device}")
-    raw, need = _stream_of(stream, device), _adapter_workspace(T, R)
-    if workspace_buf is None and stream is None and T >= 48 and torch._C._cuda_isCurrentStreamCapturing():
-        # (fewer rows keep nothing there) a graph gets memory of its own: two that share the stream's would race
-        # when they run at once
-        workspace_buf = torch.empty(need, dtype=torch.uint8, device=x.device)
-    wp, wn = _workspace_arg(workspace_buf, need, x.device, stream, raw)
-    rc = lib().exl3_adapter_add(xp, xs, yp, ys, op, os_, _IO_DTYPES[dtype], adapters._address, plan.address, T,
-                                plan.batch, wp, wn, raw)
+    raw, (need, scratch_need) = _stream_of(stream, device), _adapter_sizes(T, R, n)
+    if not apart and workspace_buf is None and scratch_need and _capturing(stream, raw, device):
+        # a graph gets scratch of its own, in its own memory: two that share the stream's would race when they
+        # run at once.  Errors are found in the stream's workspace, as every captured call's are.
+        with torch.cuda.stream(stream):
+            scratch = torch.empty(scratch_need, dtype=torch.uint8, device=x.device)
+        apart = True
+    if apart:
+        wp, wn = _workspace_arg(workspace_buf, 256, x.device, stream, raw)
+        sp, sn = (None, 0) if scratch is None else (_ptr(scratch, "scratch"), scratch.numel() * scratch.element_size())
+        if scratch is not None and scratch.get_device() != device:
+            raise ValueError(f"the scratch is on {scratch.device}, x on cuda:{device}")
+        rc = lib().exl3_adapter_add_scratch(xp, xs, yp, ys, op, os_, _IO_DTYPES[dtype], adapters._address, plan.address, T,
+                                            plan.batch, wp, wn, sp, sn, raw)
+    else:
+        wp, wn = _workspace_arg(workspace_buf, need, x.device, stream, raw)
+        rc = lib().exl3_adapter_add(xp, xs, yp, ys, op, os_, _IO_DTYPES[dtype], adapters._address, plan.address, T,
+                                    plan.batch, wp, wn, raw)
     if rc:
         _check(rc)
     return out

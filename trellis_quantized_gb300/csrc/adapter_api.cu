@@ -56,6 +56,76 @@ int check_stride(const char *name, int64_t stride, int width, int per16) {
   return EXL3_OK;
 }
 
+int check_call(const uint16_t *x, int64_t x_stride, const void *y, int64_t y_stride, void *out, int64_t out_stride,
+               int dtype, const exl3_adapters *ad, const void *plan, int T, int batch) {
+  if (!ad) return exl3_fail(EXL3_ERR_ARG, "adapters is NULL");
+  if (dtype != EXL3_OUT_F16 && dtype != EXL3_OUT_F32) return exl3_fail(EXL3_ERR_ARG, "dtype %d invalid", dtype);
+  if (!plan_shape_ok(T, batch, ad->count))
+    return exl3_fail(EXL3_ERR_SHAPE, "T = %d (0..2^22), batch = %d (1..2^20) or count = %d (1..%d) out of range", T,
+                     batch, ad->count, exl3::ad::kMaxCount);
+  if (!rank_ok(ad->max_rank))
+    return exl3_fail(EXL3_ERR_SHAPE, "max_rank = %d must be a multiple of 8 in 8..%d", ad->max_rank, exl3::ad::kMaxRank);
+  if (ad->k < 128 || ad->k % 128 || ad->n < 128 || ad->n % 128 || ad->k > (1 << 20) || ad->n > (1 << 20))
+    return exl3_fail(EXL3_ERR_SHAPE, "k = %d and n = %d must be multiples of 128 up to 2^20", ad->k, ad->n);
+  EXL3_TRY(check_ptr(ad->a, "adapters.a"));
+  EXL3_TRY(check_ptr(ad->b, "adapters.b"));
+  EXL3_TRY(check_words(ad->scale, "adapters.scale"));
+  EXL3_TRY(check_words(ad->rank, "adapters.rank", false));
+  EXL3_TRY(check_ptr(x, "x"));
+  EXL3_TRY(check_ptr(y, "y"));
+  EXL3_TRY(check_ptr(out, "out"));
+  const int per16 = dtype == EXL3_OUT_F32 ? 4 : 8;
+  EXL3_TRY(check_stride("x", x_stride, ad->k, 8));
+  EXL3_TRY(check_stride("y", y_stride, ad->n, per16));
+  EXL3_TRY(check_stride("out", out_stride, ad->n, per16));
+  if (out == y && out_stride != y_stride)
+    return exl3_fail(EXL3_ERR_SHAPE, "out is y, but their strides differ: %lld and %lld", (long long)out_stride,
+                     (long long)y_stride);
+  if (!plan) return exl3_fail(EXL3_ERR_ARG, "plan is NULL");
+  if (reinterpret_cast<uintptr_t>(plan) & (kAlign - 1))
+    return exl3_fail(EXL3_ERR_ARG, "plan is not %zu-byte aligned", kAlign);
+  return EXL3_OK;
+}
+
+// A checked call; `scratch`: add_ws's parts from h on.
+int launch(const uint16_t *x, int64_t x_stride, const void *y, int64_t y_stride, void *out, int64_t out_stride,
+           int dtype, const exl3_adapters *ad, const void *plan, int T, int batch, void *workspace, void *scratch,
+           exl3_stream_t stream) {
+  if (T == 0) return EXL3_OK;
+  const exl3::ad::PlanLayout L = exl3::ad::plan_layout(T, batch, ad->count);
+  exl3::ad::Args a = {};
+  a.x = reinterpret_cast<const __half *>(x);
+  a.y = y;
+  a.out = out;
+  a.x_stride = x_stride;
+  a.y_stride = y_stride;
+  a.out_stride = out_stride;
+  a.a = reinterpret_cast<const __half *>(ad->a);
+  a.b = reinterpret_cast<const __half *>(ad->b);
+  a.scale = ad->scale;
+  a.rank = ad->rank;
+  a.N = ad->count;
+  a.R = ad->max_rank;
+  a.k = ad->k;
+  a.n = ad->n;
+  a.T = T;
+  a.B = batch;
+  const auto in_plan = [&](size_t off) { return static_cast<const char *>(plan) + off; };
+  a.ctrl = reinterpret_cast<const int *>(in_plan(0));
+  a.perm = reinterpret_cast<const int *>(in_plan(L.perm));
+  a.err = at<int>(workspace, 0);
+  if (large_tiles(T, ad->max_rank, ad->n)) {
+    a.tiles = reinterpret_cast<const int4 *>(in_plan(L.tc_tiles));
+    a.max_tiles = L.max_tc_tiles;
+    a.h = at<__half>(scratch, 0);
+    a.back = at<float>(scratch, add_ws(T, ad->max_rank).back - kDataOff);
+    return exl3_launch_adapter_tc(a, dtype == EXL3_OUT_F32, stream);
+  }
+  a.tiles = reinterpret_cast<const int4 *>(in_plan(L.step_tiles));
+  a.max_tiles = L.max_step_tiles;
+  return exl3_cuda_check(exl3_launch_adapter_step(a, dtype == EXL3_OUT_F32, stream), "adapter launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -95,71 +165,35 @@ size_t exl3_adapter_add_workspace_size(int T, int max_rank) {
   return add_ws(T, max_rank).total;
 }
 
+size_t exl3_adapter_scratch_size(int T, int max_rank, int n) {
+  if (T < 0 || T > (1 << 22) || !rank_ok(max_rank) || n < 128 || n > (1 << 20)) return 0;
+  return large_tiles(T, max_rank, n) ? add_ws(T, max_rank).total - kDataOff : 0;
+}
+
 int exl3_adapter_add(const uint16_t *x, int64_t x_stride, const void *y, int64_t y_stride, void *out,
                      int64_t out_stride, int dtype, const exl3_adapters *ad, const void *plan, int T, int batch,
                      void *workspace, size_t ws_bytes, exl3_stream_t stream) {
   exl3_clear_error();
-  if (!ad) return exl3_fail(EXL3_ERR_ARG, "adapters is NULL");
-  if (dtype != EXL3_OUT_F16 && dtype != EXL3_OUT_F32) return exl3_fail(EXL3_ERR_ARG, "dtype %d invalid", dtype);
-  if (!plan_shape_ok(T, batch, ad->count))
-    return exl3_fail(EXL3_ERR_SHAPE, "T = %d (0..2^22), batch = %d (1..2^20) or count = %d (1..%d) out of range", T,
-                     batch, ad->count, exl3::ad::kMaxCount);
-  if (!rank_ok(ad->max_rank))
-    return exl3_fail(EXL3_ERR_SHAPE, "max_rank = %d must be a multiple of 8 in 8..%d", ad->max_rank, exl3::ad::kMaxRank);
-  if (ad->k < 128 || ad->k % 128 || ad->n < 128 || ad->n % 128 || ad->k > (1 << 20) || ad->n > (1 << 20))
-    return exl3_fail(EXL3_ERR_SHAPE, "k = %d and n = %d must be multiples of 128 up to 2^20", ad->k, ad->n);
-  EXL3_TRY(check_ptr(ad->a, "adapters.a"));
-  EXL3_TRY(check_ptr(ad->b, "adapters.b"));
-  EXL3_TRY(check_words(ad->scale, "adapters.scale"));
-  EXL3_TRY(check_words(ad->rank, "adapters.rank", false));
-  EXL3_TRY(check_ptr(x, "x"));
-  EXL3_TRY(check_ptr(y, "y"));
-  EXL3_TRY(check_ptr(out, "out"));
-  const int per16 = dtype == EXL3_OUT_F32 ? 4 : 8;
-  EXL3_TRY(check_stride("x", x_stride, ad->k, 8));
-  EXL3_TRY(check_stride("y", y_stride, ad->n, per16));
-  EXL3_TRY(check_stride("out", out_stride, ad->n, per16));
-  if (out == y && out_stride != y_stride)
-    return exl3_fail(EXL3_ERR_SHAPE, "out is y, but their strides differ: %lld and %lld", (long long)out_stride,
-                     (long long)y_stride);
-  const exl3::ad::PlanLayout L = exl3::ad::plan_layout(T, batch, ad->count);
-  if (!plan) return exl3_fail(EXL3_ERR_ARG, "plan is NULL");
-  if (reinterpret_cast<uintptr_t>(plan) & (kAlign - 1))
-    return exl3_fail(EXL3_ERR_ARG, "plan is not %zu-byte aligned", kAlign);
-  const AddWs W = add_ws(T, ad->max_rank);
-  EXL3_TRY(check_workspace(workspace, ws_bytes, W.total));
-  if (T == 0) return EXL3_OK;
-  exl3::ad::Args a = {};
-  a.x = reinterpret_cast<const __half *>(x);
-  a.y = y;
-  a.out = out;
-  a.x_stride = x_stride;
-  a.y_stride = y_stride;
-  a.out_stride = out_stride;
-  a.a = reinterpret_cast<const __half *>(ad->a);
-  a.b = reinterpret_cast<const __half *>(ad->b);
-  a.scale = ad->scale;
-  a.rank = ad->rank;
-  a.N = ad->count;
-  a.R = ad->max_rank;
-  a.k = ad->k;
-  a.n = ad->n;
-  a.T = T;
-  a.B = batch;
-  const auto in_plan = [&](size_t off) { return static_cast<const char *>(plan) + off; };
-  a.ctrl = reinterpret_cast<const int *>(in_plan(0));
-  a.perm = reinterpret_cast<const int *>(in_plan(L.perm));
-  a.err = at<int>(workspace, 0);
-  if (large_tiles(T, ad->max_rank, ad->n)) {
-    a.tiles = reinterpret_cast<const int4 *>(in_plan(L.tc_tiles));
-    a.max_tiles = L.max_tc_tiles;
-    a.h = at<__half>(workspace, W.h);
-    a.back = at<float>(workspace, W.back);
-    return exl3_launch_adapter_tc(a, dtype == EXL3_OUT_F32, stream);
-  }
-  a.tiles = reinterpret_cast<const int4 *>(in_plan(L.step_tiles));
-  a.max_tiles = L.max_step_tiles;
-  return exl3_cuda_check(exl3_launch_adapter_step(a, dtype == EXL3_OUT_F32, stream), "adapter launch");
+  EXL3_TRY(check_call(x, x_stride, y, y_stride, out, out_stride, dtype, ad, plan, T, batch));
+  EXL3_TRY(check_workspace(workspace, ws_bytes, add_ws(T, ad->max_rank).total));
+  return launch(x, x_stride, y, y_stride, out, out_stride, dtype, ad, plan, T, batch, workspace,
+                at<char>(workspace, kDataOff), stream);
+}
+
+int exl3_adapter_add_scratch(const uint16_t *x, int64_t x_stride, const void *y, int64_t y_stride, void *out,
+                             int64_t out_stride, int dtype, const exl3_adapters *ad, const void *plan, int T,
+                             int batch, void *workspace, size_t ws_bytes, void *scratch, size_t scratch_bytes,
+                             exl3_stream_t stream) {
+  exl3_clear_error();
+  EXL3_TRY(check_call(x, x_stride, y, y_stride, out, out_stride, dtype, ad, plan, T, batch));
+  EXL3_TRY(check_workspace(workspace, ws_bytes, kCtrlBytes));
+  const size_t need = exl3_adapter_scratch_size(T, ad->max_rank, ad->n);
+  if (need && !scratch) return exl3_fail(EXL3_ERR_WORKSPACE, "scratch is NULL (%zu bytes needed)", need);
+  if (need && reinterpret_cast<uintptr_t>(scratch) & (kAlign - 1))
+    return exl3_fail(EXL3_ERR_WORKSPACE, "scratch must be %zu-byte aligned", kAlign);
+  if (scratch_bytes < need)
+    return exl3_fail(EXL3_ERR_WORKSPACE, "scratch has %zu bytes, %zu needed", scratch_bytes, need);
+  return launch(x, x_stride, y, y_stride, out, out_stride, dtype, ad, plan, T, batch, workspace, scratch, stream);
 }
 
 }  // extern "C"
