@@ -612,6 +612,8 @@ int exl3_router_pack(const float *w, int E, int k, uint16_t *packed, float *scal
  *   Up to 8 rows run on CUDA cores, more on the tensor cores; the split of k
  *   depends on T, so a row's bits may differ between calls of different T.
  *   The same call gives the same bits every time.
+ *   Infinities in x give what the formula gives, +-infinity or NaN (packed
+ *   weights below 2^-38 of their row's largest count as zeros there).
  */
 size_t exl3_router_logits_workspace_size(void);
 int exl3_router_logits(const uint16_t *x, int64_t x_stride, int T, const exl3_router *router, float *logits,

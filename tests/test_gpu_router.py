@@ -320,3 +320,38 @@ def test_sizes_of_a_router_stay():
         with pytest.raises(AttributeError, match="size"):
             setattr(r, name, 128)
     _check_logits(x, w, None, tq.exl3_router_logits(x, r))
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("T,k,E", [(1, 256, 24), (8, 256, 24), (9, 256, 24), (64, 2048, 256), (300, 1048, 60), (4096, 512, 256)])
+def test_infinities_in_x(T, k, E, fp32):
+    """+-infinity times a weight's sign, NaN for a weight of zero or infinities that meet; other rows as they were."""
+    x, w = _inputs(T, k, E, fp32, seed=21)
+    w = torch.where(w.abs() < 2.0 ** -14, torch.full_like(w, 2.0 ** -14), w)     # (none that packing takes for zero)
+    w[3, 5], w[E - 1, k - 1] = 0, 0
+    w[7, 9] = 2.0 ** -10                                   # (of a low part of zero)
+    r = tq.router(w)
+    clean = tq.exl3_router_logits(x, r)
+    rows = sorted({0, T // 2, T - 1})
+    x[0, 5] = math.inf
+    x[T // 2, 9] = -math.inf
+    x[T - 1, k - 1], x[T - 1, k // 2] = math.inf, math.inf
+    got = tq.exl3_router_logits(x, r)
+    want = (x[rows].double()[:, None] * w.double()).sum(-1)
+    assert torch.equal(got[rows].isnan(), want.isnan()) and not want.isfinite().any()
+    inf = want.isinf()
+    assert inf.any() and want.isnan().any() and torch.equal(got[rows][inf].double(), want[inf])
+    rest = [t for t in range(T) if t not in rows]
+    assert torch.equal(got[rest], clean[rest])
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_rows_of_weights_that_are_not_finite(T):
+    """NaN for their expert, nothing for the others, whatever the number of rows."""
+    x, w = _inputs(T, 256, 24, True, seed=22)
+    clean = tq.exl3_router_logits(x, tq.router(w))
+    w[4, 10], w[9, 200], w[20, 0] = math.inf, math.nan, -math.inf
+    got = tq.exl3_router_logits(x, tq.router(w))
+    bad = [4, 9, 20]
+    rest = [e for e in range(24) if e not in bad]
+    assert got[:, bad].isnan().all() and torch.equal(got[:, rest], clean[:, rest])

@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const float *__restrict__ w, 
   const float f = scalbnf(1.0f, p);
   for (int j = threadIdx.x; j < k; j += blockDim.x) {
     const float v = row[j] * f;
-    const __half hi = __float2half_rn(v);
+    const __half hi = isfinite(v) ? __float2half_rn(v) : __float2half_rn(__int_as_float(0x7fffffff));
     out[(int64_t)e * k + j] = hi;
     out[(int64_t)(E + e) * k + j] = __float2half_rn((v - __half2float(hi)) * 0x1p11f);
   }
@@ -237,6 +237,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) logits_tc_kernel(const __gri
       const int row = 32 * (warp & 3) + lane;
       const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
       float *dst = reinterpret_cast<float *>(smem) + row * a.pitch;
+      bool far = false;
       for (int c = 0; c < a.bn; c += 32) {
         float v[32];
         tc::tmem_ld32(from + c, v);
@@ -244,6 +245,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) logits_tc_kernel(const __gri
           float lo[32];
           tc::tmem_ld32(from + a.bn + c, lo);
           tc::tmem_ld_wait();
+          far |= !isfinite(v[0]);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = fmaf(lo[i], kLoScale, v[i]);
         }
@@ -252,6 +254,18 @@ __global__ void __launch_bounds__(kLogitThreads, 1) logits_tc_kernel(const __gri
         for (int i = 0; i < 32; i += 4)
           if (c + i < a.bn) *reinterpret_cast<float4 *>(dst + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
+      // An infinity in x makes a row's high parts infinite or NaN for all experts; the low
+      // parts, whose signs are their own, are left out of it.  (Here, since among the
+      // columns above it cost 0.2 us of 7.2.)
+      if (PACKED && __any_sync(0xffffffffu, far))
+        for (int c = 0; c < a.bn; c += 32) {
+          float v[32];
+          tc::tmem_ld32(from + c, v);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < a.bn && isinf(v[i])) dst[c + i] = v[i];
+        }
     }
   }
   tc::tc_fence_before();
