@@ -709,10 +709,11 @@ int exl3_adapter_plan(const int32_t *q_start, const int32_t *adapter, int T, int
  *            once
  *   workspace of exl3_adapter_add_workspace_size(T, max_rank) bytes
  *   x A^T is summed in fp32 and enters the second product as two fp16 parts (22
- *   bits); the sum with y is rounded once.  T = 0 enqueues nothing.  What lies in the pool past an
- *   adapter's rank is not used, but in B it has to be finite up to the next
- *   multiple of 16.  The same call gives the same bits every time; a row's bits do
- *   not depend on what other rows hold, but may on how many rows share its adapter.
+ *   bits); the sum with y is rounded once.  Infinities give what the formula gives.
+ *   T = 0 enqueues nothing.  What lies in the pool past an adapter's rank is not
+ *   used, but in B it has to be finite up to the next multiple of 16.  The same
+ *   call gives the same bits every time; a row's bits do not depend on what other
+ *   rows hold, but may on how many rows share its adapter.
  */
 size_t exl3_adapter_add_workspace_size(int T, int max_rank);
 int exl3_adapter_add(const uint16_t *x, int64_t x_stride, const void *y, int64_t y_stride, void *out,

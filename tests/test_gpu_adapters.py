@@ -524,3 +524,66 @@ def test_scratch_apart_from_the_error_word(T, R, n):
             tq.exl3_adapter_add_scratch(x, y, ad, plan, buf[:need - 1], out=out, workspace_buf=ws)
         with pytest.raises(tq.Exl3Error, match="scratch is NULL"):
             tq.exl3_adapter_add_scratch(x, y, ad, plan, None, out=out, workspace_buf=ws)
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("T,R,n", [(1, 16, 256), (8, 64, 256), (9, 16, 256), (40, 128, 384), (140, 24, 256), (140, 128, 16384)])
+def test_infinities_in_x(T, R, n, fp32):
+    """What the formula gives: +-infinity with one rank, and with ranks of one sign; NaN for infinity
+    times zero; other rows as they were."""
+    assert _large(T, R, n) == (n > 1000)
+    k, N = 256, 3
+    a, b, scale, _ = _pool(N, R, k, n)
+    a[1], b[1] = a[1].abs() + 2.0 ** -10, b[1].abs() + 2.0 ** -10
+    a[0] = torch.where(a[0].abs() < 2.0 ** -10, torch.full_like(a[0], 2.0 ** -10), a[0])
+    a[2] = 0.0                                             # (infinity times zero)
+    b[0] = torch.where(b[0].abs() < 2.0 ** -10, torch.full_like(b[0], 2.0 ** -10), b[0])
+    ranks = [1, R, R]
+    pool = (a, b, scale, _i32(ranks))
+    for i, r in enumerate(ranks[:2]):
+        a[i, r:], b[i, :, r:] = 0, 0
+    x = torch.randn((T, k), generator=_gen(1), device="cuda").half()
+    y = torch.randn((T, n), generator=_gen(2), device="cuda").to(torch.float32 if fp32 else torch.float16)
+    third = T // 3
+    rows, ids = ([T], [0]) if T == 1 else ([third, third, T - 2 * third], [0, 1, 2])
+    plan, ad = tq.exl3_adapter_plan(_i32(_starts(rows)), _i32(ids), T, N), tq.adapters(*pool)
+    clean = tq.exl3_adapter_add(x, y, ad, plan, out=torch.empty_like(y))
+    bad = [0] if T == 1 else [0, third, T - 1]
+    x[bad[0], 7] = math.inf
+    if T > 1:
+        x[bad[1], 9] = -math.inf
+        x[bad[2], 11] = math.inf
+    got = tq.exl3_adapter_add(x, y, ad, plan, out=torch.empty_like(y))
+    for t, i in zip(bad, ids):
+        A, B = a[i, :ranks[i]].double(), b[i, :, :ranks[i]].double()
+        h = (x[t].double() * A).sum(-1)
+        want = (y[t].double() + float(scale[i]) * (h * B).sum(-1)).to(y.dtype)
+        assert torch.equal(got[t].isnan(), want.isnan()) and torch.equal(got[t].nan_to_num(0.5), want.nan_to_num(0.5))
+        assert want.isnan().all() if i == 2 else want.isinf().all()
+    rest = [t for t in range(T) if t not in bad]
+    assert torch.equal(got[rest], clean[rest])
+
+
+@pytest.mark.parametrize("T,R,n", [(5, 16, 256), (12, 16, 256), (140, 128, 16384)])
+def test_finite_ranks_beside_an_infinite_one(T, R, n):
+    """h = (infinity, 1e6 of either sign): the finite one is above fp16's range and adds nothing."""
+    assert _large(T, R, n) == (n > 1000)
+    k = 128
+    a = torch.zeros((1, R, k), dtype=torch.float16, device="cuda")
+    b = torch.ones((1, n, R), dtype=torch.float16, device="cuda")
+    a[0, :, 0] = 60000.0                                   # every rank 60000 * 60000 * 2 in each row,
+    a[0, 1::2, 0] = -60000.0
+    x = torch.zeros((T, k), dtype=torch.float16, device="cuda")
+    x[:, 0] = 60000.0
+    y = torch.zeros((T, n), device="cuda")
+    scale = torch.ones(1, device="cuda")
+    plan, ad = tq.exl3_adapter_plan(_i32([0, T]), _i32([0]), T, 1), tq.adapters(a, b, scale)
+    got = tq.exl3_adapter_add(x, y, ad, plan, out=torch.empty_like(y))
+    assert (got == 0).all()                                # which cancel
+    a[0, 2, 1] = math.inf                                  # and one of them infinite where x has a 1
+    a[0, :, 1] = torch.where(a[0, :, 1].isinf(), a[0, :, 1], torch.zeros_like(a[0, :, 1]))
+    x[T // 2, 1] = 1.0
+    x[:T // 2, 1] = 0.25
+    x[T // 2 + 1:, 1] = -2.0
+    got = tq.exl3_adapter_add(x, y, tq.adapters(a, b, scale), plan, out=torch.empty_like(y))
+    assert (got[:T // 2 + 1] == math.inf).all() and (got[T // 2 + 1:] == -math.inf).all()

@@ -133,5 +133,14 @@ __device__ __forceinline__ int row_exponent(float top) {
   return min(14 - ilogbf(top), 126);
 }
 
+// z (an h times its row's power of two) as hi + lo.  `far`: the row's largest is
+// infinite; its infinities and NaN decide every output then, so the finite ones,
+// which may lie above fp16's range, become zeros, and nothing is left for lo.
+__device__ __forceinline__ void split_h(float z, bool far, __half &hi, __half &lo) {
+  if (far && isfinite(z)) z = 0.0f;
+  hi = __float2half_rn(z);
+  lo = __float2half_rn(far ? 0.0f : z - __half2float(hi));
+}
+
 }  // namespace ad
 }  // namespace exl3

@@ -215,12 +215,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) adapter_step_kernel(const Arg
     const float f = scalbnf(1.0f, p);
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (c0 + 16 * i < RMAX) {
-        const float z = v[i] * f;
-        const __half hi = __float2half_rn(z);
-        hs[0][r][c0 + 16 * i] = hi;
-        hs[1][r][c0 + 16 * i] = __float2half_rn(z - __half2float(hi));
-      }
+      if (c0 + 16 * i < RMAX) split_h(v[i] * f, isinf(top), hs[0][r][c0 + 16 * i], hs[1][r][c0 + 16 * i]);
     if (c0 == 0) back[r] = __ldg(a.scale + tile.x) * scalbnf(1.0f, -p);
   }
   cluster_arrive();                                             // (its sums may go once the others have read them)

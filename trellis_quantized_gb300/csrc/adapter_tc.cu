@@ -332,9 +332,9 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float z0 = v[2 * i] * f, z1 = v[2 * i + 1] * f;
-        const __half2 h = __floats2half2_rn(z0, z1);
-        const __half2 l = __floats2half2_rn(z0 - __low2float(h), z1 - __high2float(h));
+        __half2 h, l;
+        split_h(v[2 * i] * f, isinf(top), h.x, l.x);
+        split_h(v[2 * i + 1] * f, isinf(top), h.y, l.y);
         hi[i] = *reinterpret_cast<const uint32_t *>(&h);
         lo[i] = *reinterpret_cast<const uint32_t *>(&l);
       }
