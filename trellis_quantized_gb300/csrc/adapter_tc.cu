@@ -53,6 +53,28 @@ struct OutArgs {
   int wide;               // out may be written 32 bytes at a time
 };
 
+// Rings of the output kernel: 224 KB hold h, blocks of B (as far ahead as y, behind
+// whose copies theirs queue: two blocks and ten pieces took 109 us on the prompts
+// above) and pieces of y.  The places for pieces are a multiple of a block's pieces, so
+// that a place always serves the same four warps: a warp that did not see each of its
+// phases could not tell them apart.
+struct Rings {
+  int stages, y_stages;
+};
+constexpr Rings out_rings(int panels, bool f32) {
+  return {panels == 1 ? 4 : f32 ? 3 : 2, panels == 1 ? 8 : f32 ? 4 : 6};
+}
+constexpr size_t out_smem(int panels, Rings r) {
+  return 1024 + ((2 + r.stages) * (size_t)panels + r.y_stages) * kPanel + (6 + 2 * kBStages + 2 * kYPlaces) * 8 + 16;
+}
+constexpr bool rings_fit(int panels, bool f32) {
+  const Rings r = out_rings(panels, f32);
+  return r.y_stages % (f32 ? 4 : 2) == 0 && r.y_stages <= kYPlaces && r.stages <= kBStages &&
+         out_smem(panels, r) <= 227 * 1024;
+}
+static_assert(rings_fit(1, false) && rings_fit(1, true) && rings_fit(2, false) && rings_fit(2, true),
+              "whole blocks of pieces, a barrier for every place, the shared memory of a CTA");
+
 // Four rows of a tensor map (its box is one row), 64 columns each.
 __device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *m, uint64_t *bar, int x, const int4 &rows) {
   asm volatile(
@@ -735,8 +757,7 @@ int launch_out(const ad::OutArgs &g, cudaStream_t s) {
     rc = map_rows(&mr, a.y, 2, dims, stride, row, F32);
     if (rc) return rc;
   }
-  const size_t smem = 1024 + ((2 + g.stages) * (size_t)g.panels + g.y_stages) * ad::kPanel +
-                      (6 + 2 * ad::kBStages + 2 * ad::kYPlaces) * 8 + 16;
+  const size_t smem = ad::out_smem(g.panels, {g.stages, g.y_stages});
   auto kfn = ad::adapter_out_kernel<F32>;
   static std::atomic<size_t> given[kMaxDevices];
   int rc = exl3_cuda_check(exl3_ensure_smem(reinterpret_cast<const void *>(kfn), smem, given), "adapter attribute");
@@ -753,13 +774,9 @@ int exl3_launch_adapter_tc(const ad::Args &a, bool f32, cudaStream_t s) {
   ad::OutArgs g = {};
   g.a = a;
   g.panels = (a.R + 63) / 64;
-  // 224 KB: h, blocks of B (as far ahead as y, behind whose copies theirs queue: two
-  // blocks and ten pieces took 109 us on the prompts above), pieces of y.  The places
-  // for pieces are a multiple of a block's pieces, so that a place always serves the
-  // same four warps: a warp that did not see each of its phases could not tell them
-  // apart.
-  g.stages = g.panels == 1 ? 4 : f32 ? 3 : 2;
-  g.y_stages = g.panels == 1 ? 8 : f32 ? 4 : 6;
+  const ad::Rings r = ad::out_rings(g.panels, f32);
+  g.stages = r.stages;
+  g.y_stages = r.y_stages;
   g.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride * (f32 ? 4 : 2) % 32 == 0;
   return f32 ? launch_out<true>(g, s) : launch_out<false>(g, s);
 }
