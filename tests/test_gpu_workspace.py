@@ -119,3 +119,36 @@ def test_a_linear_captured_without_a_call_before(stream):
         torch.cuda.synchronize()
         assert torch.equal(y, want)
     assert tq.exl3_check_device_error(ws) == 0
+
+
+def test_a_stream_is_its_handle(stream):
+    """Other libraries' stream objects: whatever has a cuda_stream."""
+    class Handle:
+        cuda_stream = stream.cuda_stream
+
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    T, k, n, R = 300, 256, 8192, 128
+    x = torch.randn((T, k), generator=g, device="cuda").half()
+    y = torch.randn((T, n), generator=g, device="cuda")
+    a = torch.randn((2, R, k), generator=g, device="cuda").half()
+    b = torch.randn((2, n, R), generator=g, device="cuda").half()
+    w = torch.randn((16, k), generator=g, device="cuda")
+    ad = tq.adapters(a, b, torch.ones(2, device="cuda"))
+    q, ids = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 70, T], [1, 0]))
+    want = tq.exl3_adapter_add(x, y, ad, tq.exl3_adapter_plan(q, ids, T, 2), out=torch.empty_like(y))
+    want_logits = tq.exl3_router_logits(x, tq.router(w))
+    out, graph = torch.empty_like(y), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    kw = dict(stream=Handle())
+    plan, router = tq.exl3_adapter_plan(q, ids, T, 2, **kw), tq.router(w, **kw)
+    logits = tq.exl3_router_logits(x, router, **kw)
+    tq.exl3_adapter_add(x, y, ad, plan, out=out, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(logits, want_logits)
+    with torch.cuda.graph(graph, stream=stream):
+        tq.exl3_adapter_add(x, y, ad, plan, out=out, **kw)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)

@@ -242,6 +242,14 @@ def _raw_stream(stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _made_on(stream):
+    """Context in which tensors are the given stream's (None: the current one's); as everywhere, all
+    that it has to have is its handle."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream.cuda_stream))
+
+
 def _stream(stream=None):
     return ctypes.c_void_p(_raw_stream(stream))
 
@@ -273,7 +281,7 @@ def workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
             _ws_outgrown.append(buf)
             nbytes = max(nbytes, 2 * size)
         on = stream if stream is not None else torch.cuda.current_stream(dev)
-        with torch.cuda.stream(on):      # (memory that another stream freed may still be in use there)
+        with _made_on(on):               # (memory that another stream freed may still be in use there)
             captured = torch.cuda.is_current_stream_capturing()
             if not captured:
                 buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
@@ -886,7 +894,7 @@ def router(w, bias=None, stream=None) -> Router:
     _on_current(w, "w")
     parts, scale = w, None
     if w.dtype == torch.float32:
-        with torch.cuda.stream(stream):
+        with _made_on(stream):
             parts = torch.empty((2, E, k), dtype=torch.float16, device=w.device)
             scale = torch.empty(E, dtype=torch.float32, device=w.device)
         _check(lib().exl3_router_pack(_ptr(w, "w"), E, k, _ptr(parts, "packed"), _ptr(scale, "scale"), _stream(stream)))
@@ -1009,7 +1017,7 @@ class AdapterPlan:
         if nbytes == 0:
             raise ValueError(f"T = {T}, batch = {batch} or count = {count} out of range")
         self.T, self.batch, self.count = T, batch, count
-        with torch.cuda.stream(stream):      # (the memory of the stream that fills it)
+        with _made_on(stream):               # (the memory of the stream that fills it)
             self.data = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.address, self.device = self.data.data_ptr(), self.data.get_device()
         exl3_workspace_clear(self.data, stream=stream)
@@ -1060,7 +1068,7 @@ def _capturing(stream, raw: int, device: int) -> bool:
         return False
     if stream is None or raw == torch._C._cuda_getCurrentRawStream(device):
         return torch._C._cuda_isCurrentStreamCapturing()
-    with torch.cuda.stream(stream):
+    with _made_on(stream):
         return torch._C._cuda_isCurrentStreamCapturing()
 
 
@@ -1098,7 +1106,7 @@ def _adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out, workspace_buf
     if not apart and workspace_buf is None and scratch_need and _capturing(stream, raw, device):
         # a graph gets scratch of its own, in its own memory: two that share the stream's would race when they
         # run at once.  Errors are found in the stream's workspace, as every captured call's are.
-        with torch.cuda.stream(stream):
+        with _made_on(stream):
             scratch = torch.empty(scratch_need, dtype=torch.uint8, device=x.device)
         apart = True
     if apart:
