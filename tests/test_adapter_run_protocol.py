@@ -66,3 +66,19 @@ def test_places_that_change_hands_are_seen(monkeypatch):
     """fp32 pieces in six places, with a copying tile between two others too."""
     assert _fault(monkeypatch, (4,), 4, 6, 2).endswith("early")
     assert _fault(monkeypatch, (2, -2, 1), 4, 6, 2).endswith("early")
+
+
+@pytest.mark.parametrize("stages", range(1, 9))
+def test_a_kernel_that_gives_up_waits_for_its_copies(stages):
+    """The waits of its last uses of a ring (use u: place u % stages, parity of phase u / stages): each blocks
+    until that use's copy has come and passes then, whatever has come of the others."""
+    for used in range(0, 3 * stages + 2):
+        last = range(max(0, used - stages), used)
+        assert len({u % stages for u in last}) == len(last)          # at most one copy on its way to each place
+        for come in (False, True):
+            for u in last:
+                phase = u // stages + come                           # phases done at the place
+                passes = (phase - 1) % 2 == u // stages % 2          # of a wait on a parity
+                assert passes == come
+        for u in range(last.start):                                  # earlier copies had come before the place was used again
+            assert any(v % stages == u % stages and v > u for v in last)

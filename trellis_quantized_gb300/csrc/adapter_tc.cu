@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
   uint8_t *ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);      // operands, then the sums
   uint64_t *full = reinterpret_cast<uint64_t *>(ring + g.ring_bytes), *empty = full + 8, *done = empty + 8;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
-  volatile int *failed = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  volatile int *failed = reinterpret_cast<volatile int *>(tmem_slot + 1), *used = failed + 1;   // (uses of the ring)
   const Args &a = g.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, split = blockIdx.x;
 
@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
     return;
   }
   const int KB = a.k / 64, kb0 = KB * split / S, kb1 = KB * (split + 1) / S;
+  if (threadIdx.x == 0) *used = kb1 - kb0;
   const int stage_bytes = kPanel + g.r16 * 128;
   const int pitch = g.r16 + 4;                                      // floats between rows of sums
   const auto bring = [&](int st, int kb) {                          // (warp 0)
@@ -261,6 +262,7 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
       const bool ok = __all_sync(0xffffffffu, lane != 0 || tc::mbar_wait(&empty[st], phase));
       if (!ok) {
         *failed = 1;
+        *used = kb - kb0;
         break;
       }
       bring(st, kb);
@@ -372,7 +374,10 @@ __global__ void __launch_bounds__(kInThreads) adapter_in_kernel(const __grid_con
   }
   cluster_arrive();
   cluster_wait();                                                   // nobody leaves while its sums are read
-  if (*failed && threadIdx.x == 0) set_device_error(a.err, kErrBounds);
+  if (*failed && threadIdx.x == 0) {
+    set_device_error(a.err, kErrBounds);
+    tc::drain(full, g.stages, *used);                               // leave no copy in flight behind
+  }
   if (warp == 1) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, g.tmem_cols);
@@ -479,7 +484,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) adapter_out_kernel(const __gri
   }
 
   int4 tile;
-  int nb0, nb1;
+  int nb0, nb1, used = 0, h_used = 0;                               // (of B's or y's ring, and of h's place)
   bool ok = true;
   if (warp == 0) {
     if (lane == 0) {
@@ -494,12 +499,14 @@ __global__ void __launch_bounds__(kOutThreads, 1) adapter_out_kernel(const __gri
         tc::mbar_arrive_expect_tx(h_full, 2 * bytes);
         for (int p = 0; p < 2 * g.panels; ++p)
           tc::tma_load_3d(hs + p * kPanel, &mh, h_full, p % g.panels * 64, tile.y, p / g.panels);
+        ++h_used;
         for (int nb = nb0; nb < nb1; ++nb) {
           ok = tc::mbar_wait(&empty[st], phase ^ 1);
           if (!ok) break;
           tc::mbar_arrive_expect_tx(&full[st], bytes);
           for (int p = 0; p < g.panels; ++p)
             tma_load_5d(ring + st * bytes + p * kPanel, &mb, &full[st], p * 64, (tile.x * run.NB + nb) * (F32 ? 4 : 2));
+          ++used;
           if (++st == g.stages) { st = 0; phase ^= 1; }
         }
       }
@@ -549,6 +556,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) adapter_out_kernel(const __gri
         if (tc::elect_one()) tc::mbar_arrive_expect_tx(&y_full[st], rows.bytes());
         __syncwarp();
         rows.copy(ys + st * kPanel, &my, &mr, &y_full[st], p * PCOLS, lane);
+        ++used;
         if (++st == g.y_stages) { st = 0; phase ^= 1; }
       }
     }
@@ -635,7 +643,15 @@ __global__ void __launch_bounds__(kOutThreads, 1) adapter_out_kernel(const __gri
   if (!ok) *failed = 1;
   tc::tc_fence_before();
   __syncthreads();
-  if (*failed && threadIdx.x == 0) set_device_error(a.err, kErrBounds);
+  if (*failed) {                                                    // leave no copy in flight behind
+    if (threadIdx.x == 0) {
+      set_device_error(a.err, kErrBounds);
+      tc::drain(full, g.stages, used);
+      tc::drain(h_full, 1, h_used);
+    } else if (warp == 2 + kEpiWarps && lane == 0) {
+      tc::drain(y_full, g.y_stages, used);
+    }
+  }
   if (warp == 1) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, kOutCols);
@@ -703,7 +719,7 @@ int launch_in(const ad::Args &a, cudaStream_t s) {
   g.stages = std::min(8, g.ring_bytes / stage);
   g.tmem_cols = 32;
   while ((int)g.tmem_cols < g.r16) g.tmem_cols *= 2;
-  const size_t smem = 1024 + g.ring_bytes + 17 * 8 + 8;
+  const size_t smem = 1024 + g.ring_bytes + 17 * 8 + 16;
   CUtensorMap mx, mt, ma;      // x for gathers of rows and for boxes; A
   {
     const cuuint64_t dims[2] = {(cuuint64_t)a.k, (cuuint64_t)a.T}, stride[1] = {(cuuint64_t)a.x_stride * 2};

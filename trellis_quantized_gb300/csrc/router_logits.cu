@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) logits_tc_kernel(const __gri
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + a.data_bytes);
   uint64_t *empty = full + a.stages, *done = empty + a.stages;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
-  volatile int *failed = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  volatile int *failed = reinterpret_cast<volatile int *>(tmem_slot + 1), *used = failed + 1;   // (uses of the ring)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = gridDim.x, split = blockIdx.x, m0 = blockIdx.y * BM, n0 = blockIdx.z * a.bn;
   const int KB = (a.k + BK - 1) / BK;
@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) logits_tc_kernel(const __gri
     }
     tc::mbar_init(done, 1);
     *failed = 0;
+    *used = kb1 - kb0;
     tc::fence_mbar_init();
     tc::prefetch_tmap(&mx);
     tc::prefetch_tmap(&mw);
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) logits_tc_kernel(const __gri
       for (int kb = ahead; kb < kb1; ++kb) {
         if (!tc::mbar_wait(&empty[st], phase)) {
           *failed = 1;
+          *used = kb - kb0;
           break;
         }
         bring(st, kb);
@@ -270,7 +272,10 @@ __global__ void __launch_bounds__(kLogitThreads, 1) logits_tc_kernel(const __gri
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (*failed && threadIdx.x == 0) set_device_error(a.err, kErrBounds);
+  if (*failed && threadIdx.x == 0) {
+    set_device_error(a.err, kErrBounds);
+    tc::drain(full, a.stages, *used);                       // leave no copy in flight behind
+  }
   if (S > 1) cluster_sync();
 
   // this CTA's rows of the tile, summed over the cluster in the order of k

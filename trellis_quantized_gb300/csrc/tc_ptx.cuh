@@ -79,6 +79,14 @@ __device__ __forceinline__ bool mbar_wait_backoff(uint64_t *bar, uint32_t parity
   return true;
 }
 
+// For a kernel that gives up, before its shared memory goes: waits (bounded) for the
+// copies of a ring whose `used`-th use was its last; full[u % stages] is in phase
+// u / stages until use u has come.  (Out of line: hardly ever called.)
+static __device__ __noinline__ void drain(uint64_t *full, int stages, int used) {
+  for (int u = used > stages ? used - stages : 0; u < used; ++u)
+    if (!mbar_wait(&full[u % stages], (u / stages) & 1)) return;
+}
+
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *m) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
