@@ -20,7 +20,10 @@ namespace {
 //   k 17408, n 5120: rank 16: 1536 rows 24 and 25, 4096 56 and 49; rank 128: 256 rows 30 and 25.
 // Rows of many short sequences gather, which costs the large tiles up to twice as much
 // (768 rows of rank 16, n 17408: 22 and 36).  Over 1200 such calls the time is 1.03 of
-// the better side's.  (The small tiles' grid stays within 2^15 tiles: T < 2^18 here.)
+// the better side's; in all of them n is 0.29 k or more.  With fewer columns beside a
+// wide input the small tiles, which read all of A for every 16 rows, are kept for too
+// long (k 17408, n 128, rank 128: to T = 6472); that was not measured.
+// (The small tiles' grid stays within 2^15 tiles: T < 2^18 here.)
 bool large_tiles(int T, int R, int n) { return T >= 48 && (int64_t)T * (R + 16) * (R + 16) * n >= (int64_t)1 << 34; }
 
 bool plan_shape_ok(int T, int batch, int count) {

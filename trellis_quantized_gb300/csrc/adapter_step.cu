@@ -21,8 +21,8 @@
 // row is brought to [2^14, 2^15) by a power of two: 22 bits of every h, so that
 // an fp32 out is as good as its fp32 sums.  Up to eight rows (most tiles of a step)
 // hi takes the upper half of the product's 16 rows and lo the lower, and the lane
-// that holds both results adds them: one product where 9 to 16 rows take two, which
-// at rank 64 are a quarter of the time (64 users: 20 us against 15 with one).
+// that holds both results adds them: one product where 9 to 16 rows take two (64 users
+// of ranks to 64, 17408 columns: 16.0 us, 17.9 with two products for every tile).
 #include "adapter.cuh"
 #include "tc_ptx.cuh"
 
@@ -328,8 +328,8 @@ cudaError_t launch_step(const ad::Args &a, bool f32, int S, cudaStream_t s) {
 cudaError_t exl3_launch_adapter_step(const ad::Args &a, bool f32, cudaStream_t s) {
   // The largest cluster of which all run at once at two CTAs per SM (30 of eight and
   // 72 of four on 152 SMs; 128 users on 48 adapters: 12.5 us in clusters of eight, 9.0 in
-  // fours); sixteen pay for single tiles only (one of rank 64, 17408 columns: 12.8 and 15
-  // us, eight of rank 16: 6.8 and 6.1)
+  // fours); sixteen pay for few tiles only (one of rank 64, 17408 columns: 12.8 and 15
+  // us, eight of rank 16: 6.8 and 6.1; the border of four lies between the two)
   const int sms = exl3_sm_count();
   const int S = a.max_tiles <= 4 ? 16 : a.max_tiles <= sms * 30 / 152 ? 8 : a.max_tiles <= sms * 72 / 152 ? 4 : 2;
   if (a.R <= 16) return launch_step<2, 1>(a, f32, S, s);

@@ -13,7 +13,7 @@
 //
 // x, y, A and B are read once and out is written once; h goes through L2.  Up to
 // 4 R / 3 operations per byte: HBM bounds it at every rank, mostly by y and out.
-// Four prompts of 6301 tokens, rank 16, 5120 -> 17408, take 100 us: 21 and 79, the
+// Four prompts of 6301 tokens, rank 16, 5120 -> 17408, take 98 us: 19 and 79, the
 // second 439 MB of y and out at 0.8 of the copy rate.  One launch (the cluster keeps h
 // and splits the columns too) took 228: 50 tiles are two rounds of clusters, one of
 // them almost empty.

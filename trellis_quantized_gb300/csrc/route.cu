@@ -21,7 +21,9 @@
 // floats (about 45 bits).  Not in 64-bit floats: this chip has so few units for
 // those that one such row took 15 us.  Neighbouring picks that are too close
 // are put in order among themselves, a lane each; only groups that are, and more
-// than 32 equal picks, take the whole row.
+// than 32 close picks, take the whole row.  Where all scores are below the bound (a
+// sigmoid of logits around -15 and a bias of zero) that is every row: 44 us for 2500
+// tokens of 256 experts, 8.2 around 0.
 #include <algorithm>
 #include <climits>
 
