@@ -152,3 +152,23 @@ def test_a_stream_is_its_handle(stream):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_a_device_too_full_for_twice_the_size(stream, monkeypatch):
+    """Then the size that was asked for has to do."""
+    empty, asked = torch.empty, []
+
+    def full(size, **kw):
+        asked.append(size)
+        if size > 3 << 20:
+            raise torch.OutOfMemoryError("full")
+        return empty(size, **kw)
+
+    with torch.cuda.stream(stream):
+        first = tq.workspace(2 << 20)
+        monkeypatch.setattr(torch, "empty", full)
+        ws = tq.workspace(3 << 20)
+        assert asked == [4 << 20, 3 << 20] and ws.numel() == 3 << 20 and not ws.any()
+        with pytest.raises(torch.OutOfMemoryError):
+            tq.workspace(5 << 20)
+        assert tq.workspace(1).data_ptr() == ws.data_ptr() != first.data_ptr()

@@ -277,20 +277,31 @@ def workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
     buf, _, size = _ws_cache.get(key, (None, 0, -1))
     if size < nbytes:
         dev = torch.device("cuda", index)
+        on = stream if stream is not None else torch.cuda.current_stream(dev)
+        sizes = [max(nbytes, 256)]
         if buf is not None and raw:
             _ws_outgrown.append(buf)
-            nbytes = max(nbytes, 2 * size)
-        on = stream if stream is not None else torch.cuda.current_stream(dev)
-        with _made_on(on):               # (memory that another stream freed may still be in use there)
-            captured = torch.cuda.is_current_stream_capturing()
-            if not captured:
-                buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        if captured:
-            buf = _outside_captures(max(nbytes, 256), dev)
-        else:
-            exl3_workspace_clear(buf, stream=on)
+            sizes.insert(0, max(nbytes, 2 * size))
+        for n in sizes:
+            try:
+                buf = _cleared(n, dev, on, raw)
+                break
+            except torch.OutOfMemoryError:
+                if n == sizes[-1]:
+                    raise
         _ws_cache[key] = (buf, buf.data_ptr(), buf.numel())
     return buf
+
+
+def _cleared(nbytes: int, device, on, raw: int) -> torch.Tensor:
+    """A zero-filled buffer of the given stream's memory (what another stream freed may still be in
+    use there)."""
+    with _made_on(on):
+        if not raw or not torch.cuda.is_current_stream_capturing():
+            buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            exl3_workspace_clear(buf, stream=on)
+            return buf
+    return _outside_captures(nbytes, device)
 
 
 def _outside_captures(nbytes: int, device) -> torch.Tensor:
